@@ -28,7 +28,8 @@ MOE_OP_DISPATCH, MOE_OP_FFN, MOE_OP_CALIBRATE, MOE_OP_TOKEN_WEIGHTS, MOE_OP_ROUT
 ROUTE_DISPATCH_MAX_T, ROUTE_DISPATCH_MAX_SLOTS = 256, 2048
 DECODE_LAYER_MAX_T = 64
 MOE_SLOT_KEPT, MOE_SLOT_REROUTED, MOE_SLOT_DROPPED = 0, 1, 2
-MOE_DEV_OK, MOE_DEV_NONFINITE, MOE_DEV_TIMEOUT, MOE_DEV_BAD_INDEX = 0, 1, 2, 3
+MOE_DEV_OK, MOE_DEV_NONFINITE, MOE_DEV_TIMEOUT, MOE_DEV_BAD_INDEX, MOE_DEV_NO_PAGES = 0, 1, 2, 3, 4
+MOE_KV4_PAGE, MOE_KV4_BLOCK = 64, 16
 
 _lock = threading.Lock()
 _lib = None
@@ -43,8 +44,30 @@ class _SereParams(ctypes.Structure):
                 ("protect", ctypes.c_void_p), ("union_bitmap", ctypes.c_void_p), ("stats", ctypes.c_void_p)]
 
 
+class _Kv4CacheParams(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("S", ctypes.c_int32), ("n_kv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class _RopeParams(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("axis", ctypes.c_void_p),
+                ("n_pos", ctypes.c_int32), ("rot", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("pairs", ctypes.c_int32)]
+
+
+class _Kv4PoolParams(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("layer_stride", ctypes.c_longlong), ("page_bytes", ctypes.c_longlong),
+                ("page_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p), ("ref", ctypes.c_void_p),
+                ("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("S", ctypes.c_int32)]
+
+
 EXPORTS = ["moe_route", "moe_route_dispatch", "moe_decode_layer", "moe_reroute_sere", "moe_dispatch_capacity", "moe_ffn_grouped", "moe_combine",
-           "moe_residual_to_bf16", "moe_token_weights", "moe_similarity_calibrate", "moe_workspace_size", "moe_status_string"]
+           "moe_residual_to_bf16", "moe_token_weights", "moe_similarity_calibrate", "moe_workspace_size", "moe_status_string",
+           "moe_qk_norm_rope", "moe_attention_kv4", "moe_attention_kv4_workspace", "moe_kv4_read", "moe_kv4_reserve",
+           "moe_kv4_assign", "moe_kv4_compact", "moe_kv4_page_bytes", "moe_kv4_pool_workspace"]
 
 
 def load(path: str = LIB_PATH):
@@ -86,6 +109,25 @@ def load(path: str = LIB_PATH):
             L.moe_workspace_size.restype = sz
             L.moe_status_string.argtypes = [i, i]
             L.moe_status_string.restype = ctypes.c_char_p
+            ll = ctypes.c_longlong
+            L.moe_kv4_page_bytes.argtypes = [i, i]
+            L.moe_kv4_page_bytes.restype = sz
+            L.moe_qk_norm_rope.argtypes = [p, i, ll, i, i, i, i, p, p, f, p, p, ll, p, ll, p, p, p, p]
+            L.moe_qk_norm_rope.restype = i
+            L.moe_kv4_read.argtypes = [p, p, i, p, p, p, p]
+            L.moe_kv4_read.restype = i
+            L.moe_attention_kv4.argtypes = [p, ll, i, i, p, p, i, f, i, p, ll, p, p, sz, p, p]
+            L.moe_attention_kv4.restype = i
+            L.moe_attention_kv4_workspace.argtypes = [i, i, i, i]
+            L.moe_attention_kv4_workspace.restype = sz
+            L.moe_kv4_reserve.argtypes = [p, p, p, sz, p, p]
+            L.moe_kv4_reserve.restype = i
+            L.moe_kv4_assign.argtypes = [p, p, p, p]
+            L.moe_kv4_assign.restype = i
+            L.moe_kv4_compact.argtypes = [p, p, p, sz, p, p]
+            L.moe_kv4_compact.restype = i
+            L.moe_kv4_pool_workspace.argtypes = [i, i]
+            L.moe_kv4_pool_workspace.restype = sz
             _lib = L
     return _lib
 
@@ -287,3 +329,243 @@ def moe_similarity_calibrate(x, w_gate, w_up, w_down, sim, workspace, st=None, s
     rc = load().moe_similarity_calibrate(_ptr(x), n, _ptr(w_gate), _ptr(w_up), _ptr(w_down), H, I, N, _ptr(sim),
                                          _ptr(workspace), ws_bytes, _ptr(st), _stream(stream))
     _check(rc, "moe_similarity_calibrate")
+
+
+# ---------------------------------------------------------------------------
+# The attention half of a layer: norms, rotary positions, the 4-bit cache
+# ---------------------------------------------------------------------------
+def _addr(t: Optional[torch.Tensor], dtype=None, what: str = "") -> Optional[int]:
+    """A CUDA tensor's address; checks its dtype and that it is dense."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise MoeError("%s: expected a CUDA tensor" % what)
+    if dtype is not None and t.dtype != dtype:
+        raise MoeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise MoeError("%s: expected a dense tensor" % what)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, width: int, dtype, what: str):
+    """(address, leading dimension) of rows of `width` numbers whose trailing
+    dimensions are dense; only the first may have a stride of its own."""
+    if not t.is_cuda:
+        raise MoeError("%s: expected a CUDA tensor" % what)
+    if t.dtype != dtype:
+        raise MoeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
+    shape, stride = t.shape, t.stride()
+    n = 1
+    for k in range(t.dim() - 1, 0, -1):
+        if stride[k] != n and shape[k] != 1:
+            raise MoeError("%s: only the rows may be strided" % what)
+        n *= shape[k]
+    if t.dim() < 2 or n != width:
+        raise MoeError("%s: expected rows of %d numbers, got %s" % (what, width, list(shape)))
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else max(stride[0], width))
+
+
+class Kv4Cache:
+    """One layer's 4-bit paged cache, as the kernels see it (moe_kv4_cache):
+    pages [n_pages][n_kv][64 * (D + D/8)] uint8, page_table [S][max_pages] and
+    seq_len [S] int32, head_dim D, optional k_scale and v_scale [n_kv] fp32.
+    Holds the tensors; keep it for as long as the cache is used."""
+
+    def __init__(self, pages, page_table, seq_len, head_dim: int, k_scale=None, v_scale=None):
+        if pages.dim() != 3 or pages.shape[2] != MOE_KV4_PAGE * (head_dim + head_dim // 8):
+            raise MoeError("pages: expected [n_pages][n_kv][%d], got %s"
+                           % (MOE_KV4_PAGE * (head_dim + head_dim // 8), list(pages.shape)))
+        if page_table.dim() != 2 or seq_len.dim() != 1 or page_table.shape[0] != seq_len.shape[0]:
+            raise MoeError("page_table is [S][max_pages] and seq_len [S]")
+        self.n_pages, self.n_kv = pages.shape[0], pages.shape[1]
+        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None and t.numel() != self.n_kv:
+                raise MoeError("%s: expected %d numbers" % (what, self.n_kv))
+        self.head_dim, self.S = head_dim, seq_len.shape[0]
+        self.tensors = (pages, page_table, seq_len, k_scale, v_scale)
+        i32, f32 = torch.int32, torch.float32
+        self._c = _Kv4CacheParams(_addr(pages, torch.uint8, "pages"), _addr(page_table, i32, "page_table"),
+                                  _addr(seq_len, i32, "seq_len"), _addr(k_scale, f32, "k_scale"),
+                                  _addr(v_scale, f32, "v_scale"), self.n_pages, page_table.shape[1], self.S,
+                                  self.n_kv, head_dim)
+        self._ref = ctypes.addressof(self._c)
+
+
+class Rope:
+    """Rotary positions (moe_rope_params): table [n_pos][rot/2][2] fp32 of
+    (cos, sin), positions [axes][T] int32 (None: the place in the sequence),
+    axis [rot/2] uint8 (None: axis 0 for every pair), pairs: neighbours are
+    rotated together instead of the two halves."""
+
+    def __init__(self, table, positions=None, axis=None, pairs: bool = False):
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise MoeError("table: expected [n_pos][rot/2][2], got %s" % list(table.shape))
+        if positions is not None and positions.dim() != 2:
+            raise MoeError("positions: expected [axes][T]")
+        if axis is not None and axis.numel() != table.shape[1]:
+            raise MoeError("axis: expected %d numbers" % table.shape[1])
+        self.tensors = (table, positions, axis)
+        self.T = None if positions is None else positions.shape[1]
+        self._c = _RopeParams(_addr(table, torch.float32, "table"), _addr(positions, torch.int32, "positions"),
+                              _addr(axis, torch.uint8, "axis"), table.shape[0], 2 * table.shape[1],
+                              1 if positions is None else positions.shape[0], 1 if pairs else 0)
+        self._ref = ctypes.addressof(self._c)
+
+
+class Kv4Pool:
+    """The pages of a cache of several layers (moe_kv4_pool): pages
+    [n_layers][n_pages][n_kv][64 * (D + D/8)] uint8, page_table
+    [S][max_pages], seq_len [S] and ref [n_pages] int32.  Holds the tensors."""
+
+    def __init__(self, pages, page_table, seq_len, ref, head_dim: int):
+        if pages.dim() != 4 or pages.shape[3] != MOE_KV4_PAGE * (head_dim + head_dim // 8):
+            raise MoeError("pages: expected [n_layers][n_pages][n_kv][%d], got %s"
+                           % (MOE_KV4_PAGE * (head_dim + head_dim // 8), list(pages.shape)))
+        if page_table.dim() != 2 or page_table.shape[0] != seq_len.numel() or ref.numel() != pages.shape[1]:
+            raise MoeError("page_table is [S][max_pages], seq_len [S] and ref [n_pages]")
+        self.tensors = (pages, page_table, seq_len, ref)
+        self.head_dim, self.n_layers, self.n_pages, self.S = head_dim, pages.shape[0], pages.shape[1], seq_len.numel()
+        i32 = torch.int32
+        page_bytes = pages.shape[2] * pages.shape[3]
+        self._c = _Kv4PoolParams(_addr(pages, torch.uint8, "pages"), self.n_pages * page_bytes, page_bytes,
+                                 _addr(page_table, i32, "page_table"), _addr(seq_len, i32, "seq_len"),
+                                 _addr(ref, i32, "ref"), self.n_layers, self.n_pages, page_table.shape[1], self.S)
+        self._ref = ctypes.addressof(self._c)
+
+    def layer(self, i: int, k_scale=None, v_scale=None) -> Kv4Cache:
+        """Layer i's cache."""
+        pages, page_table, seq_len, _ = self.tensors
+        return Kv4Cache(pages[i], page_table, seq_len, self.head_dim, k_scale, v_scale)
+
+
+def kv4_page_bytes(n_kv: int, head_dim: int) -> int:
+    return int(load().moe_kv4_page_bytes(n_kv, head_dim))
+
+
+def attention_kv4_workspace(T: int, n_q: int, n_kv: int, head_dim: int) -> int:
+    return int(load().moe_attention_kv4_workspace(T, n_q, n_kv, head_dim))
+
+
+def kv4_pool_workspace(pool: Kv4Pool) -> int:
+    return int(load().moe_kv4_pool_workspace(pool.S, pool.n_pages))
+
+
+def _raw_stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _check_starts(q_start, S: int):
+    if q_start.numel() != S + 1:
+        raise MoeError("q_start: expected %d numbers, got %d" % (S + 1, q_start.numel()))
+    return _addr(q_start, torch.int32, "q_start")
+
+
+def moe_qk_norm_rope(qkv, n_q: int, n_kv: int, q_out, k_out=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                     rope: Optional[Rope] = None, cache: Optional[Kv4Cache] = None, q_start=None, st=None,
+                     stream=None):
+    """Norms of q and k for each head (q_weight, k_weight [D] fp32; None = no
+    norm), rotary positions and the append of k and v to `cache` (with q_start
+    [S+1] int32), in one launch.  qkv [T][(n_q + 2 n_kv) D] bf16 or fp32, q_out
+    [T][n_q][D] and k_out [T][n_kv][D] of the same dtype; rows may be strided,
+    and q_out may be qkv's own query part."""
+    T, width = qkv.shape[0], 1
+    for d in qkv.shape[1:]:
+        width *= d
+    if n_q + 2 * n_kv < 1 or width % (n_q + 2 * n_kv):
+        raise MoeError("qkv: rows of %d numbers are not %d heads" % (width, n_q + 2 * n_kv))
+    D = width // (n_q + 2 * n_kv)
+    x, ld = _rows(qkv, width, qkv.dtype, "qkv")
+    q, ld_q = (None, 0) if n_q == 0 else _rows(q_out, n_q * D, qkv.dtype, "q_out")
+    k, ld_k = (None, 0) if k_out is None else _rows(k_out, n_kv * D, qkv.dtype, "k_out")
+    for t, what in ((None if n_q == 0 else q_out, "q_out"), (k_out, "k_out")):
+        if t is not None and t.shape[0] != T:
+            raise MoeError("%s: expected %d rows, got %d" % (what, T, t.shape[0]))
+    for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None and t.numel() != D:
+            raise MoeError("%s: expected %d numbers" % (what, D))
+    if rope is not None and rope.T is not None and rope.T != T:
+        raise MoeError("positions: expected %d tokens, got %d" % (T, rope.T))
+    if cache is not None and q_start is None:
+        raise MoeError("a cache needs q_start")
+    f32 = torch.float32
+    rc = load().moe_qk_norm_rope(x, _dtype_code(qkv), ld, T, n_q, n_kv, D, _addr(q_weight, f32, "q_weight"),
+                                 _addr(k_weight, f32, "k_weight"), eps, None if rope is None else rope._ref, q, ld_q, k,
+                                 ld_k, None if cache is None else cache._ref,
+                                 None if cache is None else _check_starts(q_start, cache.S),
+                                 _addr(st, torch.int32, "st"), _raw_stream(stream))
+    _check(rc, "moe_qk_norm_rope")
+
+
+def moe_kv4_read(cache: Kv4Cache, q_start, k_out=None, v_out=None, st=None, stream=None):
+    """The last q_start[s+1] - q_start[s] tokens of every sequence as values:
+    k_out, v_out [T][n_kv][D] bf16."""
+    T = 0
+    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            if t.dim() != 3 or t.shape[1] != cache.n_kv or t.shape[2] != cache.head_dim or (T and t.shape[0] != T):
+                raise MoeError("%s: expected [T][%d][%d], got %s" % (what, cache.n_kv, cache.head_dim, list(t.shape)))
+            T = t.shape[0]
+    bf = torch.bfloat16
+    rc = load().moe_kv4_read(cache._ref, _check_starts(q_start, cache.S), T, _addr(k_out, bf, "k_out"),
+                             _addr(v_out, bf, "v_out"), _addr(st, torch.int32, "st"), _raw_stream(stream))
+    _check(rc, "moe_kv4_read")
+
+
+def moe_attention_kv4(q, cache: Kv4Cache, q_start, out, scale: float, max_new: int, window: int = 0, lse=None,
+                      workspace=None, st=None, stream=None):
+    """Attention over the cache: rows q_start[s] .. q_start[s+1]-1 of q
+    [T][n_q][D] bf16 are the last tokens of sequence s; out like q, lse
+    [T][n_q] fp32.  max_new bounds the rows of a sequence.  workspace:
+    attention_kv4_workspace(...) bytes, zero-filled before its first use; when
+    omitted a buffer is allocated for this call (not graph-capturable)."""
+    D = cache.head_dim
+    if q.dim() != 3 or q.shape[2] != D:
+        raise MoeError("q: expected [T][n_q][%d], got %s" % (D, list(q.shape)))
+    T, n_q = q.shape[0], q.shape[1]
+    if out.shape[0] != T:
+        raise MoeError("out: expected %d rows, got %d" % (T, out.shape[0]))
+    qp, ld_q = _rows(q, n_q * D, torch.bfloat16, "q")
+    op, ld_o = _rows(out, n_q * D, torch.bfloat16, "out")
+    if lse is not None and lse.numel() != T * n_q:
+        raise MoeError("lse: expected [%d][%d]" % (T, n_q))
+    if workspace is None:
+        n = attention_kv4_workspace(T, n_q, cache.n_kv, D)
+        workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
+    rc = load().moe_attention_kv4(qp, ld_q, T, n_q, cache._ref, _check_starts(q_start, cache.S), max_new, scale, window,
+                                  op, ld_o, _addr(lse, torch.float32, "lse"), _addr(workspace, None, "workspace"),
+                                  workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
+                                  _raw_stream(stream))
+    _check(rc, "moe_attention_kv4")
+
+
+def _pool_vector(t, pool: Kv4Pool, what: str) -> int:
+    if t.numel() != pool.S:
+        raise MoeError("%s: expected %d numbers, got %d" % (what, pool.S, t.numel()))
+    return _addr(t, torch.int32, what)
+
+
+def moe_kv4_reserve(pool: Kv4Pool, n_new, workspace, st=None, stream=None):
+    """Room for n_new [S] int32 more tokens of every sequence (negative: fewer),
+    shared last pages copied first.  workspace: kv4_pool_workspace(pool) bytes,
+    zero-filled before its first use."""
+    rc = load().moe_kv4_reserve(pool._ref, _pool_vector(n_new, pool, "n_new"), _addr(workspace, None, "workspace"),
+                                workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
+                                _raw_stream(stream))
+    _check(rc, "moe_kv4_reserve")
+
+
+def moe_kv4_assign(pool: Kv4Pool, parent, st=None, stream=None):
+    """Every sequence becomes what parent[s] was (parent [S] int32, -1 = empty):
+    forking, reordering and freeing."""
+    rc = load().moe_kv4_assign(pool._ref, _pool_vector(parent, pool, "parent"), _addr(st, torch.int32, "st"),
+                               _raw_stream(stream))
+    _check(rc, "moe_kv4_assign")
+
+
+def moe_kv4_compact(pool: Kv4Pool, n_live, workspace, st=None, stream=None):
+    """Moves the pool's pages in use to its lowest page numbers; n_live [1]
+    int32 out (or None): their count."""
+    rc = load().moe_kv4_compact(pool._ref, _addr(n_live, torch.int32, "n_live"), _addr(workspace, None, "workspace"),
+                                workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
+                                _raw_stream(stream))
+    _check(rc, "moe_kv4_compact")

@@ -16,6 +16,29 @@ bool sere_ok(const moe_sere_params* p, int N, int k) {
     return p->sim != nullptr && p->k_primary >= 1 && p->k_primary <= k && !(p->rho != p->rho) && N <= MOE_MAX_EXPERTS;
 }
 
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+// A cache's own fields; MOE_OK if they are usable.
+moe_status_t check_cache(const moe_kv4_cache* c) {
+    if (c == nullptr || c->n_kv < 1 || c->S < 0 || c->n_pages < 0 || c->max_pages < 0) return MOE_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return MOE_ERR_UNSUPPORTED;
+    if (c->S > moe::kAttnMaxSeqs || c->n_kv > 1024) return MOE_ERR_UNSUPPORTED;
+    if (c->S > 0 && (c->pages == nullptr || c->page_table == nullptr || c->seq_len == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(c->pages)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+moe_status_t check_pool(const moe_kv4_pool* p) {
+    if (p == nullptr || p->S < 0 || p->n_pages < 0 || p->max_pages < 0 || p->n_layers < 1) return MOE_ERR_INVALID_ARG;
+    if (p->S > moe::kPoolMaxSeqs) return MOE_ERR_UNSUPPORTED;
+    if (p->page_bytes < 16 || p->page_bytes % 16 != 0 || p->layer_stride % 16 != 0) return MOE_ERR_INVALID_ARG;
+    if (p->page_bytes > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+    if (p->S > 0 && (p->page_table == nullptr || p->seq_len == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (p->n_pages > 0 && (p->pages == nullptr || p->ref == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(p->pages)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -269,13 +292,120 @@ moe_status_t moe_residual_to_bf16(const float* x, void* y, long long n, void* st
     return from_cuda(moe::launch_residual_to_bf16(x, y, n, as_stream(stream)));
 }
 
+size_t moe_kv4_page_bytes(int n_kv, int head_dim) {
+    if (n_kv < 1 || (head_dim != 64 && head_dim != 128)) return 0;
+    return static_cast<size_t>(n_kv) * MOE_KV4_PAGE * (head_dim + head_dim / 8);
+}
+
+moe_status_t moe_qk_norm_rope(const void* qkv, int dtype, long long ld, int T, int n_q, int n_kv, int head_dim,
+                              const float* q_weight, const float* k_weight, float eps, const moe_rope_params* rope,
+                              void* q_out, long long ld_q, void* k_out, long long ld_k, const moe_kv4_cache* cache,
+                              const int32_t* q_start, moe_dev_status* st, void* stream) {
+    if (T < 0 || n_q < 0 || n_kv < 1) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return MOE_ERR_UNSUPPORTED;
+    if (static_cast<long long>(n_q) + 2ll * n_kv > 1024) return MOE_ERR_UNSUPPORTED;
+    if (!(eps >= 0.f) || eps - eps != 0.f) return MOE_ERR_INVALID_ARG;
+    if (cache != nullptr) {
+        const moe_status_t rc = check_cache(cache);
+        if (rc != MOE_OK) return rc;
+        if (cache->n_kv != n_kv || cache->head_dim != head_dim || q_start == nullptr) return MOE_ERR_INVALID_ARG;
+    }
+    if (rope != nullptr) {
+        if (rope->rot < 32 || rope->rot > head_dim || rope->n_pos < 1 || rope->table == nullptr) return MOE_ERR_INVALID_ARG;
+        if (rope->rot % 32 != 0) return MOE_ERR_UNSUPPORTED;
+        if (!aligned16(rope->table)) return MOE_ERR_INVALID_ARG;
+        if (rope->positions == nullptr ? cache == nullptr : rope->axes < 1) return MOE_ERR_INVALID_ARG;
+    }
+    if (T == 0) return MOE_OK;
+    const int per16 = dtype == MOE_DTYPE_BF16 ? 8 : 4;
+    const long long width = static_cast<long long>(n_q + 2 * n_kv) * head_dim;
+    if (qkv == nullptr || !aligned16(qkv) || ld < width || ld % per16 != 0) return MOE_ERR_INVALID_ARG;
+    if (n_q > 0 && (q_out == nullptr || !aligned16(q_out) || ld_q < static_cast<long long>(n_q) * head_dim || ld_q % per16 != 0))
+        return MOE_ERR_INVALID_ARG;
+    if (k_out != nullptr && (!aligned16(k_out) || ld_k < static_cast<long long>(n_kv) * head_dim || ld_k % per16 != 0))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(q_weight) || !aligned16(k_weight)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_qk_norm_rope(qkv, dtype, ld, T, n_q, n_kv, head_dim, q_weight, k_weight, eps, rope,
+                                              q_out, ld_q, k_out, ld_k, cache, q_start, st, as_stream(stream)));
+}
+
+moe_status_t moe_kv4_read(const moe_kv4_cache* cache, const int32_t* q_start, int T, void* k_out, void* v_out,
+                          moe_dev_status* st, void* stream) {
+    const moe_status_t rc = check_cache(cache);
+    if (rc != MOE_OK) return rc;
+    if (T < 0 || q_start == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || !aligned16(v_out)) return MOE_ERR_INVALID_ARG;
+    if (T == 0 || (k_out == nullptr && v_out == nullptr)) return MOE_OK;
+    return from_cuda(moe::launch_kv4_read(*cache, q_start, T, k_out, v_out, st, as_stream(stream)));
+}
+
+size_t moe_attention_kv4_workspace(int T, int n_q, int n_kv, int head_dim) {
+    if (T < 0 || n_kv < 1 || n_q < 1 || n_q % n_kv != 0 || (head_dim != 64 && head_dim != 128)) return 0;
+    return moe::attention_kv4_workspace(T, n_q, n_kv, head_dim);
+}
+
+moe_status_t moe_attention_kv4(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache* cache,
+                               const int32_t* q_start, int max_new, float scale, int window, void* out,
+                               long long ld_out, float* lse, void* workspace, size_t ws_bytes, moe_dev_status* st,
+                               void* stream) {
+    const moe_status_t rc = check_cache(cache);
+    if (rc != MOE_OK) return rc;
+    if (T < 0 || n_q < 1 || n_q % cache->n_kv != 0 || max_new < 0 || window < 0 || q_start == nullptr)
+        return MOE_ERR_INVALID_ARG;
+    if (!(scale == scale) || scale - scale != 0.f) return MOE_ERR_INVALID_ARG;   // finite
+    if (n_q > 1024 || static_cast<long long>(T) * (n_q / cache->n_kv) > 0x7ffffff0LL) return MOE_ERR_UNSUPPORTED;
+    if (T == 0 || cache->S == 0) return MOE_OK;
+    const long long width = static_cast<long long>(n_q) * cache->head_dim;
+    if (q == nullptr || !aligned16(q) || ld_q < width || ld_q % 8 != 0) return MOE_ERR_INVALID_ARG;
+    if (out == nullptr || !aligned16(out) || ld_out < width || ld_out % 8 != 0) return MOE_ERR_INVALID_ARG;
+    if (workspace == nullptr || ws_bytes < moe::attention_kv4_workspace(T, n_q, cache->n_kv, cache->head_dim)) return MOE_ERR_WORKSPACE;
+    if (!aligned256(workspace)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_attention_kv4(q, ld_q, T, n_q, *cache, q_start, max_new, scale, window, out, ld_out, lse,
+                                               workspace, st, as_stream(stream)));
+}
+
+size_t moe_kv4_pool_workspace(int S, int n_pages) {
+    if (S < 0 || n_pages < 0) return 0;
+    return moe::kv4_pool_workspace(S, n_pages);
+}
+
+moe_status_t moe_kv4_reserve(const moe_kv4_pool* pool, const int32_t* n_new, void* workspace, size_t ws_bytes,
+                             moe_dev_status* st, void* stream) {
+    const moe_status_t rc = check_pool(pool);
+    if (rc != MOE_OK) return rc;
+    if (pool->S == 0) return MOE_OK;
+    if (n_new == nullptr) return MOE_ERR_INVALID_ARG;
+    if (workspace == nullptr || ws_bytes < moe::kv4_pool_workspace(pool->S, pool->n_pages)) return MOE_ERR_WORKSPACE;
+    if (!aligned256(workspace)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_kv4_reserve(*pool, n_new, workspace, st, as_stream(stream)));
+}
+
+moe_status_t moe_kv4_assign(const moe_kv4_pool* pool, const int32_t* parent, moe_dev_status* st, void* stream) {
+    const moe_status_t rc = check_pool(pool);
+    if (rc != MOE_OK) return rc;
+    if (pool->S == 0) return MOE_OK;
+    if (parent == nullptr) return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_kv4_assign(*pool, parent, st, as_stream(stream)));
+}
+
+moe_status_t moe_kv4_compact(const moe_kv4_pool* pool, int32_t* n_live, void* workspace, size_t ws_bytes,
+                             moe_dev_status* st, void* stream) {
+    const moe_status_t rc = check_pool(pool);
+    if (rc != MOE_OK) return rc;
+    if (workspace == nullptr || ws_bytes < moe::kv4_pool_workspace(pool->S, pool->n_pages)) return MOE_ERR_WORKSPACE;
+    if (!aligned256(workspace)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_kv4_compact(*pool, n_live, workspace, st, as_stream(stream)));
+}
+
 const char* moe_status_string(int code, int device) {
     if (device) {
         switch (code) {
             case MOE_DEV_OK: return "ok";
-            case MOE_DEV_NONFINITE: return "non-finite router logit or token weight";
+            case MOE_DEV_NONFINITE: return "non-finite router logit, token weight, key or value";
             case MOE_DEV_TIMEOUT: return "on-chip wait timed out";
-            case MOE_DEV_BAD_INDEX: return "expert id or row index out of range";
+            case MOE_DEV_BAD_INDEX: return "expert id, row index, position or page out of range";
+            case MOE_DEV_NO_PAGES: return "too few free pages";
             default: return "unknown device status";
         }
     }

@@ -1,0 +1,754 @@
+// attn_kv4.cu -- attention over the 4-bit paged cache for few query rows a
+// sequence (single tokens, drafts): a streaming kernel bound by the cache's
+// bytes.
+//
+// For one (sequence, key head) the rows are the new tokens' query heads of
+// that key head, token-major.  A tile of 8 or 16 rows takes one pass over its
+// pages with the running maximum m, sum l and sum O of a softmax:
+//     S^T = K Q^T (64 tokens x rows),  P = 2^(f S - m),  O^T += V^T P^T
+// on m16n8k16 tensor-core products with the cached numbers as the 16-row
+// operand, so that eight query heads that share a key head fill the products'
+// other side and no row is padding.  The layout of a page puts what a lane's
+// fragments need into 16-byte runs: a warp reads a head's page (9216 bytes at
+// D = 128) with 18 shared-memory loads a lane, and a fragment register is one
+// conversion of a byte of codes and one multiplication by a scale, both
+// exact.
+//
+// Work: the pages of all tiles form one sequence of units, cut into equal
+// runs for the CTAs and again for their warps, whatever the contexts' lengths
+// are.  A warp fetches a page ahead of the one it works on (one bulk copy each).  Tiles that
+// cross warps are joined in shared memory and tiles that cross CTAs by the
+// last CTA to arrive, in the order of the pages: nothing waits, and
+// results do not depend on timing.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "kv4.cuh"
+#include "launch.h"
+#include "tmap.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 2;
+constexpr int kSiteKvPage = 21;
+constexpr float kLog2e = 0x1.715476p+0f;
+constexpr float kLn2f = 0x1.62e430p-1f;
+
+struct AttnArgs {
+    const __nv_bfloat16* q;
+    long long ld_q;
+    int T, n_q, group;          // group: query heads of a key head
+    moe_kv4_cache c;
+    const int32_t* q_start;
+    float scale;
+    int window;
+    __nv_bfloat16* out;
+    long long ld_out;
+    float* lse;
+    int* counters;              // one of a CTA: arrivals at the tile that starts there and goes on
+    float* partial;             // [CTAs][2] slots of NR * (D + 2) floats
+    moe_dev_status* st;
+};
+
+// A sequence's rows and what they may see.
+struct Seq {
+    int q0, n, len;
+};
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int s) {
+    Seq r;
+    r.q0 = a.q_start[s];
+    r.n = a.q_start[s + 1] - r.q0;
+    r.len = a.c.seq_len[s];
+    if (r.n < 0 || r.q0 < 0 || r.q0 + r.n > a.T || r.len < 0 || r.len > static_cast<long long>(a.c.max_pages) * kPage) {
+        r.n = 0;
+        r.len = -1;
+    }
+    return r;
+}
+
+// The tile's pages [lo, hi): those that its first row's window or its last row's place reaches.
+template <int NR>
+__device__ __forceinline__ void tile_pages(const AttnArgs& a, const Seq& s, int tile, int& lo, int& hi) {
+    const int i0 = tile * NR / a.group, i1 = min(s.n - 1, (tile * NR + NR - 1) / a.group);
+    const int p0 = s.len - s.n + i0, p1 = s.len - s.n + i1;
+    hi = p1 >= 0 ? p1 / kPage + 1 : 0;
+    lo = a.window > 0 && p0 - a.window + 1 > 0 ? min((p0 - a.window + 1) / kPage, hi) : 0;
+}
+template <int NR>
+__device__ __forceinline__ int seq_tiles(const AttnArgs& a, const Seq& s) {
+    return (s.n * a.group + NR - 1) / NR;
+}
+// Units of one key head of a sequence; a tile that sees nothing still has one, to write its rows.
+template <int NR>
+__device__ __forceinline__ long long seq_units(const AttnArgs& a, const Seq& s) {
+    long long u = 0;
+    const int tiles = seq_tiles<NR>(a, s);
+    for (int i = 0; i < tiles; ++i) {
+        int lo, hi;
+        tile_pages<NR>(a, s, i, lo, hi);
+        u += max(1, hi - lo);
+    }
+    return u;
+}
+
+// A place in the sequence of units: sequence, key head, tile, and page of the tile.
+template <int NR>
+struct Cursor {
+    int s, h, tile, tiles;
+    int page, lo, hi;          // the tile's pages; lo == hi: one unit without a page
+    int item_left;             // units of the tile from here on
+    long long item_begin;      // unit of the tile's first page
+    long long unit;
+    Seq q;
+
+    __device__ void set_tile(const AttnArgs& a) {
+        tile_pages<NR>(a, q, tile, lo, hi);
+        page = lo;
+        item_left = max(1, hi - lo);
+        item_begin = unit;
+    }
+    __device__ void next_seq(const AttnArgs& a) {   // the next sequence with rows
+        do {
+            ++s;
+            if (s >= a.c.S) { tiles = 0; return; }
+            q = load_seq(a, s);
+            tiles = seq_tiles<NR>(a, q);
+        } while (tiles == 0);
+        h = 0;
+        tile = 0;
+    }
+    __device__ void next_item(const AttnArgs& a) {
+        if (++tile >= tiles) {
+            tile = 0;
+            if (++h >= a.c.n_kv) next_seq(a);
+        }
+        if (s < a.c.S) set_tile(a);
+    }
+    __device__ void advance(const AttnArgs& a) {
+        ++unit;
+        ++page;
+        if (--item_left == 0) next_item(a);
+    }
+    // from the first unit of (sequence s, head 0) to unit `to` of the same sequence
+    __device__ void seek(const AttnArgs& a, int seq, long long seq_begin, long long seq_head_units, long long to) {
+        s = seq;
+        q = load_seq(a, s);
+        tiles = seq_tiles<NR>(a, q);
+        h = static_cast<int>((to - seq_begin) / seq_head_units);
+        unit = seq_begin + h * seq_head_units;
+        tile = 0;
+        set_tile(a);
+        while (unit + item_left <= to) {
+            unit += item_left;
+            if (++tile >= tiles) break;   // cannot happen: `to` is in this head
+            set_tile(a);
+        }
+        const int skip = static_cast<int>(to - unit);
+        page += skip;
+        item_left -= skip;
+        unit = to;
+    }
+    __device__ bool same_item(const Cursor& o) const { return item_begin == o.item_begin; }
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ float ex2(float u) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(u));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    uint32_t r;
+    memcpy(&r, &h, 4);
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void lds(uint32_t (&v)[N], const uint8_t* p) {
+    if constexpr (N == 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        v[0] = x.x; v[1] = x.y;
+    }
+}
+
+// A tile's state in one warp.  Lane (g, t) = (lane / 4, lane % 4) holds, of
+// row 8 n + 2 t + c, the numbers (D/8) g + 2 i + e of O in o[n][i][2 e + c].
+template <int D, int NT>
+struct Tile {
+    static constexpr int KS = D / 16;     // products of 16 numbers of a head
+    static constexpr int MD = D / 16;     // 16-row tiles of V^T
+    uint32_t qf[NT][KS][2];
+    float f[NT][2];                       // the scores' factor of row 8 n + 2 t + c, in powers of two
+    float m[NT][2], l[NT][2];
+    float o[NT][MD][4];
+};
+
+// The tile's queries as fragments: row 8 n + g, numbers (D/4) t + 4 ks + 0..3.
+// A row is multiplied by a power of two that puts its largest magnitude into
+// [2^10, 2^11): its bf16 numbers down to 2^-27 of that are then exact in fp16.
+template <int D, int NT>
+__device__ __forceinline__ void load_queries(Tile<D, NT>& w, const AttnArgs& a, const Seq& s, int h, int tile, int lane) {
+    constexpr int NR = 8 * NT;
+    const int g = lane >> 2, t = lane & 3;
+    const float k_scale = a.c.k_scale != nullptr ? a.c.k_scale[h] : 1.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int r = tile * NR + 8 * n + g;
+        const bool live = r < s.n * a.group;
+        uint32_t raw[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) raw[i] = 0u;
+        if (live) {
+            const __nv_bfloat16* p = a.q + static_cast<long long>(s.q0 + r / a.group) * a.ld_q +
+                                     static_cast<long long>(h * a.group + r % a.group) * D + (D / 4) * t;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+                raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
+            }
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(raw[i] << 16)), fabsf(__uint_as_float(raw[i] & 0xffff0000u))));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+        // exponent of the power of two, 0 for rows that are zero or not finite
+        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        e = (top > 0.f && e < 128) ? max(-100, min(100, 10 - e)) : 0;
+        const float up = __int_as_float((e + 127) << 23);
+        float f = a.scale * kLog2e * k_scale * __int_as_float((127 - e) << 23);
+        f = live ? f : 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            w.qf[n][i / 2][i & 1] = pack_f16(__uint_as_float(raw[i] << 16) * up, __uint_as_float(raw[i] & 0xffff0000u) * up);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            w.f[n][c] = __shfl_sync(kFull, f, (2 * t + c) * 4);
+            w.m[n][c] = -INFINITY;
+            w.l[n][c] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w.o[n][i][c] = 0.f;
+    }
+}
+
+// One page of the tile.  `base`: the head's part of the page in shared memory.
+template <int D, int NT>
+__device__ __forceinline__ void do_page(Tile<D, NT>& w, const AttnArgs& a, const uint8_t* base, const Seq& s, int tile,
+                                        int page, int lane) {
+    using L = Kv4Layout<D>;
+    constexpr int NR = 8 * NT;
+    constexpr int KS = D / 16, W = D / 32;      // code words of a lane's run
+    const int g = lane >> 2, t = lane & 3;
+
+    // S^T: rows 16 mt + 8 e + g (tokens), columns 8 n + 2 t + c (queries) in acc[mt][n][2 e + c]
+    float acc[4][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[mt][n][c] = 0.f;
+    uint32_t ks[W];                             // scales of tokens g + 8 i: R bytes each
+    lds<W>(ks, base + L::kScales + (t * 8 + g) * 8 * L::R);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+        uint32_t w0[W], w1[W];
+        lds<W>(w0, base + (16 * mt + g) * (D / 2) + t * (D / 8));
+        lds<W>(w1, base + (16 * mt + 8 + g) * (D / 2) + t * (D / 8));
+        uint32_t s0[L::R], s1[L::R];            // both halves the same scale
+        if constexpr (L::R == 2) {
+            const uint32_t p0 = e4m3x2_to_f16(ks[mt] & 0xffffu), p1 = e4m3x2_to_f16(ks[mt] >> 16);
+            s0[0] = __byte_perm(p0, 0, 0x1010); s0[1] = __byte_perm(p0, 0, 0x3232);
+            s1[0] = __byte_perm(p1, 0, 0x1010); s1[1] = __byte_perm(p1, 0, 0x3232);
+        } else {
+            const uint32_t p = e4m3x2_to_f16((ks[mt / 2] >> (16 * (mt & 1))) & 0xffffu);
+            s0[0] = __byte_perm(p, 0, 0x1010);
+            s1[0] = __byte_perm(p, 0, 0x3232);
+        }
+#pragma unroll
+        for (int k2 = 0; k2 < W; ++k2) {        // a word: two products' worth
+            uint32_t c0[4], c1[4];
+            e2m1x8_to_f16(w0[k2], c0[0], c0[1], c0[2], c0[3]);
+            e2m1x8_to_f16(w1[k2], c1[0], c1[1], c1[2], c1[3]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int k = 2 * k2 + e, r = k / 4;
+                const uint32_t af[4] = {hmul2_u(c0[2 * e], s0[r]), hmul2_u(c1[2 * e], s1[r]),
+                                        hmul2_u(c0[2 * e + 1], s0[r]), hmul2_u(c1[2 * e + 1], s1[r])};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_f16(acc[mt][n], af, w.qf[n][k][0], w.qf[n][k][1]);
+            }
+        }
+    }
+
+    // softmax: scale, hide, maximum over the page
+    const int key0 = page * kPage;
+    const int i_last = min(s.n - 1, (tile * NR + NR - 1) / a.group);
+    const int p_first = s.len - s.n + tile * NR / a.group, p_last = s.len - s.n + i_last;
+    const bool edge = key0 + kPage - 1 > p_first || (a.window > 0 && key0 <= p_last - a.window);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float top[2] = {-INFINITY, -INFINITY};
+        if (edge) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int p = s.len - s.n + (tile * NR + 8 * n + 2 * t + c) / a.group;
+                const int last = min(p, s.len - 1), first = a.window > 0 ? p - a.window + 1 : 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int key = key0 + 8 * i + g;
+                    float& x = acc[i >> 1][n][2 * (i & 1) + c];
+                    x = key <= last && key >= first ? x * w.f[n][c] : -INFINITY;
+                    top[c] = fmaxf(top[c], x);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float& x = acc[i >> 1][n][2 * (i & 1) + c];
+                    x *= w.f[n][c];
+                    top[c] = fmaxf(top[c], x);
+                }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            top[c] = fmaxf(top[c], __shfl_xor_sync(kFull, top[c], 4));
+            top[c] = fmaxf(top[c], __shfl_xor_sync(kFull, top[c], 8));
+            top[c] = fmaxf(top[c], __shfl_xor_sync(kFull, top[c], 16));
+            top[c] = fmaxf(top[c], w.m[n][c]);
+        }
+        if (__any_sync(kFull, top[0] > w.m[n][0] || top[1] > w.m[n][1])) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                // while nothing has been seen m is -inf and O, l are 0
+                const float r = w.m[n][c] == -INFINITY ? 0.f : ex2(w.m[n][c] - top[c]);
+                w.m[n][c] = top[c];
+                w.l[n][c] *= r;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    w.o[n][i][c] *= r;
+                    w.o[n][i][2 + c] *= r;
+                }
+            }
+        }
+        const float m0 = w.m[n][0] == -INFINITY ? 0.f : w.m[n][0], m1 = w.m[n][1] == -INFINITY ? 0.f : w.m[n][1];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float& x0 = acc[i >> 1][n][2 * (i & 1)];
+            float& x1 = acc[i >> 1][n][2 * (i & 1) + 1];
+            x0 = ex2(x0 - m0);
+            x1 = ex2(x1 - m1);
+            w.l[n][0] += x0;
+            w.l[n][1] += x1;
+        }
+    }
+
+    // O^T += V^T P^T, 16 tokens at a time
+    uint32_t vs[4];                             // scale pairs of tokens 8 i + 2 t, 8 i + 2 t + 1
+    lds<4>(vs, base + L::vScales + (((D == 128 ? g : g / 2) * 4 + t) * 8) * 2);
+    // tokens that the sequence does not have: their bytes may be anything, a NaN scale among it
+    const int left = s.len - key0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t sc[2], v[2][W];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 2 * k + e;
+            uint32_t two = (vs[i / 2] >> (16 * (i & 1))) & 0xffffu;
+            if (left < kPage) {
+                const int tok = 8 * i + 2 * t;
+                two = tok + 1 < left ? two : (tok < left ? (two & 0xffu) : 0u);
+            }
+            sc[e] = e4m3x2_to_f16(two);
+            lds<W>(v[e], base + L::vCodes + ((i * 8 + g) * 4 + t) * L::U);
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                pf[n][e] = transpose8x8(pack_f16(acc[k][n][2 * e], acc[k][n][2 * e + 1]));
+#pragma unroll
+        for (int j = 0; j < W; ++j) {           // a word: four numbers of two tokens, i.e. two tiles of V^T
+            uint32_t c0[4], c1[4];
+            e2m1x8_to_f16(v[0][j], c0[0], c0[1], c0[2], c0[3]);
+            e2m1x8_to_f16(v[1][j], c1[0], c1[1], c1[2], c1[3]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t af[4] = {hmul2_u(c0[2 * e], sc[0]), hmul2_u(c0[2 * e + 1], sc[0]),
+                                        hmul2_u(c1[2 * e], sc[1]), hmul2_u(c1[2 * e + 1], sc[1])};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_f16(w.o[n][2 * j + e], af, pf[n][0], pf[n][1]);
+            }
+        }
+    }
+}
+
+// The tile's sums over the lanes of a row.
+template <int D, int NT>
+__device__ __forceinline__ void sum_lanes(Tile<D, NT>& w) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            w.l[n][c] += __shfl_xor_sync(kFull, w.l[n][c], 4);
+            w.l[n][c] += __shfl_xor_sync(kFull, w.l[n][c], 8);
+            w.l[n][c] += __shfl_xor_sync(kFull, w.l[n][c], 16);
+        }
+}
+
+// Where a tile's pieces lie in shared memory: O [NR][D + 4], then m [NR], l [NR].
+template <int D, int NR>
+struct Piece {
+    static constexpr int ld = D + 4;
+    static constexpr int m = NR * ld, l = m + NR, floats = l + NR;
+};
+struct PieceInfo {
+    long long item;            // first unit of the tile, -1: none
+    int s, h, tile, units;     // units of the whole tile
+};
+
+template <int D>
+__device__ __forceinline__ void write_out4(const AttnArgs& a, const Seq& s, int h, int r, int d, float4 v) {
+    __nv_bfloat16* p = a.out + static_cast<long long>(s.q0 + r / a.group) * a.ld_out +
+                       static_cast<long long>(h * a.group + r % a.group) * D + d;
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+    uint2 u;
+    memcpy(&u.x, &x, 4);
+    memcpy(&u.y, &y, 4);
+    *reinterpret_cast<uint2*>(p) = u;
+}
+__device__ __forceinline__ void write_lse(const AttnArgs& a, const Seq& s, int h, int r, float m, float l) {
+    if (a.lse == nullptr) return;
+    a.lse[static_cast<long long>(s.q0 + r / a.group) * a.n_q + h * a.group + r % a.group] = l > 0.f || l != l ? m * kLn2f + logf(l) : -INFINITY;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1) attn_kv4_stream_kernel(const AttnArgs a) {
+    using L = Kv4Layout<D>;
+    constexpr int NR = 8 * NT;
+    using P = Piece<D, NR>;
+    constexpr int kRing = kStages * L::bytes;
+    static_assert(P::floats * 4 <= kRing, "a warp's last piece fits its ring");
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[kWarps * kStages];
+    __shared__ PieceInfo info[2 * kWarps];
+    __shared__ long long s_scan[kWarps], w_begin[kWarps], w_units[kWarps];
+    __shared__ int w_seq[kWarps], s_ticket;
+    __shared__ volatile int s_abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&bars[i]), 1);
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    pdl_wait();
+    pdl_trigger();
+
+    // The units of all sequences; every CTA adds them up for itself.
+    const int per = (a.c.S + kThreads - 1) / kThreads;
+    const int sa = min(a.c.S, static_cast<int>(threadIdx.x) * per), sb = min(a.c.S, sa + per);
+    long long mine = 0;
+    for (int s = sa; s < sb; ++s) {
+        const Seq q = load_seq(a, s);
+        if (q.len < 0 && blockIdx.x == 0) report(a.st, MOE_DEV_BAD_INDEX, s);
+        mine += seq_units<NR>(a, q) * a.c.n_kv;
+    }
+    long long inc = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long v = __shfl_up_sync(kFull, inc, off);
+        if (lane >= off) inc += v;
+    }
+    if (lane == 31) s_scan[warp] = inc;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += s_scan[i];
+        total += s_scan[i];
+    }
+    before += inc - mine;
+    if (total == 0) return;
+    // Equal runs of units for the CTAs, at least a page for each warp.
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    share = share < kWarps ? kWarps : share;
+    const long long u0 = min(total, share * blockIdx.x), u1 = min(total, u0 + share);
+    if (u0 >= u1) return;
+    const long long n_cta = u1 - u0;
+    const long long w0 = u0 + n_cta * warp / kWarps, w1 = u0 + n_cta * (warp + 1) / kWarps;
+    // The sequence that a warp's run starts in is found by the thread that added it up.
+    if (mine > 0 && before < u1 && before + mine > u0) {
+        long long b = before;
+        for (int s = sa; s < sb; ++s) {
+            const Seq q = load_seq(a, s);
+            const long long hu = seq_units<NR>(a, q), u = hu * a.c.n_kv;
+            for (int i = 0; i < kWarps; ++i) {
+                const long long at = u0 + n_cta * i / kWarps;
+                if (at >= b && at < b + u) {
+                    w_seq[i] = s;
+                    w_begin[i] = b;
+                    w_units[i] = hu;
+                }
+            }
+            b += u;
+        }
+    }
+    if (lane < 2) info[2 * warp + lane].item = -1;
+    __syncthreads();
+
+    uint8_t* ring = smem + warp * kRing;
+    float* pieces = reinterpret_cast<float*>(ring);
+    const uint32_t bar0 = smem_u32(&bars[warp * kStages]);
+    if (w0 < w1) {
+        Cursor<NR> rd, wr;      // the unit being computed, and the next one to fetch
+        rd.seek(a, w_seq[warp], w_begin[warp], w_units[warp], w0);
+        wr = rd;
+        uint32_t fetched = 0;   // bit st: the stage holds a page
+        auto page_of = [&](const Cursor<NR>& c) {
+            return c.page < c.hi ? a.c.page_table[static_cast<long long>(c.s) * a.c.max_pages + c.page] : -1;
+        };
+        int next_id = page_of(wr);
+        auto fetch = [&](int stage) {
+            if (wr.unit >= w1) { fetched &= ~(1u << stage); return; }
+            const int id = next_id;
+            const bool ok = wr.page < wr.hi && id >= 0 && id < a.c.n_pages;
+            if (!ok && wr.page < wr.hi && lane == 0) report(a.st, MOE_DEV_BAD_INDEX, id);
+            if (ok) {
+                if (lane == 0) {
+                    const uint8_t* src = static_cast<const uint8_t*>(a.c.pages) + (static_cast<long long>(id) * a.c.n_kv + wr.h) * L::bytes;
+                    mbar_arrive_expect_tx(bar0 + 8 * stage, L::bytes);
+                    bulk_copy_g2s(smem_u32(ring + stage * L::bytes), src, L::bytes, bar0 + 8 * stage);
+                }
+                fetched |= 1u << stage;
+            } else {
+                fetched &= ~(1u << stage);
+            }
+            wr.advance(a);
+            if (wr.unit < w1) next_id = page_of(wr);
+        };
+        for (int st = 0; st < kStages; ++st) fetch(st);
+
+        Tile<D, NT> w;
+        load_queries(w, a, rd.q, rd.h, rd.tile, lane);
+        bool piece_open = rd.page != rd.lo;     // began in an earlier run
+        int stage = 0;
+        uint32_t phases = 0;                    // bit st: parity that the stage completes next
+        bool ok = true;
+        while (ok) {
+            if (fetched & (1u << stage)) {
+                ok = mbar_wait(bar0 + 8 * stage, (phases >> stage) & 1u, &s_abort, a.st, kSiteKvPage);
+                ok = __all_sync(kFull, ok);
+                phases ^= 1u << stage;
+                if (!ok) break;
+                do_page<D, NT>(w, a, ring + stage * L::bytes, rd.q, rd.tile, rd.page, lane);
+                __syncwarp();
+            }
+            const Cursor<NR> was = rd;
+            rd.advance(a);
+            const bool item_done = rd.unit >= w1 || !rd.same_item(was);
+            fetch(stage);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+            if (!item_done) continue;
+            sum_lanes(w);
+            const bool complete = !piece_open && was.item_left == 1;
+            const int g = lane >> 2, t = lane & 3;
+            if (complete) {
+                const float vs = a.c.v_scale != nullptr ? a.c.v_scale[was.h] : 1.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int r = was.tile * NR + 8 * n + 2 * t + c;
+                        if (r >= was.q.n * a.group) continue;
+                        const float inv = w.l[n][c] == 0.f ? 0.f : vs / w.l[n][c];
+#pragma unroll
+                        for (int i = 0; i < D / 16; i += 2)
+                            write_out4<D>(a, was.q, was.h, r, (D / 8) * g + 2 * i,
+                                          make_float4(w.o[n][i][c] * inv, w.o[n][i][2 + c] * inv, w.o[n][i + 1][c] * inv,
+                                                      w.o[n][i + 1][2 + c] * inv));
+                        if (g == 0) write_lse(a, was.q, was.h, r, w.m[n][c], w.l[n][c]);
+                    }
+            } else {
+                // only a run's first and last tile can be incomplete: the first has a place after the
+                // rings, the last takes the ring, which is free by then
+                float* dst = rd.unit >= w1 ? pieces : reinterpret_cast<float*>(smem + kWarps * kRing) + warp * P::floats;
+                const int which = rd.unit >= w1 ? 1 : 0;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int r = 8 * n + 2 * t + c;
+#pragma unroll
+                        for (int i = 0; i < D / 16; i += 2)
+                            *reinterpret_cast<float4*>(dst + r * P::ld + (D / 8) * g + 2 * i) =
+                                make_float4(w.o[n][i][c], w.o[n][i][2 + c], w.o[n][i + 1][c], w.o[n][i + 1][2 + c]);
+                        if (g == 0) {
+                            dst[P::m + r] = w.m[n][c];
+                            dst[P::l + r] = w.l[n][c];
+                        }
+                    }
+                if (lane == 0) {
+                    PieceInfo& p = info[2 * warp + which];
+                    p.item = was.item_begin;
+                    p.s = was.s;
+                    p.h = was.h;
+                    p.tile = was.tile;
+                    p.units = max(1, was.hi - was.lo);
+                }
+            }
+            if (rd.unit >= w1) break;
+            load_queries(w, a, rd.q, rd.h, rd.tile, lane);
+            piece_open = false;
+        }
+        if (!ok) {
+            // copies still in flight land before the CTA's shared memory is given up
+            for (int st = 0; st < kStages; ++st)
+                if (fetched & (1u << st)) mbar_drain(bar0 + 8 * st, (phases >> st) & 1u);
+        }
+    }
+    __syncthreads();
+    if (s_abort) return;
+
+    // Join the pieces of each tile, in the order of the pages.
+    const float* first_pieces = reinterpret_cast<const float*>(smem + kWarps * kRing);
+    auto piece = [&](int i) {
+        return (i & 1) ? reinterpret_cast<const float*>(smem + (i >> 1) * kRing) : first_pieces + (i >> 1) * P::floats;
+    };
+    for (int i = 0; i < 2 * kWarps;) {
+        if (info[i].item < 0) { ++i; continue; }
+        const PieceInfo p = info[i];
+        int j = i + 1;
+        while (j < 2 * kWarps && (info[j].item < 0 || info[j].item == p.item)) ++j;
+        const Seq q = load_seq(a, p.s);
+        const float vs = a.c.v_scale != nullptr ? a.c.v_scale[p.h] : 1.f;
+        const bool here = p.item >= u0 && p.item + p.units <= u1;   // the whole tile is this CTA's
+        const int my_slot = p.item < u0 ? 0 : 1;
+        float* part = a.partial + (static_cast<long long>(blockIdx.x) * 2 + my_slot) * (NR * (D + 2));
+        for (int x = threadIdx.x; x < NR * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), d = x % (D / 4) * 4;
+            float m = -INFINITY;
+            for (int k = i; k < j; ++k)
+                if (info[k].item >= 0) m = fmaxf(m, piece(k)[P::m + r]);
+            float l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = i; k < j; ++k) {
+                if (info[k].item < 0) continue;
+                const float* pc = piece(k);
+                const float mk = pc[P::m + r];
+                const float e = mk == -INFINITY ? 0.f : ex2(mk - m);
+                const float4 v = *reinterpret_cast<const float4*>(pc + r * P::ld + d);
+                l += e * pc[P::l + r];
+                o.x += e * v.x; o.y += e * v.y; o.z += e * v.z; o.w += e * v.w;
+            }
+            if (here) {
+                const int row = p.tile * NR + r;
+                if (row < q.n * a.group) {
+                    const float inv = l == 0.f ? 0.f : vs / l;
+                    write_out4<D>(a, q, p.h, row, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+                    if (d == 0) write_lse(a, q, p.h, row, m, l);
+                }
+            } else {
+                __stcg(reinterpret_cast<float4*>(part + r * D + d), o);
+                if (d == 0) {
+                    __stcg(part + NR * D + r, m);
+                    __stcg(part + NR * D + NR + r, l);
+                }
+            }
+        }
+        if (!here) {
+            // the CTAs that hold pieces of this tile: b0 (slot 1) .. b1 (slot 0)
+            const int b0 = static_cast<int>(p.item / share), b1 = static_cast<int>((p.item + p.units - 1) / share);
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                __threadfence();
+                s_ticket = atom_add_acq_rel_gpu(a.counters + b0, 1);
+            }
+            __syncthreads();
+            if (s_ticket == b1 - b0) {
+                __threadfence();
+                if (threadIdx.x == 0) a.counters[b0] = 0;
+                for (int x = threadIdx.x; x < NR * (D / 4); x += kThreads) {
+                    const int r = x / (D / 4), d = x % (D / 4) * 4;
+                    const int row = p.tile * NR + r;
+                    if (row >= q.n * a.group) continue;
+                    float m = -INFINITY, l = 0.f;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int b = b0; b <= b1; ++b) {
+                        const float* pc = a.partial + (static_cast<long long>(b) * 2 + (b == b0 ? 1 : 0)) * (NR * (D + 2));
+                        const float mk = __ldcg(pc + NR * D + r), lk = __ldcg(pc + NR * D + NR + r);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(pc + r * D + d));
+                        const float mn = fmaxf(m, mk);
+                        const float e0 = m == -INFINITY ? 0.f : ex2(m - mn), e1 = mk == -INFINITY ? 0.f : ex2(mk - mn);
+                        m = mn;
+                        l = l * e0 + lk * e1;
+                        o.x = o.x * e0 + v.x * e1; o.y = o.y * e0 + v.y * e1;
+                        o.z = o.z * e0 + v.z * e1; o.w = o.w * e0 + v.w * e1;
+                    }
+                    const float inv = l == 0.f ? 0.f : vs / l;
+                    write_out4<D>(a, q, p.h, row, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+                    if (d == 0) write_lse(a, q, p.h, row, m, l);
+                }
+            }
+        }
+        i = j;
+    }
+}
+
+constexpr int kMaxCtas = 304;
+constexpr size_t kCounterBytes = 2048;
+
+template <int D, int NT>
+cudaError_t launch_stream(const AttnArgs& a, cudaStream_t s) {
+    constexpr int smem = kWarps * kStages * Kv4Layout<D>::bytes + kWarps * Piece<D, 8 * NT>::floats * 4;
+    auto* k = attn_kv4_stream_kernel<D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k, dim3(min(sm_count(), kMaxCtas)), dim3(kThreads), smem, s, a);
+}
+
+}  // namespace
+
+size_t attention_kv4_workspace(int T, int n_q, int n_kv, int D) {
+    (void)T; (void)n_q; (void)n_kv;
+    return kCounterBytes + static_cast<size_t>(kMaxCtas) * 2 * 16 * (D + 2) * sizeof(float);
+}
+
+cudaError_t launch_attention_kv4(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache& c,
+                                 const int32_t* q_start, int max_new, float scale, int window, void* out,
+                                 long long ld_out, float* lse, void* ws, moe_dev_status* st, cudaStream_t s) {
+    AttnArgs a = {};
+    a.q = static_cast<const __nv_bfloat16*>(q); a.ld_q = ld_q; a.T = T; a.n_q = n_q; a.group = n_q / c.n_kv;
+    a.c = c; a.q_start = q_start; a.scale = scale; a.window = window;
+    a.out = static_cast<__nv_bfloat16*>(out); a.ld_out = ld_out; a.lse = lse;
+    a.counters = static_cast<int*>(ws);
+    a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
+    a.st = st;
+    const bool one = static_cast<long long>(max_new) * a.group <= 8;
+    if (c.head_dim == 128) return one ? launch_stream<128, 1>(a, s) : launch_stream<128, 2>(a, s);
+    return one ? launch_stream<64, 1>(a, s) : launch_stream<64, 2>(a, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,358 @@
+// kv4_pages.cu -- the pages of the 4-bit cache: growing and truncating
+// sequences with copy on write, forking/reordering/freeing them, and packing
+// the pool.  The bookkeeping is a few kilobytes of whole numbers: one CTA
+// plans (prefix sums give every sequence its pages without any order of
+// arrival), and a grid then copies the listed pages of all layers, which is
+// bound by device memory.
+#include "common.cuh"
+#include "launch.h"
+#include "tmap.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kAssignCols = 8;        // table columns of a CTA: one 32-byte sector of each row
+constexpr int kAssignThreads = 256;
+constexpr int kHeader = 64;           // words before the lists
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVec = 3;           // 16-byte words in flight of a thread
+
+// Workspace: header (copies), copy list [n_pages], page scratch [2][n_pages].
+struct PoolWs {
+    int* header;     // [0] copies
+    int2* copies;    // (from, to)
+    int* a;          // reserve: growing sequences that share a page; compact: new numbers
+    int* b;          // reserve: the last of them + 1; compact: free pages
+    int* place;      // reserve: the pages handed out, ascending
+};
+__host__ __device__ inline PoolWs pool_ws(void* ws, int n_pages) {
+    PoolWs w;
+    w.header = static_cast<int*>(ws);
+    w.copies = reinterpret_cast<int2*>(w.header + kHeader);
+    w.a = reinterpret_cast<int*>(w.copies + n_pages);
+    w.b = w.a + n_pages;
+    w.place = w.b + n_pages;
+    return w;
+}
+
+// Exclusive prefix sum of (x, y) over the CTA, and their totals.
+struct Sum2 {
+    long long x, y;
+};
+__device__ __forceinline__ Sum2 scan2(Sum2 v, Sum2& total, Sum2* s_warp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sum2 inc = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long x = __shfl_up_sync(kFull, inc.x, off), y = __shfl_up_sync(kFull, inc.y, off);
+        if (lane >= off) { inc.x += x; inc.y += y; }
+    }
+    __syncthreads();                 // s_warp may still be read from the scan before
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    Sum2 before = {0, 0};
+    total = {0, 0};
+    for (int i = 0; i < kPlanWarps; ++i) {
+        if (i < warp) { before.x += s_warp[i].x; before.y += s_warp[i].y; }
+        total.x += s_warp[i].x;
+        total.y += s_warp[i].y;
+    }
+    return {before.x + inc.x - v.x, before.y + inc.y - v.y};
+}
+
+__device__ __forceinline__ int pages_of(int len) { return (len + MOE_KV4_PAGE - 1) / MOE_KV4_PAGE; }
+
+// One CTA.  Thread i takes sequences [i * per, (i+1) * per).
+__global__ void __launch_bounds__(kPlanThreads, 1) kv4_reserve_plan_kernel(const moe_kv4_pool p, const int32_t* n_new,
+                                                                           void* ws, moe_dev_status* st) {
+    __shared__ Sum2 s_warp[kPlanWarps];
+    __shared__ int s_bad;
+    const PoolWs w = pool_ws(ws, p.n_pages);
+    const int tid = threadIdx.x;
+    if (tid == 0) s_bad = -1;
+    pdl_wait();
+    pdl_trigger();
+    const int per = (p.S + kPlanThreads - 1) / kPlanThreads;
+    const int s0 = min(p.S, tid * per), s1 = min(p.S, s0 + per);
+    auto row = [&](int s) { return p.page_table + static_cast<long long>(s) * p.max_pages; };
+    // the partly filled last page of a sequence that grows, or -1
+    auto part_page = [&](int s, int len, int add) {
+        return add > 0 && len % MOE_KV4_PAGE != 0 ? row(s)[len / MOE_KV4_PAGE] : -1;
+    };
+    __syncthreads();
+    for (int s = s0; s < s1; ++s) {
+        const int len = p.seq_len[s], add = n_new[s];
+        const long long after = static_cast<long long>(len) + add;
+        const long long most = min(static_cast<long long>(p.max_pages) * MOE_KV4_PAGE, 0x7fffffffll);
+        if (len < 0 || len > most || after > most) { s_bad = s; continue; }
+        const int g = part_page(s, len, add);
+        if (add > 0 && len % MOE_KV4_PAGE != 0 && (g < 0 || g >= p.n_pages)) { s_bad = s; continue; }
+        for (int c = pages_of(static_cast<int>(max(after, 0ll))); c < pages_of(len); ++c) {
+            const int id = row(s)[c];
+            if (id < 0 || id >= p.n_pages) s_bad = s;
+        }
+        if (g >= 0) {
+            atomicAdd(&w.a[g], 1);
+            atomicMax(&w.b[g], s + 1);
+        }
+    }
+    __threadfence_block();
+    __syncthreads();
+    const bool bad = s_bad >= 0;
+    // a sequence's copy (0 or 1) and pages in all
+    auto needs = [&](int s, int& copy, int& fresh) {
+        copy = fresh = 0;
+        const int len = p.seq_len[s], add = n_new[s];
+        if (add <= 0) return -1;
+        const int g = part_page(s, len, add);
+        if (g >= 0 && p.ref[g] > 1) {
+            const bool keeps = __ldcg(&w.a[g]) == p.ref[g] && __ldcg(&w.b[g]) == s + 1;
+            copy = keeps ? 0 : 1;
+        }
+        fresh = pages_of(len + add) - pages_of(len);
+        return g;
+    };
+    Sum2 mine = {0, 0}, total, base = {0, 0};
+    if (!bad) {
+        for (int s = s0; s < s1; ++s) {
+            int copy, fresh;
+            needs(s, copy, fresh);
+            mine.x += copy + fresh;
+            mine.y += copy;
+        }
+    }
+    base = scan2(mine, total, s_warp);
+    const long long want = total.x, copies = total.y;
+    // free pages in ascending order, as many as are wanted
+    const int chunk = ((p.n_pages + kPlanThreads - 1) / kPlanThreads + 3) & ~3;
+    const int g0 = min(static_cast<long long>(p.n_pages), static_cast<long long>(tid) * chunk);
+    const int g1 = min(p.n_pages, g0 + chunk);
+    Sum2 free_mine = {0, 0}, free_total;
+    for (int g = g0; g < g1; ++g) free_mine.x += p.ref[g] == 0;
+    const Sum2 free_base = scan2(free_mine, free_total, s_warp);
+    const bool short_of = want > free_total.x;
+    if (!bad && !short_of) {
+        long long k = free_base.x;
+        for (int g = g0; g < g1 && k < want; ++g)
+            if (p.ref[g] == 0) w.place[k++] = g;
+    }
+    __syncthreads();
+    // decisions read references and lengths; they change only after this barrier
+    int copy_flag[4];                 // per <= 4 (S <= 4096)
+    int fresh_n[4], part[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        copy_flag[i] = fresh_n[i] = 0;
+        part[i] = -1;
+        if (s0 + i < s1 && !bad) part[i] = needs(s0 + i, copy_flag[i], fresh_n[i]);
+    }
+    __syncthreads();
+    if (!bad && !short_of) {
+        long long at = base.x, at_copy = base.y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + i;
+            if (s >= s1) break;
+            const int len = p.seq_len[s], add = n_new[s];
+            const int held = pages_of(len);
+            int32_t* r = row(s);
+            if (copy_flag[i]) {
+                const int g = w.place[at++];
+                w.copies[at_copy++] = make_int2(part[i], g);
+                r[len / MOE_KV4_PAGE] = g;
+                p.ref[g] = 1;
+                atomicSub(&p.ref[part[i]], 1);
+            }
+            for (int c = 0; c < fresh_n[i]; ++c) {
+                const int g = w.place[at++];
+                r[held + c] = g;
+                p.ref[g] = 1;
+            }
+            if (add < 0) {
+                const int after = max(0, len + add);
+                for (int c = pages_of(after); c < held; ++c) {
+                    atomicSub(&p.ref[r[c]], 1);
+                    r[c] = -1;
+                }
+                p.seq_len[s] = after;
+            } else if (add > 0) {
+                p.seq_len[s] = len + add;
+            }
+        }
+    }
+    // the scratch goes back to zero
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (part[i] >= 0) {
+            w.a[part[i]] = 0;
+            w.b[part[i]] = 0;
+        }
+    if (bad) {
+        for (int g = g0; g < g1; ++g) w.a[g] = w.b[g] = 0;
+    }
+    if (tid == 0) {
+        w.header[0] = bad || short_of ? 0 : static_cast<int>(copies);
+        if (bad) report(st, MOE_DEV_BAD_INDEX, s_bad);
+        else if (short_of) report(st, MOE_DEV_NO_PAGES, static_cast<int>(want - free_total.x));
+    }
+}
+
+// Copies the listed pages of every layer; a CTA takes a part of a page at a time.
+__device__ __forceinline__ void copy_pages(const moe_kv4_pool& p, const PoolWs& w) {
+    const int n = w.header[0];
+    const int vecs = static_cast<int>(p.page_bytes / 16);
+    constexpr int kPart = kCopyThreads * kCopyVec;
+    const int parts = (vecs + kPart - 1) / kPart;
+    const long long items = static_cast<long long>(n) * p.n_layers * parts;
+    for (long long i = blockIdx.x; i < items; i += gridDim.x) {
+        const int part = static_cast<int>(i % parts);
+        const long long rest = i / parts;
+        const int layer = static_cast<int>(rest % p.n_layers);
+        const int2 c = w.copies[rest / p.n_layers];
+        uint8_t* base = static_cast<uint8_t*>(p.pages) + layer * p.layer_stride;
+        const uint4* src = reinterpret_cast<const uint4*>(base + c.x * p.page_bytes);
+        uint4* dst = reinterpret_cast<uint4*>(base + c.y * p.page_bytes);
+        uint4 v[kCopyVec];
+        const int at = part * kPart + threadIdx.x;
+#pragma unroll
+        for (int k = 0; k < kCopyVec; ++k)
+            if (at + k * kCopyThreads < vecs) v[k] = __ldcs(src + at + k * kCopyThreads);
+#pragma unroll
+        for (int k = 0; k < kCopyVec; ++k)
+            if (at + k * kCopyThreads < vecs) __stcs(dst + at + k * kCopyThreads, v[k]);
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) kv4_copy_kernel(const moe_kv4_pool p, void* ws) {
+    pdl_wait();
+    pdl_trigger();
+    copy_pages(p, pool_ws(ws, p.n_pages));
+}
+
+// A CTA takes kAssignCols columns of the table for all sequences: it reads
+// them all before it writes any, so the table changes in place.
+__global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const moe_kv4_pool p, const int32_t* parent,
+                                                                    moe_dev_status* st) {
+    extern __shared__ int s_old[];    // [S][kAssignCols]; the first CTA's lengths follow
+    pdl_wait();
+    pdl_trigger();
+    const int c0 = blockIdx.x * kAssignCols, cols = min(kAssignCols, p.max_pages - c0);
+    for (int x = threadIdx.x; x < p.S * kAssignCols; x += kAssignThreads) {
+        const int s = x / kAssignCols, c = x % kAssignCols;
+        s_old[x] = c < cols ? p.page_table[static_cast<long long>(s) * p.max_pages + c0 + c] : -1;
+    }
+    int* s_len = s_old + p.S * kAssignCols;
+    if (blockIdx.x == 0)
+        for (int s = threadIdx.x; s < p.S; s += kAssignThreads) s_len[s] = p.seq_len[s];
+    __syncthreads();
+    for (int x = threadIdx.x; x < p.S * kAssignCols; x += kAssignThreads) {
+        const int s = x / kAssignCols, c = x % kAssignCols;
+        int from = parent[s];
+        if (from < -1 || from >= p.S) {
+            if (c == 0 && blockIdx.x == 0) report(st, MOE_DEV_BAD_INDEX, from);
+            from = s;
+        }
+        if (from == s) continue;
+        if (c < cols) {
+            const int old = s_old[x], now = from >= 0 ? s_old[from * kAssignCols + c] : -1;
+            if (old != now) {
+                if (old >= 0 && old < p.n_pages) atomicSub(&p.ref[old], 1);
+                if (now >= 0 && now < p.n_pages) atomicAdd(&p.ref[now], 1);
+                p.page_table[static_cast<long long>(s) * p.max_pages + c0 + c] = now;
+            }
+        }
+        if (c == 0 && blockIdx.x == 0) p.seq_len[s] = from >= 0 ? s_len[from] : 0;
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) kv4_compact_plan_kernel(const moe_kv4_pool p, int32_t* n_live,
+                                                                           void* ws) {
+    __shared__ Sum2 s_warp[kPlanWarps];
+    const PoolWs w = pool_ws(ws, p.n_pages);
+    const int tid = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    const int chunk = ((p.n_pages + kPlanThreads - 1) / kPlanThreads + 3) & ~3;
+    const int g0 = min(static_cast<long long>(p.n_pages), static_cast<long long>(tid) * chunk);
+    const int g1 = min(p.n_pages, g0 + chunk);
+    Sum2 mine = {0, 0}, total;
+    for (int g = g0; g < g1; ++g) mine.x += p.ref[g] != 0;
+    scan2(mine, total, s_warp);
+    const int n = static_cast<int>(total.x);
+    // x: live pages from n on, y: free ones below n; there are as many of either
+    mine = {0, 0};
+    for (int g = g0; g < g1; ++g) {
+        const bool live = p.ref[g] != 0;
+        if (live && g >= n) ++mine.x;
+        if (!live && g < n) ++mine.y;
+    }
+    const Sum2 base = scan2(mine, total, s_warp);
+    long long x = base.x, y = base.y;
+    for (int g = g0; g < g1; ++g) {
+        const bool live = p.ref[g] != 0;
+        if (live && g >= n) w.copies[x++].x = g;
+        if (!live && g < n) w.copies[y++].y = g;
+    }
+    __threadfence_block();
+    __syncthreads();
+    for (int i = tid; i < static_cast<int>(total.x); i += kPlanThreads) {
+        const int2 c = w.copies[i];
+        w.place[c.x] = c.y;
+        p.ref[c.y] = p.ref[c.x];
+        p.ref[c.x] = 0;
+    }
+    if (tid == 0) {
+        w.header[0] = static_cast<int>(total.x);
+        w.header[1] = n;
+        if (n_live != nullptr) *n_live = n;
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) kv4_compact_kernel(const moe_kv4_pool p, void* ws) {
+    pdl_wait();
+    pdl_trigger();
+    const PoolWs w = pool_ws(ws, p.n_pages);
+    const int n = w.header[1];
+    const long long entries = static_cast<long long>(p.S) * p.max_pages;
+    for (long long i = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x; i < entries;
+         i += static_cast<long long>(gridDim.x) * kCopyThreads) {
+        const int g = p.page_table[i];
+        if (g < n || g >= p.n_pages) continue;
+        // a live page from n on is in the list; an entry that names a free page (no valid table has one) stays
+        const int to = w.place[g];
+        if (to >= 0 && to < n) p.page_table[i] = to;
+    }
+    copy_pages(p, w);
+}
+
+}  // namespace
+
+size_t kv4_pool_workspace(int S, int n_pages) {
+    (void)S;
+    return kHeader * sizeof(int) + static_cast<size_t>(n_pages) * (sizeof(int2) + 3 * sizeof(int));
+}
+
+cudaError_t launch_kv4_reserve(const moe_kv4_pool& p, const int32_t* n_new, void* ws, moe_dev_status* st, cudaStream_t s) {
+    cudaError_t e = launch_pdl(kv4_reserve_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p, n_new, ws, st);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kv4_copy_kernel, dim3(8 * sm_count()), dim3(kCopyThreads), 0, s, p, ws);
+}
+
+cudaError_t launch_kv4_assign(const moe_kv4_pool& p, const int32_t* parent, moe_dev_status* st, cudaStream_t s) {
+    if (p.max_pages < 1) return cudaSuccess;
+    const size_t smem = static_cast<size_t>(p.S) * (kAssignCols + 1) * sizeof(int);
+    cudaError_t e = cudaFuncSetAttribute(kv4_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kv4_assign_kernel, dim3((p.max_pages + kAssignCols - 1) / kAssignCols), dim3(kAssignThreads), smem, s, p, parent, st);
+}
+
+cudaError_t launch_kv4_compact(const moe_kv4_pool& p, int32_t* n_live, void* ws, moe_dev_status*, cudaStream_t s) {
+    cudaError_t e = launch_pdl(kv4_compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p, n_live, ws);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kv4_compact_kernel, dim3(8 * sm_count()), dim3(kCopyThreads), 0, s, p, ws);
+}
+
+}  // namespace moe

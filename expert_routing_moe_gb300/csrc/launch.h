@@ -117,6 +117,29 @@ cudaError_t launch_token_weights(const void* x, int x_dtype, int T, int H, const
                                  cudaStream_t s);
 cudaError_t launch_residual_to_bf16(const float* x, void* y, long long n, cudaStream_t s);
 
+// ---- q/k norms, rotary positions and the append to the 4-bit cache (qk_rope.cu) ----
+cudaError_t launch_qk_norm_rope(const void* qkv, int dtype, long long ld, int T, int n_q, int n_kv, int D,
+                                const float* q_w, const float* k_w, float eps, const moe_rope_params* rope,
+                                void* q_out, long long ld_q, void* k_out, long long ld_k,
+                                const moe_kv4_cache* cache, const int32_t* q_start, moe_dev_status* st,
+                                cudaStream_t s);
+cudaError_t launch_kv4_read(const moe_kv4_cache& c, const int32_t* q_start, int T, void* k_out, void* v_out,
+                            moe_dev_status* st, cudaStream_t s);
+
+// ---- attention over the 4-bit cache (attn_kv4.cu) ----
+constexpr int kAttnMaxSeqs = 16384;
+size_t attention_kv4_workspace(int T, int n_q, int n_kv, int D);
+cudaError_t launch_attention_kv4(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache& c,
+                                 const int32_t* q_start, int max_new, float scale, int window, void* out,
+                                 long long ld_out, float* lse, void* ws, moe_dev_status* st, cudaStream_t s);
+
+// ---- the 4-bit cache's pages (kv4_pages.cu) ----
+constexpr int kPoolMaxSeqs = 4096;
+size_t kv4_pool_workspace(int S, int n_pages);
+cudaError_t launch_kv4_reserve(const moe_kv4_pool& p, const int32_t* n_new, void* ws, moe_dev_status* st, cudaStream_t s);
+cudaError_t launch_kv4_assign(const moe_kv4_pool& p, const int32_t* parent, moe_dev_status* st, cudaStream_t s);
+cudaError_t launch_kv4_compact(const moe_kv4_pool& p, int32_t* n_live, void* ws, moe_dev_status* st, cudaStream_t s);
+
 cudaError_t launch_combine(const float* rows_out, const int32_t* slot_row, const float* slot_gate, int T, int H,
                            int k, float* y, cudaStream_t s);
 

@@ -25,6 +25,18 @@
  *                                the SERE similarity matrix from the experts'
  *                                outputs on calibration tokens
  *
+ * and, beside that layer, the attention half of a decoder layer for serving:
+ *
+ *               moe_qk_norm_rope per-head norms of q and k, rotary positions
+ *                                (one or several axes) and the append of k and
+ *                                v to a paged cache held in 4 bits
+ *               moe_attention_kv4  attention over that cache, for single
+ *                                tokens, drafts and prompt chunks
+ *               moe_kv4_read     cached tokens back as values
+ *               moe_kv4_reserve, moe_kv4_assign, moe_kv4_compact
+ *                                the cache's pages: growing, copying on write,
+ *                                forking, reordering, freeing and packing
+ *
  * Conventions for every entry point
  *  - Pointers named "host" are host memory; every other pointer is device
  *    memory (cudaMalloc / PyTorch CUDA tensors).  The caller owns all memory;
@@ -65,9 +77,10 @@ typedef struct moe_dev_status {
     int32_t detail;  /* code-specific: token index, expert id, or wait site */
 } moe_dev_status;
 #define MOE_DEV_OK 0
-#define MOE_DEV_NONFINITE 1        /* a router logit was NaN or infinite (detail = token) */
+#define MOE_DEV_NONFINITE 1        /* a router logit, k or v was NaN or infinite (detail = token) */
 #define MOE_DEV_TIMEOUT 2          /* a bounded on-chip wait gave up (detail = wait site) */
-#define MOE_DEV_BAD_INDEX 3        /* an expert id or row index was out of range (detail = value) */
+#define MOE_DEV_BAD_INDEX 3        /* an expert id, row, position or page was out of range (detail = value) */
+#define MOE_DEV_NO_PAGES 4         /* the pool has too few free pages (detail = pages missing) */
 
 #define MOE_DTYPE_F32 0
 #define MOE_DTYPE_BF16 1
@@ -421,6 +434,199 @@ moe_status_t moe_combine(const float* rows_out, const int32_t* slot_row, const f
  *   with no launch; n = 0 is a no-op.
  */
 moe_status_t moe_residual_to_bf16(const float* x, void* y, long long n, void* stream);
+
+/* ---------------------------------------------------------------- */
+/* The cache in 4 bits                                                */
+/* ---------------------------------------------------------------- */
+#define MOE_KV4_PAGE 64            /* tokens of a page */
+#define MOE_KV4_BLOCK 16           /* neighbouring numbers of a head that share a scale */
+
+/*
+ * One layer's cache of keys and values in 4 bits, in pages of 64 tokens.
+ *
+ * A block of 16 neighbouring numbers y of a head is held as
+ *     z = y * (1/hs)          hs = k_scale[head] or v_scale[head], 1 if NULL
+ *     s = e4m3(max|z| * (1/6))   8 bits, nearest, at most 448
+ *     c = e2m1(z * (1/s))        4 bits each, nearest, at most 6 (0 if s is 0)
+ * and stands for c * s * hs.  Each operation is one fp32 operation, rounded
+ * to nearest; 1/6 is the fp32 nearest to it.  c * s has at most 6 significant
+ * bits, so it is exact in fp16 and bf16.  4.5 bits a number in all.
+ *
+ * pages   [n_pages][n_kv][64 * (D + D/8)] bytes, 16-byte aligned; a head's
+ *         part of a page holds, in this order (D = head_dim; i, e = number of
+ *         the head; tok = token of the page, g = tok % 8, j = tok / 2):
+ *           key codes    [64][D/2]: byte tok*(D/2) + i/2, even i in the low half
+ *           key scales   block b = t*(D/64) + r (t < 4):
+ *                        byte ((t*8 + g)*8 + tok/8)*(D/64) + r
+ *           value codes  e = g'*(D/8) + u (g' < 8): byte
+ *                        (((j/4)*8 + g')*4 + j%4)*(D/8) + u, even tok in the low half
+ *           value scales block b: byte ((b*4 + j%4)*8 + j/4)*2 + tok%2
+ *         (each lane of a warp then finds what its tensor-core fragments need
+ *         in 16-byte runs, and a head's part of a page is one bulk copy).
+ * page_table [S][max_pages] page of every 64 tokens of a sequence, -1 = none
+ * seq_len    [S] tokens of each sequence
+ * Bytes of a page that no token has been written to may hold anything.
+ */
+typedef struct moe_kv4_cache {
+    void* pages;
+    const int32_t* page_table;
+    const int32_t* seq_len;
+    const float* k_scale;   /* [n_kv] > 0, or NULL */
+    const float* v_scale;   /* [n_kv] > 0, or NULL */
+    int32_t n_pages;
+    int32_t max_pages;      /* columns of page_table */
+    int32_t S;
+    int32_t n_kv;
+    int32_t head_dim;       /* D: 64 or 128 */
+} moe_kv4_cache;
+
+/* Bytes of one page of one layer (all heads); 0 for unsupported sizes. */
+size_t moe_kv4_page_bytes(int n_kv, int head_dim);
+
+/*
+ * Rotary positions.  Pair i of a head (a, b) becomes
+ *     (a cos - b sin, b cos + a sin),  (cos, sin) = table[p][i],
+ * where p = positions[axis[i]][token].  Pairs are (i, i + rot/2), or
+ * (2i, 2i + 1) with `pairs`; numbers from rot on pass through.  The table
+ * brings any frequency scaling, and far positions keep the precision that
+ * its maker gave them.
+ */
+typedef struct moe_rope_params {
+    const float* table;        /* [n_pos][rot/2][2] (cos, sin), 16-byte aligned */
+    const int32_t* positions;  /* [axes][T], or NULL: the token's place in its sequence (needs a cache) */
+    const uint8_t* axis;       /* [rot/2] axis of each pair (e.g. time, height, width), or NULL: axis 0 */
+    int32_t n_pos;
+    int32_t rot;               /* rotated numbers: a multiple of 32, at most head_dim */
+    int32_t axes;              /* rows of positions */
+    int32_t pairs;             /* nonzero: neighbours form the pairs */
+} moe_rope_params;
+
+/*
+ * Norms of q and k for each head, rotary positions, and the append to the
+ * cache, in one launch.
+ *
+ *   qkv      [T][ld] rows of n_q query heads, n_kv key heads and n_kv value
+ *            heads of D numbers, BF16 or F32 (16-byte aligned, ld * size a
+ *            multiple of 16)
+ *   q_weight, k_weight  [D] fp32: y = x * (1/sqrt(mean(x^2) + eps)) * weight for
+ *            each head; NULL = that side is not normed
+ *   rope     NULL = no rotation
+ *   q_out    [T][ld_q], n_q heads, same dtype as qkv; may be qkv itself (with
+ *            ld_q = ld)
+ *   k_out    [T][ld_k], n_kv heads, or NULL; may be qkv's key part
+ *   cache, q_start  NULL, or the cache that k and v are appended to: rows
+ *            q_start[s] .. q_start[s+1]-1 (q_start [S+1], ascending) are the
+ *            last tokens of sequence s, whose seq_len already counts them and
+ *            whose pages are there (moe_kv4_reserve).  A row whose place would
+ *            be negative (a sequence of length 0 in a padded batch) is not
+ *            appended.  The key is quantised from its fp32 value after the
+ *            rotation, the value from its input.
+ * Arithmetic is fp32, rounded once to the outputs' type; the sum of a key's
+ * squares is carried in two fp32 words, so that a key's code does not depend
+ * on the order of the sum.  A NaN or infinite k or v is stored as zero and
+ * reported (MOE_DEV_NONFINITE, detail = row); a position outside the table or
+ * a page outside the pool is reported (MOE_DEV_BAD_INDEX) and not written.
+ * Limits: D is 64 or 128; n_q >= 0, n_kv >= 1, n_q + 2 n_kv <= 1024.
+ */
+moe_status_t moe_qk_norm_rope(const void* qkv, int dtype, long long ld, int T, int n_q, int n_kv, int head_dim,
+                              const float* q_weight, const float* k_weight, float eps,
+                              const moe_rope_params* rope, void* q_out, long long ld_q, void* k_out,
+                              long long ld_k, const moe_kv4_cache* cache, const int32_t* q_start,
+                              moe_dev_status* st, void* stream);
+
+/*
+ * The cached tokens q_start[s] .. q_start[s+1]-1 of moe_qk_norm_rope's rows
+ * (a sequence's last tokens) as values c * s * hs, rounded to bf16.
+ *   k_out, v_out  [T][n_kv][D] bf16; either may be NULL.  Rows without a
+ *                 place in the cache are zero.
+ */
+moe_status_t moe_kv4_read(const moe_kv4_cache* cache, const int32_t* q_start, int T, void* k_out, void* v_out,
+                          moe_dev_status* st, void* stream);
+
+/*
+ * Attention over the cache: for row q_start[s] + i of sequence s, at place
+ * p = seq_len[s] - (q_start[s+1] - q_start[s]) + i, and head h (key head
+ * h / (n_q / n_kv)),
+ *     out = sum_j softmax_j(scale * q . k_j) v_j   over p - window < j <= p
+ * (window 0: all j <= p).  A row that sees nothing (p < 0) gives zeros.
+ *
+ *   q        [T][ld_q] bf16, n_q heads of D (16-byte aligned, ld_q % 8 == 0)
+ *   max_new  an upper bound of the rows of a sequence; it only chooses the
+ *            kernels
+ *   out      [T][ld_out] bf16, n_q heads of D
+ *   lse      [T][n_q] fp32 out: log of the sum of exp(scale * q . k_j), -inf for
+ *            a row that sees nothing; may be NULL
+ *   workspace  moe_attention_kv4_workspace() bytes, 256-byte aligned, ZERO-FILLED
+ *            before its first use (every call leaves its counters at zero);
+ *            serves one call at a time
+ * The products run on the tensor cores in fp16 (q scaled by a power of two of
+ * its row, the cached numbers exact) with fp32 sums; softmax in fp32, its
+ * probabilities rounded to fp16 before the second product.  Results are
+ * reproducible bit for bit.  A page outside the pool or a bad q_start is
+ * reported (MOE_DEV_BAD_INDEX) and treated as unseen.
+ * Limits: D is 64 or 128; n_q a multiple of n_kv; S <= 16384.
+ */
+moe_status_t moe_attention_kv4(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache* cache,
+                               const int32_t* q_start, int max_new, float scale, int window, void* out,
+                               long long ld_out, float* lse, void* workspace, size_t ws_bytes,
+                               moe_dev_status* st, void* stream);
+size_t moe_attention_kv4_workspace(int T, int n_q, int n_kv, int head_dim);
+
+/*
+ * The pages of a cache of several layers.  A page number names the same page
+ * in every layer; ref counts the table entries that hold it (a caller may add
+ * references of its own), 0 = free.  Entries of a row beyond a sequence's
+ * pages are -1.
+ */
+typedef struct moe_kv4_pool {
+    void* pages;               /* layer l's pages start at pages + l * layer_stride */
+    long long layer_stride;    /* bytes, a multiple of 16 */
+    long long page_bytes;      /* bytes of a page of one layer, a multiple of 16 */
+    int32_t* page_table;       /* [S][max_pages] */
+    int32_t* seq_len;          /* [S] */
+    int32_t* ref;              /* [n_pages] */
+    int32_t n_layers;
+    int32_t n_pages;
+    int32_t max_pages;
+    int32_t S;
+} moe_kv4_pool;
+
+/*
+ * Room for n_new[s] more tokens of every sequence (0: unchanged; negative:
+ * the sequence loses its last -n_new[s] tokens and the pages that it no
+ * longer needs).  Where a sequence grows into a partly filled page that
+ * others hold too, it first gets a copy of it (of every layer); of the
+ * sequences that share such a page in this call the last keeps it if nobody
+ * else holds it.  Pages are taken from the free ones in ascending order, in
+ * the order of the sequences, a copy before new pages.  Pages freed by the call
+ * are free for the next one.  All or nothing: with too few free pages
+ * (MOE_DEV_NO_PAGES), or a length beyond the table or a held page outside the
+ * pool (MOE_DEV_BAD_INDEX, detail = sequence), nothing changes.
+ *   workspace  moe_kv4_pool_workspace(S, n_pages) bytes, 256-byte aligned, zero-filled
+ *            before its first use; serves one call at a time.
+ * Limits: S <= 4096.
+ */
+moe_status_t moe_kv4_reserve(const moe_kv4_pool* pool, const int32_t* n_new, void* workspace, size_t ws_bytes,
+                             moe_dev_status* st, void* stream);
+
+/*
+ * Every sequence becomes what parent[s] was before the call: its table row
+ * and length; -1 = empty.  Pages gain and lose references accordingly; none
+ * is copied.  So parent = s keeps, another sequence's number forks it (or
+ * reorders beams), -1 frees.  A parent outside [-1, S) is reported
+ * (MOE_DEV_BAD_INDEX) and its sequence kept.  Limits: S <= 4096.
+ */
+moe_status_t moe_kv4_assign(const moe_kv4_pool* pool, const int32_t* parent, moe_dev_status* st, void* stream);
+
+/*
+ * Packs the pool: with n pages in use, those numbered n and above move, in
+ * ascending order, to the free pages below n, in every layer; tables and
+ * references follow.  n_live [1] out (may be NULL): n.
+ *   workspace  as for moe_kv4_reserve.
+ */
+moe_status_t moe_kv4_compact(const moe_kv4_pool* pool, int32_t* n_live, void* workspace, size_t ws_bytes,
+                             moe_dev_status* st, void* stream);
+size_t moe_kv4_pool_workspace(int S, int n_pages);
 
 /* ---------------------------------------------------------------- */
 /* Workspace sizes and status strings                                 */
