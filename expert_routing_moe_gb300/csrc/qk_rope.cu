@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
             // older puts its half beside the codes that are there.
             const int n_new_end = with_cache && seq >= 0 ? a.c.seq_len[seq] : 0;
             const bool odd = place & 1;
-            const bool partner = is_v && page_base != nullptr && !odd && place + 1 < n_new_end;
+            const bool partner = is_v && page_base != nullptr && !odd && place + 1 < n_new_end && t + 1 < a.T;
             const bool skip = odd && place - 1 >= first_new && place - 1 >= 0;
             float z[8];
             bool bad2 = false;
