@@ -22,6 +22,7 @@
 // results do not depend on timing.
 #include <cuda_bf16.h>
 
+#include "attn_kv4.cuh"
 #include "common.cuh"
 #include "kv4.cuh"
 #include "launch.h"
@@ -35,125 +36,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
 constexpr int kSiteKvPage = 21;
-constexpr float kLog2e = 0x1.715476p+0f;
-constexpr float kLn2f = 0x1.62e430p-1f;
-
-struct AttnArgs {
-    const __nv_bfloat16* q;
-    long long ld_q;
-    int T, n_q, group;          // group: query heads of a key head
-    moe_kv4_cache c;
-    const int32_t* q_start;
-    float scale;
-    int window;
-    __nv_bfloat16* out;
-    long long ld_out;
-    float* lse;
-    int* counters;              // one of a CTA: arrivals at the tile that starts there and goes on
-    float* partial;             // [CTAs][2] slots of NR * (D + 2) floats
-    moe_dev_status* st;
-};
-
-// A sequence's rows and what they may see.
-struct Seq {
-    int q0, n, len;
-};
-__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int s) {
-    Seq r;
-    r.q0 = a.q_start[s];
-    r.n = a.q_start[s + 1] - r.q0;
-    r.len = a.c.seq_len[s];
-    if (r.n < 0 || r.q0 < 0 || r.q0 + r.n > a.T || r.len < 0 || r.len > static_cast<long long>(a.c.max_pages) * kPage) {
-        r.n = 0;
-        r.len = -1;
-    }
-    return r;
-}
-
-// The tile's pages [lo, hi): those that its first row's window or its last row's place reaches.
-template <int NR>
-__device__ __forceinline__ void tile_pages(const AttnArgs& a, const Seq& s, int tile, int& lo, int& hi) {
-    const int i0 = tile * NR / a.group, i1 = min(s.n - 1, (tile * NR + NR - 1) / a.group);
-    const int p0 = s.len - s.n + i0, p1 = s.len - s.n + i1;
-    hi = p1 >= 0 ? p1 / kPage + 1 : 0;
-    lo = a.window > 0 && p0 - a.window + 1 > 0 ? min((p0 - a.window + 1) / kPage, hi) : 0;
-}
-template <int NR>
-__device__ __forceinline__ int seq_tiles(const AttnArgs& a, const Seq& s) {
-    return (s.n * a.group + NR - 1) / NR;
-}
-// Units of one key head of a sequence; a tile that sees nothing still has one, to write its rows.
-template <int NR>
-__device__ __forceinline__ long long seq_units(const AttnArgs& a, const Seq& s) {
-    long long u = 0;
-    const int tiles = seq_tiles<NR>(a, s);
-    for (int i = 0; i < tiles; ++i) {
-        int lo, hi;
-        tile_pages<NR>(a, s, i, lo, hi);
-        u += max(1, hi - lo);
-    }
-    return u;
-}
-
-// A place in the sequence of units: sequence, key head, tile, and page of the tile.
-template <int NR>
-struct Cursor {
-    int s, h, tile, tiles;
-    int page, lo, hi;          // the tile's pages; lo == hi: one unit without a page
-    int item_left;             // units of the tile from here on
-    long long item_begin;      // unit of the tile's first page
-    long long unit;
-    Seq q;
-
-    __device__ void set_tile(const AttnArgs& a) {
-        tile_pages<NR>(a, q, tile, lo, hi);
-        page = lo;
-        item_left = max(1, hi - lo);
-        item_begin = unit;
-    }
-    __device__ void next_seq(const AttnArgs& a) {   // the next sequence with rows
-        do {
-            ++s;
-            if (s >= a.c.S) { tiles = 0; return; }
-            q = load_seq(a, s);
-            tiles = seq_tiles<NR>(a, q);
-        } while (tiles == 0);
-        h = 0;
-        tile = 0;
-    }
-    __device__ void next_item(const AttnArgs& a) {
-        if (++tile >= tiles) {
-            tile = 0;
-            if (++h >= a.c.n_kv) next_seq(a);
-        }
-        if (s < a.c.S) set_tile(a);
-    }
-    __device__ void advance(const AttnArgs& a) {
-        ++unit;
-        ++page;
-        if (--item_left == 0) next_item(a);
-    }
-    // from the first unit of (sequence s, head 0) to unit `to` of the same sequence
-    __device__ void seek(const AttnArgs& a, int seq, long long seq_begin, long long seq_head_units, long long to) {
-        s = seq;
-        q = load_seq(a, s);
-        tiles = seq_tiles<NR>(a, q);
-        h = static_cast<int>((to - seq_begin) / seq_head_units);
-        unit = seq_begin + h * seq_head_units;
-        tile = 0;
-        set_tile(a);
-        while (unit + item_left <= to) {
-            unit += item_left;
-            if (++tile >= tiles) break;   // cannot happen: `to` is in this head
-            set_tile(a);
-        }
-        const int skip = static_cast<int>(to - unit);
-        page += skip;
-        item_left -= skip;
-        unit = to;
-    }
-    __device__ bool same_item(const Cursor& o) const { return item_begin == o.item_begin; }
-};
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -163,17 +45,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-__device__ __forceinline__ float ex2(float u) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(u));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    uint32_t r;
-    memcpy(&r, &h, 4);
     return r;
 }
 template <int N>
@@ -257,7 +128,7 @@ __device__ __forceinline__ void do_page(Tile<D, NT>& w, const AttnArgs& a, const
                                         int page, int lane) {
     using L = Kv4Layout<D>;
     constexpr int NR = 8 * NT;
-    constexpr int KS = D / 16, W = D / 32;      // code words of a lane's run
+    constexpr int W = D / 32;                   // code words of a lane's run
     const int g = lane >> 2, t = lane & 3;
 
     // S^T: rows 16 mt + 8 e + g (tokens), columns 8 n + 2 t + c (queries) in acc[mt][n][2 e + c]
@@ -429,21 +300,6 @@ struct PieceInfo {
     long long item;            // first unit of the tile, -1: none
     int s, h, tile, units;     // units of the whole tile
 };
-
-template <int D>
-__device__ __forceinline__ void write_out4(const AttnArgs& a, const Seq& s, int h, int r, int d, float4 v) {
-    __nv_bfloat16* p = a.out + static_cast<long long>(s.q0 + r / a.group) * a.ld_out +
-                       static_cast<long long>(h * a.group + r % a.group) * D + d;
-    const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
-    uint2 u;
-    memcpy(&u.x, &x, 4);
-    memcpy(&u.y, &y, 4);
-    *reinterpret_cast<uint2*>(p) = u;
-}
-__device__ __forceinline__ void write_lse(const AttnArgs& a, const Seq& s, int h, int r, float m, float l) {
-    if (a.lse == nullptr) return;
-    a.lse[static_cast<long long>(s.q0 + r / a.group) * a.n_q + h * a.group + r % a.group] = l > 0.f || l != l ? m * kLn2f + logf(l) : -INFINITY;
-}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) attn_kv4_stream_kernel(const AttnArgs a) {
@@ -731,9 +587,16 @@ cudaError_t launch_stream(const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t attention_kv4_workspace(int T, int n_q, int n_kv, int D) {
-    (void)T; (void)n_q; (void)n_kv;
+// Rows of a sequence that the streaming kernel takes; more go to the prefill kernel.
+constexpr int kStreamRows = 64;
+
+constexpr size_t stream_workspace(int D) {
     return kCounterBytes + static_cast<size_t>(kMaxCtas) * 2 * 16 * (D + 2) * sizeof(float);
+}
+
+size_t attention_kv4_workspace(int T, int n_q, int n_kv, int D) {
+    const bool prefill = static_cast<long long>(T) * (n_q / n_kv) > kStreamRows;
+    return (stream_workspace(D) + 255) / 256 * 256 + (prefill ? attn_prefill_workspace(D) : 0);
 }
 
 cudaError_t launch_attention_kv4(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache& c,
@@ -746,6 +609,19 @@ cudaError_t launch_attention_kv4(const void* q, long long ld_q, int T, int n_q, 
     a.counters = static_cast<int*>(ws);
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
     a.st = st;
+    a.rows_lo = 1;
+    a.rows_hi = kStreamRows;
+    const bool prefill = static_cast<long long>(T) * a.group > kStreamRows;   // some sequence may have more rows
+    if (prefill) {
+        AttnArgs b = a;
+        b.rows_lo = kStreamRows + 1;
+        b.rows_hi = 0x7fffffff;
+        uint8_t* ws2 = static_cast<uint8_t*>(ws) + (stream_workspace(c.head_dim) + 255) / 256 * 256;
+        b.counters = reinterpret_cast<int*>(ws2);
+        b.partial = reinterpret_cast<float*>(ws2 + kCounterBytes);
+        cudaError_t e = launch_attn_prefill(b, s);
+        if (e != cudaSuccess) return e;
+    }
     const bool one = static_cast<long long>(max_new) * a.group <= 8;
     if (c.head_dim == 128) return one ? launch_stream<128, 1>(a, s) : launch_stream<128, 2>(a, s);
     return one ? launch_stream<64, 1>(a, s) : launch_stream<64, 2>(a, s);
