@@ -21,6 +21,7 @@
 // the CTAs; an item that crosses CTAs is joined by the last to arrive,
 // in the order of the pages.
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "attn_kv4.cuh"
 #include "common.cuh"
@@ -77,6 +78,12 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// One lane of the converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 // fp16 A and B, fp32 D, both K-major: as idesc_bf16_f32 with the operand formats 0.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -91,7 +98,7 @@ struct Pf {
     static constexpr int o_v = o_k + kBuf * k_tile;
     static constexpr int o_raw = o_v + kBuf * v_tile;
     static constexpr int smem = o_raw + kRaw * raw + 1024;   // slack for 1024-byte alignment
-    // TMEM columns of a tile
+    // TMEM columns of a tile; all 512 are taken, so the first is column 0
     static constexpr int c_s = 0, c_q = 64, c_o = 128, tile_cols = 256;
 };
 
@@ -332,75 +339,93 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         }
     } else if (warp == 12) {
         // ---------------- products ----------------
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_f16_f32(kTile, kPage), id_o = idesc_f16_f32(kTile, D);
-            Walk w;
-            w.begin(a, start, u0, u1);
-            uint32_t n_k = 0, n_v = 0, n_p[2] = {0, 0}, n_q[2] = {0, 0};   // waits done so far
-            auto issue_s = [&](int t, uint32_t n) {
-                const uint32_t kb = smem_u32(smem + C::o_k + (n % kBuf) * C::k_tile);
+        // The warp walks together and one elected lane issues: addresses and
+        // descriptors then stay in uniform registers.
+        constexpr uint32_t id_s = idesc_f16_f32(kTile, kPage), id_o = idesc_f16_f32(kTile, D);
+        const uint64_t k_desc = sw128_desc(smem_u32(smem + C::o_k)), v_desc = sw128_desc(smem_u32(smem + C::o_v));
+        Walk w;
+        w.begin(a, start, u0, u1);
+        uint32_t kb = 0, kp = 0, vb = 0, vp = 0;     // buffer and parity of the next keys and values
+        uint32_t pp0 = 0, pp1 = 0, qp0 = 0, qp1 = 0;
+        auto wait = [&](int i, uint32_t parity, int site) {
+            ok = mbar_wait(bar(i), parity, &s_abort, a.st, site);
+            ok = __all_sync(kFull, ok);
+            return ok;
+        };
+        auto issue_s = [&](auto tc) {
+            constexpr uint32_t t = decltype(tc)::value;
+            const uint64_t d = k_desc + kb * (C::k_tile >> 4);
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    tc_mma_ts(tmem + t * C::tile_cols + C::c_s, tmem + t * C::tile_cols + C::c_q + 8 * k,
-                              sw128_desc(kb + (k / 4) * (kPage * 128) + (k % 4) * 32), id_s, k > 0);
+                    tc_mma_ts(t * C::tile_cols + C::c_s, t * C::tile_cols + C::c_q + 8 * k, d + (k / 4) * (kPage * 128 >> 4) + (k % 4) * 2, id_s, k > 0);
                 tc_commit(bar(B_S + t));
-            };
-            while (ok) {
-                int x[2], y[2];
-                w.half(a, 0, x[0], y[0]);
-                w.half(a, 1, x[1], y[1]);
-                if (w.pa < w.pb) {
-                    for (int t = 0; t < 2 && ok; ++t)
-                        if (x[t] < y[t]) ok = mbar_wait(bar(B_Q + t), n_q[t]++ & 1, &s_abort, a.st, kSiteQ);
-                    if (ok) ok = mbar_wait(bar(B_KF + n_k % kBuf), (n_k / kBuf) & 1, &s_abort, a.st, kSiteKFull);
-                    if (!ok) break;
-                    tc_fence_after();
-                    for (int t = 0; t < 2; ++t)
-                        if (x[t] <= w.pa && w.pa < y[t]) issue_s(t, n_k);
-                    tc_commit(bar(B_KE + n_k % kBuf));
-                    ++n_k;
-                    for (int j = w.pa; j < w.pb && ok; ++j) {
-                        const bool more = j + 1 < w.pb;
-                        for (int t = 0; t < 2 && ok; ++t) {
-                            if (x[t] <= j && j < y[t]) {
-                                ok = mbar_wait(bar(B_P + t), n_p[t]++ & 1, &s_abort, a.st, kSiteP);
-                                if (ok) ok = mbar_wait(bar(B_VF + n_v % kBuf), (n_v / kBuf) & 1, &s_abort, a.st, kSiteVFull);
-                                if (!ok) break;
-                                tc_fence_after();
-                                const uint32_t vb = smem_u32(smem + C::o_v + (n_v % kBuf) * C::v_tile);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    tc_mma_ts(tmem + t * C::tile_cols + C::c_o, tmem + t * C::tile_cols + C::c_s + 8 * k, sw128_desc(vb + 32 * k),
-                                              id_o, j > x[t] || k > 0);
-                                if (j + 1 == y[t]) tc_commit(bar(B_O + t));
-                            }
-                            if (more && x[t] <= j + 1 && j + 1 < y[t]) {
-                                ok = mbar_wait(bar(B_KF + n_k % kBuf), (n_k / kBuf) & 1, &s_abort, a.st, kSiteKFull);
-                                if (!ok) break;
-                                tc_fence_after();
-                                issue_s(t, n_k);
-                            }
-                        }
-                        if (!ok) break;
-                        // the buffers' waits count even where neither tile used them
-                        ok = mbar_wait(bar(B_VF + n_v % kBuf), (n_v / kBuf) & 1, &s_abort, a.st, kSiteVFull);
-                        tc_commit(bar(B_VE + n_v % kBuf));
-                        ++n_v;
-                        if (more && ok) {
-                            ok = mbar_wait(bar(B_KF + n_k % kBuf), (n_k / kBuf) & 1, &s_abort, a.st, kSiteKFull);
-                            tc_commit(bar(B_KE + n_k % kBuf));
-                            ++n_k;
-                        }
-                    }
-                    if (!ok) break;
-                }
-                w.next(a, u1);
-                if (w.unit >= u1) break;
             }
-            // every product is done before TMEM and shared memory are given up
-            tc_commit(bar(B_DRAIN));
-            mbar_drain(bar(B_DRAIN), 0);
+            __syncwarp();
+        };
+        auto issue_o = [&](auto tc, bool add, bool last) {
+            constexpr uint32_t t = decltype(tc)::value;
+            const uint64_t d = v_desc + vb * (C::v_tile >> 4);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc_mma_ts(t * C::tile_cols + C::c_o, t * C::tile_cols + C::c_s + 8 * k, d + 2 * k, id_o, add || k > 0);
+                if (last) tc_commit(bar(B_O + t));
+            }
+            __syncwarp();
+        };
+        constexpr std::integral_constant<uint32_t, 0> T0{};
+        constexpr std::integral_constant<uint32_t, 1> T1{};
+        while (ok) {
+            int x0, y0, x1, y1;
+            w.half(a, 0, x0, y0);
+            w.half(a, 1, x1, y1);
+            if (w.pa < w.pb) {
+                if (!wait(B_KF + kb, kp, kSiteKFull)) break;
+                if (x0 < y0) { if (!wait(B_Q, qp0, kSiteQ)) break; qp0 ^= 1; tc_fence_after(); if (x0 == w.pa) issue_s(T0); }
+                if (x1 < y1) { if (!wait(B_Q + 1, qp1, kSiteQ)) break; qp1 ^= 1; tc_fence_after(); if (x1 == w.pa) issue_s(T1); }
+                if (elect_one()) tc_commit(bar(B_KE + kb));
+                __syncwarp();
+                kb ^= 1; kp ^= kb == 0;
+                for (int j = w.pa; j < w.pb; ++j) {
+                    const bool more = j + 1 < w.pb;
+                    if (!wait(B_VF + vb, vp, kSiteVFull)) break;
+                    if (x0 <= j && j < y0) {
+                        if (!wait(B_P, pp0, kSiteP)) break;
+                        pp0 ^= 1;
+                        tc_fence_after();
+                        issue_o(T0, j > x0, j + 1 == y0);
+                    }
+                    if (more) {
+                        if (!wait(B_KF + kb, kp, kSiteKFull)) break;
+                        tc_fence_after();
+                        if (x0 <= j + 1 && j + 1 < y0) issue_s(T0);
+                    }
+                    if (x1 <= j && j < y1) {
+                        if (!wait(B_P + 1, pp1, kSiteP)) break;
+                        pp1 ^= 1;
+                        tc_fence_after();
+                        issue_o(T1, j > x1, j + 1 == y1);
+                    }
+                    if (elect_one()) tc_commit(bar(B_VE + vb));
+                    __syncwarp();
+                    vb ^= 1; vp ^= vb == 0;
+                    if (more) {
+                        if (x1 <= j + 1 && j + 1 < y1) issue_s(T1);
+                        if (elect_one()) tc_commit(bar(B_KE + kb));
+                        __syncwarp();
+                        kb ^= 1; kp ^= kb == 0;
+                    }
+                }
+                if (!ok) break;
+            }
+            w.next(a, u1);
+            if (w.unit >= u1) break;
         }
+        // every product is done before TMEM and shared memory are given up
+        if (elect_one()) tc_commit(bar(B_DRAIN));
+        __syncwarp();
+        mbar_drain(bar(B_DRAIN), 0);
     } else if (warp >= 8) {
         // ---------------- 4 bits to fp16 operands ----------------
         const int cw = warp - 8;
