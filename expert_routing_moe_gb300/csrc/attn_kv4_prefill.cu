@@ -5,17 +5,16 @@
 // that key head, token-major; a work item is 256 of them, in two tiles of 128
 // (TMEM lanes) that share every page of keys and values:
 //     S = Q K^T (128 x 64, fp32 in TMEM),  P = 2^(f S - m) (fp16, over S),
-//     O += P V (128 x D, fp32 in TMEM)
-// Q and P are the products' A operands in TMEM, so shared memory feeds only
-// the 64-token operands and the conversion that writes them: with Q there
-// too its reads alone would take the products' time.  TMEM of a tile: S/P 64
-// columns, Q D/2, O D; two tiles fill the 512 columns.
+//     O += P V (128 x D, fp32 in TMEM; P is the A operand in TMEM)
+// S has two buffers a tile: the next page's scores are there before the
+// softmax asks for them, so the softmax warps, not the round trip through the
+// tensor cores, set the pace.  TMEM of a tile: S/P 2 x 64 columns, O D.
 //
-// Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (a thread is a row), 8-11
-// convert 4-bit pages to fp16 operands (exact), 12 issues the products, 13
-// copies pages (one bulk copy each).  While one tile's softmax runs, the
-// other tile's products do.  O is scaled only when a row's maximum grows by
-// more than 2^8, which fp16's range allows for P.
+// Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (a thread is a row), 8-9
+// convert the keys' pages and 10-11 the values' to fp16 operands (exact), 12-13
+// issue the tiles' products, 14 copies pages (one bulk copy each), 15 brings the
+// next item's queries.  O is scaled only when a row's maximum grows by more
+// than 2^8, which fp16's range allows for P.
 //
 // The pages of all items form one sequence of units, cut into equal runs for
 // the CTAs; an item that crosses CTAs is joined by the last to arrive,
@@ -35,16 +34,16 @@ namespace {
 
 constexpr int kRows = 256;          // of an item
 constexpr int kTile = 128;
-constexpr int kPfThreads = 14 * 32;
+constexpr int kPfThreads = 16 * 32;
 constexpr int kPfWarps = kPfThreads / 32;
 constexpr int kRaw = 3;             // pages in 4 bits in flight
 constexpr int kBuf = 2;             // pages as fp16 operands
 constexpr int kMaxCtasPf = 160;
 constexpr int kCounterBytesPf = 2048;
-constexpr int kChunk = 1024;        // sequences whose units are held in shared memory
+constexpr int kChunk = 256;         // sequences whose units are held in shared memory
 constexpr float kGrow = 8.f;        // log2 of the growth that O waits for
 
-enum Site : int { kSiteRaw = 31, kSiteRawFree, kSiteKFree, kSiteVFree, kSiteKFull, kSiteVFull, kSiteQ, kSiteP, kSiteS, kSiteO };
+enum Site : int { kSiteRaw = 31, kSiteRawFree, kSiteKFree, kSiteVFree, kSiteKFull, kSiteVFull, kSiteQ, kSiteP, kSiteS, kSiteO, kSiteQFree };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile(
@@ -78,6 +77,39 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// Two fp32 operations in one instruction, and the largest of three.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 // One lane of the converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -94,12 +126,14 @@ struct Pf {
     static constexpr int raw = Kv4Layout<D>::bytes;
     static constexpr int k_tile = kPage * D * 2;      // D/64 halves of [64 tokens][64 numbers], 128-byte rows
     static constexpr int v_tile = kPage * D * 2;      // [D numbers][64 tokens], 128-byte rows
-    static constexpr int o_k = 0;
+    static constexpr int q_tile = kTile * D * 2;      // D/64 halves of [128 rows][64 numbers], 128-byte rows
+    static constexpr int o_q = 0;                     // two buffers of two tiles
+    static constexpr int o_k = o_q + 4 * q_tile;
     static constexpr int o_v = o_k + kBuf * k_tile;
     static constexpr int o_raw = o_v + kBuf * v_tile;
     static constexpr int smem = o_raw + kRaw * raw + 1024;   // slack for 1024-byte alignment
-    // TMEM columns of a tile; all 512 are taken, so the first is column 0
-    static constexpr int c_s = 0, c_q = 64, c_o = 128, tile_cols = 256;
+    // TMEM columns of a tile (S: two buffers); all 512 are taken, so the first is column 0
+    static constexpr int c_s = 0, c_o = 128, tile_cols = 256;
 };
 
 // Where a run starts.
@@ -160,13 +194,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     enum { B_RAWF = 0, B_RAWE = B_RAWF + kRaw, B_KF = B_RAWE + kRaw, B_KE = B_KF + kBuf, B_VF = B_KE + kBuf, B_VE = B_VF + kBuf,
-           B_Q = B_VE + kBuf, B_S = B_Q + 2, B_P = B_S + 2, B_O = B_P + 2, B_DRAIN = B_O + 2, B_N };
+           B_QF = B_VE + kBuf, B_QE = B_QF + 2, B_S = B_QE + 2, B_P = B_S + 4, B_O = B_P + 4, B_DRAIN = B_O + 4, B_N = B_DRAIN + 2 };
     __shared__ __align__(8) uint64_t bars[B_N];
     __shared__ uint32_t s_tmem;
     __shared__ long long s_units[kChunk], s_warp[kPfWarps];
     __shared__ int s_list[kChunk], s_list_n, s_ticket;
     __shared__ Start s_start;
     __shared__ uint8_t s_bad[kRaw];
+    __shared__ float s_f[2][kRows];
     __shared__ volatile int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -174,14 +209,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRaw; ++i) { mbar_init(bar(B_RAWF + i), 1); mbar_init(bar(B_RAWE + i), 4); }
         for (int i = 0; i < kBuf; ++i) {
-            mbar_init(bar(B_KF + i), 4); mbar_init(bar(B_KE + i), 1);
-            mbar_init(bar(B_VF + i), 4); mbar_init(bar(B_VE + i), 1);
+            mbar_init(bar(B_KF + i), 2); mbar_init(bar(B_KE + i), 2);
+            mbar_init(bar(B_VF + i), 2); mbar_init(bar(B_VE + i), 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(B_Q + i), 4); mbar_init(bar(B_S + i), 1);
-            mbar_init(bar(B_P + i), 4); mbar_init(bar(B_O + i), 1);
+            mbar_init(bar(B_QF + i), 1);
+            mbar_init(bar(B_QE + i), 2 + 8);       // the products' and the softmax warps'
+            mbar_init(bar(B_DRAIN + i), 1);
         }
-        mbar_init(bar(B_DRAIN), 1);
+        for (int i = 0; i < 4; ++i) { mbar_init(bar(B_S + i), 1); mbar_init(bar(B_P + i), 4); mbar_init(bar(B_O + i), 1); }
         s_abort = 0;
         fence_mbar_init();
     }
@@ -291,8 +327,84 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
     const uint32_t tmem = s_tmem;
     const Start start = s_start;
 
+    // An item's queries to buffer b, rows of `rows_at` + warp's share: D/8 lanes
+    // hold a row, scaled by a power of two of its own (see the streaming
+    // kernel) to fp16, into the products' layout.
+    auto load_q = [&](const Walk& w, uint32_t b, int r_begin, int r_end) {
+        constexpr int G = D / 8, RW = 32 / G;          // lanes of a row, rows of a warp
+        constexpr int kAhead = 16 / RW;                // loads in flight: 16 rows, a warp's share of the first item
+        const int c = lane % G;
+        const int rows = w.q.n * a.group;
+        const float f_all = a.scale * kLog2e * (a.c.k_scale != nullptr ? a.c.k_scale[w.h] : 1.f);
+        for (int r0 = r_begin; r0 < r_end; r0 += RW * kAhead) {
+            uint4 v[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int r = w.tile * kRows + r0 + i * RW + lane / G;
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows)
+                    v[i] = *reinterpret_cast<const uint4*>(a.q + static_cast<long long>(w.q.q0 + r / a.group) * a.ld_q +
+                                                           static_cast<long long>(w.h * a.group + r % a.group) * D + 8 * c);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int rt = r0 + i * RW + lane / G;
+                const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                float top = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u))));
+#pragma unroll
+                for (int off = G / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+                int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+                e = (top > 0.f && e < 128) ? max(-100, min(100, 10 - e)) : 0;
+                float up = __int_as_float((e + 127) << 23);
+                float f = f_all * __int_as_float((127 - e) << 23);
+                // the maximum is taken before the factor: it has to be positive
+                if (f < 0.f) { f = -f; up = -up; }
+                if (c == 0) s_f[b][rt] = fmaxf(f, 1e-37f);
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    h[k] = pack_f16(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xffff0000u) * up);
+                uint8_t* dst = smem + C::o_q + (2 * b + rt / kTile) * C::q_tile + (c / 8) * (kTile * 128) + (rt % kTile) * 128;
+                *reinterpret_cast<uint4*>(dst + (((c % 8) ^ (rt & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+        }
+        fence_proxy_async_smem();
+    };
+    // the first item's by all warps
+    {
+        Walk w;
+        w.begin(a, start, u0, u1);
+        while (w.pa >= w.pb && w.unit < u1) w.next(a, u1);
+        if (w.unit < u1) load_q(w, 0, warp * (kRows / kPfWarps), (warp + 1) * (kRows / kPfWarps));
+    }
+    __syncthreads();
+
     bool ok = true;
-    if (warp == 13) {
+    if (warp == 15) {
+        // ---------------- the next items' queries ----------------
+        Walk w;
+        w.begin(a, start, u0, u1);
+        uint32_t b = 0, ph = 1;
+        bool first = true;
+        while (ok) {
+            if (w.pa < w.pb) {
+                ok = mbar_wait(bar(B_QE + b), ph, &s_abort, a.st, kSiteQFree);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                if (!first) load_q(w, b, 0, kRows);
+                first = false;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_QF + b));
+                b ^= 1;
+                ph ^= b == 0;
+            }
+            w.next(a, u1);
+            if (w.unit >= u1) break;
+        }
+    } else if (warp == 14) {
         // ---------------- pages from device memory ----------------
         Walk w;
         w.begin(a, start, u0, u1);
@@ -337,98 +449,107 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                 mbar_drain(bar(B_RAWF + i), 1);
             }
         }
-    } else if (warp == 12) {
+    } else if (warp >= 12) {
         // ---------------- products ----------------
-        // The warp walks together and one elected lane issues: addresses and
-        // descriptors then stay in uniform registers.
+        // A warp for each tile: waits and commits cost issue time, which the
+        // other tile's products then fill.  The warp walks together and one
+        // elected lane issues: addresses and descriptors stay in uniform registers.
         constexpr uint32_t id_s = idesc_f16_f32(kTile, kPage), id_o = idesc_f16_f32(kTile, D);
-        const uint64_t k_desc = sw128_desc(smem_u32(smem + C::o_k)), v_desc = sw128_desc(smem_u32(smem + C::o_v));
-        Walk w;
-        w.begin(a, start, u0, u1);
-        uint32_t kb = 0, kp = 0, vb = 0, vp = 0;     // buffer and parity of the next keys and values
-        uint32_t pp0 = 0, pp1 = 0, qp0 = 0, qp1 = 0;
+        const uint32_t t = warp - 12;
+        const uint64_t q_desc = sw128_desc(smem_u32(smem + C::o_q) + t * C::q_tile), k_desc = sw128_desc(smem_u32(smem + C::o_k)),
+                       v_desc = sw128_desc(smem_u32(smem + C::o_v));
+        const uint32_t ts = t * C::tile_cols + C::c_s, to = t * C::tile_cols + C::c_o;
+        const uint32_t bar_s = bar(B_S + 2 * t), bar_o = bar(B_O + 2 * t);
         auto wait = [&](int i, uint32_t parity, int site) {
             ok = mbar_wait(bar(i), parity, &s_abort, a.st, site);
             ok = __all_sync(kFull, ok);
             return ok;
         };
-        auto issue_s = [&](auto tc) {
-            constexpr uint32_t t = decltype(tc)::value;
-            const uint64_t d = k_desc + kb * (C::k_tile >> 4);
+        Walk w;
+        w.begin(a, start, u0, u1);
+        uint32_t kv = 0, vv = 0;                       // pages of keys and values so far
+        uint32_t ns = 0, no = 0;                       // scores and outputs issued
+        uint32_t nq = 0;                               // items
+        auto scores = [&](bool active, bool last) {    // of the next page of keys
+            if (!wait(B_KF + kv % kBuf, (kv / kBuf) & 1, kSiteKFull)) return;
+            tc_fence_after();
             if (elect_one()) {
+                if (active) {
+                    const uint64_t d = k_desc + (kv % kBuf) * (C::k_tile >> 4), q = q_desc + (nq & 1) * (2 * C::q_tile >> 4);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc_mma_ts(t * C::tile_cols + C::c_s, t * C::tile_cols + C::c_q + 8 * k, d + (k / 4) * (kPage * 128 >> 4) + (k % 4) * 2, id_s, k > 0);
-                tc_commit(bar(B_S + t));
-            }
-            __syncwarp();
-        };
-        auto issue_o = [&](auto tc, bool add, bool last) {
-            constexpr uint32_t t = decltype(tc)::value;
-            const uint64_t d = v_desc + vb * (C::v_tile >> 4);
-            if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    tc_mma_ts(t * C::tile_cols + C::c_o, t * C::tile_cols + C::c_s + 8 * k, d + 2 * k, id_o, add || k > 0);
-                if (last) tc_commit(bar(B_O + t));
-            }
-            __syncwarp();
-        };
-        constexpr std::integral_constant<uint32_t, 0> T0{};
-        constexpr std::integral_constant<uint32_t, 1> T1{};
-        while (ok) {
-            int x0, y0, x1, y1;
-            w.half(a, 0, x0, y0);
-            w.half(a, 1, x1, y1);
-            if (w.pa < w.pb) {
-                if (!wait(B_KF + kb, kp, kSiteKFull)) break;
-                if (x0 < y0) { if (!wait(B_Q, qp0, kSiteQ)) break; qp0 ^= 1; tc_fence_after(); if (x0 == w.pa) issue_s(T0); }
-                if (x1 < y1) { if (!wait(B_Q + 1, qp1, kSiteQ)) break; qp1 ^= 1; tc_fence_after(); if (x1 == w.pa) issue_s(T1); }
-                if (elect_one()) tc_commit(bar(B_KE + kb));
-                __syncwarp();
-                kb ^= 1; kp ^= kb == 0;
-                for (int j = w.pa; j < w.pb; ++j) {
-                    const bool more = j + 1 < w.pb;
-                    if (!wait(B_VF + vb, vp, kSiteVFull)) break;
-                    if (x0 <= j && j < y0) {
-                        if (!wait(B_P, pp0, kSiteP)) break;
-                        pp0 ^= 1;
-                        tc_fence_after();
-                        issue_o(T0, j > x0, j + 1 == y0);
-                    }
-                    if (more) {
-                        if (!wait(B_KF + kb, kp, kSiteKFull)) break;
-                        tc_fence_after();
-                        if (x0 <= j + 1 && j + 1 < y0) issue_s(T0);
-                    }
-                    if (x1 <= j && j < y1) {
-                        if (!wait(B_P + 1, pp1, kSiteP)) break;
-                        pp1 ^= 1;
-                        tc_fence_after();
-                        issue_o(T1, j > x1, j + 1 == y1);
-                    }
-                    if (elect_one()) tc_commit(bar(B_VE + vb));
-                    __syncwarp();
-                    vb ^= 1; vp ^= vb == 0;
-                    if (more) {
-                        if (x1 <= j + 1 && j + 1 < y1) issue_s(T1);
-                        if (elect_one()) tc_commit(bar(B_KE + kb));
-                        __syncwarp();
-                        kb ^= 1; kp ^= kb == 0;
-                    }
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma_bf16(ts + 64 * (ns & 1), q + (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2,
+                                    d + (k / 4) * (kPage * 128 >> 4) + (k % 4) * 2, id_s, k > 0);
+                    tc_commit(bar_s + 8 * (ns & 1));
                 }
-                if (!ok) break;
+                tc_commit(bar(B_KE + kv % kBuf));
+                if (last) tc_commit(bar(B_QE + (nq & 1)));
             }
+            __syncwarp();
+            ns += active;
+            ++kv;
+        };
+        // the scores run a page ahead of the outputs, also from one item to the next
+        int x = 0, y = 0, j = 0;                       // the tile's pages of the item whose outputs are next
+        bool begun = false;
+        while (ok) {
+            const bool some = w.pa < w.pb;
+            int nx = 0, ny = 0;
+            if (some) {
+                w.half(a, t, nx, ny);
+                if (!wait(B_QF + (nq & 1), (nq >> 1) & 1, kSiteQ)) break;
+            }
+            // one step for each page: its scores, then the outputs of the page before
+            for (int p = w.pa; p < w.pb; ++p) {
+                scores(nx <= p && p < ny, p + 1 == w.pb);
+                if (!ok) break;
+                if (begun) {
+                    if (!wait(B_VF + vv % kBuf, (vv / kBuf) & 1, kSiteVFull)) break;
+                    const bool active = x <= j && j < y;
+                    if (active && !wait(B_P + 2 * t + (no & 1), (no >> 1) & 1, kSiteP)) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (active) {
+                            const uint64_t d = v_desc + (vv % kBuf) * (C::v_tile >> 4);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) tc_mma_ts(to, ts + 64 * (no & 1) + 8 * k, d + 2 * k, id_o, j > x || k > 0);
+                            tc_commit(bar_o + 8 * (no & 1));
+                        }
+                        tc_commit(bar(B_VE + vv % kBuf));
+                    }
+                    __syncwarp();
+                    no += active;
+                    ++vv;
+                }
+                begun = true;
+                x = nx; y = ny; j = p;
+            }
+            if (!ok) break;
+            if (some) ++nq;
             w.next(a, u1);
             if (w.unit >= u1) break;
         }
+        if (ok && begun) {                              // the last page's outputs
+            const bool active = x <= j && j < y;
+            if (wait(B_VF + vv % kBuf, (vv / kBuf) & 1, kSiteVFull) && (!active || wait(B_P + 2 * t + (no & 1), (no >> 1) & 1, kSiteP))) {
+                tc_fence_after();
+                if (elect_one() && active) {
+                    const uint64_t d = v_desc + (vv % kBuf) * (C::v_tile >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tc_mma_ts(to, ts + 64 * (no & 1) + 8 * k, d + 2 * k, id_o, j > x || k > 0);
+                    tc_commit(bar_o + 8 * (no & 1));
+                }
+                __syncwarp();
+            }
+        }
         // every product is done before TMEM and shared memory are given up
-        if (elect_one()) tc_commit(bar(B_DRAIN));
+        if (elect_one()) tc_commit(bar(B_DRAIN + t));
         __syncwarp();
-        mbar_drain(bar(B_DRAIN), 0);
-    } else if (warp >= 8) {
+        mbar_drain(bar(B_DRAIN + t), 0);
+    } else if (warp >= 8 && warp < 12) {
         // ---------------- 4 bits to fp16 operands ----------------
-        const int cw = warp - 8;
+        const bool keys = warp < 10;
+        const int cw = (warp - 8) & 1;        // which of the two warps
         Walk w;
         w.begin(a, start, u0, u1);
         uint32_t n = 0, st = 0, ph = 0;
@@ -436,96 +557,98 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         uint32_t v_off[8];           // byte of (row k of an 8-row group, 8-token chunk i8, token pair t)
 #pragma unroll
         for (int k = 0; k < 8; ++k) v_off[k] = static_cast<uint32_t>(k * 128 + ((i8 ^ k) * 16) + t * 4);
+        const int b_free = keys ? B_KE : B_VE, b_full = keys ? B_KF : B_VF;
         while (ok) {
             for (int j = w.pa; j < w.pb && ok; ++j) {
                 ok = mbar_wait(bar(B_RAWF + st), ph, &s_abort, a.st, kSiteRaw);
-                if (ok) ok = mbar_wait(bar(B_KE + n % kBuf), ((n / kBuf) & 1) ^ 1, &s_abort, a.st, kSiteKFree);
+                if (ok) ok = mbar_wait(bar(b_free + n % kBuf), ((n / kBuf) & 1) ^ 1, &s_abort, a.st, keys ? kSiteKFree : kSiteVFree);
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
                 const uint8_t* raw = smem + C::o_raw + st * C::raw;
                 const bool bad = s_bad[st];
-                uint8_t* kt = smem + C::o_k + (n % kBuf) * C::k_tile;
-                // keys: a thread converts runs of D/4 numbers of a token
                 constexpr int W = D / 32;           // words of a run
+                if (keys) {
+                    uint8_t* kt = smem + C::o_k + (n % kBuf) * C::k_tile;
+                    // a thread converts runs of D/4 numbers of four tokens
+                    uint32_t c[4][W], sc[4][L::R];
+                    const int kt4 = lane & 3;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int x = u * 128 + cw * 32 + lane, tok = x >> 2, kt4 = x & 3;
-                    uint32_t c[W], sc[L::R];
-                    const uint8_t* p = raw + tok * (D / 2) + kt4 * (D / 8);
-                    if constexpr (W == 4) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(p);
-                        c[0] = v.x; c[1] = v.y; c[2] = v.z; c[3] = v.w;
-                        const uint32_t two = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(raw + L::kScales + ((kt4 * 8 + (tok & 7)) * 8 + (tok >> 3)) * 2));
-                        sc[0] = __byte_perm(two, 0, 0x1010);
-                        sc[1] = __byte_perm(two, 0, 0x3232);
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2*>(p);
-                        c[0] = v.x; c[1] = v.y;
-                        sc[0] = __byte_perm(e4m3x2_to_f16(raw[L::kScales + (kt4 * 8 + (tok & 7)) * 8 + (tok >> 3)]), 0, 0x1010);
-                    }
-                    if (bad) {
-#pragma unroll
-                        for (int i = 0; i < L::R; ++i) sc[i] = 0u;
+                    for (int u = 0; u < 4; ++u) {
+                        const int tok = u * 16 + cw * 8 + i8;
+                        const uint8_t* p = raw + tok * (D / 2) + kt4 * (D / 8);
+                        if constexpr (W == 4) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(p);
+                            c[u][0] = v.x; c[u][1] = v.y; c[u][2] = v.z; c[u][3] = v.w;
+                            sc[u][0] = *reinterpret_cast<const uint16_t*>(raw + L::kScales + ((kt4 * 8 + i8) * 8 + (tok >> 3)) * 2);
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(p);
+                            c[u][0] = v.x; c[u][1] = v.y;
+                            sc[u][0] = raw[L::kScales + (kt4 * 8 + i8) * 8 + (tok >> 3)];
+                        }
                     }
                     // numbers (D/4) kt4 + 8 i ..: half, 16-byte chunk of the row
                     const int half = D == 128 ? kt4 >> 1 : 0;
                     const int chunk0 = D == 128 ? (kt4 & 1) * 4 : kt4 * 2;
 #pragma unroll
-                    for (int i0 = 0; i0 < W; ++i0) {
-                        // the upper half's runs go in another order, so that eight threads' chunks differ in their banks
-                        const int i = D == 128 ? i0 ^ (half * 2) : i0;
-                        const uint32_t cw_ = D == 128 ? (half ? c[(i0 ^ 2) % W] : c[i0]) : c[i0];
-                        const uint32_t sr = D == 128 ? (i < 2 ? sc[0] : sc[L::R - 1]) : sc[0];
-                        uint32_t f[4];
-                        e2m1x8_to_f16(cw_, f[0], f[1], f[2], f[3]);
-                        const uint4 v = make_uint4(hmul2_u(f[0], sr), hmul2_u(f[1], sr), hmul2_u(f[2], sr), hmul2_u(f[3], sr));
-                        *reinterpret_cast<uint4*>(kt + half * (kPage * 128) + tok * 128 + (((chunk0 + i) ^ (tok & 7)) * 16)) = v;
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_KF + n % kBuf));
-                ok = mbar_wait(bar(B_VE + n % kBuf), ((n / kBuf) & 1) ^ 1, &s_abort, a.st, kSiteVFree);
-                ok = __all_sync(kFull, ok);
-                if (!ok) break;
-                // values: a thread converts a token pair's run of D/8 numbers, for two of the eight runs
-                uint8_t* vt = smem + C::o_v + (n % kBuf) * C::v_tile;
-                const int left = w.q.len - j * kPage;
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t two = e4m3x2_to_f16(bad ? 0u : sc[u][0]);
+                        sc[u][0] = __byte_perm(two, 0, 0x1010);
+                        if constexpr (L::R == 2) sc[u][1] = __byte_perm(two, 0, 0x3232);
+                        uint8_t* row = kt + half * (kPage * 128) + (u * 16 + cw * 8 + i8) * 128;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int g = 2 * cw + u;
-                    constexpr int WV = D / 32;      // words of a run of D/8 bytes
-                    uint32_t c[WV];
-                    const uint8_t* p = raw + L::vCodes + ((i8 * 8 + g) * 4 + t) * L::U;
-                    if constexpr (WV == 4) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(p);
-                        c[0] = v.x; c[1] = v.y; c[2] = v.z; c[3] = v.w;
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2*>(p);
-                        c[0] = v.x; c[1] = v.y;
+                        for (int i0 = 0; i0 < W; ++i0) {
+                            // the upper half's runs go in another order, so that eight threads' chunks differ in their banks
+                            const int i = D == 128 ? i0 ^ (half * 2) : i0;
+                            const uint32_t word = D == 128 ? (half ? c[u][(i0 ^ 2) % W] : c[u][i0]) : c[u][i0];
+                            const uint32_t sr = D == 128 ? (i < 2 ? sc[u][0] : sc[u][L::R - 1]) : sc[u][0];
+                            uint32_t f[4];
+                            e2m1x8_to_f16(word, f[0], f[1], f[2], f[3]);
+                            *reinterpret_cast<uint4*>(row + (((chunk0 + i) ^ i8) * 16)) =
+                                make_uint4(hmul2_u(f[0], sr), hmul2_u(f[1], sr), hmul2_u(f[2], sr), hmul2_u(f[3], sr));
+                        }
                     }
-                    uint32_t two = *reinterpret_cast<const uint16_t*>(raw + L::vScales + (((D == 128 ? g : g / 2) * 4 + t) * 8 + i8) * 2);
-                    // tokens that the sequence does not have: their bytes may be anything
-                    if (left < kPage) {
-                        const int tok = 8 * i8 + 2 * t;
-                        two = tok + 1 < left ? two : (tok < left ? (two & 0xffu) : 0u);
+                } else {
+                    uint8_t* vt = smem + C::o_v + (n % kBuf) * C::v_tile;
+                    // a thread converts a token pair's runs of D/8 numbers, four of the eight
+                    uint32_t c[4][W], sc[4];
+                    const int left = w.q.len - j * kPage;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int g = 4 * cw + u;
+                        const uint8_t* p = raw + L::vCodes + ((i8 * 8 + g) * 4 + t) * L::U;
+                        if constexpr (W == 4) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(p);
+                            c[u][0] = v.x; c[u][1] = v.y; c[u][2] = v.z; c[u][3] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(p);
+                            c[u][0] = v.x; c[u][1] = v.y;
+                        }
+                        sc[u] = *reinterpret_cast<const uint16_t*>(raw + L::vScales + (((D == 128 ? g : g / 2) * 4 + t) * 8 + i8) * 2);
                     }
-                    uint32_t sc = e4m3x2_to_f16(two);
-                    if (bad) sc = 0u;
-                    uint8_t* row = vt + g * (L::U * 128);
 #pragma unroll
-                    for (int i = 0; i < WV; ++i) {
-                        uint32_t f[4];
-                        e2m1x8_to_f16(c[i], f[0], f[1], f[2], f[3]);
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t two = bad ? 0u : sc[u];
+                        // tokens that the sequence does not have: their bytes may be anything
+                        if (left < kPage) {
+                            const int tok = 8 * i8 + 2 * t;
+                            two = tok + 1 < left ? two : (tok < left ? (two & 0xffu) : 0u);
+                        }
+                        const uint32_t s2 = e4m3x2_to_f16(two);
+                        uint8_t* row = vt + (4 * cw + u) * (L::U * 128);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<uint32_t*>(row + (i / 2) * 1024 + v_off[(4 * i + k) % 8]) = hmul2_u(f[k], sc);
+                        for (int i = 0; i < W; ++i) {
+                            uint32_t f[4];
+                            e2m1x8_to_f16(c[u][i], f[0], f[1], f[2], f[3]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                *reinterpret_cast<uint32_t*>(row + (i / 2) * 1024 + v_off[(4 * i + k) % 8]) = hmul2_u(f[k], s2);
+                        }
                     }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(bar(B_VF + n % kBuf));
+                    mbar_arrive(bar(b_full + n % kBuf));
                     mbar_arrive(bar(B_RAWE + st));
                 }
                 ++n;
@@ -543,7 +666,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         const uint32_t tb = tmem + t * C::tile_cols + lanes;
         Walk w;
         w.begin(a, start, u0, u1);
-        uint32_t n_s = 0, n_o = 0;
+        uint32_t n = 0;              // pages of this tile so far
+        uint32_t qb = 0, qp = 0;
         // after a wait that ran out (ok = false) the items are walked to the end all the same, without
         // waiting: the two tiles' warps meet at barriers below
         while (true) {
@@ -551,62 +675,33 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
             w.half(a, t, x, y);
             const int r = w.tile * kRows + t * kTile + r_tile;   // row of the (sequence, head)
             const bool live = r < w.q.n * a.group;
-            const int p_row = w.q.len - w.q.n + r / a.group;     // place of the row
             float m = -INFINITY, l = 0.f;                        // m in powers of two
-            if (x < y && ok) {
-                // queries to TMEM, scaled by a power of two of the row (see the streaming kernel)
-                // (read twice, once for the row's largest magnitude: the row would take D/2 registers)
-                const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(w.q.q0 + r / a.group) * a.ld_q +
-                                                                  static_cast<long long>(w.h * a.group + r % a.group) * D);
-                float top = 0.f;
-                if (live) {
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 v = src[i];
-                        const uint32_t c[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(c[k] << 16)), fabsf(__uint_as_float(c[k] & 0xffff0000u))));
-                    }
-                }
-                int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-                e = (top > 0.f && e < 128) ? max(-100, min(100, 10 - e)) : 0;
-                float up = __int_as_float((e + 127) << 23);
-                float f = a.scale * kLog2e * (a.c.k_scale != nullptr ? a.c.k_scale[w.h] : 1.f) * __int_as_float((127 - e) << 23);
-                // the maximum is taken before the factor: it has to be positive
-                if (f < 0.f) { f = -f; up = -up; }
-                f = fmaxf(f, 1e-37f);
-#pragma unroll 1
-                for (int i = 0; i < D / 64; ++i) {
-                    uint32_t h[32];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint4 v = live ? src[8 * i + k] : make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t c[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            h[4 * k + z] = pack_f16(__uint_as_float(c[z] << 16) * up, __uint_as_float(c[z] & 0xffff0000u) * up);
-                    }
-                    tmem_st32(tb + C::c_q + 32 * i, h);
-                }
-                tmem_st_wait();
-                tc_fence_before();
+            // Outputs of pages n - 1 and n - 2 may both be outstanding (the scores run ahead), so they
+            // signal two barriers in turn: the one waited on is never two phases behind.
+            if (w.pa < w.pb && ok) {
+                ok = mbar_wait(bar(B_QF + qb), qp, &s_abort, a.st, kSiteQ);
+                ok = __all_sync(kFull, ok);
+                const float f = s_f[qb][t * kTile + r_tile];
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_Q + t));
-
-                // places of the tile's first and last row, for the pages that need no mask
+                if (lane == 0) mbar_arrive(bar(B_QE + qb));
+                qb ^= 1;
+                qp ^= qb == 0;
+                // places of the row and of the tile's first and last row, for the pages that need no mask
+                const int p_row = w.q.len - w.q.n + r / a.group;
                 const int rt0 = w.tile * kRows + t * kTile, rt1 = min(w.q.n * a.group, rt0 + kTile) - 1;
                 const int p_first = w.q.len - w.q.n + rt0 / a.group, p_last = w.q.len - w.q.n + rt1 / a.group;
                 const int first_key = a.window > 0 ? p_row - a.window + 1 : 0;
                 float mf = -INFINITY;                            // the maximum in use, before the factor
-                for (int j = x; j < y; ++j) {
-                    ok = mbar_wait(bar(B_S + t), n_s++ & 1, &s_abort, a.st, kSiteS);
+                float2 l2 = make_float2(0.f, 0.f);
+                for (int j = x; j < y && ok; ++j, ++n) {
+                    ok = mbar_wait(bar(B_S + 2 * t + (n & 1)), (n >> 1) & 1, &s_abort, a.st, kSiteS);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
                     tc_fence_after();
+                    const uint32_t ts = tb + C::c_s + 64 * (n & 1);
                     uint32_t s0[32], s1[32];
-                    tmem_ld32(tb + C::c_s, s0);
-                    tmem_ld32(tb + C::c_s + 32, s1);
+                    tmem_ld32(ts, s0);
+                    tmem_ld32(ts + 32, s1);
                     tmem_ld_wait();
                     const int key0 = j * kPage;
                     if (key0 + kPage - 1 > p_first || (a.window > 0 && key0 <= p_last - a.window)) {
@@ -617,54 +712,68 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                             if (k + 32 > last || k + 32 < first) s1[k] = 0xff800000u;
                         }
                     }
-                    float t0 = __uint_as_float(s0[0]), t1 = __uint_as_float(s1[0]);
+                    float t4[4] = {__uint_as_float(s0[0]), __uint_as_float(s0[16]), __uint_as_float(s1[0]), __uint_as_float(s1[16])};
 #pragma unroll
-                    for (int k = 1; k < 32; ++k) {
-                        t0 = fmaxf(t0, __uint_as_float(s0[k]));
-                        t1 = fmaxf(t1, __uint_as_float(s1[k]));
+                    for (int k = 1; k < 15; k += 2) {
+                        t4[0] = max3(t4[0], __uint_as_float(s0[k]), __uint_as_float(s0[k + 1]));
+                        t4[1] = max3(t4[1], __uint_as_float(s0[16 + k]), __uint_as_float(s0[17 + k]));
+                        t4[2] = max3(t4[2], __uint_as_float(s1[k]), __uint_as_float(s1[k + 1]));
+                        t4[3] = max3(t4[3], __uint_as_float(s1[16 + k]), __uint_as_float(s1[17 + k]));
                     }
-                    const float now = fmaxf(t0, t1);
+                    const float now = max3(max3(t4[0], __uint_as_float(s0[15]), t4[1]), max3(__uint_as_float(s0[31]), t4[2], __uint_as_float(s1[15])),
+                                           fmaxf(t4[3], __uint_as_float(s1[31])));
                     // in use: the maximum so far, unless it has grown by more than 2^kGrow
                     if (__any_sync(kFull, now > mf && (mf == -INFINITY || (now - mf) * f > kGrow))) {
                         const float nm = fmaxf(mf, now);
                         const float sc = mf == -INFINITY ? 0.f : ex2((mf - nm) * f);
                         mf = nm;
-                        l *= sc;
+                        l2.x *= sc;
+                        l2.y *= sc;
                         if (j > x) {
+                            // the outputs so far are complete when page n - 1's are
+                            ok = mbar_wait(bar(B_O + 2 * t + ((n - 1) & 1)), ((n - 1) >> 1) & 1, &s_abort, a.st, kSiteO);
+                            ok = __all_sync(kFull, ok);
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll 1
-                            for (int i = 0; i < D / 32; ++i) {
-                                uint32_t o[32];
-                                tmem_ld32(tb + C::c_o + 32 * i, o);
+                            for (int i = 0; i < D / 16; ++i) {
+                                uint32_t o[16];
+                                tmem_ld16(tb + C::c_o + 16 * i, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sc);
-                                tmem_st32(tb + C::c_o + 32 * i, o);
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sc);
+                                tmem_st16(tb + C::c_o + 16 * i, o);
                             }
                         }
                     }
                     const float base = mf == -INFINITY ? 0.f : -mf * f;
-                    uint32_t h[32];
-                    float l0 = 0.f, l1 = 0.f;
+                    const float2 f2 = make_float2(f, f), b2 = make_float2(base, base);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float e0 = ex2(fmaf(__uint_as_float(s0[2 * k]), f, base)), e1 = ex2(fmaf(__uint_as_float(s0[2 * k + 1]), f, base));
-                        const float e2 = ex2(fmaf(__uint_as_float(s1[2 * k]), f, base)), e3 = ex2(fmaf(__uint_as_float(s1[2 * k + 1]), f, base));
-                        l0 += e0 + e1;
-                        l1 += e2 + e3;
-                        h[k] = pack_f16(e0, e1);
-                        h[16 + k] = pack_f16(e2, e3);
+                        float2 p0 = fma2(make_float2(__uint_as_float(s0[2 * k]), __uint_as_float(s0[2 * k + 1])), f2, b2);
+                        float2 p1 = fma2(make_float2(__uint_as_float(s1[2 * k]), __uint_as_float(s1[2 * k + 1])), f2, b2);
+                        p0.x = ex2(p0.x); p0.y = ex2(p0.y);
+                        p1.x = ex2(p1.x); p1.y = ex2(p1.y);
+                        l2 = add2(l2, add2(p0, p1));
+                        s0[k] = pack_f16(p0.x, p0.y);
+                        s1[k] = pack_f16(p1.x, p1.y);
                     }
-                    l += l0 + l1;
-                    tmem_st32(tb + C::c_s, h);
+                    uint32_t h[32];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) { h[k] = s0[k]; h[16 + k] = s1[k]; }
+                    tmem_st32(ts, h);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_P + t));
+                    if (lane == 0) mbar_arrive(bar(B_P + 2 * t + (n & 1)));
                 }
+                l = l2.x + l2.y;
                 m = mf == -INFINITY ? -INFINITY : mf * f;
-                if (ok) ok = mbar_wait(bar(B_O + t), n_o++ & 1, &s_abort, a.st, kSiteO);
-                ok = __all_sync(kFull, ok);
-                tc_fence_after();
+                if (ok && x < y) {
+                    ok = mbar_wait(bar(B_O + 2 * t + ((n - 1) & 1)), ((n - 1) >> 1) & 1, &s_abort, a.st, kSiteO);
+                    ok = __all_sync(kFull, ok);
+                    tc_fence_after();
+                }
             }
             // ---- the piece's result ----
             const bool whole = w.pa == w.lo && w.pb == w.hi;
@@ -710,7 +819,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                                                             __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])));
                 }
             }
-            tc_fence_before();      // O and S are read: the next item's products may follow (through B_Q and B_P)
+            tc_fence_before();      // O is read: the next item's products follow through B_P
             if (whole) {
                 if (live) write_lse(a, w.q, w.h, r, m, l);
             } else {
