@@ -42,6 +42,10 @@ constexpr int kMaxCtasPf = 160;
 constexpr int kCounterBytesPf = 2048;
 constexpr int kChunk = 256;         // sequences whose units are held in shared memory
 constexpr float kGrow = 8.f;        // log2 of the growth that O waits for
+// What an item costs beside its pages (its queries, its outputs, the pipeline's
+// start and end), in pages: the runs are cut by cost, so that a CTA with many
+// short items gets fewer pages.
+constexpr int kItemCost = 6;
 
 enum Site : int { kSiteRaw = 31, kSiteRawFree, kSiteKFree, kSiteVFree, kSiteKFull, kSiteVFull, kSiteQ, kSiteP, kSiteS, kSiteO, kSiteQFree };
 
@@ -110,6 +114,14 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return r;
 }
 
+// The larger magnitudes of two packed bf16 pairs (a NaN gives way to a number:
+// the row's products are NaN whatever its power of two is).
+__device__ __forceinline__ uint32_t bf2_max_abs(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x & 0x7fff7fffu), "r"(y & 0x7fff7fffu));
+    return r;
+}
+
 // One lane of the converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -136,31 +148,47 @@ struct Pf {
     static constexpr int c_s = 0, c_o = 128, tile_cols = 256;
 };
 
+// Units of an item: its own cost, then one for each page.
+template <int NR>
+__device__ __forceinline__ int item_units(const AttnArgs& a, const Seq& s, int tile) {
+    int lo, hi;
+    tile_pages<NR>(a, s, tile, lo, hi);
+    return kItemCost + hi - lo;
+}
+
 // Where a run starts.
 struct Start {
     int s, h, tile, skip;
-    long long item_begin;
 };
 
 // The units of a run, item by item: the same walk in every role.
 struct Walk {
     int s, h, tile, tiles;
-    long long unit;
+    long long item;    // first unit of the item
     Seq q;
     int lo, hi;        // pages of the item
     int pa, pb;        // those of this run's piece
+    bool end;
+    // A run's piece of the item: a page belongs to the run that holds its unit, and an item without
+    // pages to the run that holds its first unit.
+    __device__ void piece(const AttnArgs& a, long long u0, long long u1) {
+        tile_pages<kRows>(a, q, tile, lo, hi);
+        const long long first = item + kItemCost;
+        pa = static_cast<int>(min(static_cast<long long>(hi), lo + max(0ll, u0 - first)));
+        pb = static_cast<int>(min(static_cast<long long>(hi), lo + max(0ll, u1 - first)));
+    }
+    __device__ bool empty_item(long long u0) const { return lo == hi && item >= u0; }
     __device__ void begin(const AttnArgs& a, const Start& st, long long u0, long long u1) {
         s = st.s; h = st.h; tile = st.tile;
         q = load_seq(a, s);
         tiles = seq_tiles<kRows>(a, q);
-        unit = u0;
-        tile_pages<kRows>(a, q, tile, lo, hi);
-        pa = lo + st.skip;
-        pb = static_cast<int>(min(static_cast<long long>(hi), pa + (u1 - unit)));
+        item = u0 - st.skip;
+        end = false;
+        piece(a, u0, u1);
     }
-    __device__ void next(const AttnArgs& a, long long u1) {
-        unit += max(1, pb - pa);
-        if (unit >= u1) return;
+    __device__ void next(const AttnArgs& a, long long u0, long long u1) {
+        item += kItemCost + hi - lo;
+        if (item >= u1) { end = true; return; }
         if (++tile >= tiles) {
             tile = 0;
             if (++h >= a.c.n_kv) {
@@ -169,12 +197,10 @@ struct Walk {
                     ++s;
                     q = load_seq(a, s);
                     tiles = seq_tiles<kRows>(a, q);
-                } while (tiles == 0);      // a later sequence has rows: unit < u1 <= total
+                } while (tiles == 0);      // a later sequence has rows: item < u1 <= total
             }
         }
-        tile_pages<kRows>(a, q, tile, lo, hi);
-        pa = lo;
-        pb = static_cast<int>(min(static_cast<long long>(hi), pa + (u1 - unit)));
+        piece(a, u0, u1);
     }
     // pages of half t (128 rows) within the piece
     __device__ void half(const AttnArgs& a, int t, int& x, int& y) const {
@@ -232,7 +258,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         __syncthreads();
         for (int i = threadIdx.x; i < n; i += kPfThreads) {
             const Seq q = load_seq(a, c0 + i);
-            if (seq_tiles<kRows>(a, q) <= 4) s_units[i] = seq_units<kRows>(a, q) * a.c.n_kv;
+            const int tiles = seq_tiles<kRows>(a, q);
+            if (tiles <= 4) {
+                long long u = 0;
+                for (int x = 0; x < tiles; ++x) u += item_units<kRows>(a, q, x);
+                s_units[i] = u * a.c.n_kv;
+            }
             else s_list[atomicAdd(&s_list_n, 1)] = i;
         }
         __syncthreads();
@@ -241,11 +272,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
             const Seq q = load_seq(a, c0 + i);
             const int tiles = seq_tiles<kRows>(a, q);
             long long u = 0;
-            for (int x = lane; x < tiles; x += 32) {
-                int lo, hi;
-                tile_pages<kRows>(a, q, x, lo, hi);
-                u += max(1, hi - lo);
-            }
+            for (int x = lane; x < tiles; x += 32) u += item_units<kRows>(a, q, x);
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) u += __shfl_xor_sync(kFull, u, off);
             if (lane == 0) s_units[i] = u * a.c.n_kv;
@@ -265,7 +292,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         for (int i = 0; i < kPfWarps; ++i) total += s_warp[i];
         __syncthreads();
     }
-    const long long share = max(4ll, (total + gridDim.x - 1) / gridDim.x);
+    const long long share = max(static_cast<long long>(kItemCost) + 4, (total + gridDim.x - 1) / gridDim.x);
     const long long u0 = min(total, share * blockIdx.x), u1 = min(total, u0 + share);
     if (u0 >= u1) return;
     // warp 0 finds the sequence, head, tile and page of unit u0
@@ -295,11 +322,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                         long long at = sb + h * per_head;
                         for (int x0 = 0; x0 < tiles; x0 += 32) {
                             long long w = 0;
-                            if (x0 + lane < tiles) {
-                                int lo, hi;
-                                tile_pages<kRows>(a, q, x0 + lane, lo, hi);
-                                w = max(1, hi - lo);
-                            }
+                            if (x0 + lane < tiles) w = item_units<kRows>(a, q, x0 + lane);
                             long long wi = w;
 #pragma unroll
                             for (int off = 1; off < 32; off <<= 1) {
@@ -307,7 +330,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                                 if (lane >= off) wi += o;
                             }
                             const long long tb = at + wi - w;
-                            if (w > 0 && u0 >= tb && u0 < tb + w) s_start = {s, h, x0 + lane, static_cast<int>(u0 - tb), tb};
+                            if (w > 0 && u0 >= tb && u0 < tb + w) s_start = {s, h, x0 + lane, static_cast<int>(u0 - tb)};
                             at += __shfl_sync(kFull, wi, 31);
                         }
                     }
@@ -327,58 +350,57 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
     const uint32_t tmem = s_tmem;
     const Start start = s_start;
 
-    // An item's queries to buffer b, rows of `rows_at` + warp's share: D/8 lanes
-    // hold a row, scaled by a power of two of its own (see the streaming
-    // kernel) to fp16, into the products' layout.
-    auto load_q = [&](const Walk& w, uint32_t b, int r_begin, int r_end) {
-        constexpr int G = D / 8, RW = 32 / G;          // lanes of a row, rows of a warp
-        constexpr int kAhead = 16 / RW;                // loads in flight: 16 rows, a warp's share of the first item
-        const int c = lane % G;
+    // Rows [32 g0, 32 g1) of an item's queries to buffer b: a lane takes a row, scaled by a power of
+    // two of its own (see the streaming kernel) to fp16, into the products' layout.
+    auto load_q = [&](const Walk& w, uint32_t b, int g0, int g1) {
         const int rows = w.q.n * a.group;
         const float f_all = a.scale * kLog2e * (a.c.k_scale != nullptr ? a.c.k_scale[w.h] : 1.f);
-        for (int r0 = r_begin; r0 < r_end; r0 += RW * kAhead) {
-            uint4 v[kAhead];
+        auto row_ptr = [&](int r) {
+            const int i = r / a.group;
+            return a.q + static_cast<long long>(w.q.q0 + i) * a.ld_q + static_cast<long long>(w.h * a.group + r - i * a.group) * D;
+        };
+        for (int g = g0; g < g1; ++g) {
+            const int rt = 32 * g + lane, r = w.tile * kRows + rt;
+            const uint4* src = reinterpret_cast<const uint4*>(row_ptr(min(r, rows - 1)));
+            uint4 v[D / 8];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int r = w.tile * kRows + r0 + i * RW + lane / G;
-                v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < rows)
-                    v[i] = *reinterpret_cast<const uint4*>(a.q + static_cast<long long>(w.q.q0 + r / a.group) * a.ld_q +
-                                                           static_cast<long long>(w.h * a.group + r % a.group) * D + 8 * c);
+            for (int i = 0; i < D / 8; ++i) v[i] = r < rows ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+            if (g + 1 < g1 && r + 32 < rows) {
+                const __nv_bfloat16* next = row_ptr(r + 32);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) asm volatile("prefetch.global.L1 [%0];" ::"l"(next + 64 * i));
             }
+            uint32_t top2 = 0u;                        // the largest magnitudes, as two bf16
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int rt = r0 + i * RW + lane / G;
+            for (int i = 0; i < D / 8; ++i)
+                top2 = bf2_max_abs(top2, bf2_max_abs(bf2_max_abs(v[i].x, v[i].y), bf2_max_abs(v[i].z, v[i].w)));
+            const float top = fmaxf(__uint_as_float(top2 << 16), __uint_as_float(top2 & 0xffff0000u));
+            int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+            e = (top > 0.f && e < 128) ? max(-100, min(100, 10 - e)) : 0;
+            float up = __int_as_float((e + 127) << 23);
+            float f = f_all * __int_as_float((127 - e) << 23);
+            // the maximum is taken before the factor: it has to be positive
+            if (f < 0.f) { f = -f; up = -up; }
+            s_f[b][rt] = fmaxf(f, 1e-37f);
+            uint8_t* dst = smem + C::o_q + (2 * b + rt / kTile) * C::q_tile + (rt % kTile) * 128;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
                 const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                float top = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u))));
-#pragma unroll
-                for (int off = G / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-                int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-                e = (top > 0.f && e < 128) ? max(-100, min(100, 10 - e)) : 0;
-                float up = __int_as_float((e + 127) << 23);
-                float f = f_all * __int_as_float((127 - e) << 23);
-                // the maximum is taken before the factor: it has to be positive
-                if (f < 0.f) { f = -f; up = -up; }
-                if (c == 0) s_f[b][rt] = fmaxf(f, 1e-37f);
                 uint32_t h[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     h[k] = pack_f16(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xffff0000u) * up);
-                uint8_t* dst = smem + C::o_q + (2 * b + rt / kTile) * C::q_tile + (c / 8) * (kTile * 128) + (rt % kTile) * 128;
-                *reinterpret_cast<uint4*>(dst + (((c % 8) ^ (rt & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(dst + (i / 8) * (kTile * 128) + (((i % 8) ^ (rt & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
         }
         fence_proxy_async_smem();
     };
-    // the first item's by all warps
+    // the first item's by eight warps
     {
         Walk w;
         w.begin(a, start, u0, u1);
-        while (w.pa >= w.pb && w.unit < u1) w.next(a, u1);
-        if (w.unit < u1) load_q(w, 0, warp * (kRows / kPfWarps), (warp + 1) * (kRows / kPfWarps));
+        while (w.pa >= w.pb && !w.end) w.next(a, u0, u1);
+        if (!w.end && warp < kRows / 32) load_q(w, 0, warp, warp + 1);
     }
     __syncthreads();
 
@@ -394,15 +416,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                 ok = mbar_wait(bar(B_QE + b), ph, &s_abort, a.st, kSiteQFree);
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
-                if (!first) load_q(w, b, 0, kRows);
+                if (!first) load_q(w, b, 0, kRows / 32);
                 first = false;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_QF + b));
                 b ^= 1;
                 ph ^= b == 0;
             }
-            w.next(a, u1);
-            if (w.unit >= u1) break;
+            w.next(a, u0, u1);
+            if (w.end) break;
         }
     } else if (warp == 14) {
         // ---------------- pages from device memory ----------------
@@ -438,8 +460,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                 }
             }
             if (!ok) break;
-            w.next(a, u1);
-            if (w.unit >= u1) break;
+            w.next(a, u0, u1);
+            if (w.end) break;
         }
         // copies in flight land before the CTA gives its shared memory up: on
         // success the converters have waited for all of them
@@ -526,8 +548,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
             }
             if (!ok) break;
             if (some) ++nq;
-            w.next(a, u1);
-            if (w.unit >= u1) break;
+            w.next(a, u0, u1);
+            if (w.end) break;
         }
         if (ok && begun) {                              // the last page's outputs
             const bool active = x <= j && j < y;
@@ -655,8 +677,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                 if (++st == kRaw) { st = 0; ph ^= 1; }
             }
             if (!ok) break;
-            w.next(a, u1);
-            if (w.unit >= u1) break;
+            w.next(a, u0, u1);
+            if (w.end) break;
         }
     } else {
         // ---------------- softmax: a thread is a row ----------------
@@ -776,16 +798,18 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                 }
             }
             // ---- the piece's result ----
-            const bool whole = w.pa == w.lo && w.pb == w.hi;
-            const long long item = w.unit - (w.pa - w.lo);
-            const int units = max(1, w.hi - w.lo);
+            // (a run that holds only units of the item's own cost has no piece)
+            const bool whole = w.pa == w.lo && w.pb == w.hi && (w.pa < w.pb || w.empty_item(u0));
+            const bool some = whole || w.pa < w.pb;
+            // the runs with pages of the item: b0 (its slot 1) .. b1 (their slots 0)
+            const int b0 = static_cast<int>((w.item + kItemCost) / share), b1 = static_cast<int>((w.item + kItemCost + w.hi - w.lo - 1) / share);
             const float vs = a.c.v_scale != nullptr ? a.c.v_scale[w.h] : 1.f;
             float* part = nullptr;
             constexpr int kSlot = kRows * (D + 2);
-            if (!whole) part = a.partial + (static_cast<long long>(blockIdx.x) * 2 + (item < u0 ? 0 : 1)) * kSlot;
+            if (!whole) part = a.partial + (static_cast<long long>(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == b0 ? 1 : 0)) * kSlot;
             const float inv = l == 0.f ? 0.f : vs / l;
 #pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) {
+            for (int i = 0; i < (some ? D / 32 : 0); ++i) {
                 uint32_t o[32];
                 if (x < y && ok) {
                     tmem_ld32(tb + C::c_o + 32 * i, o);
@@ -822,10 +846,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
             tc_fence_before();      // O is read: the next item's products follow through B_P
             if (whole) {
                 if (live) write_lse(a, w.q, w.h, r, m, l);
-            } else {
+            } else if (some) {
                 __stcg(part + kRows * D + t * kTile + r_tile, m);
                 __stcg(part + kRows * D + kRows + t * kTile + r_tile, l);
-                const int b0 = static_cast<int>(item / share), b1 = static_cast<int>((item + units - 1) / share);
                 asm volatile("bar.sync 2, 256;" ::: "memory");
                 if (threadIdx.x == 0) {
                     __threadfence();
@@ -844,27 +867,35 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                         gl += mk == -INFINITY ? 0.f : ex2(mk - gm) * __ldcg(slot(b) + kRows * D + kRows + row);
                     }
                     const float ginv = gl == 0.f ? 0.f : vs / gl;
+                    // 32 numbers at a time, so that eight loads are in flight
 #pragma unroll 1
-                    for (int i = 0; i < D / 8; ++i) {
-                        float4 o0 = make_float4(0.f, 0.f, 0.f, 0.f), o1 = o0;
+                    for (int i = 0; i < D / 32; ++i) {
+                        float4 o[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                         for (int b = b0; b <= b1; ++b) {
                             const float mk = __ldcg(slot(b) + kRows * D + row);
+                            const float4* src = reinterpret_cast<const float4*>(slot(b)) + static_cast<long long>(8 * i) * kRows + row;
+                            float4 v[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + k * kRows);
                             const float ek = mk == -INFINITY ? 0.f : ex2(mk - gm) * ginv;
-                            const float4* src = reinterpret_cast<const float4*>(slot(b)) + static_cast<long long>(2 * i) * kRows + row;
-                            const float4 v0 = __ldcg(src), v1 = __ldcg(src + kRows);
-                            o0.x = fmaf(ek, v0.x, o0.x); o0.y = fmaf(ek, v0.y, o0.y); o0.z = fmaf(ek, v0.z, o0.z); o0.w = fmaf(ek, v0.w, o0.w);
-                            o1.x = fmaf(ek, v1.x, o1.x); o1.y = fmaf(ek, v1.y, o1.y); o1.z = fmaf(ek, v1.z, o1.z); o1.w = fmaf(ek, v1.w, o1.w);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                o[k].x = fmaf(ek, v[k].x, o[k].x); o[k].y = fmaf(ek, v[k].y, o[k].y);
+                                o[k].z = fmaf(ek, v[k].z, o[k].z); o[k].w = fmaf(ek, v[k].w, o[k].w);
+                            }
                         }
                         if (live) {
-                            write_out4<D>(a, w.q, w.h, r, 8 * i, o0);
-                            write_out4<D>(a, w.q, w.h, r, 8 * i + 4, o1);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) write_out4<D>(a, w.q, w.h, r, 32 * i + 4 * k, o[k]);
                         }
                     }
                     if (live) write_lse(a, w.q, w.h, r, gm, gl);
                 }
             }
-            w.next(a, u1);
-            if (w.unit >= u1) break;
+            w.next(a, u0, u1);
+            if (w.end) break;
         }
     }
     __syncthreads();
