@@ -114,6 +114,18 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return r;
 }
 
+// Four 8 x 8 matrices of 16-bit numbers to shared memory; lane 8 m + r gives the address of row r of matrix m.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+// 32 bytes to a 32-byte boundary of device memory: a whole sector from each lane.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[16], int at) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[at]), "r"(v[at + 1]), "r"(v[at + 2]),
+                 "r"(v[at + 3]), "r"(v[at + 4]), "r"(v[at + 5]), "r"(v[at + 6]), "r"(v[at + 7])
+                 : "memory");
+}
+
 // The larger magnitudes of two packed bf16 pairs (a NaN gives way to a number:
 // the row's products are NaN whatever its power of two is).
 __device__ __forceinline__ uint32_t bf2_max_abs(uint32_t x, uint32_t y) {
@@ -576,9 +588,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         w.begin(a, start, u0, u1);
         uint32_t n = 0, st = 0, ph = 0;
         const int i8 = lane >> 2, t = lane & 3;
-        uint32_t v_off[8];           // byte of (row k of an 8-row group, 8-token chunk i8, token pair t)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v_off[k] = static_cast<uint32_t>(k * 128 + ((i8 ^ k) * 16) + t * 4);
+        // A byte of value codes is a number of two tokens; over a warp, the 8 x 8 matrix (token chunk i8, token of
+        // the chunk) of one number.  Four of them are stored at once: this lane gives the address of row
+        // lane % 8 of matrix lane / 8, for numbers 0-3 and 4-7 of an 8-row group.
+        const uint32_t vm = lane >> 3, vr = lane & 7;
+        const uint32_t v_off[2] = {vm * 128 + ((vr ^ vm) * 16), (vm + 4) * 128 + ((vr ^ (vm + 4)) * 16)};
         const int b_free = keys ? B_KE : B_VE, b_full = keys ? B_KF : B_VF;
         while (ok) {
             for (int j = w.pa; j < w.pb && ok; ++j) {
@@ -630,7 +644,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                         }
                     }
                 } else {
-                    uint8_t* vt = smem + C::o_v + (n % kBuf) * C::v_tile;
+                    const uint32_t vt = smem_u32(smem + C::o_v) + (n % kBuf) * C::v_tile;
                     // a thread converts a token pair's runs of D/8 numbers, four of the eight
                     uint32_t c[4][W], sc[4];
                     const int left = w.q.len - j * kPage;
@@ -656,14 +670,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                             two = tok + 1 < left ? two : (tok < left ? (two & 0xffu) : 0u);
                         }
                         const uint32_t s2 = e4m3x2_to_f16(two);
-                        uint8_t* row = vt + (4 * cw + u) * (L::U * 128);
+                        const uint32_t row = vt + (4 * cw + u) * (L::U * 128);
 #pragma unroll
                         for (int i = 0; i < W; ++i) {
                             uint32_t f[4];
                             e2m1x8_to_f16(c[u][i], f[0], f[1], f[2], f[3]);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                *reinterpret_cast<uint32_t*>(row + (i / 2) * 1024 + v_off[(4 * i + k) % 8]) = hmul2_u(f[k], s2);
+                            stmatrix4(row + (i / 2) * 1024 + v_off[i & 1], hmul2_u(f[0], s2), hmul2_u(f[1], s2), hmul2_u(f[2], s2), hmul2_u(f[3], s2));
                         }
                     }
                 }
@@ -690,6 +702,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         w.begin(a, start, u0, u1);
         uint32_t n = 0;              // pages of this tile so far
         uint32_t qb = 0, qp = 0;
+        const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.ld_out % 16 == 0;
         // after a wait that ran out (ok = false) the items are walked to the end all the same, without
         // waiting: the two tiles' warps meet at barriers below
         while (true) {
@@ -820,18 +833,21 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                 }
                 if (whole) {
                     if (live) {
-                        uint4* out = reinterpret_cast<uint4*>(a.out + static_cast<long long>(w.q.q0 + r / a.group) * a.ld_out +
-                                                              static_cast<long long>(w.h * a.group + r % a.group) * D + 32 * i);
+                        __nv_bfloat16* out = a.out + static_cast<long long>(w.q.q0 + r / a.group) * a.ld_out +
+                                             static_cast<long long>(w.h * a.group + r % a.group) * D + 32 * i;
+                        uint32_t v[16];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t v[4];
+                        for (int k = 0; k < 16; ++k) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+                            memcpy(&v[k], &b, 4);
+                        }
+                        if (out32) {
+                            st_global_32(out, v, 0);
+                            st_global_32(out + 16, v, 8);
+                        } else {
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                // a row that has seen nothing has l = 0: its O is not a number only if the page's is
-                                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * c]) * inv, __uint_as_float(o[8 * k + 2 * c + 1]) * inv);
-                                memcpy(&v[c], &b, 4);
-                            }
-                            out[k] = make_uint4(v[0], v[1], v[2], v[3]);
+                            for (int k = 0; k < 4; ++k)
+                                reinterpret_cast<uint4*>(out)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                         }
                     }
                 } else {
