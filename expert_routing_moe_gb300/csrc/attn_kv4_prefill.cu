@@ -12,8 +12,8 @@
 //
 // Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (a thread is a row), 8-9
 // convert the keys' pages and 10-11 the values' to fp16 operands (exact), 12-13
-// issue the tiles' products, 14 copies pages (one bulk copy each), 15 brings the
-// next item's queries.  O is scaled only when a row's maximum grows by more
+// issue the tiles' products, 14 copies pages (one bulk copy each), 15 the next
+// item's queries, which the softmax warps turn to fp16 between two items.  O is scaled only when a row's maximum grows by more
 // than 2^8, which fp16's range allows for P.
 //
 // The pages of all items form one sequence of units, cut into equal runs for
@@ -151,8 +151,9 @@ struct Pf {
     static constexpr int k_tile = kPage * D * 2;      // D/64 halves of [64 tokens][64 numbers], 128-byte rows
     static constexpr int v_tile = kPage * D * 2;      // [D numbers][64 tokens], 128-byte rows
     static constexpr int q_tile = kTile * D * 2;      // D/64 halves of [128 rows][64 numbers], 128-byte rows
-    static constexpr int o_q = 0;                     // two buffers of two tiles
-    static constexpr int o_k = o_q + 4 * q_tile;
+    static constexpr int o_q = 0;                     // two tiles
+    static constexpr int o_qraw = o_q + 2 * q_tile;   // an item's queries as they come: [256 rows][D] bf16
+    static constexpr int o_k = o_qraw + 2 * q_tile;
     static constexpr int o_v = o_k + kBuf * k_tile;
     static constexpr int o_raw = o_v + kBuf * v_tile;
     static constexpr int smem = o_raw + kRaw * raw + 1024;   // slack for 1024-byte alignment
@@ -232,14 +233,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     enum { B_RAWF = 0, B_RAWE = B_RAWF + kRaw, B_KF = B_RAWE + kRaw, B_KE = B_KF + kBuf, B_VF = B_KE + kBuf, B_VE = B_VF + kBuf,
-           B_QF = B_VE + kBuf, B_QE = B_QF + 2, B_S = B_QE + 2, B_P = B_S + 4, B_O = B_P + 4, B_DRAIN = B_O + 4, B_N = B_DRAIN + 2 };
+           B_QF = B_VE + kBuf, B_QRF = B_QF + 2, B_QRE = B_QRF + 1, B_S = B_QRE + 1, B_P = B_S + 4, B_O = B_P + 4, B_DRAIN = B_O + 4, B_N = B_DRAIN + 2 };
     __shared__ __align__(8) uint64_t bars[B_N];
     __shared__ uint32_t s_tmem;
     __shared__ long long s_units[kChunk], s_warp[kPfWarps];
     __shared__ int s_list[kChunk], s_list_n, s_ticket;
     __shared__ Start s_start;
     __shared__ uint8_t s_bad[kRaw];
-    __shared__ float s_f[2][kRows];
+    __shared__ float s_f[kRows];
     __shared__ volatile int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -251,11 +252,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
             mbar_init(bar(B_VF + i), 2); mbar_init(bar(B_VE + i), 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(B_QF + i), 1);
-            mbar_init(bar(B_QE + i), 2 + 8);       // the products' and the softmax warps'
+            mbar_init(bar(B_QF + i), 4);
             mbar_init(bar(B_DRAIN + i), 1);
         }
         for (int i = 0; i < 4; ++i) { mbar_init(bar(B_S + i), 1); mbar_init(bar(B_P + i), 4); mbar_init(bar(B_O + i), 1); }
+        mbar_init(bar(B_QRF), 1);
+        mbar_init(bar(B_QRE), 8);
         s_abort = 0;
         fence_mbar_init();
     }
@@ -362,84 +364,41 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
     const uint32_t tmem = s_tmem;
     const Start start = s_start;
 
-    // Rows [32 g0, 32 g1) of an item's queries to buffer b: a lane takes a row, scaled by a power of
-    // two of its own (see the streaming kernel) to fp16, into the products' layout.
-    auto load_q = [&](const Walk& w, uint32_t b, int g0, int g1) {
-        const int rows = w.q.n * a.group;
-        const float f_all = a.scale * kLog2e * (a.c.k_scale != nullptr ? a.c.k_scale[w.h] : 1.f);
-        auto row_ptr = [&](int r) {
-            const int i = r / a.group;
-            return a.q + static_cast<long long>(w.q.q0 + i) * a.ld_q + static_cast<long long>(w.h * a.group + r - i * a.group) * D;
-        };
-        for (int g = g0; g < g1; ++g) {
-            const int rt = 32 * g + lane, r = w.tile * kRows + rt;
-            const uint4* src = reinterpret_cast<const uint4*>(row_ptr(min(r, rows - 1)));
-            uint4 v[D / 8];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) v[i] = r < rows ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-            if (g + 1 < g1 && r + 32 < rows) {
-                const __nv_bfloat16* next = row_ptr(r + 32);
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) asm volatile("prefetch.global.L1 [%0];" ::"l"(next + 64 * i));
-            }
-            uint32_t top2 = 0u;                        // the largest magnitudes, as two bf16
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                top2 = bf2_max_abs(top2, bf2_max_abs(bf2_max_abs(v[i].x, v[i].y), bf2_max_abs(v[i].z, v[i].w)));
-            const float top = fmaxf(__uint_as_float(top2 << 16), __uint_as_float(top2 & 0xffff0000u));
-            int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-            e = (top > 0.f && e < 128) ? max(-100, min(100, 10 - e)) : 0;
-            float up = __int_as_float((e + 127) << 23);
-            float f = f_all * __int_as_float((127 - e) << 23);
-            // the maximum is taken before the factor: it has to be positive
-            if (f < 0.f) { f = -f; up = -up; }
-            s_f[b][rt] = fmaxf(f, 1e-37f);
-            uint8_t* dst = smem + C::o_q + (2 * b + rt / kTile) * C::q_tile + (rt % kTile) * 128;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                uint32_t h[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    h[k] = pack_f16(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xffff0000u) * up);
-                *reinterpret_cast<uint4*>(dst + (i / 8) * (kTile * 128) + (((i % 8) ^ (rt & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-        }
-        fence_proxy_async_smem();
-    };
-    // the first item's by eight warps
-    {
-        Walk w;
-        w.begin(a, start, u0, u1);
-        while (w.pa >= w.pb && !w.end) w.next(a, u0, u1);
-        if (!w.end && warp < kRows / 32) load_q(w, 0, warp, warp + 1);
-    }
-    __syncthreads();
-
+    // The roles deal the 512 x 128 registers anew: 256 x 152 + 128 x 96 + 128 x 104 = 64,512 of 65,536.
     bool ok = true;
     if (warp == 15) {
         // ---------------- the next items' queries ----------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        // A token's query heads of the key head lie side by side: one copy for each token.
         Walk w;
         w.begin(a, start, u0, u1);
-        uint32_t b = 0, ph = 1;
-        bool first = true;
+        uint32_t ph = 1;
         while (ok) {
             if (w.pa < w.pb) {
-                ok = mbar_wait(bar(B_QE + b), ph, &s_abort, a.st, kSiteQFree);
+                ok = mbar_wait(bar(B_QRE), ph, &s_abort, a.st, kSiteQFree);
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
-                if (!first) load_q(w, b, 0, kRows / 32);
-                first = false;
+                ph ^= 1;
+                const int r0 = w.tile * kRows, r1 = min(w.q.n * a.group, r0 + kRows);
+                if (lane == 0) mbar_arrive_expect_tx(bar(B_QRF), (r1 - r0) * (D * 2));
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_QF + b));
-                b ^= 1;
-                ph ^= b == 0;
+                for (int i = r0 / a.group + lane; i * a.group < r1; i += 32) {
+                    const int x = max(r0, i * a.group), y = min(r1, (i + 1) * a.group);
+                    bulk_copy_g2s(smem_u32(smem + C::o_qraw) + (x - r0) * (D * 2),
+                                  a.q + static_cast<long long>(w.q.q0 + i) * a.ld_q + static_cast<long long>(w.h * a.group + x - i * a.group) * D,
+                                  (y - x) * (D * 2), bar(B_QRF));
+                }
             }
             w.next(a, u0, u1);
             if (w.end) break;
         }
+        if (!ok) {       // copies in flight land before the CTA gives its shared memory up
+            mbar_drain(bar(B_QRF), 0);
+            mbar_drain(bar(B_QRF), 1);
+        }
     } else if (warp == 14) {
         // ---------------- pages from device memory ----------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         Walk w;
         w.begin(a, start, u0, u1);
         int st = 0;
@@ -485,6 +444,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         }
     } else if (warp >= 12) {
         // ---------------- products ----------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         // A warp for each tile: waits and commits cost issue time, which the
         // other tile's products then fill.  The warp walks together and one
         // elected lane issues: addresses and descriptors stay in uniform registers.
@@ -504,77 +464,57 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         uint32_t kv = 0, vv = 0;                       // pages of keys and values so far
         uint32_t ns = 0, no = 0;                       // scores and outputs issued
         uint32_t nq = 0;                               // items
-        auto scores = [&](bool active, bool last) {    // of the next page of keys
+        auto scores = [&](bool active) {               // of the next page of keys
             if (!wait(B_KF + kv % kBuf, (kv / kBuf) & 1, kSiteKFull)) return;
             tc_fence_after();
             if (elect_one()) {
                 if (active) {
-                    const uint64_t d = k_desc + (kv % kBuf) * (C::k_tile >> 4), q = q_desc + (nq & 1) * (2 * C::q_tile >> 4);
+                    const uint64_t d = k_desc + (kv % kBuf) * (C::k_tile >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        tc_mma_bf16(ts + 64 * (ns & 1), q + (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2,
+                        tc_mma_bf16(ts + 64 * (ns & 1), q_desc + (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2,
                                     d + (k / 4) * (kPage * 128 >> 4) + (k % 4) * 2, id_s, k > 0);
                     tc_commit(bar_s + 8 * (ns & 1));
                 }
                 tc_commit(bar(B_KE + kv % kBuf));
-                if (last) tc_commit(bar(B_QE + (nq & 1)));
             }
             __syncwarp();
             ns += active;
             ++kv;
         };
-        // the scores run a page ahead of the outputs, also from one item to the next
-        int x = 0, y = 0, j = 0;                       // the tile's pages of the item whose outputs are next
-        bool begun = false;
-        while (ok) {
-            const bool some = w.pa < w.pb;
-            int nx = 0, ny = 0;
-            if (some) {
-                w.half(a, t, nx, ny);
-                if (!wait(B_QF + (nq & 1), (nq >> 1) & 1, kSiteQ)) break;
-            }
-            // one step for each page: its scores, then the outputs of the page before
-            for (int p = w.pa; p < w.pb; ++p) {
-                scores(nx <= p && p < ny, p + 1 == w.pb);
-                if (!ok) break;
-                if (begun) {
-                    if (!wait(B_VF + vv % kBuf, (vv / kBuf) & 1, kSiteVFull)) break;
-                    const bool active = x <= j && j < y;
-                    if (active && !wait(B_P + 2 * t + (no & 1), (no >> 1) & 1, kSiteP)) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        if (active) {
-                            const uint64_t d = v_desc + (vv % kBuf) * (C::v_tile >> 4);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) tc_mma_ts(to, ts + 64 * (no & 1) + 8 * k, d + 2 * k, id_o, j > x || k > 0);
-                            tc_commit(bar_o + 8 * (no & 1));
-                        }
-                        tc_commit(bar(B_VE + vv % kBuf));
-                    }
-                    __syncwarp();
-                    no += active;
-                    ++vv;
-                }
-                begun = true;
-                x = nx; y = ny; j = p;
-            }
-            if (!ok) break;
-            if (some) ++nq;
-            w.next(a, u0, u1);
-            if (w.end) break;
-        }
-        if (ok && begun) {                              // the last page's outputs
-            const bool active = x <= j && j < y;
-            if (wait(B_VF + vv % kBuf, (vv / kBuf) & 1, kSiteVFull) && (!active || wait(B_P + 2 * t + (no & 1), (no >> 1) & 1, kSiteP))) {
-                tc_fence_after();
-                if (elect_one() && active) {
+        auto outputs = [&](bool active, bool add) {    // of the next page of values
+            if (!wait(B_VF + vv % kBuf, (vv / kBuf) & 1, kSiteVFull)) return;
+            if (active && !wait(B_P + 2 * t + (no & 1), (no >> 1) & 1, kSiteP)) return;
+            tc_fence_after();
+            if (elect_one()) {
+                if (active) {
                     const uint64_t d = v_desc + (vv % kBuf) * (C::v_tile >> 4);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tc_mma_ts(to, ts + 64 * (no & 1) + 8 * k, d + 2 * k, id_o, j > x || k > 0);
+                    for (int k = 0; k < 4; ++k) tc_mma_ts(to, ts + 64 * (no & 1) + 8 * k, d + 2 * k, id_o, add || k > 0);
                     tc_commit(bar_o + 8 * (no & 1));
                 }
-                __syncwarp();
+                tc_commit(bar(B_VE + vv % kBuf));
             }
+            __syncwarp();
+            no += active;
+            ++vv;
+        };
+        // The scores run a page ahead of the outputs within an item.
+        while (ok) {
+            if (w.pa < w.pb) {
+                int x, y;
+                w.half(a, t, x, y);
+                if (!wait(B_QF + t, nq & 1, kSiteQ)) break;
+                ++nq;
+                scores(x <= w.pa && w.pa < y);
+                for (int p = w.pa; ok && p < w.pb; ++p) {
+                    if (p + 1 < w.pb) scores(x <= p + 1 && p + 1 < y);
+                    if (ok) outputs(x <= p && p < y, p > x);
+                }
+                if (!ok) break;
+            }
+            w.next(a, u0, u1);
+            if (w.end) break;
         }
         // every product is done before TMEM and shared memory are given up
         if (elect_one()) tc_commit(bar(B_DRAIN + t));
@@ -582,6 +522,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         mbar_drain(bar(B_DRAIN + t), 0);
     } else if (warp >= 8 && warp < 12) {
         // ---------------- 4 bits to fp16 operands ----------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         const bool keys = warp < 10;
         const int cw = (warp - 8) & 1;        // which of the two warps
         Walk w;
@@ -694,6 +635,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         }
     } else {
         // ---------------- softmax: a thread is a row ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         const int t = warp >> 2;                              // tile
         const int r_tile = (warp & 3) * 32 + lane;            // row of the tile = TMEM lane
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -701,8 +643,65 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         Walk w;
         w.begin(a, start, u0, u1);
         uint32_t n = 0;              // pages of this tile so far
-        uint32_t qb = 0, qp = 0;
+        uint32_t qp = 0;
+        float f = 0.f;               // the row's factor of the item at hand
         const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.ld_out % 16 == 0;
+        // The warp's 32 rows of an item's queries to fp16, in the products' layout: eight lanes hold a row,
+        // scaled by a power of two of its own (see the streaming kernel).  Called when the tile's scores of
+        // the item before are done.
+        auto convert_q = [&](const Walk& w) {
+            ok = mbar_wait(bar(B_QRF), qp, &s_abort, a.st, kSiteQ);
+            ok = __all_sync(kFull, ok);
+            if (!ok) return;
+            qp ^= 1;
+            const float f_all = a.scale * kLog2e * (a.c.k_scale != nullptr ? a.c.k_scale[w.h] : 1.f);
+            const int rows = w.q.n * a.group - w.tile * kRows;
+            const int c = lane & 7;
+            constexpr int H = D / 64;                  // 64-number halves of a row
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) {
+                const int rl = (warp & 3) * 32 + 4 * i + (lane >> 3), rt = t * kTile + rl;
+                uint4 v[H];
+                uint32_t top2 = 0u;                    // the largest magnitudes, as two bf16
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    v[k] = rt < rows ? *reinterpret_cast<const uint4*>(smem + C::o_qraw + rt * (D * 2) + k * 128 + c * 16) : make_uint4(0u, 0u, 0u, 0u);
+                    top2 = bf2_max_abs(top2, bf2_max_abs(bf2_max_abs(v[k].x, v[k].y), bf2_max_abs(v[k].z, v[k].w)));
+                }
+                float top = fmaxf(__uint_as_float(top2 << 16), __uint_as_float(top2 & 0xffff0000u));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+                int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+                e = (top > 0.f && e < 128) ? max(-100, min(100, 10 - e)) : 0;
+                float up = __int_as_float((e + 127) << 23), fr = f_all * __int_as_float((127 - e) << 23);
+                // the maximum is taken before the factor: it has to be positive
+                if (fr < 0.f) { fr = -fr; up = -up; }
+                if (c == 0) s_f[rt] = fmaxf(fr, 1e-37f);
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                    uint32_t h[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        h[z] = pack_f16(__uint_as_float(u[z] << 16) * up, __uint_as_float(u[z] & 0xffff0000u) * up);
+                    *reinterpret_cast<uint4*>(smem + C::o_q + t * C::q_tile + k * (kTile * 128) + rl * 128 + ((c ^ (rl & 7)) * 16)) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            f = s_f[t * kTile + r_tile];
+            if (lane == 0) {
+                mbar_arrive(bar(B_QF + t));
+                mbar_arrive(bar(B_QRE));
+            }
+        };
+        {
+            Walk nw = w;
+            while (!nw.end && nw.pa >= nw.pb) nw.next(a, u0, u1);
+            if (!nw.end) convert_q(nw);
+        }
         // after a wait that ran out (ok = false) the items are walked to the end all the same, without
         // waiting: the two tiles' warps meet at barriers below
         while (true) {
@@ -714,13 +713,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
             // Outputs of pages n - 1 and n - 2 may both be outstanding (the scores run ahead), so they
             // signal two barriers in turn: the one waited on is never two phases behind.
             if (w.pa < w.pb && ok) {
-                ok = mbar_wait(bar(B_QF + qb), qp, &s_abort, a.st, kSiteQ);
-                ok = __all_sync(kFull, ok);
-                const float f = s_f[qb][t * kTile + r_tile];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_QE + qb));
-                qb ^= 1;
-                qp ^= qb == 0;
                 // places of the row and of the tile's first and last row, for the pages that need no mask
                 const int p_row = w.q.len - w.q.n + r / a.group;
                 const int rt0 = w.tile * kRows + t * kTile, rt1 = min(w.q.n * a.group, rt0 + kTile) - 1;
@@ -728,16 +720,18 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                 const int first_key = a.window > 0 ? p_row - a.window + 1 : 0;
                 float mf = -INFINITY;                            // the maximum in use, before the factor
                 float2 l2 = make_float2(0.f, 0.f);
-                for (int j = x; j < y && ok; ++j, ++n) {
-                    ok = mbar_wait(bar(B_S + 2 * t + (n & 1)), (n >> 1) & 1, &s_abort, a.st, kSiteS);
+                uint32_t s0[32], s1[32];                         // a page's scores
+                auto wait_s = [&](uint32_t i) {
+                    ok = mbar_wait(bar(B_S + 2 * t + (i & 1)), (i >> 1) & 1, &s_abort, a.st, kSiteS);
                     ok = __all_sync(kFull, ok);
-                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t ts = tb + C::c_s + 64 * (n & 1);
-                    uint32_t s0[32], s1[32];
-                    tmem_ld32(ts, s0);
-                    tmem_ld32(ts + 32, s1);
-                    tmem_ld_wait();
+                    return ok;
+                };
+                auto load_s = [&](uint32_t i) {
+                    tmem_ld32(tb + C::c_s + 64 * (i & 1), s0);
+                    tmem_ld32(tb + C::c_s + 64 * (i & 1) + 32, s1);
+                };
+                auto hide = [&](int j) {
                     const int key0 = j * kPage;
                     if (key0 + kPage - 1 > p_first || (a.window > 0 && key0 <= p_last - a.window)) {
                         const int last = p_row - key0, first = first_key - key0;
@@ -747,17 +741,47 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                             if (k + 32 > last || k + 32 < first) s1[k] = 0xff800000u;
                         }
                     }
-                    float t4[4] = {__uint_as_float(s0[0]), __uint_as_float(s0[16]), __uint_as_float(s1[0]), __uint_as_float(s1[16])};
+                };
+                if (x < y && wait_s(n)) {
+                    load_s(n);
+                    tmem_ld_wait();
+                    hide(x);
+                    float t0 = __uint_as_float(s0[0]), t1 = __uint_as_float(s1[0]);
 #pragma unroll
-                    for (int k = 1; k < 15; k += 2) {
-                        t4[0] = max3(t4[0], __uint_as_float(s0[k]), __uint_as_float(s0[k + 1]));
-                        t4[1] = max3(t4[1], __uint_as_float(s0[16 + k]), __uint_as_float(s0[17 + k]));
-                        t4[2] = max3(t4[2], __uint_as_float(s1[k]), __uint_as_float(s1[k + 1]));
-                        t4[3] = max3(t4[3], __uint_as_float(s1[16 + k]), __uint_as_float(s1[17 + k]));
+                    for (int k = 1; k < 31; k += 2) {
+                        t0 = max3(t0, __uint_as_float(s0[k]), __uint_as_float(s0[k + 1]));
+                        t1 = max3(t1, __uint_as_float(s1[k]), __uint_as_float(s1[k + 1]));
                     }
-                    const float now = max3(max3(t4[0], __uint_as_float(s0[15]), t4[1]), max3(__uint_as_float(s0[31]), t4[2], __uint_as_float(s1[15])),
-                                           fmaxf(t4[3], __uint_as_float(s1[31])));
-                    // in use: the maximum so far, unless it has grown by more than 2^kGrow
+                    mf = fmaxf(max3(t0, t1, __uint_as_float(s0[31])), __uint_as_float(s1[31]));
+                }
+                for (int j = x; j < y && ok; ++j, ++n) {
+                    // The exponentials use the maximum so far and the page's own is found beside them: only
+                    // when it is more than 2^kGrow above is the page done over, with O and l scaled.
+                    uint32_t h[32];
+                    float2 sum;
+                    auto exponentials = [&]() {
+                        const float base = mf == -INFINITY ? 0.f : -mf * f;
+                        const float2 f2 = make_float2(f, f), b2 = make_float2(base, base);
+                        float t0 = -INFINITY, t1 = -INFINITY;
+                        sum = make_float2(0.f, 0.f);
+                        float2 sum1 = sum;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            t0 = max3(t0, __uint_as_float(s0[2 * k]), __uint_as_float(s0[2 * k + 1]));
+                            t1 = max3(t1, __uint_as_float(s1[2 * k]), __uint_as_float(s1[2 * k + 1]));
+                            float2 p0 = fma2(make_float2(__uint_as_float(s0[2 * k]), __uint_as_float(s0[2 * k + 1])), f2, b2);
+                            float2 p1 = fma2(make_float2(__uint_as_float(s1[2 * k]), __uint_as_float(s1[2 * k + 1])), f2, b2);
+                            p0.x = ex2(p0.x); p0.y = ex2(p0.y);
+                            p1.x = ex2(p1.x); p1.y = ex2(p1.y);
+                            sum = add2(sum, p0);
+                            sum1 = add2(sum1, p1);
+                            h[k] = pack_f16(p0.x, p0.y);
+                            h[16 + k] = pack_f16(p1.x, p1.y);
+                        }
+                        sum = add2(sum, sum1);
+                        return fmaxf(t0, t1);
+                    };
+                    const float now = exponentials();
                     if (__any_sync(kFull, now > mf && (mf == -INFINITY || (now - mf) * f > kGrow))) {
                         const float nm = fmaxf(mf, now);
                         const float sc = mf == -INFINITY ? 0.f : ex2((mf - nm) * f);
@@ -780,30 +804,35 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                                 tmem_st16(tb + C::c_o + 16 * i, o);
                             }
                         }
+                        load_s(n);
+                        tmem_ld_wait();
+                        hide(j);
+                        exponentials();
                     }
-                    const float base = mf == -INFINITY ? 0.f : -mf * f;
-                    const float2 f2 = make_float2(f, f), b2 = make_float2(base, base);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float2 p0 = fma2(make_float2(__uint_as_float(s0[2 * k]), __uint_as_float(s0[2 * k + 1])), f2, b2);
-                        float2 p1 = fma2(make_float2(__uint_as_float(s1[2 * k]), __uint_as_float(s1[2 * k + 1])), f2, b2);
-                        p0.x = ex2(p0.x); p0.y = ex2(p0.y);
-                        p1.x = ex2(p1.x); p1.y = ex2(p1.y);
-                        l2 = add2(l2, add2(p0, p1));
-                        s0[k] = pack_f16(p0.x, p0.y);
-                        s1[k] = pack_f16(p1.x, p1.y);
+                    l2 = add2(l2, sum);
+                    // the next page's scores come in while this page's P goes out
+                    const bool more = j + 1 < y;
+                    if (more) {
+                        if (!wait_s(n + 1)) break;
+                        tmem_ld32(tb + C::c_s + 64 * ((n + 1) & 1), s0);
                     }
-                    uint32_t h[32];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) { h[k] = s0[k]; h[16 + k] = s1[k]; }
-                    tmem_st32(ts, h);
+                    tmem_st32(tb + C::c_s + 64 * (n & 1), h);
+                    if (more) tmem_ld32(tb + C::c_s + 64 * ((n + 1) & 1) + 32, s1);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_P + 2 * t + (n & 1)));
+                    if (more) {
+                        tmem_ld_wait();
+                        hide(j + 1);
+                    }
                 }
                 l = l2.x + l2.y;
                 m = mf == -INFINITY ? -INFINITY : mf * f;
+                // the queries of the next item, while the last outputs are summed
+                Walk nw = w;
+                do nw.next(a, u0, u1); while (!nw.end && nw.pa >= nw.pb);
+                if (!nw.end && ok) convert_q(nw);
                 if (ok && x < y) {
                     ok = mbar_wait(bar(B_O + 2 * t + ((n - 1) & 1)), ((n - 1) >> 1) & 1, &s_abort, a.st, kSiteO);
                     ok = __all_sync(kFull, ok);
