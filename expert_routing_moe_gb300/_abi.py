@@ -73,6 +73,8 @@ EXPORTS = ["moe_route", "moe_route_dispatch", "moe_decode_layer", "moe_reroute_s
 def load(path: str = LIB_PATH):
     """Load the shared library (no GPU needed to load it)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -338,31 +340,31 @@ def _addr(t: Optional[torch.Tensor], dtype=None, what: str = "") -> Optional[int
     """A CUDA tensor's address; checks its dtype and that it is dense."""
     if t is None:
         return None
+    if t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise MoeError("%s: expected a CUDA tensor" % what)
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise MoeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
-    if not t.is_contiguous():
-        raise MoeError("%s: expected a dense tensor" % what)
-    return t.data_ptr()
+    raise MoeError("%s: expected a dense tensor" % what)
 
 
-def _rows(t: torch.Tensor, width: int, dtype, what: str):
-    """(address, leading dimension) of rows of `width` numbers whose trailing
+def _rows(t: torch.Tensor, T: int, width: int, dtype, what: str):
+    """(address, leading dimension) of T rows of `width` numbers whose trailing
     dimensions are dense; only the first may have a stride of its own."""
     if not t.is_cuda:
         raise MoeError("%s: expected a CUDA tensor" % what)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise MoeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
     shape, stride = t.shape, t.stride()
     n = 1
-    for k in range(t.dim() - 1, 0, -1):
+    for k in range(len(shape) - 1, 0, -1):
         if stride[k] != n and shape[k] != 1:
             raise MoeError("%s: only the rows may be strided" % what)
         n *= shape[k]
-    if t.dim() < 2 or n != width:
-        raise MoeError("%s: expected rows of %d numbers, got %s" % (what, width, list(shape)))
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else max(stride[0], width))
+    if len(shape) < 2 or n != width or shape[0] != T:
+        raise MoeError("%s: expected %d rows of %d numbers, got %s" % (what, T, width, list(shape)))
+    return t.data_ptr(), (stride[0] if T > 1 else max(stride[0], width))
 
 
 class Kv4Cache:
@@ -450,8 +452,10 @@ def kv4_pool_workspace(pool: Kv4Pool) -> int:
     return int(load().moe_kv4_pool_workspace(pool.S, pool.n_pages))
 
 
-def _raw_stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    """The given stream, or the current one of the tensor's device (read
+    without building a Stream object, which takes longer than a launch)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _check_starts(q_start, S: int):
@@ -474,15 +478,12 @@ def moe_qk_norm_rope(qkv, n_q: int, n_kv: int, q_out, k_out=None, q_weight=None,
     if n_q + 2 * n_kv < 1 or width % (n_q + 2 * n_kv):
         raise MoeError("qkv: rows of %d numbers are not %d heads" % (width, n_q + 2 * n_kv))
     D = width // (n_q + 2 * n_kv)
-    x, ld = _rows(qkv, width, qkv.dtype, "qkv")
-    q, ld_q = (None, 0) if n_q == 0 else _rows(q_out, n_q * D, qkv.dtype, "q_out")
-    k, ld_k = (None, 0) if k_out is None else _rows(k_out, n_kv * D, qkv.dtype, "k_out")
-    for t, what in ((None if n_q == 0 else q_out, "q_out"), (k_out, "k_out")):
-        if t is not None and t.shape[0] != T:
-            raise MoeError("%s: expected %d rows, got %d" % (what, T, t.shape[0]))
-    for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None and t.numel() != D:
-            raise MoeError("%s: expected %d numbers" % (what, D))
+    dt = qkv.dtype
+    x, ld = _rows(qkv, T, width, dt, "qkv")
+    q, ld_q = (None, 0) if n_q == 0 else _rows(q_out, T, n_q * D, dt, "q_out")
+    k, ld_k = (None, 0) if k_out is None else _rows(k_out, T, n_kv * D, dt, "k_out")
+    if q_weight is not None and q_weight.numel() != D or k_weight is not None and k_weight.numel() != D:
+        raise MoeError("q_weight, k_weight: expected %d numbers" % D)
     if rope is not None and rope.T is not None and rope.T != T:
         raise MoeError("positions: expected %d tokens, got %d" % (T, rope.T))
     if cache is not None and q_start is None:
@@ -492,7 +493,7 @@ def moe_qk_norm_rope(qkv, n_q: int, n_kv: int, q_out, k_out=None, q_weight=None,
                                  _addr(k_weight, f32, "k_weight"), eps, None if rope is None else rope._ref, q, ld_q, k,
                                  ld_k, None if cache is None else cache._ref,
                                  None if cache is None else _check_starts(q_start, cache.S),
-                                 _addr(st, torch.int32, "st"), _raw_stream(stream))
+                                 _addr(st, torch.int32, "st"), _raw_stream(stream, qkv))
     _check(rc, "moe_qk_norm_rope")
 
 
@@ -507,7 +508,7 @@ def moe_kv4_read(cache: Kv4Cache, q_start, k_out=None, v_out=None, st=None, stre
             T = t.shape[0]
     bf = torch.bfloat16
     rc = load().moe_kv4_read(cache._ref, _check_starts(q_start, cache.S), T, _addr(k_out, bf, "k_out"),
-                             _addr(v_out, bf, "v_out"), _addr(st, torch.int32, "st"), _raw_stream(stream))
+                             _addr(v_out, bf, "v_out"), _addr(st, torch.int32, "st"), _raw_stream(stream, q_start))
     _check(rc, "moe_kv4_read")
 
 
@@ -522,10 +523,8 @@ def moe_attention_kv4(q, cache: Kv4Cache, q_start, out, scale: float, max_new: i
     if q.dim() != 3 or q.shape[2] != D:
         raise MoeError("q: expected [T][n_q][%d], got %s" % (D, list(q.shape)))
     T, n_q = q.shape[0], q.shape[1]
-    if out.shape[0] != T:
-        raise MoeError("out: expected %d rows, got %d" % (T, out.shape[0]))
-    qp, ld_q = _rows(q, n_q * D, torch.bfloat16, "q")
-    op, ld_o = _rows(out, n_q * D, torch.bfloat16, "out")
+    qp, ld_q = _rows(q, T, n_q * D, torch.bfloat16, "q")
+    op, ld_o = _rows(out, T, n_q * D, torch.bfloat16, "out")
     if lse is not None and lse.numel() != T * n_q:
         raise MoeError("lse: expected [%d][%d]" % (T, n_q))
     if workspace is None:
@@ -534,7 +533,7 @@ def moe_attention_kv4(q, cache: Kv4Cache, q_start, out, scale: float, max_new: i
     rc = load().moe_attention_kv4(qp, ld_q, T, n_q, cache._ref, _check_starts(q_start, cache.S), max_new, scale, window,
                                   op, ld_o, _addr(lse, torch.float32, "lse"), _addr(workspace, None, "workspace"),
                                   workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
-                                  _raw_stream(stream))
+                                  _raw_stream(stream, q))
     _check(rc, "moe_attention_kv4")
 
 
@@ -550,7 +549,7 @@ def moe_kv4_reserve(pool: Kv4Pool, n_new, workspace, st=None, stream=None):
     zero-filled before its first use."""
     rc = load().moe_kv4_reserve(pool._ref, _pool_vector(n_new, pool, "n_new"), _addr(workspace, None, "workspace"),
                                 workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
-                                _raw_stream(stream))
+                                _raw_stream(stream, n_new))
     _check(rc, "moe_kv4_reserve")
 
 
@@ -558,7 +557,7 @@ def moe_kv4_assign(pool: Kv4Pool, parent, st=None, stream=None):
     """Every sequence becomes what parent[s] was (parent [S] int32, -1 = empty):
     forking, reordering and freeing."""
     rc = load().moe_kv4_assign(pool._ref, _pool_vector(parent, pool, "parent"), _addr(st, torch.int32, "st"),
-                               _raw_stream(stream))
+                               _raw_stream(stream, parent))
     _check(rc, "moe_kv4_assign")
 
 
@@ -567,5 +566,5 @@ def moe_kv4_compact(pool: Kv4Pool, n_live, workspace, st=None, stream=None):
     int32 out (or None): their count."""
     rc = load().moe_kv4_compact(pool._ref, _addr(n_live, torch.int32, "n_live"), _addr(workspace, None, "workspace"),
                                 workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
-                                _raw_stream(stream))
+                                _raw_stream(stream, workspace))
     _check(rc, "moe_kv4_compact")

@@ -45,7 +45,7 @@ constexpr float kGrow = 8.f;        // log2 of the growth that O waits for
 // What an item costs beside its pages (its queries, its outputs, the pipeline's
 // start and end), in pages: the runs are cut by cost, so that a CTA with many
 // short items gets fewer pages.
-constexpr int kItemCost = 6;
+constexpr int kItemCost = 8;
 
 enum Site : int { kSiteRaw = 31, kSiteRawFree, kSiteKFree, kSiteVFree, kSiteKFull, kSiteVFull, kSiteQ, kSiteP, kSiteS, kSiteO, kSiteQFree };
 
