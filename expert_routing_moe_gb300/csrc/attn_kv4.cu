@@ -35,6 +35,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
+constexpr int kMaxCtas = 160;       // one for each SM
+constexpr int kAhead = 16;          // pieces in flight when a tile's are joined
 constexpr int kSiteKvPage = 21;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -298,7 +300,9 @@ struct Piece {
 };
 struct PieceInfo {
     long long item;            // first unit of the tile, -1: none
-    int s, h, tile, units;     // units of the whole tile
+    int h, tile, units;        // units of the whole tile
+    float v_scale;
+    Seq q;
 };
 
 template <int D, int NT>
@@ -311,8 +315,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv4_stream_kernel(const Attn
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps * kStages];
     __shared__ PieceInfo info[2 * kWarps];
-    __shared__ long long s_scan[kWarps], w_begin[kWarps], w_units[kWarps];
-    __shared__ int w_seq[kWarps], s_ticket;
+    __shared__ long long s_scan[kWarps], w_begin[kWarps], s_u0, s_u1;
+    __shared__ int s_items[kWarps], s_most[kWarps], w_units[kWarps], w_seq[kWarps];
+    __shared__ PieceInfo s_piece[2];
+    __shared__ int s_last[2], s_b0[2], s_n[2];
     __shared__ volatile int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -320,53 +326,124 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv4_stream_kernel(const Attn
         for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&bars[i]), 1);
         fence_mbar_init();
         s_abort = 0;
+        s_last[0] = s_last[1] = 0;
+        s_n[0] = s_n[1] = 0;
     }
     pdl_wait();
     pdl_trigger();
 
-    // The units of all sequences; every CTA adds them up for itself.
+    // The units of all sequences; every CTA adds them up for itself.  (A
+    // sequence's own are a 32-bit number: its pages fit the device's memory.)
     const int per = (a.c.S + kThreads - 1) / kThreads;
     const int sa = min(a.c.S, static_cast<int>(threadIdx.x) * per), sb = min(a.c.S, sa + per);
     long long mine = 0;
+    int items = 0, most = 0, hu = 0;
+    Seq q0 = {0, 0, 0};
     for (int s = sa; s < sb; ++s) {
-        const Seq q = load_seq(a, s);
-        if (q.len < 0 && blockIdx.x == 0) report(a.st, MOE_DEV_BAD_INDEX, s);
-        mine += seq_units<NR>(a, q) * a.c.n_kv;
+        q0 = load_seq(a, s);
+        if (q0.len < 0 && blockIdx.x == 0) report(a.st, MOE_DEV_BAD_INDEX, s);
+        hu = seq_units<NR>(a, q0, most);
+        mine += static_cast<long long>(hu) * a.c.n_kv;
+        items += seq_tiles<NR>(a, q0) * a.c.n_kv;
     }
     long long inc = mine;
+    int inc_items = items;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const long long v = __shfl_up_sync(kFull, inc, off);
-        if (lane >= off) inc += v;
+        const int k = __shfl_up_sync(kFull, inc_items, off);
+        if (lane >= off) { inc += v; inc_items += k; }
     }
-    if (lane == 31) s_scan[warp] = inc;
+    most = __reduce_max_sync(kFull, most);
+    if (lane == 31) {
+        s_scan[warp] = inc;
+        s_items[warp] = inc_items;
+        s_most[warp] = most;
+    }
     __syncthreads();
     long long before = 0, total = 0;
+    int items_before = 0, all_items = 0;
+#pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) before += s_scan[i];
+        if (i < warp) { before += s_scan[i]; items_before += s_items[i]; }
         total += s_scan[i];
+        all_items += s_items[i];
+        most = max(most, s_most[i]);
     }
     before += inc - mine;
+    items_before += inc_items - items;
     if (total == 0) return;
-    // Equal runs of units for the CTAs, at least a page for each warp.
-    long long share = (total + gridDim.x - 1) / gridDim.x;
-    share = share < kWarps ? kWarps : share;
-    const long long u0 = min(total, share * blockIdx.x), u1 = min(total, u0 + share);
-    if (u0 >= u1) return;
+    // Few short tiles: one for each CTA, so that none is joined across CTAs.  Else equal runs
+    // of units for the CTAs, at least a page for each warp.  (A batch of one with 333 tokens: 4 tiles of six pages,
+    // each on its own CTA, instead of three runs of eight and a join.)
+    const bool by_item = all_items <= static_cast<int>(gridDim.x) && most <= 2 * kWarps;
+    // Few tiles of one size (a batch of one): as many CTAs for each, so that no CTA has two tiles to join.  (131071
+    // tokens, four tiles: 38 CTAs for each; with runs across tiles the CTAs between two tiles joined both.)
+    const int per_item = static_cast<int>(gridDim.x) / max(1, all_items);
+    const bool even = !by_item && per_item >= 4 && total == static_cast<long long>(most) * all_items;
+    const int bid = static_cast<int>(blockIdx.x);
+    long long share = 0, u0, u1;
+    if (by_item) {
+        if (bid >= all_items) return;
+        if (bid >= items_before && bid < items_before + items) {
+            long long b = before;
+            int k = items_before;
+            for (int s = sa; s < sb; ++s) {
+                const Seq q = per == 1 ? q0 : load_seq(a, s);
+                const int tiles = seq_tiles<NR>(a, q), n = tiles * a.c.n_kv;
+                if (bid >= k + n) {
+                    int unused = 0;
+                    b += static_cast<long long>(per == 1 ? hu : seq_units<NR>(a, q, unused)) * a.c.n_kv;
+                    k += n;
+                    continue;
+                }
+                const int h = (bid - k) / tiles, tile = (bid - k) - h * tiles;
+                int unused = 0, lo, hi;
+                b += static_cast<long long>(h) * (per == 1 ? hu : seq_units<NR>(a, q, unused));
+                for (int i = 0; i < tile; ++i) {
+                    tile_pages<NR>(a, q, i, lo, hi);
+                    b += max(1, hi - lo);
+                }
+                tile_pages<NR>(a, q, tile, lo, hi);
+                s_u0 = b;
+                s_u1 = b + max(1, hi - lo);
+                break;
+            }
+        }
+        __syncthreads();
+        u0 = s_u0;
+        u1 = s_u1;
+    } else if (even) {
+        share = max(kWarps, (most + per_item - 1) / per_item);
+        if (bid >= per_item * all_items) return;
+        const long long begin = static_cast<long long>(bid / per_item) * most;
+        u0 = begin + share * (bid % per_item);
+        u1 = min(begin + most, u0 + share);
+        if (u0 >= u1) return;
+    } else {
+        const int grid = static_cast<int>(gridDim.x);
+        share = total < 0x7fffffff - grid ? (static_cast<int>(total) + grid - 1) / grid : (total + grid - 1) / grid;
+        share = share < kWarps ? kWarps : share;
+        u0 = min(total, share * bid);
+        u1 = min(total, u0 + share);
+        if (u0 >= u1) return;
+    }
     const long long n_cta = u1 - u0;
     const long long w0 = u0 + n_cta * warp / kWarps, w1 = u0 + n_cta * (warp + 1) / kWarps;
     // The sequence that a warp's run starts in is found by the thread that added it up.
     if (mine > 0 && before < u1 && before + mine > u0) {
         long long b = before;
         for (int s = sa; s < sb; ++s) {
-            const Seq q = load_seq(a, s);
-            const long long hu = seq_units<NR>(a, q), u = hu * a.c.n_kv;
+            int unused = 0;
+            const int h_units = per == 1 ? hu : seq_units<NR>(a, load_seq(a, s), unused);
+            const long long u = static_cast<long long>(h_units) * a.c.n_kv;
+#pragma unroll
             for (int i = 0; i < kWarps; ++i) {
                 const long long at = u0 + n_cta * i / kWarps;
                 if (at >= b && at < b + u) {
                     w_seq[i] = s;
                     w_begin[i] = b;
-                    w_units[i] = hu;
+                    w_units[i] = h_units;
                 }
             }
             b += u;
@@ -469,10 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv4_stream_kernel(const Attn
                 if (lane == 0) {
                     PieceInfo& p = info[2 * warp + which];
                     p.item = was.item_begin;
-                    p.s = was.s;
                     p.h = was.h;
                     p.tile = was.tile;
                     p.units = max(1, was.hi - was.lo);
+                    p.v_scale = a.c.v_scale != nullptr ? a.c.v_scale[was.h] : 1.f;
+                    p.q = was.q;
                 }
             }
             if (rd.unit >= w1) break;
@@ -488,37 +566,86 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv4_stream_kernel(const Attn
     __syncthreads();
     if (s_abort) return;
 
-    // Join the pieces of each tile, in the order of the pages.
+    // Join the pieces of each tile, in the order of the pages: a thread's part
+    // is four numbers of a row at a time.
     const float* first_pieces = reinterpret_cast<const float*>(smem + kWarps * kRing);
     auto piece = [&](int i) {
         return (i & 1) ? reinterpret_cast<const float*>(smem + (i >> 1) * kRing) : first_pieces + (i >> 1) * P::floats;
     };
-    for (int i = 0; i < 2 * kWarps;) {
-        if (info[i].item < 0) { ++i; continue; }
+    constexpr int kPieces = 2 * kWarps, kRowW = kPieces + 2;
+    float* const weight = reinterpret_cast<float*>(smem + kWarps * kRing) + kWarps * P::floats;   // [NR][kMaxCtas] at the end
+    static_assert(kWarps * kRowW <= kMaxCtas, "the warps' weights fit");
+    float* const mine_w = weight + warp * NR * kRowW;
+    uint32_t have = 0, starts = 0;           // pieces that there are, and those that are a tile's first
+    long long seen = -1;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        const long long id = info[i].item;
+        if (id < 0) continue;
+        have |= 1u << i;
+        if (id != seen) starts |= 1u << i;
+        seen = id;
+    }
+    // one tile: all threads; several: the threads in two, four or eight groups that take them in turn
+    const int tiles_here = __popc(starts);
+    const int groups = tiles_here <= 1 ? 1 : tiles_here == 2 ? 2 : tiles_here <= 4 ? 4 : 8;
+    const int g_threads = kThreads / groups, g_tid = static_cast<int>(threadIdx.x) % g_threads;
+    int turn = static_cast<int>(threadIdx.x) / g_threads;
+    for (uint32_t left = starts; left != 0; left &= left - 1) {
+        if (turn-- != 0) continue;
+        turn = groups - 1;
+        const int i = __ffs(left) - 1;
         const PieceInfo p = info[i];
-        int j = i + 1;
-        while (j < 2 * kWarps && (info[j].item < 0 || info[j].item == p.item)) ++j;
-        const Seq q = load_seq(a, p.s);
-        const float vs = a.c.v_scale != nullptr ? a.c.v_scale[p.h] : 1.f;
+        // the tile's pieces: from its first to the next tile's
+        const uint32_t rest = left & (left - 1);
+        const uint32_t set = have & ~((1u << i) - 1) & (rest != 0 ? (1u << (__ffs(rest) - 1)) - 1 : ~0u);
+        const Seq q = p.q;
+        const float vs = p.v_scale;
         const bool here = p.item >= u0 && p.item + p.units <= u1;   // the whole tile is this CTA's
         const int my_slot = p.item < u0 ? 0 : 1;
-        float* part = a.partial + (static_cast<long long>(blockIdx.x) * 2 + my_slot) * (NR * (D + 2));
-        for (int x = threadIdx.x; x < NR * (D / 4); x += kThreads) {
-            const int r = x / (D / 4), d = x % (D / 4) * 4;
-            float m = -INFINITY;
-            for (int k = i; k < j; ++k)
-                if (info[k].item >= 0) m = fmaxf(m, piece(k)[P::m + r]);
-            float l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = i; k < j; ++k) {
-                if (info[k].item < 0) continue;
-                const float* pc = piece(k);
-                const float mk = pc[P::m + r];
-                const float e = mk == -INFINITY ? 0.f : ex2(mk - m);
-                const float4 v = *reinterpret_cast<const float4*>(pc + r * P::ld + d);
-                l += e * pc[P::l + r];
-                o.x += e * v.x; o.y += e * v.y; o.z += e * v.z; o.w += e * v.w;
+        float* part = a.partial + (static_cast<long long>(bid) * 2 + my_slot) * (NR * (D + 2));
+        // each row's weights 2^(m - max) of the pieces, and its sum; every warp for itself, a lane for a row and
+        // every (32 / NR)th piece
+        {
+            constexpr int kStep = 32 / NR;
+            const int r = lane % NR;
+            float mk[kPieces / kStep], lk[kPieces / kStep], m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int i = 0; i < kPieces / kStep; ++i) {
+                const int k = lane / NR + i * kStep;
+                const bool in = (set >> k) & 1;
+                mk[i] = in ? piece(k)[P::m + r] : -INFINITY;
+                lk[i] = in ? piece(k)[P::l + r] : 0.f;
+                m = fmaxf(m, mk[i]);
             }
+#pragma unroll
+            for (int off = NR; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+#pragma unroll
+            for (int i = 0; i < kPieces / kStep; ++i) {
+                // a piece that has seen nothing has l = 0, or a NaN that stays
+                const float e = mk[i] == -INFINITY ? (lk[i] == lk[i] ? 0.f : 1.f) : ex2(mk[i] - m);
+                mine_w[r * kRowW + lane / NR + i * kStep] = e;
+                l = fmaf(e, lk[i], l);
+            }
+#pragma unroll
+            for (int off = NR; off < 32; off <<= 1) l += __shfl_xor_sync(kFull, l, off);
+            if (lane < NR) {
+                mine_w[r * kRowW + kPieces] = m;
+                mine_w[r * kRowW + kPieces + 1] = l;
+            }
+        }
+        __syncwarp();
+        for (int x = g_tid; x < NR * (D / 4); x += g_threads) {
+            const int r = x / (D / 4), d = x % (D / 4) * 4;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (uint32_t b = set; b != 0; b &= b - 1) {
+                const int k = __ffs(b) - 1;
+                const float e = mine_w[r * kRowW + k];
+                const float4 v = *reinterpret_cast<const float4*>(piece(k) + r * P::ld + d);
+                o.x = fmaf(e, v.x, o.x); o.y = fmaf(e, v.y, o.y);
+                o.z = fmaf(e, v.z, o.z); o.w = fmaf(e, v.w, o.w);
+            }
+            const float m = mine_w[r * kRowW + kPieces], l = mine_w[r * kRowW + kPieces + 1];
             if (here) {
                 const int row = p.tile * NR + r;
                 if (row < q.n * a.group) {
@@ -534,51 +661,101 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv4_stream_kernel(const Attn
                 }
             }
         }
-        if (!here) {
-            // the CTAs that hold pieces of this tile: b0 (slot 1) .. b1 (slot 0)
-            const int b0 = static_cast<int>(p.item / share), b1 = static_cast<int>((p.item + p.units - 1) / share);
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                __threadfence();
-                s_ticket = atom_add_acq_rel_gpu(a.counters + b0, 1);
+        __syncwarp();                        // the next tile's weights take the same memory
+        if (here) continue;
+        // the CTAs that hold pieces of this tile: b0 (slot 1) .. b1 (slots 0); a tile's units are a 32-bit number
+        int b0 = bid - bid % per_item, b1 = b0 + (p.units - 1) / static_cast<int>(share);
+        if (!even) {
+            const unsigned sh = static_cast<unsigned>(share);
+            b0 = p.item >= u0 ? bid : bid - static_cast<int>((static_cast<unsigned>(u0 - p.item) + sh - 1) / sh);
+            b1 = b0 + static_cast<int>((static_cast<unsigned>(p.item - share * b0) + p.units - 1) / sh);
+        }
+        if (g_tid == 0) {
+            s_b0[my_slot] = b0;
+            s_n[my_slot] = b1 - b0 + 1;
+            s_piece[my_slot] = p;
+        }
+    }
+    __syncthreads();
+    if (lane == 0 && warp < 2 && s_n[warp] > 0) {
+        const bool last = atom_add_acq_rel_gpu(a.counters + s_b0[warp], 1) == s_n[warp] - 1;
+        s_last[warp] = last;
+        if (last) a.counters[s_b0[warp]] = 0;
+    }
+    __syncthreads();
+    // Tiles whose last piece was this CTA's: at most the one that came in and the one that goes on.
+    float* sums = reinterpret_cast<float*>(smem);                                           // [NR]; the rings are free
+    for (int which = 0; which < 2; ++which) {
+        if (!s_last[which]) continue;
+        const PieceInfo p = s_piece[which];
+        const int b0 = s_b0[which], n = s_n[which], pad = (n + kAhead - 1) / kAhead * kAhead;
+        const float* base = a.partial + static_cast<long long>(b0) * 2 * (NR * (D + 2));
+        auto slot = [&](int k) { return base + (2 * k + (k == 0 ? 1 : 0)) * (NR * (D + 2)); };
+        // the first pieces' numbers are on their way while the weights are found
+        float4 v[kAhead];
+        auto load = [&](int x, int k0) {
+            const int at = x / (D / 4) * D + x % (D / 4) * 4;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(slot(min(k0 + k, n - 1)) + at));
+        };
+        if (threadIdx.x < NR * (D / 4)) load(threadIdx.x, 0);
+        // a warp for each row: the pieces' weights 2^(m - max) and the sum of their l
+        for (int r = warp; r < NR; r += kWarps) {
+            float m = -INFINITY, l = 0.f;
+            float mk[kMaxCtas / 32], lk[kMaxCtas / 32];
+#pragma unroll
+            for (int i = 0; i < kMaxCtas / 32; ++i) {
+                const int k = 32 * i + lane;
+                mk[i] = k < n ? __ldcg(slot(k) + NR * D + r) : -INFINITY;
+                lk[i] = k < n ? __ldcg(slot(k) + NR * D + NR + r) : 0.f;
+                m = fmaxf(m, mk[i]);
             }
-            __syncthreads();
-            if (s_ticket == b1 - b0) {
-                __threadfence();
-                if (threadIdx.x == 0) a.counters[b0] = 0;
-                for (int x = threadIdx.x; x < NR * (D / 4); x += kThreads) {
-                    const int r = x / (D / 4), d = x % (D / 4) * 4;
-                    const int row = p.tile * NR + r;
-                    if (row >= q.n * a.group) continue;
-                    float m = -INFINITY, l = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int b = b0; b <= b1; ++b) {
-                        const float* pc = a.partial + (static_cast<long long>(b) * 2 + (b == b0 ? 1 : 0)) * (NR * (D + 2));
-                        const float mk = __ldcg(pc + NR * D + r), lk = __ldcg(pc + NR * D + NR + r);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(pc + r * D + d));
-                        const float mn = fmaxf(m, mk);
-                        const float e0 = m == -INFINITY ? 0.f : ex2(m - mn), e1 = mk == -INFINITY ? 0.f : ex2(mk - mn);
-                        m = mn;
-                        l = l * e0 + lk * e1;
-                        o.x = o.x * e0 + v.x * e1; o.y = o.y * e0 + v.y * e1;
-                        o.z = o.z * e0 + v.z * e1; o.w = o.w * e0 + v.w * e1;
-                    }
-                    const float inv = l == 0.f ? 0.f : vs / l;
-                    write_out4<D>(a, q, p.h, row, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-                    if (d == 0) write_lse(a, q, p.h, row, m, l);
-                }
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+#pragma unroll
+            for (int i = 0; i < kMaxCtas / 32; ++i) {
+                const int k = 32 * i + lane;
+                // a piece that has seen nothing counts for nothing; a NaN sum stays
+                const float e = mk[i] == -INFINITY ? (lk[i] == lk[i] ? 0.f : 1.f) : ex2(mk[i] - m);
+                l = fmaf(e, lk[i], l);
+                if (k < pad) weight[r * kMaxCtas + k] = e;
+            }
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
+            if (lane == 0) {
+                sums[r] = l;
+                const int row = p.tile * NR + r;
+                if (row < p.q.n * a.group) write_lse(a, p.q, p.h, row, m, l);
             }
         }
-        i = j;
+        __syncthreads();
+        for (int x = threadIdx.x; x < NR * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), d = x % (D / 4) * 4;
+            const int row = p.tile * NR + r;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k0 = 0; k0 < n; k0 += kAhead) {
+                if (k0 > 0 || x >= kThreads) load(x, k0);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const float e = weight[r * kMaxCtas + k0 + k];
+                    o.x = fmaf(e, v[k].x, o.x); o.y = fmaf(e, v[k].y, o.y);
+                    o.z = fmaf(e, v[k].z, o.z); o.w = fmaf(e, v[k].w, o.w);
+                }
+            }
+            if (row >= p.q.n * a.group) continue;
+            const float l = sums[r], inv = l == 0.f ? 0.f : p.v_scale / l;
+            write_out4<D>(a, p.q, p.h, row, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        }
+        __syncthreads();                     // the next tile's weights take the same memory
     }
 }
 
-constexpr int kMaxCtas = 304;
 constexpr size_t kCounterBytes = 2048;
 
 template <int D, int NT>
 cudaError_t launch_stream(const AttnArgs& a, cudaStream_t s) {
-    constexpr int smem = kWarps * kStages * Kv4Layout<D>::bytes + kWarps * Piece<D, 8 * NT>::floats * 4;
+    constexpr int smem = kWarps * kStages * Kv4Layout<D>::bytes + kWarps * Piece<D, 8 * NT>::floats * 4 + kMaxCtas * 8 * NT * 4;
+    static_assert(smem <= 226 * 1024, "shared memory of a CTA");
     auto* k = attn_kv4_stream_kernel<D, NT>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -610,9 +787,12 @@ cudaError_t launch_attention_kv4(const void* q, long long ld_q, int T, int n_q, 
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
     a.st = st;
     a.rows_lo = 1;
-    a.rows_hi = kStreamRows;
-    const bool prefill = static_cast<long long>(T) * a.group > kStreamRows;   // some sequence may have more rows
+    a.rows_hi = 0x7fffffff;
+    // Without a sequence of many rows (as max_new promises) the streaming kernel is launched alone;
+    // sequences that have more all the same are right there, only slower.
+    const bool prefill = static_cast<long long>(max_new) * a.group > kStreamRows && static_cast<long long>(T) * a.group > kStreamRows;
     if (prefill) {
+        a.rows_hi = kStreamRows;
         AttnArgs b = a;
         b.rows_lo = kStreamRows + 1;
         b.rows_hi = 0x7fffffff;

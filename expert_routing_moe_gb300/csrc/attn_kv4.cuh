@@ -60,15 +60,18 @@ __device__ __forceinline__ int seq_tiles(const AttnArgs& a, const Seq& s) {
     const int rows = s.n * a.group;
     return rows < a.rows_lo || rows > a.rows_hi ? 0 : (rows + NR - 1) / NR;
 }
-// Units of one key head of a sequence; a tile that sees nothing still has one, to write its rows.
+// Units of one key head of a sequence, and the most that a tile has; a tile
+// that sees nothing still has one, to write its rows.
 template <int NR>
-__device__ __forceinline__ long long seq_units(const AttnArgs& a, const Seq& s) {
-    long long u = 0;
+__device__ __forceinline__ int seq_units(const AttnArgs& a, const Seq& s, int& most) {
+    int u = 0;
     const int tiles = seq_tiles<NR>(a, s);
     for (int i = 0; i < tiles; ++i) {
         int lo, hi;
         tile_pages<NR>(a, s, i, lo, hi);
-        u += max(1, hi - lo);
+        const int n = max(1, hi - lo);
+        most = max(most, n);
+        u += n;
     }
     return u;
 }
@@ -112,12 +115,12 @@ struct Cursor {
         if (--item_left == 0) next_item(a);
     }
     // from the first unit of (sequence s, head 0) to unit `to` of the same sequence
-    __device__ void seek(const AttnArgs& a, int seq, long long seq_begin, long long seq_head_units, long long to) {
+    __device__ void seek(const AttnArgs& a, int seq, long long seq_begin, int seq_head_units, long long to) {
         s = seq;
         q = load_seq(a, s);
         tiles = seq_tiles<NR>(a, q);
-        h = static_cast<int>((to - seq_begin) / seq_head_units);
-        unit = seq_begin + h * seq_head_units;
+        h = static_cast<int>(to - seq_begin) / seq_head_units;
+        unit = seq_begin + static_cast<long long>(h) * seq_head_units;
         tile = 0;
         set_tile(a);
         while (unit + item_left <= to) {
