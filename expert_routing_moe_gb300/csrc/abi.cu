@@ -314,7 +314,7 @@ moe_status_t moe_qk_norm_rope(const void* qkv, int dtype, long long ld, int T, i
     if (rope != nullptr) {
         if (rope->rot < 32 || rope->rot > head_dim || rope->n_pos < 1 || rope->table == nullptr) return MOE_ERR_INVALID_ARG;
         if (rope->rot % 32 != 0) return MOE_ERR_UNSUPPORTED;
-        if (!aligned16(rope->table)) return MOE_ERR_INVALID_ARG;
+        if (!aligned16(rope->table) || (reinterpret_cast<uintptr_t>(rope->axis) & 7u) != 0) return MOE_ERR_INVALID_ARG;
         if (rope->positions == nullptr ? cache == nullptr : rope->axes < 1) return MOE_ERR_INVALID_ARG;
     }
     if (T == 0) return MOE_OK;

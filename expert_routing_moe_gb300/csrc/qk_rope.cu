@@ -8,13 +8,15 @@
 // device memory bounds it for prompts and the chain of loads (row, position,
 // table) for single tokens.
 //
-// D/8 threads hold one head's row, eight numbers each: the four pairs
-// 4j..4j+3, i.e. two runs of four numbers (pairs i, i + rot/2) or one run of
-// eight (pairs of neighbours).  Both members of a pair are then in one
-// thread, and a block of 16 numbers that shares a scale is in two or four
-// neighbouring threads.  A thread keeps its position's four (cos, sin) in registers for
-// all heads of its token that it takes: the table is read once per thread
-// and not once per head.
+// D/16 threads hold one head's row, sixteen numbers each: the eight pairs
+// 8j..8j+7, i.e. two runs of eight numbers (pairs i, i + rot/2) or one run of
+// sixteen (pairs of neighbours).  Both members of a pair are then in one
+// thread, loads are 16 bytes, and a block of 16 numbers that shares a scale is in one thread or
+// two neighbours.  What bounds the pass for many tokens is instructions, not
+// yet memory: so a thread multiplies its position's (cos, sin) by the norm's
+// weights once for all heads of its token that it takes, and pairs of fp32
+// operations go in one instruction.  Cached keys take a path of their own whose every
+// rounding is fixed: their codes must not depend on how sums are ordered.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -25,49 +27,57 @@ namespace moe {
 
 namespace {
 
-constexpr int kRopeThreads = 128;
+constexpr int kReadThreads = 128;
 constexpr float kSixth = 0x1.555556p-3f;   // 1/6, nearest fp32
 
+// Sixteen numbers as loaded, in two runs of eight.
 template <typename XT>
-struct Row8;   // eight numbers as loaded, in two runs of four
+struct Row16;
 template <>
-struct Row8<__nv_bfloat16> {
-    uint2 a, b;
+struct Row16<__nv_bfloat16> {
+    uint4 a, b;
     __device__ void load(const __nv_bfloat16* p, int i, int k) {
-        a = *reinterpret_cast<const uint2*>(p + i);
-        b = *reinterpret_cast<const uint2*>(p + k);
+        a = *reinterpret_cast<const uint4*>(p + i);
+        b = *reinterpret_cast<const uint4*>(p + k);
     }
-    __device__ void get(float (&x)[8]) const {
-        const uint32_t u[4] = {a.x, a.y, b.x, b.y};
+    __device__ void get(float (&x)[16]) const {
+        const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
             x[2 * j] = __uint_as_float(u[j] << 16);
             x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
         }
     }
 };
 template <>
-struct Row8<float> {
-    float4 a, b;
+struct Row16<float> {
+    float4 v[4];
     __device__ void load(const float* p, int i, int k) {
-        a = *reinterpret_cast<const float4*>(p + i);
-        b = *reinterpret_cast<const float4*>(p + k);
+        v[0] = *reinterpret_cast<const float4*>(p + i);
+        v[1] = *reinterpret_cast<const float4*>(p + i + 4);
+        v[2] = *reinterpret_cast<const float4*>(p + k);
+        v[3] = *reinterpret_cast<const float4*>(p + k + 4);
     }
-    __device__ void get(float (&x)[8]) const {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    __device__ void get(float (&x)[16]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[4 * j] = v[j].x; x[4 * j + 1] = v[j].y; x[4 * j + 2] = v[j].z; x[4 * j + 3] = v[j].w;
+        }
     }
 };
 
-__device__ __forceinline__ void store4(float* p, const float* y) {
-    *reinterpret_cast<float4*>(p) = make_float4(y[0], y[1], y[2], y[3]);
+__device__ __forceinline__ void store8(float* p, const float* y) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* y) {
-    const __nv_bfloat162 l = __floats2bfloat162_rn(y[0], y[1]), h = __floats2bfloat162_rn(y[2], y[3]);
-    uint2 v;
-    memcpy(&v.x, &l, 4);
-    memcpy(&v.y, &h, 4);
-    *reinterpret_cast<uint2*>(p) = v;
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* y) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+        memcpy(&u[i], &h, 4);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 // hi + lo += v, exactly but for lo's own rounding (Knuth's two-sum).
@@ -78,21 +88,14 @@ __device__ __forceinline__ void two_add(float& hi, float& lo, float v) {
     hi = s;
 }
 
-// Sum of the squares of a head's row over its G threads.  `exact` (keys that
-// are cached) carries it in two words: a key's code then depends on the sum's
-// nearest fp32 and not on the order of its terms.
+// Sum of the squares of a cached key's row over its G threads, carried in two
+// words: the key's codes then depend on the sum's nearest fp32 and not on the
+// order of its terms.
 template <int G>
-__device__ __forceinline__ float row_squares(const float (&x)[8], bool exact) {
+__device__ __forceinline__ float exact_squares(const float (&x)[16]) {
     float hi = 0.f, lo = 0.f;
-    if (!exact) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) hi = fmaf(x[j], x[j], hi);
-#pragma unroll
-        for (int off = G / 2; off >= 1; off >>= 1) hi += __shfl_xor_sync(kFull, hi, off);
-        return hi;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 16; ++j) {
         const float p = __fmul_rn(x[j], x[j]);
         lo = __fadd_rn(lo, __fmaf_rn(x[j], x[j], -p));
         two_add(hi, lo, p);
@@ -142,61 +145,202 @@ struct RopeArgs {
 };
 
 // One CTA: `rows` heads of one token (blockIdx.x), from blockIdx.y * rows on.
-// MAXR rows a thread group are loaded before the first is used.
-template <typename XT, int D, int MAXR>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a) {
-    constexpr int G = D / 8;                    // threads of a row
-    constexpr int NG = kRopeThreads / G;        // rows at a time
+// R rows of a thread group are loaded before the first is used.
+template <typename XT, int D, bool PAIRS, int R, int TH>
+__global__ void __launch_bounds__(TH) qk_norm_rope_kernel(const RopeArgs a) {
+    constexpr int G = D / 16;                   // threads of a row
+    constexpr int NG = TH / G;                  // rows at a time
     using L = Kv4Layout<D>;
     pdl_wait();
     pdl_trigger();
     const int t = blockIdx.x;
     const int grp = threadIdx.x / G, j = threadIdx.x % G;
-    const int n_rows = a.n_q + 2 * a.n_kv;
-    const int h0 = blockIdx.y * a.rows;
-    const int h1 = min(h0 + a.rows, a.c.pages != nullptr ? n_rows : a.n_q + a.n_kv);
+    const bool with_cache = a.c.pages != nullptr;
+    const int n_qk = a.n_q + a.n_kv;
+    const int h0 = blockIdx.y * a.rows, h1 = min(h0 + a.rows, with_cache ? n_qk + a.n_kv : n_qk);
     const XT* x_row = static_cast<const XT*>(a.qkv) + static_cast<long long>(t) * a.ld;
 
-    // the thread's two runs of four numbers in a rotated head
+    // the thread's two runs of eight numbers in a rotated head
     int ia, ib;
     bool turn = false;
-    if (a.pairs || a.rot == 0) {
-        ia = 8 * j;
-        ib = ia + 4;
+    if (PAIRS) {
+        ia = 16 * j;
+        ib = ia + 8;
         turn = ia < a.rot;
-    } else if (4 * j < a.rot / 2) {
-        ia = 4 * j;
+    } else if (8 * j < a.rot / 2) {
+        ia = 8 * j;
         ib = ia + a.rot / 2;
         turn = true;
     } else {                                    // numbers that pass through, in the same two halves
-        ia = a.rot + 4 * j - a.rot / 2;
+        ia = a.rot + 8 * j - a.rot / 2;
         ib = ia + (D - a.rot) / 2;
     }
-
-    Row8<XT> raw[MAXR];
-    auto load_rows = [&](int first) {
+    // numbers u[i], v[i] of pair i among the sixteen
+    auto split = [&](const float (&x)[16], float (&u)[8], float (&v)[8]) {
 #pragma unroll
-        for (int r = 0; r < MAXR; ++r) {
-            const int h = first + r * NG + grp;
-            if (h >= h1) break;
-            const bool val = h >= a.n_q + a.n_kv;
-            raw[r].load(x_row + static_cast<long long>(h) * D, val ? 8 * j : ia, val ? 8 * j + 4 : ib);
+        for (int i = 0; i < 8; ++i) {
+            u[i] = PAIRS ? x[2 * i] : x[i];
+            v[i] = PAIRS ? x[2 * i + 1] : x[8 + i];
         }
     };
-    load_rows(h0);
+    auto join = [&](const float (&u)[8], const float (&v)[8], float (&x)[16]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[PAIRS ? 2 * i : i] = u[i];
+            x[PAIRS ? 2 * i + 1 : 8 + i] = v[i];
+        }
+    };
+
+    // first rows on their way
+    Row16<XT> raw[R];
+    auto load_rows = [&](int first, int end) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int h = first + r * NG + grp;
+            if (h < end) raw[r].load(x_row + static_cast<long long>(h) * D, ia, ib);
+        }
+    };
+    const int q_end = min(h1, with_cache ? a.n_q : n_qk);   // rows of the plain path
+    load_rows(h0, q_end);
 
     // the token's place in the cache, and its page
-    int seq = -1, place = -1, first_new = 0;
-    const bool with_cache = a.c.pages != nullptr;
+    int seq = -1, place = -1, first_new = 0, len = 0;
     if (with_cache) {
         seq = find_seq(a.q_start, a.c.S, t);
         if (seq >= 0) {
             const int q0 = a.q_start[seq];
-            const int n = a.q_start[seq + 1] - q0;
-            first_new = a.c.seq_len[seq] - n;
+            len = a.c.seq_len[seq];
+            first_new = len - (a.q_start[seq + 1] - q0);
             place = first_new + (t - q0);
         }
     }
+
+    // (cos, sin) of the thread's eight pairs
+    float cs[8], sn[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        cs[i] = 1.f;
+        sn[i] = 0.f;
+    }
+    if (turn) {
+        const int half = a.rot / 2;
+        auto row_of = [&](int ax) {
+            int p = place;
+            if (a.positions != nullptr) p = ax < a.axes ? a.positions[static_cast<long long>(ax) * a.T + t] : -1;
+            else if (p < 0) p = 0;              // a row of a padded batch: not appended
+            if (p < 0 || p >= a.n_pos) {
+                report(a.st, MOE_DEV_BAD_INDEX, p);
+                p = 0;
+            }
+            return p;
+        };
+        if (a.axis == nullptr) {
+            const float4* src = reinterpret_cast<const float4*>(a.table + static_cast<long long>(row_of(0)) * half + 8 * j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = src[i];
+                cs[2 * i] = v.x; sn[2 * i] = v.y; cs[2 * i + 1] = v.z; sn[2 * i + 1] = v.w;
+            }
+        } else {
+            const uint2 axes = *reinterpret_cast<const uint2*>(a.axis + 8 * j);
+            int last_ax = -1, p = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int ax = ((i < 4 ? axes.x : axes.y) >> (8 * (i % 4))) & 0xff;
+                if (ax != last_ax) p = row_of(ax);
+                last_ax = ax;
+                const float2 v = a.table[static_cast<long long>(p) * half + 8 * j + i];
+                cs[i] = v.x;
+                sn[i] = v.y;
+            }
+        }
+    }
+
+    // ---- rows of the plain path: queries, and keys that are not cached ----
+    // y_u = inv (u (w_u cos) - v (w_v sin)),  y_v = inv (v (w_v cos) + u (w_u sin)): the products in
+    // brackets are the same for all heads
+    auto plain = [&](int begin, int end, const float* w, XT* out, long long ld_out, int h_out) {
+        float2 uc[4], vs[4], vc[4], us[4];
+        {
+            float x[16], wu[8], wv[8];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = 1.f;
+            if (w != nullptr) {
+                Row16<float> ww;
+                ww.load(w, ia, ib);
+                ww.get(x);
+            }
+            split(x, wu, wv);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uc[i] = make_float2(wu[2 * i] * cs[2 * i], wu[2 * i + 1] * cs[2 * i + 1]);
+                us[i] = make_float2(wu[2 * i] * sn[2 * i], wu[2 * i + 1] * sn[2 * i + 1]);
+                vc[i] = make_float2(wv[2 * i] * cs[2 * i], wv[2 * i + 1] * cs[2 * i + 1]);
+                vs[i] = make_float2(-wv[2 * i] * sn[2 * i], -wv[2 * i + 1] * sn[2 * i + 1]);
+            }
+        }
+        for (int first = begin; first < end; first += R * NG) {
+            if (first != h0) load_rows(first, end);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int h = first + r * NG + grp;
+                // whole warps leave together: the shuffles below want every lane
+                if (first + r * NG + (static_cast<int>(threadIdx.x) & ~31) / G >= end) break;
+                float x[16], u[8], v[8];
+                raw[r].get(x);
+                split(x, u, v);
+                float inv = 1.f;
+                if (w != nullptr) {
+                    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 p = make_float2(x[2 * i], x[2 * i + 1]);
+                        s2 = fma2(p, p, s2);
+                    }
+                    float ss = s2.x + s2.y;
+#pragma unroll
+                    for (int off = G / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(kFull, ss, off);
+                    // 1 / sqrt, refined once from the approximate one (rows of zeros with eps = 0 give inf * 0 = NaN, as the formula)
+                    const float mean = fmaf(ss, 1.0f / D, a.eps);
+                    inv = rsqrtf(mean);
+                    const float e = fmaf(-mean * inv, inv, 1.f);
+                    if (isfinite(e)) inv = fmaf(0.5f * inv, e, inv);
+                }
+                const float2 i2 = make_float2(inv, inv);
+                float yu[8], yv[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 u2 = make_float2(u[2 * i], u[2 * i + 1]), v2 = make_float2(v[2 * i], v[2 * i + 1]);
+                    float2 p = mul2(u2, uc[i]), q = mul2(v2, vc[i]);
+                    if (turn) {                 // numbers that pass through keep an infinity to themselves
+                        p = fma2(v2, vs[i], p);
+                        q = fma2(u2, us[i], q);
+                    }
+                    if (w != nullptr) {
+                        p = mul2(p, i2);
+                        q = mul2(q, i2);
+                    }
+                    yu[2 * i] = p.x; yu[2 * i + 1] = p.y;
+                    yv[2 * i] = q.x; yv[2 * i + 1] = q.y;
+                }
+                join(yu, yv, x);
+                if (h < end && out != nullptr) {
+                    XT* o = out + static_cast<long long>(t) * ld_out + static_cast<long long>(h - h_out) * D;
+                    store8(o + ia, x);
+                    store8(o + ib, x + 8);
+                }
+            }
+        }
+    };
+    if (h0 < min(h1, a.n_q)) plain(h0, min(h1, a.n_q), a.q_w, static_cast<XT*>(a.q_out), a.ld_q, 0);
+    if (!with_cache) {
+        const int begin = max(h0, a.n_q);
+        if (begin < h1) plain(begin, h1, a.k_w, static_cast<XT*>(a.k_out), a.ld_k, a.n_q);
+        return;
+    }
+    if (h1 <= a.n_q) return;
+
+    // ---- keys and values into the cache ----
     int page = -1;
     if (place >= 0) {
         const int col = place / kPage;
@@ -206,181 +350,148 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
             page = -1;
         }
     }
-    uint8_t* page_base = nullptr;
-    if (page >= 0) page_base = static_cast<uint8_t*>(a.c.pages) + static_cast<long long>(page) * a.c.n_kv * L::bytes;
-
-    // (cos, sin) of the thread's four pairs
-    float2 cs[4];
-    if (turn) {
+    uint8_t* page_base = page >= 0 ? static_cast<uint8_t*>(a.c.pages) + static_cast<long long>(page) * a.c.n_kv * L::bytes : nullptr;
+    const int tok = place >= 0 ? place % kPage : 0;
+    for (int first = max(h0, a.n_q); first < h1; first += NG) {
+        const int h = first + grp;
+        const bool is_k = h < h1 && h < n_qk, is_v = h < h1 && h >= n_qk;
+        const int kv = is_v ? h - n_qk : h - a.n_q;
+        float x[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int f = 4 * j + i;
-            int p = place;
-            if (a.positions != nullptr) {
-                const int ax = a.axis != nullptr ? a.axis[f] : 0;
-                if (ax < a.axes) p = a.positions[static_cast<long long>(ax) * a.T + t];
-                else p = -1;
-            } else if (p < 0) {
-                p = 0;                          // a row of a padded batch: not appended
-            }
-            if (p < 0 || p >= a.n_pos) {
-                report(a.st, MOE_DEV_BAD_INDEX, p);
-                p = 0;
-            }
-            cs[i] = a.table[static_cast<long long>(p) * (a.rot / 2) + f];
+        for (int i = 0; i < 16; ++i) x[i] = 0.f;
+        if (h < h1) {
+            Row16<XT> row;
+            row.load(x_row + static_cast<long long>(h) * D, is_v ? 16 * j : ia, is_v ? 16 * j + 8 : ib);
+            row.get(x);
         }
-    }
-
-    for (int first = h0; first < h1; first += MAXR * NG) {
-        if (first != h0) load_rows(first);
+        if (__any_sync(kFull, is_k)) {
+            float u[8], v[8];
+            if (a.k_w != nullptr) {
+                const float ss = exact_squares<G>(x);
+                const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.0f / D), a.eps)));
+                if (is_k) {
+                    Row16<float> ww;
+                    float w[16];
+                    ww.load(a.k_w, ia, ib);
+                    ww.get(w);
 #pragma unroll
-        for (int r = 0; r < MAXR; ++r) {
-            const int h = first + r * NG + grp;
-            // whole warps leave together: the shuffles below want every lane
-            if (first + r * NG + (static_cast<int>(threadIdx.x) & ~31) / G >= h1) break;
-            const bool live = h < h1;
-            const bool is_k = live && h >= a.n_q && h < a.n_q + a.n_kv, is_v = live && h >= a.n_q + a.n_kv;
-            float y[8];
-            if (live) raw[r].get(y);
-            else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = 0.f;
-            }
-            const float* w = h < a.n_q ? a.q_w : a.k_w;
-            // keys that are cached take the two-word sum; a warp's rows may be of both kinds
-            const bool any_k = __any_sync(kFull, is_k && with_cache);
-            const float ss = row_squares<G>(y, any_k);
-            if (live && !is_v) {
-                if (w != nullptr) {
-                    const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.0f / D), a.eps)));
-                    const float4 wa = *reinterpret_cast<const float4*>(w + ia), wb = *reinterpret_cast<const float4*>(w + ib);
-                    const float wv[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(__fmul_rn(y[i], inv), wv[i]);
+                    for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], inv), w[i]);
                 }
+            }
+            if (is_k) {
                 if (turn) {
+                    split(x, u, v);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int pa = a.pairs ? 2 * i : i, pb = a.pairs ? 2 * i + 1 : i + 4;
-                        const float u = y[pa], v = y[pb];
-                        y[pa] = __fsub_rn(__fmul_rn(u, cs[i].x), __fmul_rn(v, cs[i].y));
-                        y[pb] = __fadd_rn(__fmul_rn(v, cs[i].x), __fmul_rn(u, cs[i].y));
+                    for (int i = 0; i < 8; ++i) {
+                        const float p = __fsub_rn(__fmul_rn(u[i], cs[i]), __fmul_rn(v[i], sn[i]));
+                        v[i] = __fadd_rn(__fmul_rn(v[i], cs[i]), __fmul_rn(u[i], sn[i]));
+                        u[i] = p;
                     }
+                    join(u, v, x);
                 }
-                XT* out = nullptr;
-                if (h < a.n_q) out = static_cast<XT*>(a.q_out) + static_cast<long long>(t) * a.ld_q + static_cast<long long>(h) * D;
-                else if (a.k_out != nullptr)
-                    out = static_cast<XT*>(a.k_out) + static_cast<long long>(t) * a.ld_k + static_cast<long long>(h - a.n_q) * D;
-                if (out != nullptr) {
-                    store4(out + ia, y);
-                    store4(out + ib, y + 4);
+                if (a.k_out != nullptr) {
+                    XT* o = static_cast<XT*>(a.k_out) + static_cast<long long>(t) * a.ld_k + static_cast<long long>(kv) * D;
+                    store8(o + ia, x);
+                    store8(o + ib, x + 8);
                 }
-            }
-            if (!__any_sync(kFull, (is_k || is_v) && page_base != nullptr)) continue;
-            // quantise: keys alone, values with the other token of their pair
-            const int kv = h - a.n_q - (is_v ? a.n_kv : 0);
-            bool bad = false;
-            float inv_h = 1.f;
-            if (is_k || is_v) {
-                const float* hs = is_k ? a.c.k_scale : a.c.v_scale;
-                if (hs != nullptr) inv_h = __frcp_rn(hs[kv]);
-            }
-            float top_a = 0.f, top_b = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                y[i] = finite_or_zero(__fmul_rn(y[i], inv_h), bad);
-                float& top = i < 4 ? top_a : top_b;
-                top = fmaxf(top, fabsf(y[i]));
-            }
-            // a block of 16: the runs of four threads (halves), or both runs of two threads
-            const bool whole = a.pairs || a.rot == 0 || is_v;
-            float ta = whole ? fmaxf(top_a, top_b) : top_a, tb = whole ? ta : top_b;
-            ta = fmaxf(ta, __shfl_xor_sync(kFull, ta, 1));
-            tb = fmaxf(tb, __shfl_xor_sync(kFull, tb, 1));
-            {
-                const float oa = __shfl_xor_sync(kFull, ta, 2), ob = __shfl_xor_sync(kFull, tb, 2);
-                if (!whole) {
-                    ta = fmaxf(ta, oa);
-                    tb = fmaxf(tb, ob);
-                }
-            }
-            float ra, rb;
-            const uint32_t sa = block_scale(ta, ra), sb = block_scale(tb, rb);
-            if (is_k && page_base != nullptr) {
-                uint8_t* base = page_base + static_cast<long long>(kv) * L::bytes;
-                const int tok = place % kPage;
-                const uint32_t c0 = f32_to_e2m1x2(__fmul_rn(y[0], ra), __fmul_rn(y[1], ra)) |
-                                    (f32_to_e2m1x2(__fmul_rn(y[2], ra), __fmul_rn(y[3], ra)) << 8);
-                const uint32_t c1 = f32_to_e2m1x2(__fmul_rn(y[4], rb), __fmul_rn(y[5], rb)) |
-                                    (f32_to_e2m1x2(__fmul_rn(y[6], rb), __fmul_rn(y[7], rb)) << 8);
-                *reinterpret_cast<uint16_t*>(base + L::k_code(tok, ia)) = static_cast<uint16_t>(c0);
-                *reinterpret_cast<uint16_t*>(base + L::k_code(tok, ib)) = static_cast<uint16_t>(c1);
-                if (whole) {
-                    if ((j & 1) == 0) base[L::k_scale(tok, ia / 16)] = static_cast<uint8_t>(sa);
-                } else if ((j & 3) == 0) {
-                    base[L::k_scale(tok, ia / 16)] = static_cast<uint8_t>(sa);
-                    base[L::k_scale(tok, ib / 16)] = static_cast<uint8_t>(sb);
-                }
-            }
-            if (bad && page_base != nullptr && (is_k || is_v)) report(a.st, MOE_DEV_NONFINITE, t);
-            if (!__any_sync(kFull, is_v)) continue;
-            // Codes of two neighbouring tokens share a byte.  The even token's row also writes
-            // the odd one's if that is new too; an odd token whose partner is
-            // older puts its half beside the codes that are there.
-            const int n_new_end = with_cache && seq >= 0 ? a.c.seq_len[seq] : 0;
-            const bool odd = place & 1;
-            const bool partner = is_v && page_base != nullptr && !odd && place + 1 < n_new_end && t + 1 < a.T;
-            const bool skip = odd && place - 1 >= first_new && place - 1 >= 0;
-            float z[8];
-            bool bad2 = false;
-            float top2 = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = 0.f;
-            if (partner) {
-                Row8<XT> o;
-                o.load(x_row + a.ld + static_cast<long long>(h) * D, 8 * j, 8 * j + 4);
-                o.get(z);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    z[i] = finite_or_zero(__fmul_rn(z[i], inv_h), bad2);
-                    top2 = fmaxf(top2, fabsf(z[i]));
-                }
-            }
-            top2 = fmaxf(top2, __shfl_xor_sync(kFull, top2, 1));
-            if (is_v && page_base != nullptr && !skip) {
-                float rz;
-                const uint32_t sz = block_scale(top2, rz);
-                uint8_t* base = page_base + static_cast<long long>(kv) * L::bytes;
-                const int tok = place % kPage, pj = tok / 2;
-                uint2* codes = reinterpret_cast<uint2*>(base + L::v_code(pj, 8 * j));
-                uint32_t c[2] = {0u, 0u};
-                if (odd) {
-                    const uint2 old = *codes;
-                    c[0] = old.x & 0x0f0f0f0fu;
-                    c[1] = old.y & 0x0f0f0f0fu;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) c[i / 4] |= f32_to_e2m1x2(0.f, __fmul_rn(y[i], ra)) << (8 * (i % 4));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        c[i / 4] |= f32_to_e2m1x2(__fmul_rn(y[i], ra), __fmul_rn(z[i], rz)) << (8 * (i % 4));
-                }
-                *codes = make_uint2(c[0], c[1]);
-                if ((j & 1) == 0) {
-                    uint8_t* s = base + L::v_scale(pj, j / 2);
-                    if (partner) *reinterpret_cast<uint16_t*>(s) = static_cast<uint16_t>(sa | (sz << 8));
-                    else s[odd] = static_cast<uint8_t>(sa);
-                }
-                if (bad2) report(a.st, MOE_DEV_NONFINITE, t + 1);
             }
         }
+        if (page_base == nullptr) continue;
+        // quantise: keys alone, values with the other token of their pair
+        bool bad = false;
+        float inv_h = 1.f;
+        if (is_k || is_v) {
+            const float* hs = is_k ? a.c.k_scale : a.c.v_scale;
+            if (hs != nullptr) inv_h = __frcp_rn(hs[kv]);
+        }
+        float ta = 0.f, tb = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            x[i] = finite_or_zero(__fmul_rn(x[i], inv_h), bad);
+            float& top = i < 8 ? ta : tb;
+            top = fmaxf(top, fabsf(x[i]));
+        }
+        // a block of 16: the thread's own, or the runs of two threads
+        const float oa = __shfl_xor_sync(kFull, ta, 1), ob = __shfl_xor_sync(kFull, tb, 1);
+        if (PAIRS || is_v) {
+            ta = tb = fmaxf(ta, tb);
+        } else {
+            ta = fmaxf(ta, oa);
+            tb = fmaxf(tb, ob);
+        }
+        float ra, rb;
+        const uint32_t sa = block_scale(ta, ra), sb = block_scale(tb, rb);
+        if (bad) report(a.st, MOE_DEV_NONFINITE, t);
+        uint8_t* base = page_base + static_cast<long long>(kv) * L::bytes;
+        if (is_k) {
+            uint32_t c[2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const float r = z ? rb : ra;
+                c[z] = 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    c[z] |= f32_to_e2m1x2(__fmul_rn(x[8 * z + 2 * i], r), __fmul_rn(x[8 * z + 2 * i + 1], r)) << (8 * i);
+            }
+            *reinterpret_cast<uint32_t*>(base + L::k_code(tok, ia)) = c[0];
+            *reinterpret_cast<uint32_t*>(base + L::k_code(tok, ib)) = c[1];
+            if (PAIRS) {
+                base[L::k_scale(tok, j)] = static_cast<uint8_t>(sa);
+            } else if ((j & 1) == 0) {
+                base[L::k_scale(tok, ia / 16)] = static_cast<uint8_t>(sa);
+                base[L::k_scale(tok, ib / 16)] = static_cast<uint8_t>(sb);
+            }
+        }
+        if (!is_v) continue;
+        // Codes of two neighbouring tokens share a byte.  The even token's row also writes
+        // the odd one's if that is new too; an odd token whose partner is
+        // older puts its half beside the codes that are there.
+        const bool odd = place & 1;
+        if (odd && place - 1 >= first_new && place - 1 >= 0) continue;
+        const bool partner = !odd && place + 1 < len && t + 1 < a.T;
+        float z[16];
+        float top2 = 0.f, rz = 0.f;
+        uint32_t sz = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = 0.f;
+        if (partner) {
+            bool bad2 = false;
+            Row16<XT> o;
+            o.load(x_row + a.ld + static_cast<long long>(h) * D, 16 * j, 16 * j + 8);
+            o.get(z);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                z[i] = finite_or_zero(__fmul_rn(z[i], inv_h), bad2);
+                top2 = fmaxf(top2, fabsf(z[i]));
+            }
+            sz = block_scale(top2, rz);
+            if (bad2) report(a.st, MOE_DEV_NONFINITE, t + 1);
+        }
+        const int pj = tok / 2;
+        uint32_t c[4] = {0u, 0u, 0u, 0u};
+        uint32_t* codes0 = reinterpret_cast<uint32_t*>(base + L::v_code(pj, 16 * j));
+        uint32_t* codes1 = reinterpret_cast<uint32_t*>(base + L::v_code(pj, 16 * j + 8));
+        if (odd) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = (i < 2 ? codes0[i] : codes1[i - 2]) & 0x0f0f0f0fu;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) c[i / 4] |= f32_to_e2m1x2(0.f, __fmul_rn(x[i], ra)) << (8 * (i % 4));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) c[i / 4] |= f32_to_e2m1x2(__fmul_rn(x[i], ra), __fmul_rn(z[i], rz)) << (8 * (i % 4));
+        }
+        *reinterpret_cast<uint2*>(codes0) = make_uint2(c[0], c[1]);
+        *reinterpret_cast<uint2*>(codes1) = make_uint2(c[2], c[3]);
+        uint8_t* s = base + L::v_scale(pj, j);
+        if (partner) *reinterpret_cast<uint16_t*>(s) = static_cast<uint16_t>(sa | (sz << 8));
+        else s[odd] = static_cast<uint8_t>(sa);
     }
 }
 
 // One CTA: one row of moe_kv4_read; D/8 threads hold eight numbers of a key
 // or value head.
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) kv4_read_kernel(const moe_kv4_cache c, const int32_t* q_start,
+__global__ void __launch_bounds__(kReadThreads) kv4_read_kernel(const moe_kv4_cache c, const int32_t* q_start,
                                                                 __nv_bfloat16* k_out, __nv_bfloat16* v_out,
                                                                 moe_dev_status* st) {
     constexpr int G = D / 8;
@@ -401,7 +512,7 @@ __global__ void __launch_bounds__(kRopeThreads) kv4_read_kernel(const moe_kv4_ca
         }
     }
     const int tok = place >= 0 ? place % kPage : 0;
-    for (int r = blockIdx.y * (kRopeThreads / G) + threadIdx.x / G; r < 2 * c.n_kv; r += gridDim.y * (kRopeThreads / G)) {
+    for (int r = blockIdx.y * (kReadThreads / G) + threadIdx.x / G; r < 2 * c.n_kv; r += gridDim.y * (kReadThreads / G)) {
         const bool is_v = r >= c.n_kv;
         const int kv = is_v ? r - c.n_kv : r;
         __nv_bfloat16* out = is_v ? v_out : k_out;
@@ -439,26 +550,29 @@ __global__ void __launch_bounds__(kRopeThreads) kv4_read_kernel(const moe_kv4_ca
             }
         }
         __nv_bfloat16* o = out + (static_cast<long long>(t) * c.n_kv + kv) * D + 8 * j;
-        store4(o, y);
-        store4(o + 4, y + 4);
+        store8(o, y);
     }
 }
 
 }  // namespace
 
-template <typename XT, int D>
+template <typename XT, int D, bool PAIRS>
 static cudaError_t launch_rope_t(RopeArgs& a, cudaStream_t s) {
-    constexpr int NG = kRopeThreads / (D / 8);
     const int heads = a.c.pages != nullptr ? a.n_q + 2 * a.n_kv : a.n_q + a.n_kv;
     // Few tokens: a head for each thread group, so that the heads' loads and
-    // reductions run side by side on many SMs.  Many tokens: a CTA takes up
-    // to six heads a group, and the table and position are read once for them.
+    // reductions run side by side on many SMs.  Many tokens: two warps take
+    // all heads of a token, and the table and position are read once for them.
     const bool few = static_cast<long long>(a.T) * heads < 32768;
-    constexpr int kMany = sizeof(XT) == 2 ? 6 : 3;
-    a.rows = few ? NG : heads;
+    constexpr int kFew = 128, kMany = 64;
+    constexpr int R = sizeof(XT) == 2 ? 5 : 2;
+    a.rows = few ? kFew / (D / 16) : heads;
     const dim3 grid(a.T, (heads + a.rows - 1) / a.rows);
-    if (few) return launch_pdl(qk_norm_rope_kernel<XT, D, 1>, grid, dim3(kRopeThreads), 0, s, a);
-    return launch_pdl(qk_norm_rope_kernel<XT, D, kMany>, grid, dim3(kRopeThreads), 0, s, a);
+    if (few) return launch_pdl(qk_norm_rope_kernel<XT, D, PAIRS, 1, kFew>, grid, dim3(kFew), 0, s, a);
+    return launch_pdl(qk_norm_rope_kernel<XT, D, PAIRS, R, kMany>, grid, dim3(kMany), 0, s, a);
+}
+template <typename XT, int D>
+static cudaError_t launch_rope_p(RopeArgs& a, cudaStream_t s) {
+    return a.pairs || a.rot == 0 ? launch_rope_t<XT, D, true>(a, s) : launch_rope_t<XT, D, false>(a, s);
 }
 
 cudaError_t launch_qk_norm_rope(const void* qkv, int dtype, long long ld, int T, int n_q, int n_kv, int D,
@@ -477,18 +591,18 @@ cudaError_t launch_qk_norm_rope(const void* qkv, int dtype, long long ld, int T,
     a.q_out = q_out; a.ld_q = ld_q; a.k_out = k_out; a.ld_k = ld_k;
     if (cache != nullptr) { a.c = *cache; a.q_start = q_start; }
     a.st = st;
-    if (dtype == MOE_DTYPE_BF16) return D == 128 ? launch_rope_t<__nv_bfloat16, 128>(a, s) : launch_rope_t<__nv_bfloat16, 64>(a, s);
-    return D == 128 ? launch_rope_t<float, 128>(a, s) : launch_rope_t<float, 64>(a, s);
+    if (dtype == MOE_DTYPE_BF16) return D == 128 ? launch_rope_p<__nv_bfloat16, 128>(a, s) : launch_rope_p<__nv_bfloat16, 64>(a, s);
+    return D == 128 ? launch_rope_p<float, 128>(a, s) : launch_rope_p<float, 64>(a, s);
 }
 
 cudaError_t launch_kv4_read(const moe_kv4_cache& c, const int32_t* q_start, int T, void* k_out, void* v_out,
                             moe_dev_status* st, cudaStream_t s) {
-    const int ng = kRopeThreads / (c.head_dim / 8);
+    const int ng = kReadThreads / (c.head_dim / 8);
     const dim3 grid(T, (2 * c.n_kv + ng - 1) / ng);
     auto* k = static_cast<__nv_bfloat16*>(k_out);
     auto* v = static_cast<__nv_bfloat16*>(v_out);
-    if (c.head_dim == 128) return launch_pdl(kv4_read_kernel<128>, grid, dim3(kRopeThreads), 0, s, c, q_start, k, v, st);
-    return launch_pdl(kv4_read_kernel<64>, grid, dim3(kRopeThreads), 0, s, c, q_start, k, v, st);
+    if (c.head_dim == 128) return launch_pdl(kv4_read_kernel<128>, grid, dim3(kReadThreads), 0, s, c, q_start, k, v, st);
+    return launch_pdl(kv4_read_kernel<64>, grid, dim3(kReadThreads), 0, s, c, q_start, k, v, st);
 }
 
 }  // namespace moe

@@ -494,7 +494,7 @@ size_t moe_kv4_page_bytes(int n_kv, int head_dim);
 typedef struct moe_rope_params {
     const float* table;        /* [n_pos][rot/2][2] (cos, sin), 16-byte aligned */
     const int32_t* positions;  /* [axes][T], or NULL: the token's place in its sequence (needs a cache) */
-    const uint8_t* axis;       /* [rot/2] axis of each pair (e.g. time, height, width), or NULL: axis 0 */
+    const uint8_t* axis;       /* [rot/2] axis of each pair (e.g. time, height, width), 8-byte aligned, or NULL: axis 0 */
     int32_t n_pos;
     int32_t rot;               /* rotated numbers: a multiple of 32, at most head_dim */
     int32_t axes;              /* rows of positions */
