@@ -55,7 +55,10 @@ class MoELayer:
         dt = abi.MOE_DTYPE_BF16 if w_gate.dtype == torch.bfloat16 else abi.MOE_DTYPE_F32
         capped = capacity_factor > 0
         wsd = abi.workspace_size(abi.MOE_OP_DISPATCH, T, H, self.I, N, k, self.R, capped, dt)
-        wsf = abi.workspace_size(abi.MOE_OP_FFN, T, H, self.I, N, k, self.R, capped, dt)
+        # batches of up to 64 tokens run the decode kernel, which keeps the activations of all N
+        # experts' padded batches: that can be more than a larger batch's rows
+        wsf = max(abi.workspace_size(abi.MOE_OP_FFN, t, H, self.I, N, k, self.R, capped, dt)
+                  for t in (T, min(T, abi.DECODE_LAYER_MAX_T)))
         self.ws_dispatch = torch.empty(max(wsd, 256), dtype=torch.uint8, device=dev)
         # the FFN keeps counters at the start of its workspace: zero before the first call
         self.ws_ffn = torch.zeros(max(wsf, 256), dtype=torch.uint8, device=dev)
