@@ -33,6 +33,7 @@ MOE_KV4_PAGE, MOE_KV4_BLOCK = 64, 16
 
 _lock = threading.Lock()
 _lib = None
+_fast = None   # the module _fastcall, once the library is loaded
 
 
 class MoeError(RuntimeError):
@@ -130,8 +131,22 @@ def load(path: str = LIB_PATH):
             L.moe_kv4_compact.restype = i
             L.moe_kv4_pool_workspace.argtypes = [i, i]
             L.moe_kv4_pool_workspace.restype = sz
+            _load_fastcall(L)
             _lib = L
     return _lib
+
+
+def _load_fastcall(L):
+    """The C module that makes the attention operators' calls; built beside
+    the library, so it is there when the library is."""
+    global _fast
+    from . import _fastcall
+    addr = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    # (a torch built without CUDA has no raw stream to read: every tensor is refused before it is asked for)
+    _fastcall.setup(torch.bfloat16, torch.float32, torch.int32, torch.uint8, getattr(torch._C, "_cuda_getCurrentRawStream", None),
+                    *(addr(f) for f in (L.moe_qk_norm_rope, L.moe_kv4_read, L.moe_attention_kv4, L.moe_kv4_reserve,
+                                        L.moe_kv4_assign, L.moe_kv4_compact)))
+    _fast = _fastcall
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -472,6 +487,13 @@ def moe_qk_norm_rope(qkv, n_q: int, n_kv: int, q_out, k_out=None, q_weight=None,
     [S+1] int32), in one launch.  qkv [T][(n_q + 2 n_kv) D] bf16 or fp32, q_out
     [T][n_q][D] and k_out [T][n_kv][D] of the same dtype; rows may be strided,
     and q_out may be qkv's own query part."""
+    if _fast is None:
+        load()
+    rc = _fast.qk_norm_rope(qkv, n_q, n_kv, q_out, k_out, q_weight, k_weight, eps, rope, cache, q_start, st) if stream is None else None
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        _check(rc, "moe_qk_norm_rope")
     T, width = qkv.shape[0], 1
     for d in qkv.shape[1:]:
         width *= d
@@ -500,6 +522,13 @@ def moe_qk_norm_rope(qkv, n_q: int, n_kv: int, q_out, k_out=None, q_weight=None,
 def moe_kv4_read(cache: Kv4Cache, q_start, k_out=None, v_out=None, st=None, stream=None):
     """The last q_start[s+1] - q_start[s] tokens of every sequence as values:
     k_out, v_out [T][n_kv][D] bf16."""
+    if _fast is None:
+        load()
+    rc = _fast.kv4_read(cache, q_start, k_out, v_out, st) if stream is None else None
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        _check(rc, "moe_kv4_read")
     T = 0
     for t, what in ((k_out, "k_out"), (v_out, "v_out")):
         if t is not None:
@@ -519,6 +548,13 @@ def moe_attention_kv4(q, cache: Kv4Cache, q_start, out, scale: float, max_new: i
     [T][n_q] fp32.  max_new bounds the rows of a sequence.  workspace:
     attention_kv4_workspace(...) bytes, zero-filled before its first use; when
     omitted a buffer is allocated for this call (not graph-capturable)."""
+    if _fast is None:
+        load()
+    rc = _fast.attention(q, cache, q_start, out, scale, max_new, window, lse, workspace, st) if stream is None else None
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        _check(rc, "moe_attention_kv4")
     D = cache.head_dim
     if q.dim() != 3 or q.shape[2] != D:
         raise MoeError("q: expected [T][n_q][%d], got %s" % (D, list(q.shape)))
@@ -547,6 +583,13 @@ def moe_kv4_reserve(pool: Kv4Pool, n_new, workspace, st=None, stream=None):
     """Room for n_new [S] int32 more tokens of every sequence (negative: fewer),
     shared last pages copied first.  workspace: kv4_pool_workspace(pool) bytes,
     zero-filled before its first use."""
+    if _fast is None:
+        load()
+    rc = _fast.reserve(pool, n_new, workspace, st) if stream is None else None
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        _check(rc, "moe_kv4_reserve")
     rc = load().moe_kv4_reserve(pool._ref, _pool_vector(n_new, pool, "n_new"), _addr(workspace, None, "workspace"),
                                 workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
                                 _raw_stream(stream, n_new))
@@ -556,6 +599,13 @@ def moe_kv4_reserve(pool: Kv4Pool, n_new, workspace, st=None, stream=None):
 def moe_kv4_assign(pool: Kv4Pool, parent, st=None, stream=None):
     """Every sequence becomes what parent[s] was (parent [S] int32, -1 = empty):
     forking, reordering and freeing."""
+    if _fast is None:
+        load()
+    rc = _fast.assign(pool, parent, None, st) if stream is None else None
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        _check(rc, "moe_kv4_assign")
     rc = load().moe_kv4_assign(pool._ref, _pool_vector(parent, pool, "parent"), _addr(st, torch.int32, "st"),
                                _raw_stream(stream, parent))
     _check(rc, "moe_kv4_assign")
@@ -564,6 +614,13 @@ def moe_kv4_assign(pool: Kv4Pool, parent, st=None, stream=None):
 def moe_kv4_compact(pool: Kv4Pool, n_live, workspace, st=None, stream=None):
     """Moves the pool's pages in use to its lowest page numbers; n_live [1]
     int32 out (or None): their count."""
+    if _fast is None:
+        load()
+    rc = _fast.compact(pool, n_live, workspace, st) if stream is None else None
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        _check(rc, "moe_kv4_compact")
     rc = load().moe_kv4_compact(pool._ref, _addr(n_live, torch.int32, "n_live"), _addr(workspace, None, "workspace"),
                                 workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
                                 _raw_stream(stream, workspace))

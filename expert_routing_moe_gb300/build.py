@@ -12,11 +12,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
+FAST = os.path.join(HERE, "_fastcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["abi.cu", "router.cu", "route_dispatch.cu", "dispatch.cu", "dispatch_static.cu", "ffn.cu",
            "ffn_decode.cu", "macs.cu", "calib.cu", "cast.cu", "qk_rope.cu", "attn_kv4.cu", "attn_kv4_prefill.cu", "kv4_pages.cu"]
 HEADERS = ["common.cuh", "launch.h", "routing.cuh", "permute.cuh", "kv4.cuh", "attn_kv4.cuh", "tmap.h", "../../include/moe_gb300.h"]
@@ -33,12 +35,27 @@ def nvcc() -> str:
 def _newest_input() -> float:
     paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
     paths.append(os.path.join(os.path.dirname(HERE), "include", "moe_gb300.h"))
+    paths.append(os.path.join(CSRC, "fastcall.c"))
     paths.append(os.path.abspath(__file__))
     return max(os.path.getmtime(p) for p in paths)
 
 
+def _build_fastcall() -> None:
+    """The CPython module that calls the attention operators without ctypes."""
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        raise RuntimeError("no C compiler found")
+    tmp = FAST + ".tmp%d" % os.getpid()
+    cmd = [cc, "-shared", "-fPIC", "-O2", "-Wall", "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "fastcall.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("building fastcall.c failed:\n%s\n%s" % (r.stdout, r.stderr))
+    os.replace(tmp, FAST)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
+    built = all(os.path.exists(p) and os.path.getmtime(p) >= _newest_input() for p in (LIB, FAST))
+    if not force and built:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -55,8 +72,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        fast = ex.submit(_build_fastcall)
         objs = list(ex.map(compile_one, SOURCES))
+        fast.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "static", "-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)
