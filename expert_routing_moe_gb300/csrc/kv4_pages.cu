@@ -16,6 +16,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kAssignCols = 8;        // table columns of a CTA: one 32-byte sector of each row
 constexpr int kAssignThreads = 256;
+constexpr int kPlaceSmem = 4096;     // pages handed out through shared memory
 constexpr int kHeader = 64;           // words before the lists
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVec = 3;           // 16-byte words in flight of a thread
@@ -65,11 +66,16 @@ __device__ __forceinline__ Sum2 scan2(Sum2 v, Sum2& total, Sum2* s_warp) {
 
 __device__ __forceinline__ int pages_of(int len) { return (len + MOE_KV4_PAGE - 1) / MOE_KV4_PAGE; }
 
-// One CTA.  Thread i takes sequences [i * per, (i+1) * per).
+// One CTA.  Thread i takes sequences [i * per, (i+1) * per).  What bounds it is
+// the chain of loads (length, last page, sharers, references): each is done
+// once, the references' scan is read ahead of it, and up to kPlaceSmem pages
+// are handed from the threads that find them to those that take them in shared
+// memory.
 __global__ void __launch_bounds__(kPlanThreads, 1) kv4_reserve_plan_kernel(const moe_kv4_pool p, const int32_t* n_new,
                                                                            void* ws, moe_dev_status* st) {
+    constexpr int kPer = 4;          // sequences of a thread: S <= 4096
     __shared__ Sum2 s_warp[kPlanWarps];
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_place[kPlaceSmem];
     const PoolWs w = pool_ws(ws, p.n_pages);
     const int tid = threadIdx.x;
     if (tid == 0) s_bad = -1;
@@ -78,125 +84,118 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv4_reserve_plan_kernel(const
     const int per = (p.S + kPlanThreads - 1) / kPlanThreads;
     const int s0 = min(p.S, tid * per), s1 = min(p.S, s0 + per);
     auto row = [&](int s) { return p.page_table + static_cast<long long>(s) * p.max_pages; };
-    // the partly filled last page of a sequence that grows, or -1
-    auto part_page = [&](int s, int len, int add) {
-        return add > 0 && len % MOE_KV4_PAGE != 0 ? row(s)[len / MOE_KV4_PAGE] : -1;
-    };
+    int len[kPer], add[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const bool in = s0 + i < s1;
+        len[i] = in ? p.seq_len[s0 + i] : 0;
+        add[i] = in ? n_new[s0 + i] : 0;
+    }
+    // the thread's pages of the pool: its free ones are counted while the sequences' chain runs
+    const int chunk = ((p.n_pages + kPlanThreads - 1) / kPlanThreads + 3) & ~3;
+    const int g0 = min(static_cast<long long>(p.n_pages), static_cast<long long>(tid) * chunk);
+    const int g1 = min(p.n_pages, g0 + chunk);
+    Sum2 free_mine = {0, 0}, free_total;
+    for (int g = g0; g < g1; ++g) free_mine.x += p.ref[g] == 0;
     __syncthreads();
-    for (int s = s0; s < s1; ++s) {
-        const int len = p.seq_len[s], add = n_new[s];
-        const long long after = static_cast<long long>(len) + add;
-        const long long most = min(static_cast<long long>(p.max_pages) * MOE_KV4_PAGE, 0x7fffffffll);
-        if (len < 0 || len > most || after > most) { s_bad = s; continue; }
-        const int g = part_page(s, len, add);
-        if (add > 0 && len % MOE_KV4_PAGE != 0 && (g < 0 || g >= p.n_pages)) { s_bad = s; continue; }
-        for (int c = pages_of(static_cast<int>(max(after, 0ll))); c < pages_of(len); ++c) {
+    int part[kPer];                  // the partly filled last page of a sequence that grows, or -1
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) part[i] = -1;
+    const long long most = min(static_cast<long long>(p.max_pages) * MOE_KV4_PAGE, 0x7fffffffll);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (s0 + i >= s1) break;
+        const int s = s0 + i;
+        const long long after = static_cast<long long>(len[i]) + add[i];
+        if (len[i] < 0 || len[i] > most || after > most) { s_bad = s; continue; }
+        if (add[i] > 0 && len[i] % MOE_KV4_PAGE != 0) {
+            const int g = row(s)[len[i] / MOE_KV4_PAGE];
+            if (g < 0 || g >= p.n_pages) { s_bad = s; continue; }
+            part[i] = g;
+        }
+        for (int c = pages_of(static_cast<int>(max(after, 0ll))); c < pages_of(len[i]); ++c) {
             const int id = row(s)[c];
             if (id < 0 || id >= p.n_pages) s_bad = s;
         }
-        if (g >= 0) {
-            atomicAdd(&w.a[g], 1);
-            atomicMax(&w.b[g], s + 1);
+        if (part[i] >= 0) {
+            atomicAdd(&w.a[part[i]], 1);
+            atomicMax(&w.b[part[i]], s + 1);
         }
     }
     __threadfence_block();
     __syncthreads();
     const bool bad = s_bad >= 0;
     // a sequence's copy (0 or 1) and pages in all
-    auto needs = [&](int s, int& copy, int& fresh) {
-        copy = fresh = 0;
-        const int len = p.seq_len[s], add = n_new[s];
-        if (add <= 0) return -1;
-        const int g = part_page(s, len, add);
-        if (g >= 0 && p.ref[g] > 1) {
-            const bool keeps = __ldcg(&w.a[g]) == p.ref[g] && __ldcg(&w.b[g]) == s + 1;
-            copy = keeps ? 0 : 1;
+    int copy[kPer], fresh[kPer];
+    Sum2 mine = {0, 0}, total;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        copy[i] = fresh[i] = 0;
+        if (bad || s0 + i >= s1 || add[i] <= 0) continue;
+        if (part[i] >= 0) {
+            const int refs = p.ref[part[i]], sharers = __ldcg(&w.a[part[i]]), last = __ldcg(&w.b[part[i]]);
+            copy[i] = refs > 1 && !(sharers == refs && last == s0 + i + 1);
         }
-        fresh = pages_of(len + add) - pages_of(len);
-        return g;
-    };
-    Sum2 mine = {0, 0}, total, base = {0, 0};
-    if (!bad) {
-        for (int s = s0; s < s1; ++s) {
-            int copy, fresh;
-            needs(s, copy, fresh);
-            mine.x += copy + fresh;
-            mine.y += copy;
-        }
+        fresh[i] = pages_of(len[i] + add[i]) - pages_of(len[i]);
+        mine.x += copy[i] + fresh[i];
+        mine.y += copy[i];
     }
-    base = scan2(mine, total, s_warp);
-    const long long want = total.x, copies = total.y;
+    const Sum2 base = scan2(mine, total, s_warp);
+    const long long want = total.x;
     // free pages in ascending order, as many as are wanted
-    const int chunk = ((p.n_pages + kPlanThreads - 1) / kPlanThreads + 3) & ~3;
-    const int g0 = min(static_cast<long long>(p.n_pages), static_cast<long long>(tid) * chunk);
-    const int g1 = min(p.n_pages, g0 + chunk);
-    Sum2 free_mine = {0, 0}, free_total;
-    for (int g = g0; g < g1; ++g) free_mine.x += p.ref[g] == 0;
     const Sum2 free_base = scan2(free_mine, free_total, s_warp);
-    const bool short_of = want > free_total.x;
-    if (!bad && !short_of) {
+    const bool go = !bad && want <= free_total.x;
+    int* place = want <= kPlaceSmem ? s_place : w.place;
+    if (go) {
         long long k = free_base.x;
         for (int g = g0; g < g1 && k < want; ++g)
-            if (p.ref[g] == 0) w.place[k++] = g;
+            if (p.ref[g] == 0) place[k++] = g;
     }
+    // decisions have read references and scratch; both change only after this barrier
     __syncthreads();
-    // decisions read references and lengths; they change only after this barrier
-    int copy_flag[4];                 // per <= 4 (S <= 4096)
-    int fresh_n[4], part[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        copy_flag[i] = fresh_n[i] = 0;
-        part[i] = -1;
-        if (s0 + i < s1 && !bad) part[i] = needs(s0 + i, copy_flag[i], fresh_n[i]);
-    }
-    __syncthreads();
-    if (!bad && !short_of) {
+    if (go) {
         long long at = base.x, at_copy = base.y;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kPer; ++i) {
             const int s = s0 + i;
             if (s >= s1) break;
-            const int len = p.seq_len[s], add = n_new[s];
-            const int held = pages_of(len);
+            const int held = pages_of(len[i]);
             int32_t* r = row(s);
-            if (copy_flag[i]) {
-                const int g = w.place[at++];
+            if (copy[i]) {
+                const int g = place[at++];
                 w.copies[at_copy++] = make_int2(part[i], g);
-                r[len / MOE_KV4_PAGE] = g;
+                r[len[i] / MOE_KV4_PAGE] = g;
                 p.ref[g] = 1;
                 atomicSub(&p.ref[part[i]], 1);
             }
-            for (int c = 0; c < fresh_n[i]; ++c) {
-                const int g = w.place[at++];
+            for (int c = 0; c < fresh[i]; ++c) {
+                const int g = place[at++];
                 r[held + c] = g;
                 p.ref[g] = 1;
             }
-            if (add < 0) {
-                const int after = max(0, len + add);
+            if (add[i] < 0) {
+                const int after = max(0, len[i] + add[i]);
                 for (int c = pages_of(after); c < held; ++c) {
                     atomicSub(&p.ref[r[c]], 1);
                     r[c] = -1;
                 }
                 p.seq_len[s] = after;
-            } else if (add > 0) {
-                p.seq_len[s] = len + add;
+            } else if (add[i] > 0) {
+                p.seq_len[s] = len[i] + add[i];
             }
         }
     }
     // the scratch goes back to zero
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kPer; ++i)
         if (part[i] >= 0) {
             w.a[part[i]] = 0;
             w.b[part[i]] = 0;
         }
-    if (bad) {
-        for (int g = g0; g < g1; ++g) w.a[g] = w.b[g] = 0;
-    }
     if (tid == 0) {
-        w.header[0] = bad || short_of ? 0 : static_cast<int>(copies);
+        w.header[0] = go ? static_cast<int>(total.y) : 0;
         if (bad) report(st, MOE_DEV_BAD_INDEX, s_bad);
-        else if (short_of) report(st, MOE_DEV_NO_PAGES, static_cast<int>(want - free_total.x));
+        else if (!go) report(st, MOE_DEV_NO_PAGES, static_cast<int>(want - free_total.x));
     }
 }
 
