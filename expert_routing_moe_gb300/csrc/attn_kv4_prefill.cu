@@ -41,7 +41,7 @@ constexpr int kBuf = 2;             // pages as fp16 operands
 constexpr int kMaxCtasPf = 160;
 constexpr int kCounterBytesPf = 2048;
 constexpr int kChunk = 256;         // sequences whose units are held in shared memory
-constexpr float kGrow = 8.f;        // log2 of the growth that O waits for
+constexpr float kGrow = 14.f;       // log2 of the growth that O waits for
 // What an item costs beside its pages (its queries, its outputs, the pipeline's
 // start and end), in pages: the runs are cut by cost, so that a CTA with many
 // short items gets fewer pages.
@@ -792,19 +792,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                         exponentials();
                     }
                     l2 = add2(l2, sum);
-                    // the next page's scores come in while this page's P goes out
+                    // P goes out before the wait for the next page's scores: the tensor cores have work in between
+                    // (the other way round, with those loads beside this store, took 547 us for 8192 tokens, not 472)
                     const bool more = j + 1 < y;
-                    if (more) {
-                        if (!wait_s(n + 1)) break;
-                        tmem_ld32(tb + C::c_s + 64 * ((n + 1) & 1), s0);
-                    }
                     tmem_st32(tb + C::c_s + 64 * (n & 1), h);
-                    if (more) tmem_ld32(tb + C::c_s + 64 * ((n + 1) & 1) + 32, s1);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_P + 2 * t + (n & 1)));
                     if (more) {
+                        if (!wait_s(n + 1)) break;
+                        load_s(n + 1);
                         tmem_ld_wait();
                         hide(j + 1);
                     }
