@@ -764,15 +764,20 @@ cudaError_t launch_stream(const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Rows of a sequence that the streaming kernel takes; more go to the prefill kernel.
-constexpr int kStreamRows = 64;
+// Rows of a sequence that the streaming kernel takes, for `rows` of all sequences; more go to the prompt
+// kernel.  Streaming costs a pass over the pages for each 16 rows, the prompt kernel a start of some 30 us.
+// us of the two (streaming/prompt), 8 query heads a key head, 4 key heads, contexts of 300, 2000, 9000:
+//     128 rows,  1 sequence  13/34 17/33 27/77     8: 22/36 25/35 43/79    32: 23/37 40/40 96/54
+//     256 rows,  1 sequence  15/38 25/36 41/57     8: 24/36 29/37 71/58    32: 32/38 63/39 187/58
+constexpr int stream_rows(long long rows) { return rows <= 1024 ? 256 : 128; }
 
 constexpr size_t stream_workspace(int D) {
     return kCounterBytes + static_cast<size_t>(kMaxCtas) * 2 * 16 * (D + 2) * sizeof(float);
 }
 
 size_t attention_kv4_workspace(int T, int n_q, int n_kv, int D) {
-    const bool prefill = static_cast<long long>(T) * (n_q / n_kv) > kStreamRows;
+    const long long rows = static_cast<long long>(T) * (n_q / n_kv);
+    const bool prefill = rows > stream_rows(rows);
     return (stream_workspace(D) + 255) / 256 * 256 + (prefill ? attn_prefill_workspace(D) : 0);
 }
 
@@ -790,11 +795,13 @@ cudaError_t launch_attention_kv4(const void* q, long long ld_q, int T, int n_q, 
     a.rows_hi = 0x7fffffff;
     // Without a sequence of many rows (as max_new promises) the streaming kernel is launched alone;
     // sequences that have more all the same are right there, only slower.
-    const bool prefill = static_cast<long long>(max_new) * a.group > kStreamRows && static_cast<long long>(T) * a.group > kStreamRows;
+    const long long rows = static_cast<long long>(T) * a.group;
+    const int few = stream_rows(rows);
+    const bool prefill = static_cast<long long>(max_new) * a.group > few && rows > few;
     if (prefill) {
-        a.rows_hi = kStreamRows;
+        a.rows_hi = few;
         AttnArgs b = a;
-        b.rows_lo = kStreamRows + 1;
+        b.rows_lo = few + 1;
         b.rows_hi = 0x7fffffff;
         uint8_t* ws2 = static_cast<uint8_t*>(ws) + (stream_workspace(c.head_dim) + 255) / 256 * 256;
         b.counters = reinterpret_cast<int*>(ws2);

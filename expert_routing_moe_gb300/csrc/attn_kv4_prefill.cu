@@ -1,24 +1,37 @@
 // attn_kv4_prefill.cu -- attention over the 4-bit paged cache for many query
-// rows a sequence (prompt chunks): tcgen05 products bound by the tensor cores.
+// rows a sequence (prompt chunks): tcgen05 products.
 //
 // For one (sequence, key head) the rows are the new tokens' query heads of
 // that key head, token-major; a work item is 256 of them, in two tiles of 128
 // (TMEM lanes) that share every page of keys and values:
 //     S = Q K^T (128 x 64, fp32 in TMEM),  P = 2^(f S - m) (fp16, over S),
 //     O += P V (128 x D, fp32 in TMEM; P is the A operand in TMEM)
-// S has two buffers a tile: the next page's scores are there before the
-// softmax asks for them, so the softmax warps, not the round trip through the
-// tensor cores, set the pace.  TMEM of a tile: S/P 2 x 64 columns, O D.
+// S has two buffers a tile: the next page's scores are computed while the
+// softmax is at this one's.  TMEM of a tile: S/P 2 x 64 columns, O D.
 //
 // Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (a thread is a row), 8-9
 // convert the keys' pages and 10-11 the values' to fp16 operands (exact), 12-13
-// issue the tiles' products, 14 copies pages (one bulk copy each), 15 the next
-// item's queries, which the softmax warps turn to fp16 between two items.  O is scaled only when a row's maximum grows by more
-// than 2^8, which fp16's range allows for P.
+// issue the tiles' products, 14 copies pages (one bulk copy each), 15 walks the
+// items and copies the next one's queries, which the softmax warps turn to fp16
+// between two items.
+//
+// P is fp16: its rounding (2^-11 of each probability) is below that of the bf16
+// output, and sums of it are taken in fp32 before it is rounded.  O is scaled
+// only when a row's maximum grows by more than 2^kGrow: P stays below 2^14 of
+// fp16's 2^16, and what lies 2^-28 under the largest is lost to its range.
 //
 // The pages of all items form one sequence of units, cut into equal runs for
 // the CTAs; an item that crosses CTAs is joined by the last to arrive,
 // in the order of the pages.
+//
+// What bounds it: a page of an item (256 rows x 64 keys, D = 128) takes about
+// 1650 clocks.  The products alone are 1280 (scores with both operands in shared
+// memory run at two thirds of the tensor cores' rate, 384 clocks a tile: operands of
+// 48 KB at 128 bytes a clock), the softmax warps' chain (load 300, exponentials
+// 700 with the other tile's warp on the same scheduler, store 135) about 1200,
+// and the two meet once a page; an item costs another 11,000 clocks (queries
+// 4000, outputs 5500).  A prompt of 8192 tokens, 32 heads on 4 (550 GFLOP):
+// 441 us, 1247 TFLOP/s.
 #include <cuda_bf16.h>
 #include <type_traits>
 
@@ -39,12 +52,14 @@ constexpr int kPfWarps = kPfThreads / 32;
 constexpr int kRaw = 3;             // pages in 4 bits in flight
 constexpr int kBuf = 2;             // pages as fp16 operands
 constexpr int kMaxCtasPf = 160;
-constexpr int kCounterBytesPf = 2048;
+constexpr int kCounterBytesPf = kMaxCtasPf * 8 * 4;   // one for each softmax warp of a CTA
 constexpr int kChunk = 256;         // sequences whose units are held in shared memory
-constexpr float kGrow = 14.f;       // log2 of the growth that O waits for
+// log2 of the growth that O waits for (8: 565 us for a prompt of 8192 tokens where 11 took 549 and 14 546)
+constexpr float kGrow = 14.f;
 // What an item costs beside its pages (its queries, its outputs, the pipeline's
 // start and end), in pages: the runs are cut by cost, so that a CTA with many
-// short items gets fewer pages.
+// short items gets fewer pages.  Costs of 2, 4, 6, 8, 10 took 553, 491, 452, 441, 445 us
+// for a prompt of 8192 tokens and 143, 116, 103, 100, 102 us for chunks behind long contexts.
 constexpr int kItemCost = 8;
 
 enum Site : int { kSiteRaw = 31, kSiteRawFree, kSiteKFree, kSiteVFree, kSiteKFull, kSiteVFull, kSiteQ, kSiteP, kSiteS, kSiteO, kSiteQFree };
@@ -101,13 +116,6 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b,
     asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
 }
-// 32 bytes to a 32-byte boundary of device memory: a whole sector from each lane.
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[16], int at) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[at]), "r"(v[at + 1]), "r"(v[at + 2]),
-                 "r"(v[at + 3]), "r"(v[at + 4]), "r"(v[at + 5]), "r"(v[at + 6]), "r"(v[at + 7])
-                 : "memory");
-}
-
 // The larger magnitudes of two packed bf16 pairs (a NaN gives way to a number:
 // the row's products are NaN whatever its power of two is).
 __device__ __forceinline__ uint32_t bf2_max_abs(uint32_t x, uint32_t y) {
@@ -132,10 +140,13 @@ struct Pf {
     static constexpr int raw = Kv4Layout<D>::bytes;
     static constexpr int k_tile = kPage * D * 2;      // D/64 halves of [64 tokens][64 numbers], 128-byte rows
     static constexpr int v_tile = kPage * D * 2;      // [D numbers][64 tokens], 128-byte rows
-    static constexpr int q_tile = kTile * D * 2;      // D/64 halves of [128 rows][64 numbers], 128-byte rows
-    static constexpr int o_q = 0;                     // two tiles
-    static constexpr int o_qraw = o_q + 2 * q_tile;   // an item's queries as they come: [256 rows][D] bf16
-    static constexpr int o_k = o_qraw + 2 * q_tile;
+    // queries: groups of 8 rows, in each D/64 halves of [8 rows][64 numbers], 128-byte rows; a group takes
+    // the bytes that its rows have in device memory, so that they are turned to fp16 in place
+    static constexpr int q_group = 8 * D * 2;
+    static constexpr int q_tile = kTile * D * 2;
+    static constexpr int q_slot = 2 * q_tile;         // an item's
+    static constexpr int o_q = 0;                     // two items: the one at hand and the next
+    static constexpr int o_k = o_q + 2 * q_slot;
     static constexpr int o_v = o_k + kBuf * k_tile;
     static constexpr int o_raw = o_v + kBuf * v_tile;
     static constexpr int smem = o_raw + kRaw * raw + 1024;   // slack for 1024-byte alignment
@@ -149,6 +160,68 @@ __device__ __forceinline__ int item_units(const AttnArgs& a, const Seq& s, int t
     int lo, hi;
     tile_pages<NR>(a, s, tile, lo, hi);
     return kItemCost + hi - lo;
+}
+
+// What the warps of an item's products and softmax get to know of it.
+struct Item {
+    int q0, n, len;      // the sequence
+    int h, tile;
+    int pa, pb;          // pages of this run's piece
+    int x[2], y[2];      // of each tile
+    int b0, b1;          // runs with pages of the item
+    int kind;            // kPart, kWhole or kEnd
+};
+enum Kind : int { kPart, kWhole, kEnd };
+
+// The queries of 8-row groups g0 .. g1 - 1 (an even number) from bf16 rows to fp16 operands, in place, by
+// one warp: four lanes hold a row, scaled by a power of two of its own (see the streaming kernel).
+template <int D>
+__device__ __forceinline__ void convert_queries(uint8_t* q, float* fs, int g0, int g1, int rows, float f_all, int lane) {
+    constexpr int Z = D / 32;                          // 16-byte chunks of a lane
+    const int rr = lane >> 2, q4 = lane & 3;
+#pragma unroll 1
+    for (int g = g0; g < g1; g += 2) {
+        uint4 v[2][Z];
+        float up[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int rt = 8 * (g + u) + rr;
+            uint32_t top2 = 0u;                        // the largest magnitudes, as two bf16
+#pragma unroll
+            for (int z = 0; z < Z; ++z) {
+                // neighbouring rows take their chunks in another order: no two lanes of a load share a bank
+                const int c = (z ^ (rr & 1)) * 4 + q4;
+                v[u][z] = rt < rows ? *reinterpret_cast<const uint4*>(q + rt * (D * 2) + c * 16) : make_uint4(0u, 0u, 0u, 0u);
+                top2 = bf2_max_abs(top2, bf2_max_abs(bf2_max_abs(v[u][z].x, v[u][z].y), bf2_max_abs(v[u][z].z, v[u][z].w)));
+            }
+            float top = fmaxf(__uint_as_float(top2 << 16), __uint_as_float(top2 & 0xffff0000u));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+            int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+            e = (top > 0.f && e < 128) ? max(-100, min(100, 10 - e)) : 0;
+            up[u] = __int_as_float((e + 127) << 23);
+            float fr = f_all * __int_as_float((127 - e) << 23);
+            // the maximum is taken before the factor: it has to be positive
+            if (fr < 0.f) { fr = -fr; up[u] = -up[u]; }
+            if (q4 == 0) fs[rt] = fmaxf(fr, 1e-37f);
+        }
+        __syncwarp();                                  // the rows are read
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int z = 0; z < Z; ++z) {
+                const int c = (z ^ (rr & 1)) * 4 + q4;
+                const uint32_t in[4] = {v[u][z].x, v[u][z].y, v[u][z].z, v[u][z].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    h[k] = pack_f16(__uint_as_float(in[k] << 16) * up[u], __uint_as_float(in[k] & 0xffff0000u) * up[u]);
+                *reinterpret_cast<uint4*>(q + (g + u) * (8 * D * 2) + (c / 8) * 1024 + rr * 128 + (((c % 8) ^ rr) * 16)) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+            }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
 }
 
 // Where a run starts.
@@ -215,14 +288,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     enum { B_RAWF = 0, B_RAWE = B_RAWF + kRaw, B_KF = B_RAWE + kRaw, B_KE = B_KF + kBuf, B_VF = B_KE + kBuf, B_VE = B_VF + kBuf,
-           B_QF = B_VE + kBuf, B_QRF = B_QF + 2, B_QRE = B_QRF + 1, B_S = B_QRE + 1, B_P = B_S + 4, B_O = B_P + 4, B_DRAIN = B_O + 4, B_N = B_DRAIN + 2 };
+           B_QF = B_VE + kBuf, B_QE = B_QF + 2, B_QRF = B_QE + 2, B_S = B_QRF + 2, B_P = B_S + 4, B_O = B_P + 4, B_DRAIN = B_O + 4, B_N = B_DRAIN + 2 };
     __shared__ __align__(8) uint64_t bars[B_N];
     __shared__ uint32_t s_tmem;
     __shared__ long long s_units[kChunk], s_warp[kPfWarps];
-    __shared__ int s_list[kChunk], s_list_n, s_ticket;
+    __shared__ int s_list[kChunk], s_list_n;
     __shared__ Start s_start;
     __shared__ uint8_t s_bad[kRaw];
-    __shared__ float s_f[kRows];
+    __shared__ float s_f[2][kRows];      // the rows' factors, of the item at hand and the next
+    __shared__ Item s_item[2];
     __shared__ volatile int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -234,12 +308,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
             mbar_init(bar(B_VF + i), 2); mbar_init(bar(B_VE + i), 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(B_QF + i), 4);
+            mbar_init(bar(B_QF + i), 8);
+            mbar_init(bar(B_QE + i), 10);
+            mbar_init(bar(B_QRF + i), 1);
             mbar_init(bar(B_DRAIN + i), 1);
         }
         for (int i = 0; i < 4; ++i) { mbar_init(bar(B_S + i), 1); mbar_init(bar(B_P + i), 4); mbar_init(bar(B_O + i), 1); }
-        mbar_init(bar(B_QRF), 1);
-        mbar_init(bar(B_QRE), 8);
         s_abort = 0;
         fence_mbar_init();
     }
@@ -346,41 +420,69 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
     const uint32_t tmem = s_tmem;
     const Start start = s_start;
 
-    // The roles deal the 512 x 128 registers anew: 256 x 152 + 128 x 96 + 128 x 104 = 64,512 of 65,536.
+    // The roles deal the 512 x 128 registers anew: 256 x 176 + 256 x 80 = 65,536.
     bool ok = true;
     if (warp == 15) {
-        // ---------------- the next items' queries ----------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        // A token's query heads of the key head lie side by side: one copy for each token.
+        // ---------------- the items and their queries ----------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        // This warp alone walks the items for the warps of products and softmax, an item ahead of them.
         Walk w;
         w.begin(a, start, u0, u1);
-        uint32_t ph = 1;
-        while (ok) {
-            if (w.pa < w.pb) {
-                ok = mbar_wait(bar(B_QRE), ph, &s_abort, a.st, kSiteQFree);
-                ok = __all_sync(kFull, ok);
-                if (!ok) break;
-                ph ^= 1;
+        uint32_t it = 0;
+        auto free_slot = [&]() {
+            ok = mbar_wait(bar(B_QE + (it & 1)), ((it >> 1) & 1) ^ 1, &s_abort, a.st, kSiteQFree);
+            ok = __all_sync(kFull, ok);
+            return ok;
+        };
+        while (true) {
+            const bool pages = w.pa < w.pb;
+            // (a run that holds only units of the item's own cost has no piece)
+            if (pages || w.empty_item(u0)) {
+                if (!free_slot()) break;
+                Item m;
+                m.q0 = w.q.q0; m.n = w.q.n; m.len = w.q.len;
+                m.h = w.h; m.tile = w.tile; m.pa = w.pa; m.pb = w.pb;
+                w.half(a, 0, m.x[0], m.y[0]);
+                w.half(a, 1, m.x[1], m.y[1]);
+                // the runs with pages of the item: b0 (its slot 1) .. b1 (their slots 0)
+                m.b0 = static_cast<int>((w.item + kItemCost) / share);
+                m.b1 = static_cast<int>((w.item + kItemCost + w.hi - w.lo - 1) / share);
+                m.kind = w.pa == w.lo && w.pb == w.hi ? kWhole : kPart;
+                if (lane == 0) s_item[it & 1] = m;
+                const uint32_t q = smem_u32(smem + C::o_q) + (it & 1) * C::q_slot;
                 const int r0 = w.tile * kRows, r1 = min(w.q.n * a.group, r0 + kRows);
-                if (lane == 0) mbar_arrive_expect_tx(bar(B_QRF), (r1 - r0) * (D * 2));
-                __syncwarp();
-                for (int i = r0 / a.group + lane; i * a.group < r1; i += 32) {
-                    const int x = max(r0, i * a.group), y = min(r1, (i + 1) * a.group);
-                    bulk_copy_g2s(smem_u32(smem + C::o_qraw) + (x - r0) * (D * 2),
-                                  a.q + static_cast<long long>(w.q.q0 + i) * a.ld_q + static_cast<long long>(w.h * a.group + x - i * a.group) * D,
-                                  (y - x) * (D * 2), bar(B_QRF));
+                if (lane == 0) {
+                    if (pages) mbar_arrive_expect_tx(bar(B_QRF + (it & 1)), (r1 - r0) * (D * 2));
+                    else mbar_arrive(bar(B_QRF + (it & 1)));
                 }
+                __syncwarp();
+                // a token's query heads of the key head lie side by side: one copy for each token
+                if (pages) {
+                    for (int i = r0 / a.group + lane; i * a.group < r1; i += 32) {
+                        const int x = max(r0, i * a.group), y = min(r1, (i + 1) * a.group);
+                        bulk_copy_g2s(q + (x - r0) * (D * 2),
+                                      a.q + static_cast<long long>(w.q.q0 + i) * a.ld_q + static_cast<long long>(w.h * a.group + x - i * a.group) * D,
+                                      (y - x) * (D * 2), bar(B_QRF + (it & 1)));
+                    }
+                }
+                ++it;
             }
             w.next(a, u0, u1);
             if (w.end) break;
         }
+        if (ok && free_slot() && lane == 0) {
+            s_item[it & 1].kind = kEnd;
+            mbar_arrive(bar(B_QRF + (it & 1)));
+        }
         if (!ok) {       // copies in flight land before the CTA gives its shared memory up
-            mbar_drain(bar(B_QRF), 0);
-            mbar_drain(bar(B_QRF), 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_drain(bar(B_QRF + i), 0);
+                mbar_drain(bar(B_QRF + i), 1);
+            }
         }
     } else if (warp == 14) {
         // ---------------- pages from device memory ----------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         Walk w;
         w.begin(a, start, u0, u1);
         int st = 0;
@@ -426,13 +528,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         }
     } else if (warp >= 12) {
         // ---------------- products ----------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         // A warp for each tile: waits and commits cost issue time, which the
         // other tile's products then fill.  The warp walks together and one
         // elected lane issues: addresses and descriptors stay in uniform registers.
         constexpr uint32_t id_s = idesc_f16_f32(kTile, kPage), id_o = idesc_f16_f32(kTile, D);
         const uint32_t t = warp - 12;
-        const uint64_t q_desc = sw128_desc(smem_u32(smem + C::o_q) + t * C::q_tile), k_desc = sw128_desc(smem_u32(smem + C::o_k)),
+        // a group of the queries is followed by the next after both halves
+        const uint64_t q_desc = sw128_desc(smem_u32(smem + C::o_q) + t * C::q_tile) + (static_cast<uint64_t>((C::q_group - 1024) >> 4) << 32), k_desc = sw128_desc(smem_u32(smem + C::o_k)),
                        v_desc = sw128_desc(smem_u32(smem + C::o_v));
         const uint32_t ts = t * C::tile_cols + C::c_s, to = t * C::tile_cols + C::c_o;
         const uint32_t bar_s = bar(B_S + 2 * t), bar_o = bar(B_O + 2 * t);
@@ -441,11 +544,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
             ok = __all_sync(kFull, ok);
             return ok;
         };
-        Walk w;
-        w.begin(a, start, u0, u1);
         uint32_t kv = 0, vv = 0;                       // pages of keys and values so far
         uint32_t ns = 0, no = 0;                       // scores and outputs issued
-        uint32_t nq = 0;                               // items
+        uint64_t qd = 0;
         auto scores = [&](bool active) {               // of the next page of keys
             if (!wait(B_KF + kv % kBuf, (kv / kBuf) & 1, kSiteKFull)) return;
             tc_fence_after();
@@ -454,7 +555,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                     const uint64_t d = k_desc + (kv % kBuf) * (C::k_tile >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        tc_mma_bf16(ts + 64 * (ns & 1), q_desc + (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2,
+                        tc_mma_bf16(ts + 64 * (ns & 1), qd + (k / 4) * (1024 >> 4) + (k % 4) * 2,
                                     d + (k / 4) * (kPage * 128 >> 4) + (k % 4) * 2, id_s, k > 0);
                     tc_commit(bar_s + 8 * (ns & 1));
                 }
@@ -482,21 +583,22 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
             ++vv;
         };
         // The scores run a page ahead of the outputs within an item.
-        while (ok) {
-            if (w.pa < w.pb) {
-                int x, y;
-                w.half(a, t, x, y);
-                if (!wait(B_QF + t, nq & 1, kSiteQ)) break;
-                ++nq;
-                scores(x <= w.pa && w.pa < y);
-                for (int p = w.pa; ok && p < w.pb; ++p) {
-                    if (p + 1 < w.pb) scores(x <= p + 1 && p + 1 < y);
+        for (uint32_t it = 0; ok; ++it) {
+            const uint32_t slot = it & 1;
+            if (!wait(B_QF + slot, (it >> 1) & 1, kSiteQ)) break;
+            const Item& w = s_item[slot];
+            if (w.kind == kEnd) break;
+            const int pa = w.pa, pb = w.pb, x = w.x[t], y = w.y[t];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_QE + slot));
+            if (pa < pb) {
+                qd = q_desc + slot * (C::q_slot >> 4);
+                scores(x <= pa && pa < y);
+                for (int p = pa; ok && p < pb; ++p) {
+                    if (p + 1 < pb) scores(x <= p + 1 && p + 1 < y);
                     if (ok) outputs(x <= p && p < y, p > x);
                 }
-                if (!ok) break;
             }
-            w.next(a, u0, u1);
-            if (w.end) break;
         }
         // every product is done before TMEM and shared memory are given up
         if (elect_one()) tc_commit(bar(B_DRAIN + t));
@@ -504,7 +606,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         mbar_drain(bar(B_DRAIN + t), 0);
     } else if (warp >= 8 && warp < 12) {
         // ---------------- 4 bits to fp16 operands ----------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const bool keys = warp < 10;
         const int cw = (warp - 8) & 1;        // which of the two warps
         Walk w;
@@ -617,88 +719,43 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         }
     } else {
         // ---------------- softmax: a thread is a row ----------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         const int t = warp >> 2;                              // tile
         const int r_tile = (warp & 3) * 32 + lane;            // row of the tile = TMEM lane
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tb = tmem + t * C::tile_cols + lanes;
-        Walk w;
-        w.begin(a, start, u0, u1);
         uint32_t n = 0;              // pages of this tile so far
-        uint32_t qp = 0;
-        float f = 0.f;               // the row's factor of the item at hand
-        const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.ld_out % 16 == 0;
-        // The warp's 32 rows of an item's queries to fp16, in the products' layout: eight lanes hold a row,
-        // scaled by a power of two of its own (see the streaming kernel).  Called when the tile's scores of
-        // the item before are done.
-        auto convert_q = [&](const Walk& w) {
-            ok = mbar_wait(bar(B_QRF), qp, &s_abort, a.st, kSiteQ);
+        // The warp's rows of an item's queries to fp16, when its tile's scores of the item before are done.
+        auto prepare = [&](uint32_t it) {
+            const uint32_t slot = it & 1;
+            ok = mbar_wait(bar(B_QRF + slot), (it >> 1) & 1, &s_abort, a.st, kSiteQ);
             ok = __all_sync(kFull, ok);
             if (!ok) return;
-            qp ^= 1;
-            const float f_all = a.scale * kLog2e * (a.c.k_scale != nullptr ? a.c.k_scale[w.h] : 1.f);
-            const int rows = w.q.n * a.group - w.tile * kRows;
-            const int c = lane & 7;
-            constexpr int H = D / 64;                  // 64-number halves of a row
-#pragma unroll 2
-            for (int i = 0; i < 8; ++i) {
-                const int rl = (warp & 3) * 32 + 4 * i + (lane >> 3), rt = t * kTile + rl;
-                uint4 v[H];
-                uint32_t top2 = 0u;                    // the largest magnitudes, as two bf16
-#pragma unroll
-                for (int k = 0; k < H; ++k) {
-                    v[k] = rt < rows ? *reinterpret_cast<const uint4*>(smem + C::o_qraw + rt * (D * 2) + k * 128 + c * 16) : make_uint4(0u, 0u, 0u, 0u);
-                    top2 = bf2_max_abs(top2, bf2_max_abs(bf2_max_abs(v[k].x, v[k].y), bf2_max_abs(v[k].z, v[k].w)));
-                }
-                float top = fmaxf(__uint_as_float(top2 << 16), __uint_as_float(top2 & 0xffff0000u));
-                top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-                top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
-                int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-                e = (top > 0.f && e < 128) ? max(-100, min(100, 10 - e)) : 0;
-                float up = __int_as_float((e + 127) << 23), fr = f_all * __int_as_float((127 - e) << 23);
-                // the maximum is taken before the factor: it has to be positive
-                if (fr < 0.f) { fr = -fr; up = -up; }
-                if (c == 0) s_f[rt] = fmaxf(fr, 1e-37f);
-#pragma unroll
-                for (int k = 0; k < H; ++k) {
-                    const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-                    uint32_t h[4];
-#pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        h[z] = pack_f16(__uint_as_float(u[z] << 16) * up, __uint_as_float(u[z] & 0xffff0000u) * up);
-                    *reinterpret_cast<uint4*>(smem + C::o_q + t * C::q_tile + k * (kTile * 128) + rl * 128 + ((c ^ (rl & 7)) * 16)) =
-                        make_uint4(h[0], h[1], h[2], h[3]);
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            f = s_f[t * kTile + r_tile];
-            if (lane == 0) {
-                mbar_arrive(bar(B_QF + t));
-                mbar_arrive(bar(B_QRE));
-            }
+            const Item& w = s_item[slot];
+            if (w.kind != kEnd && w.pa < w.pb)
+                convert_queries<D>(smem + C::o_q + slot * C::q_slot, s_f[slot], 4 * warp, 4 * warp + 4, w.n * a.group - w.tile * kRows,
+                                   a.scale * kLog2e * (a.c.k_scale != nullptr ? a.c.k_scale[w.h] : 1.f), lane);
+            if (lane == 0) mbar_arrive(bar(B_QF + slot));
         };
-        {
-            Walk nw = w;
-            while (!nw.end && nw.pa >= nw.pb) nw.next(a, u0, u1);
-            if (!nw.end) convert_q(nw);
-        }
-        // after a wait that ran out (ok = false) the items are walked to the end all the same, without
-        // waiting: the two tiles' warps meet at barriers below
-        while (true) {
-            int x, y;
-            w.half(a, t, x, y);
+        prepare(0);
+        for (uint32_t it = 0; ok; ++it) {
+            const uint32_t slot = it & 1;
+            uint8_t* q = smem + C::o_q + slot * C::q_slot;
+            const Item& w = s_item[slot];
+            if (w.kind == kEnd) break;
+            const int x = w.x[t], y = w.y[t];
             const int r = w.tile * kRows + t * kTile + r_tile;   // row of the (sequence, head)
-            const bool live = r < w.q.n * a.group;
+            const bool live = r < w.n * a.group;
+            const int tok = r / a.group, head = w.h * a.group + r - tok * a.group;
+            const float f = s_f[slot][t * kTile + r_tile];
             float m = -INFINITY, l = 0.f;                        // m in powers of two
             // Outputs of pages n - 1 and n - 2 may both be outstanding (the scores run ahead), so they
             // signal two barriers in turn: the one waited on is never two phases behind.
-            if (w.pa < w.pb && ok) {
+            if (x < y) {
                 // places of the row and of the tile's first and last row, for the pages that need no mask
-                const int p_row = w.q.len - w.q.n + r / a.group;
-                const int rt0 = w.tile * kRows + t * kTile, rt1 = min(w.q.n * a.group, rt0 + kTile) - 1;
-                const int p_first = w.q.len - w.q.n + rt0 / a.group, p_last = w.q.len - w.q.n + rt1 / a.group;
+                const int p_row = w.len - w.n + tok;
+                const int rt0 = w.tile * kRows + t * kTile, rt1 = min(w.n * a.group, rt0 + kTile) - 1;
+                const int p_first = w.len - w.n + rt0 / a.group, p_last = w.len - w.n + rt1 / a.group;
                 const int first_key = a.window > 0 ? p_row - a.window + 1 : 0;
                 float mf = -INFINITY;                            // the maximum in use, before the factor
                 float2 l2 = make_float2(0.f, 0.f);
@@ -724,7 +781,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                         }
                     }
                 };
-                if (x < y && wait_s(n)) {
+                if (wait_s(n)) {
                     load_s(n);
                     tmem_ld_wait();
                     hide(x);
@@ -809,59 +866,69 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                 }
                 l = l2.x + l2.y;
                 m = mf == -INFINITY ? -INFINITY : mf * f;
-                // the queries of the next item, while the last outputs are summed
-                Walk nw = w;
-                do nw.next(a, u0, u1); while (!nw.end && nw.pa >= nw.pb);
-                if (!nw.end && ok) convert_q(nw);
-                if (ok && x < y) {
-                    ok = mbar_wait(bar(B_O + 2 * t + ((n - 1) & 1)), ((n - 1) >> 1) & 1, &s_abort, a.st, kSiteO);
-                    ok = __all_sync(kFull, ok);
-                    tc_fence_after();
-                }
             }
+            if (ok) prepare(it + 1);
+            if (ok && x < y) {
+                ok = mbar_wait(bar(B_O + 2 * t + ((n - 1) & 1)), ((n - 1) >> 1) & 1, &s_abort, a.st, kSiteO);
+                ok = __all_sync(kFull, ok);
+                tc_fence_after();
+            }
+            if (!ok) break;
             // ---- the piece's result ----
-            // (a run that holds only units of the item's own cost has no piece)
-            const bool whole = w.pa == w.lo && w.pb == w.hi && (w.pa < w.pb || w.empty_item(u0));
-            const bool some = whole || w.pa < w.pb;
-            // the runs with pages of the item: b0 (its slot 1) .. b1 (their slots 0)
-            const int b0 = static_cast<int>((w.item + kItemCost) / share), b1 = static_cast<int>((w.item + kItemCost + w.hi - w.lo - 1) / share);
+            // Rows leave through shared memory, so that a warp stores whole rows and not 32 bytes of each of 32
+            // (an item's 64 KB of outputs then take 5000 clocks): the warp's rows of queries are not needed any
+            // more once its tile's last scores are there.
+            uint8_t* stage = q + (t * kTile + (warp & 3) * 32) * (D * 2);
+            auto put = [&](int i, const float (&o)[32], float by) {   // numbers 32 i .. of the lane's row
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * k + 2 * z] * by, o[8 * k + 2 * z + 1] * by);
+                        memcpy(&v[z], &b, 4);
+                    }
+                    *reinterpret_cast<uint4*>(stage + lane * (D * 2) + (((4 * i + k) ^ (lane & 7)) * 16)) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            };
+            auto flush = [&](float m, float l) {
+                const long long at = live ? static_cast<long long>(w.q0 + tok) * a.ld_out + static_cast<long long>(head) * D : -1;
+                constexpr int LR = D / 8, RP = 32 / LR;              // lanes of a row, rows of a pass
+                const int c = lane % LR;
+                __syncwarp();
+#pragma unroll 8
+                for (int k = 0; k < LR; ++k) {
+                    const int row = k * RP + lane / LR;
+                    const uint4 v = *reinterpret_cast<const uint4*>(stage + row * (D * 2) + ((c ^ (row & 7)) * 16));
+                    const long long to = __shfl_sync(kFull, at, row);
+                    if (to >= 0) *reinterpret_cast<uint4*>(a.out + to + c * 8) = v;
+                }
+                if (live && a.lse != nullptr)
+                    a.lse[static_cast<long long>(w.q0 + tok) * a.n_q + head] = l > 0.f || l != l ? m * kLn2f + logf(l) : -INFINITY;
+            };
             const float vs = a.c.v_scale != nullptr ? a.c.v_scale[w.h] : 1.f;
-            float* part = nullptr;
             constexpr int kSlot = kRows * (D + 2);
-            if (!whole) part = a.partial + (static_cast<long long>(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == b0 ? 1 : 0)) * kSlot;
+            const int row = t * kTile + r_tile;
+            auto part = [&](int b) { return a.partial + (static_cast<long long>(b) * 2 + (b == w.b0 ? 1 : 0)) * kSlot; };
             const float inv = l == 0.f ? 0.f : vs / l;
 #pragma unroll 1
-            for (int i = 0; i < (some ? D / 32 : 0); ++i) {
+            for (int i = 0; i < D / 32; ++i) {
                 uint32_t o[32];
-                if (x < y && ok) {
+                if (x < y) {
                     tmem_ld32(tb + C::c_o + 32 * i, o);
                     tmem_ld_wait();
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = 0u;
                 }
-                if (whole) {
-                    if (live) {
-                        __nv_bfloat16* out = a.out + static_cast<long long>(w.q.q0 + r / a.group) * a.ld_out +
-                                             static_cast<long long>(w.h * a.group + r % a.group) * D + 32 * i;
-                        uint32_t v[16];
+                if (w.kind == kWhole) {
+                    float v[32];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-                            memcpy(&v[k], &b, 4);
-                        }
-                        if (out32) {
-                            st_global_32(out, v, 0);
-                            st_global_32(out + 16, v, 8);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                reinterpret_cast<uint4*>(out)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                        }
-                    }
+                    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]);
+                    put(i, v, inv);
                 } else {
                     // columns in fours, rows side by side: a warp's stores are dense
-                    float4* dst = reinterpret_cast<float4*>(part) + (static_cast<long long>(8 * i) * kRows + t * kTile + r_tile);
+                    float4* dst = reinterpret_cast<float4*>(part(blockIdx.x)) + (8 * i * kRows + row);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         __stcg(dst + k * kRows, make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
@@ -869,58 +936,68 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                 }
             }
             tc_fence_before();      // O is read: the next item's products follow through B_P
-            if (whole) {
-                if (live) write_lse(a, w.q, w.h, r, m, l);
-            } else if (some) {
-                __stcg(part + kRows * D + t * kTile + r_tile, m);
-                __stcg(part + kRows * D + kRows + t * kTile + r_tile, l);
-                asm volatile("bar.sync 2, 256;" ::: "memory");
-                if (threadIdx.x == 0) {
+            if (w.kind == kWhole) {
+                flush(m, l);
+            } else {
+                // A warp's rows are joined by the warp that is the last to arrive with them.
+                __stcg(part(blockIdx.x) + kRows * D + row, m);
+                __stcg(part(blockIdx.x) + kRows * D + kRows + row, l);
+                __syncwarp();
+                int* counter = a.counters + w.b0 * 8 + warp;
+                int ticket = 0;
+                if (lane == 0) {
                     __threadfence();
-                    s_ticket = atom_add_acq_rel_gpu(a.counters + b0, 1);
+                    ticket = atom_add_acq_rel_gpu(counter, 1);
+                    if (ticket == w.b1 - w.b0) *counter = 0;
                 }
-                asm volatile("bar.sync 2, 256;" ::: "memory");
-                if (s_ticket == b1 - b0) {
+                ticket = __shfl_sync(kFull, ticket, 0);
+                if (ticket == w.b1 - w.b0) {
                     __threadfence();
-                    if (threadIdx.x == 0) a.counters[b0] = 0;
-                    const int row = t * kTile + r_tile;
-                    auto slot = [&](int b) { return a.partial + (static_cast<long long>(b) * 2 + (b == b0 ? 1 : 0)) * kSlot; };
                     float gm = -INFINITY, gl = 0.f;
-                    for (int b = b0; b <= b1; ++b) gm = fmaxf(gm, __ldcg(slot(b) + kRows * D + row));
-                    for (int b = b0; b <= b1; ++b) {
-                        const float mk = __ldcg(slot(b) + kRows * D + row);
-                        gl += mk == -INFINITY ? 0.f : ex2(mk - gm) * __ldcg(slot(b) + kRows * D + kRows + row);
+                    for (int b = w.b0; b <= w.b1; ++b) gm = fmaxf(gm, __ldcg(part(b) + kRows * D + row));
+                    for (int b = w.b0; b <= w.b1; ++b) {
+                        const float mk = __ldcg(part(b) + kRows * D + row);
+                        gl += mk == -INFINITY ? 0.f : ex2(mk - gm) * __ldcg(part(b) + kRows * D + kRows + row);
                     }
                     const float ginv = gl == 0.f ? 0.f : vs / gl;
-                    // 32 numbers at a time, so that eight loads are in flight
+                    // 32 numbers of a piece at a time, and the next 32 on their way
+                    float4 v[8];
+                    float mk;
+                    auto load = [&](int i, int b) {
+                        mk = __ldcg(part(b) + kRows * D + row);
+                        const float4* src = reinterpret_cast<const float4*>(part(b)) + (8 * i * kRows + row);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + k * kRows);
+                    };
+                    load(0, w.b0);
 #pragma unroll 1
                     for (int i = 0; i < D / 32; ++i) {
-                        float4 o[8];
+                        float o[32];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int b = b0; b <= b1; ++b) {
-                            const float mk = __ldcg(slot(b) + kRows * D + row);
-                            const float4* src = reinterpret_cast<const float4*>(slot(b)) + static_cast<long long>(8 * i) * kRows + row;
-                            float4 v[8];
+                        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+#pragma unroll 1
+                        for (int b = w.b0; b <= w.b1; ++b) {
+                            float4 u[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + k * kRows);
-                            const float ek = mk == -INFINITY ? 0.f : ex2(mk - gm) * ginv;
+                            for (int k = 0; k < 8; ++k) u[k] = v[k];
+                            const float ek = mk == -INFINITY ? 0.f : ex2(mk - gm);
+                            if (b < w.b1) load(i, b + 1);
+                            else if (i + 1 < D / 32) load(i + 1, w.b0);
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
-                                o[k].x = fmaf(ek, v[k].x, o[k].x); o[k].y = fmaf(ek, v[k].y, o[k].y);
-                                o[k].z = fmaf(ek, v[k].z, o[k].z); o[k].w = fmaf(ek, v[k].w, o[k].w);
+                                o[4 * k] = fmaf(ek, u[k].x, o[4 * k]); o[4 * k + 1] = fmaf(ek, u[k].y, o[4 * k + 1]);
+                                o[4 * k + 2] = fmaf(ek, u[k].z, o[4 * k + 2]); o[4 * k + 3] = fmaf(ek, u[k].w, o[4 * k + 3]);
                             }
                         }
-                        if (live) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) write_out4<D>(a, w.q, w.h, r, 32 * i + 4 * k, o[k]);
-                        }
+                        put(i, o, ginv);
                     }
-                    if (live) write_lse(a, w.q, w.h, r, gm, gl);
+                    flush(gm, gl);
                 }
             }
-            w.next(a, u0, u1);
-            if (w.end) break;
+            // the slot's bytes were read and written here; the next copy into them follows
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_QE + slot));
         }
     }
     __syncthreads();

@@ -101,6 +101,27 @@ def test_rows_before_their_sequence():
     _check(np.random.default_rng(5), [3, 0], [6, 40], 8, 2, 128)
 
 
+@pytest.mark.parametrize("window", [0, 30])
+def test_prompt_rows_before_their_sequence(window):
+    """Whole blocks of a prompt's rows that see nothing, before, between and after ones that do."""
+    _check(np.random.default_rng(15), [70, 3, 0, 500], [300, 6, 200, 400], 8, 2, 128, window=window, pad=8, repeat=2)
+
+
+@pytest.mark.parametrize("n_q,n_kv,D,window", [(16, 2, 128, 0), (14, 2, 64, 40)])
+def test_many_short_prompts(n_q, n_kv, D, window):
+    """Several blocks of rows for each CTA, each with a few pages."""
+    rng = np.random.default_rng(16 + window)
+    new = [int(x) for x in rng.integers(1, 90, 120)]
+    _check(rng, [x + int(rng.integers(0, 100)) for x in new], new, n_q, n_kv, D, window=window, repeat=2)
+
+
+@pytest.mark.parametrize("new", [16, 17, 32, 33, 128, 129])
+def test_rows_around_the_kernels_bounds(new):
+    """Rows of a sequence on both sides of what goes to the one kernel or the other, alone and among others."""
+    _check(np.random.default_rng(new), [200], [new], 8, 1, 128)
+    _check(np.random.default_rng(new), [200, 150, 170], [new, 120, 1], 8, 1, 128, max_new=120)
+
+
 def test_non_finite_queries_stay_in_their_rows():
     rng = np.random.default_rng(6)
     for new in (1, 100):
