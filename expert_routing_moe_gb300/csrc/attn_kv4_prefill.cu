@@ -21,8 +21,8 @@
 // fp16's 2^16, and what lies 2^-28 under the largest is lost to its range.
 //
 // The pages of all items form one sequence of units, cut into equal runs for
-// the CTAs; an item that crosses CTAs is joined by the last to arrive,
-// in the order of the pages.
+// the CTAs.  An item of few pages goes whole to one of them; a longer one that
+// crosses CTAs is joined by the last to arrive, in the order of the pages.
 //
 // What bounds it: a page of an item (256 rows x 64 keys, D = 128) takes about
 // 1650 clocks.  The products alone are 1280 (scores with both operands in shared
@@ -61,6 +61,9 @@ constexpr float kGrow = 14.f;
 // short items gets fewer pages.  Costs of 2, 4, 6, 8, 10 took 553, 491, 452, 441, 445 us
 // for a prompt of 8192 tokens and 143, 116, 103, 100, 102 us for chunks behind long contexts.
 constexpr int kItemCost = 8;
+// Pages of an item that is not cut: joining its pieces costs more (5 us; 64 new tokens behind 236 took 32 us
+// with every item cut where a run ends, 20 with limits of 8 to 32).
+constexpr int kUncut = 16;
 
 enum Site : int { kSiteRaw = 31, kSiteRawFree, kSiteKFree, kSiteVFree, kSiteKFull, kSiteVFull, kSiteQ, kSiteP, kSiteS, kSiteO, kSiteQFree };
 
@@ -236,16 +239,23 @@ struct Walk {
     Seq q;
     int lo, hi;        // pages of the item
     int pa, pb;        // those of this run's piece
-    bool end;
-    // A run's piece of the item: a page belongs to the run that holds its unit, and an item without
-    // pages to the run that holds its first unit.
+    bool end, own;     // own: an item that is not cut is this run's
+    // A run's piece of the item: a page belongs to the run that holds its unit, and an item of few pages or
+    // none to the run that holds its middle unit.
     __device__ void piece(const AttnArgs& a, long long u0, long long u1) {
         tile_pages<kRows>(a, q, tile, lo, hi);
+        own = false;
+        if (hi - lo <= kUncut) {
+            const long long mid = item + (kItemCost + hi - lo) / 2;
+            own = mid >= u0 && mid < u1;
+            pa = lo;
+            pb = own ? hi : lo;
+            return;
+        }
         const long long first = item + kItemCost;
         pa = static_cast<int>(min(static_cast<long long>(hi), lo + max(0ll, u0 - first)));
         pb = static_cast<int>(min(static_cast<long long>(hi), lo + max(0ll, u1 - first)));
     }
-    __device__ bool empty_item(long long u0) const { return lo == hi && item >= u0; }
     __device__ void begin(const AttnArgs& a, const Start& st, long long u0, long long u1) {
         s = st.s; h = st.h; tile = st.tile;
         q = load_seq(a, s);
@@ -362,7 +372,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         for (int i = 0; i < kPfWarps; ++i) total += s_warp[i];
         __syncthreads();
     }
-    const long long share = max(static_cast<long long>(kItemCost) + 4, (total + gridDim.x - 1) / gridDim.x);
+    // (no run is shorter than an item's own cost: short items then have a CTA each)
+    const long long share = max(static_cast<long long>(kItemCost), (total + gridDim.x - 1) / gridDim.x);
     const long long u0 = min(total, share * blockIdx.x), u1 = min(total, u0 + share);
     if (u0 >= u1) return;
     // warp 0 finds the sequence, head, tile and page of unit u0
@@ -437,7 +448,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
         while (true) {
             const bool pages = w.pa < w.pb;
             // (a run that holds only units of the item's own cost has no piece)
-            if (pages || w.empty_item(u0)) {
+            if (pages || w.own) {
                 if (!free_slot()) break;
                 Item m;
                 m.q0 = w.q.q0; m.n = w.q.n; m.len = w.q.len;
