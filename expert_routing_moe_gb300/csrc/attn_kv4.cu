@@ -374,13 +374,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv4_stream_kernel(const Attn
     items_before += inc_items - items;
     if (total == 0) return;
     // Few short tiles: one for each CTA, so that none is joined across CTAs.  Else equal runs
-    // of units for the CTAs, at least a page for each warp.  (A batch of one with 333 tokens: 4 tiles of six pages,
-    // each on its own CTA, instead of three runs of eight and a join.)
+    // of units for the CTAs, at least a page for each warp.  (Four heads of keys; batches of 4, 16 and 32 sequences
+    // with 333, 500 and 1000 tokens: 8.3, 8.6, 10.6 us by tiles, 10.6, 11.2, 12.8 by runs; one of 333: 8.3, 8.2.)
     const bool by_item = all_items <= static_cast<int>(gridDim.x) && most <= 2 * kWarps;
-    // Few tiles of one size (a batch of one): as many CTAs for each, so that no CTA has two tiles to join.  (131071
-    // tokens, four tiles: 38 CTAs for each; with runs across tiles the CTAs between two tiles joined both.)
+    // Few tiles of one size (a batch of one or two): as many CTAs for each, so that no CTA has two tiles to join.
+    // (Four tiles of 32, 47, 141, 625, 2048 pages: 10.7, 10.7, 11.6, 15.8, 25.0 us; with runs across tiles 10.1, 11.6,
+    // 12.2, 17.0, 28.3.  16 and 32 tiles of 141 pages: 12.3, 12.7, with runs 12.1, 12.3.)
     const int per_item = static_cast<int>(gridDim.x) / max(1, all_items);
-    const bool even = !by_item && per_item >= 4 && total == static_cast<long long>(most) * all_items;
+    const bool even = !by_item && per_item >= 16 && most > 4 * kWarps && total == static_cast<long long>(most) * all_items;
     const int bid = static_cast<int>(blockIdx.x);
     long long share = 0, u0, u1;
     if (by_item) {

@@ -583,7 +583,9 @@ static cudaError_t launch_rope_t(RopeArgs& a, cudaStream_t s) {
     // heads of a token, four rows a thread group in flight, and what the token
     // needs besides its rows is read and multiplied once (8192 tokens of 40
     // heads, no cache: one warp 29 us, two 33, four 45; two rows in flight 32, eight 32).
-    const bool few = static_cast<long long>(a.T) * heads < 32768;
+    // us of few/many for 256, 512, 1024, 2048 tokens of 32 + 4 + 4 heads: 4.4/4.3 5.8/4.4 9.2/5.0 16.1/6.6, and
+    // with the cache (read back in the same time) 8.5/10.5 11.0/10.9 16.0/11.5 25.5/14.2.
+    const bool few = static_cast<long long>(a.T) * heads < (a.c.pages != nullptr ? 20480 : 9216);
     constexpr int kFew = 128, kMany = 32;
     constexpr int R = sizeof(XT) == 2 ? 4 : 2;
     a.rows = few ? kFew / (D / 16) : heads;
@@ -620,8 +622,9 @@ cudaError_t launch_kv4_read(const moe_kv4_cache& c, const int32_t* q_start, int 
                             moe_dev_status* st, cudaStream_t s) {
     const int ng = kReadThreads / (c.head_dim / 8);
     // Few tokens: a CTA each (and one for every eight heads).  Many: four tokens a CTA, whose
-    // look-ups then run side by side (8192 tokens: 10.3 -> 9.4 us).
-    const bool many = T >= 2048;
+    // look-ups then run side by side.  us of few/many, 4 key heads: 1024 tokens 3.0/4.4, 2048 4.1/4.8, 4096 6.2/5.6,
+    // 8192 10.4/9.3, 16384 18.7/14.4.
+    const bool many = T >= 4096;
     const int tokens = many ? kReadTokens : 1;
     const dim3 grid((T + tokens - 1) / tokens, many ? 1 : (2 * c.n_kv + ng - 1) / ng);
     auto* k = static_cast<__nv_bfloat16*>(k_out);
