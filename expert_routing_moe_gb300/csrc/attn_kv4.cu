@@ -20,6 +20,17 @@
 // cross warps are joined in shared memory and tiles that cross CTAs by the
 // last CTA to arrive, in the order of the pages: nothing waits, and
 // results do not depend on timing.
+//
+// P is rounded to fp16 (2^-11 of each probability, below the bf16 output's
+// rounding); m, l and O are fp32.
+//
+// What bounds it: the bytes of the pages for long contexts, which stream at
+// 6.4 TB/s (one sequence of 131071 tokens, 32 heads on 4: 75.5 MB in 24.8 us,
+// 12 us of it the launch, the search for a CTA's first page and the joins; 32
+// sequences of up to 8192: 18.6 MB in 16.4 us).  For short ones the chain of
+// dependent steps does: 8.5 us for 333 tokens.  fp32 arithmetic or a wider
+// conversion of the codes would take the issue slots that the loads leave: a
+// page costs a warp about 1000 instructions and 42% of the slots are used.
 #include <cuda_bf16.h>
 
 #include "attn_kv4.cuh"
@@ -806,7 +817,7 @@ cudaError_t launch_attention_kv4(const void* q, long long ld_q, int T, int n_q, 
         b.rows_hi = 0x7fffffff;
         uint8_t* ws2 = static_cast<uint8_t*>(ws) + (stream_workspace(c.head_dim) + 255) / 256 * 256;
         b.counters = reinterpret_cast<int*>(ws2);
-        b.partial = reinterpret_cast<float*>(ws2 + kCounterBytes);
+        b.partial = reinterpret_cast<float*>(ws2 + kPromptCounterBytes);
         cudaError_t e = launch_attn_prefill(b, s);
         if (e != cudaSuccess) return e;
     }

@@ -162,6 +162,9 @@ __device__ __forceinline__ void write_lse(const AttnArgs& a, const Seq& s, int h
     a.lse[static_cast<long long>(s.q0 + r / a.group) * a.n_q + h * a.group + r % a.group] = l > 0.f || l != l ? m * kLn2f + logf(l) : -INFINITY;
 }
 
+// Counters of the prompt kernel at the start of its workspace: one for each softmax warp of each CTA.
+constexpr int kPromptMaxCtas = 160;
+constexpr size_t kPromptCounterBytes = kPromptMaxCtas * 8 * 4;
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s);
 size_t attn_prefill_workspace(int D);
 

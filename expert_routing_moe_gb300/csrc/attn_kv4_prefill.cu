@@ -51,8 +51,6 @@ constexpr int kPfThreads = 16 * 32;
 constexpr int kPfWarps = kPfThreads / 32;
 constexpr int kRaw = 3;             // pages in 4 bits in flight
 constexpr int kBuf = 2;             // pages as fp16 operands
-constexpr int kMaxCtasPf = 160;
-constexpr int kCounterBytesPf = kMaxCtasPf * 8 * 4;   // one for each softmax warp of a CTA
 constexpr int kChunk = 256;         // sequences whose units are held in shared memory
 // log2 of the growth that O waits for (8: 565 us for a prompt of 8192 tokens where 11 took 549 and 14 546)
 constexpr float kGrow = 14.f;
@@ -1023,13 +1021,13 @@ cudaError_t launch_pf(const AttnArgs& a, cudaStream_t s) {
     auto* k = attn_kv4_prefill_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Pf<D>::smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k, dim3(min(sm_count(), kMaxCtasPf)), dim3(kPfThreads), Pf<D>::smem, s, a);
+    return launch_pdl(k, dim3(min(sm_count(), kPromptMaxCtas)), dim3(kPfThreads), Pf<D>::smem, s, a);
 }
 
 }  // namespace
 
 size_t attn_prefill_workspace(int D) {
-    return kCounterBytesPf + static_cast<size_t>(kMaxCtasPf) * 2 * kRows * (D + 2) * sizeof(float);
+    return kPromptCounterBytes + static_cast<size_t>(kPromptMaxCtas) * 2 * kRows * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {

@@ -558,12 +558,15 @@ moe_status_t moe_kv4_read(const moe_kv4_cache* cache, const int32_t* q_start, in
  *            a row that sees nothing; may be NULL
  *   workspace  moe_attention_kv4_workspace() bytes, 256-byte aligned, ZERO-FILLED
  *            before its first use (every call leaves its counters at zero);
- *            serves one call at a time
+ *            serves one call at a time.  2.7 MB for D = 128 while
+ *            T * (n_q / n_kv) <= 256, else 45 MB
  * The products run on the tensor cores in fp16 (q scaled by a power of two of
  * its row, the cached numbers exact) with fp32 sums; softmax in fp32, its
  * probabilities rounded to fp16 before the second product.  Results are
- * reproducible bit for bit.  A page outside the pool or a bad q_start is
- * reported (MOE_DEV_BAD_INDEX) and treated as unseen.
+ * reproducible bit for bit.  A page outside the pool, a length beyond the
+ * table or a bad q_start is reported (MOE_DEV_BAD_INDEX) and nothing is read
+ * through it; that sequence's rows of out and lse are then unspecified.
+ * After MOE_DEV_TIMEOUT the workspace has to be zero-filled again.
  * Limits: D is 64 or 128; n_q a multiple of n_kv; S <= 16384.
  */
 moe_status_t moe_attention_kv4(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache* cache,
