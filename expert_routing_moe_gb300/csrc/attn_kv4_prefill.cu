@@ -18,7 +18,7 @@
 // P is fp16: its rounding (2^-11 of each probability) is below that of the bf16
 // output, and sums of it are taken in fp32 before it is rounded.  O is scaled
 // only when a row's maximum grows by more than 2^kGrow: P stays below 2^14 of
-// fp16's 2^16, and what lies 2^-28 under the largest is lost to its range.
+// fp16's 2^16, and a probability of 2^-25 of the maximum in use or less is lost.
 //
 // The pages of all items form one sequence of units, cut into equal runs for
 // the CTAs.  An item of few pages goes whole to one of them; a longer one that
@@ -885,8 +885,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
             if (!ok) break;
             // ---- the piece's result ----
             // Rows leave through shared memory, so that a warp stores whole rows and not 32 bytes of each of 32
-            // (an item's 64 KB of outputs then take 5000 clocks): the warp's rows of queries are not needed any
-            // more once its tile's last scores are there.
+            // (an item's 64 KB of outputs: 5500 clocks, 6700 the other way): the warp's rows of queries are not
+            // needed any more once its tile's last scores are there.
             uint8_t* stage = q + (t * kTile + (warp & 3) * 32) * (D * 2);
             auto put = [&](int i, const float (&o)[32], float by) {   // numbers 32 i .. of the lane's row
 #pragma unroll
