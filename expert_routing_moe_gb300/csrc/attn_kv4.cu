@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv4_stream_kernel(const Attn
     }
 }
 
-constexpr size_t kCounterBytes = 2048;
+static_assert(kMaxCtas * 4 <= kStreamCounterBytes && kCounterBytes % 256 == 0, "places of the counters");
 
 template <int D, int NT>
 cudaError_t launch_stream(const AttnArgs& a, cudaStream_t s) {
@@ -790,7 +790,7 @@ constexpr size_t stream_workspace(int D) {
 size_t attention_kv4_workspace(int T, int n_q, int n_kv, int D) {
     const long long rows = static_cast<long long>(T) * (n_q / n_kv);
     const bool prefill = rows > stream_rows(rows);
-    return (stream_workspace(D) + 255) / 256 * 256 + (prefill ? attn_prefill_workspace(D) : 0);
+    return (stream_workspace(D) + 255) / 256 * 256 + (prefill ? attn_prefill_pieces(D) : 0);
 }
 
 cudaError_t launch_attention_kv4(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache& c,
@@ -815,9 +815,8 @@ cudaError_t launch_attention_kv4(const void* q, long long ld_q, int T, int n_q, 
         AttnArgs b = a;
         b.rows_lo = few + 1;
         b.rows_hi = 0x7fffffff;
-        uint8_t* ws2 = static_cast<uint8_t*>(ws) + (stream_workspace(c.head_dim) + 255) / 256 * 256;
-        b.counters = reinterpret_cast<int*>(ws2);
-        b.partial = reinterpret_cast<float*>(ws2 + kPromptCounterBytes);
+        b.counters = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kStreamCounterBytes);
+        b.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + (stream_workspace(c.head_dim) + 255) / 256 * 256);
         cudaError_t e = launch_attn_prefill(b, s);
         if (e != cudaSuccess) return e;
     }

@@ -162,10 +162,13 @@ __device__ __forceinline__ void write_lse(const AttnArgs& a, const Seq& s, int h
     a.lse[static_cast<long long>(s.q0 + r / a.group) * a.n_q + h * a.group + r % a.group] = l > 0.f || l != l ? m * kLn2f + logf(l) : -INFINITY;
 }
 
-// Counters of the prompt kernel at the start of its workspace: one for each softmax warp of each CTA.
+// Workspace: the counters of both kernels, then the streaming kernel's pieces, then the prompt kernel's.  The counters
+// lie where no call writes pieces, whatever its sizes: so they are zero between any two calls.
 constexpr int kPromptMaxCtas = 160;
-constexpr size_t kPromptCounterBytes = kPromptMaxCtas * 8 * 4;
+constexpr size_t kStreamCounterBytes = 2048;                          // one for each CTA
+constexpr size_t kPromptCounterBytes = kPromptMaxCtas * 8 * 4;        // one for each softmax warp of each CTA
+constexpr size_t kCounterBytes = kStreamCounterBytes + kPromptCounterBytes;
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s);
-size_t attn_prefill_workspace(int D);
+size_t attn_prefill_pieces(int D);
 
 }  // namespace moe

@@ -1026,8 +1026,8 @@ cudaError_t launch_pf(const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t attn_prefill_workspace(int D) {
-    return kPromptCounterBytes + static_cast<size_t>(kPromptMaxCtas) * 2 * kRows * (D + 2) * sizeof(float);
+size_t attn_prefill_pieces(int D) {
+    return static_cast<size_t>(kPromptMaxCtas) * 2 * kRows * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {

@@ -557,8 +557,9 @@ moe_status_t moe_kv4_read(const moe_kv4_cache* cache, const int32_t* q_start, in
  *   lse      [T][n_q] fp32 out: log of the sum of exp(scale * q . k_j), -inf for
  *            a row that sees nothing; may be NULL
  *   workspace  moe_attention_kv4_workspace() bytes, 256-byte aligned, ZERO-FILLED
- *            before its first use (every call leaves its counters at zero);
- *            serves one call at a time.  2.7 MB for D = 128 while
+ *            before its first use (every call leaves its counters at zero, at
+ *            places that no size changes: one buffer serves calls of any
+ *            sizes in turn); serves one call at a time.  2.7 MB for D = 128 while
  *            T * (n_q / n_kv) <= 256, else 45 MB
  * The products run on the tensor cores in fp16 (q scaled by a power of two of
  * its row, the cached numbers exact) with fp32 sums; softmax in fp32, its
