@@ -581,8 +581,7 @@ def _pool_vector(t, pool: Kv4Pool, what: str) -> int:
 
 def moe_kv4_reserve(pool: Kv4Pool, n_new, workspace, st=None, stream=None):
     """Room for n_new [S] int32 more tokens of every sequence (negative: fewer),
-    shared last pages copied first.  workspace: kv4_pool_workspace(pool) bytes,
-    zero-filled before its first use."""
+    shared last pages copied first.  workspace: kv4_pool_workspace(pool) bytes."""
     if _fast is None:
         load()
     rc = _fast.reserve(pool, n_new, workspace, st) if stream is None else None

@@ -24,13 +24,14 @@ constexpr int kHeader = 64;           // words before the lists
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVec = 3;           // 16-byte words in flight of a thread
 
-// Workspace: header (copies), copy list [n_pages], page scratch [2][n_pages].
+// Workspace: header, copy list [n_pages], three words a page.  Every call sets what it reads, so that it does not
+// matter what a call on another pool has left.
 struct PoolWs {
-    int* header;     // [0] copies
+    int* header;     // [0] copies, [1] compact: pages in use
     int2* copies;    // (from, to)
-    int* a;          // reserve: growing sequences that share a page; compact: new numbers
-    int* b;          // reserve: the last of them + 1; compact: free pages
-    int* place;      // reserve: the pages handed out, ascending
+    int* a;          // reserve: growing sequences that share a page
+    int* b;          // reserve: the last of them + 1
+    int* place;      // reserve: the pages handed out, ascending; compact: new numbers
 };
 __host__ __device__ inline PoolWs pool_ws(void* ws, int n_pages) {
     PoolWs w;
@@ -121,10 +122,18 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv4_reserve_plan_kernel(const
             if (id < 0 || id >= p.n_pages) s_bad = s;
         }
         if (part[i] >= 0) {
-            atomicAdd(&w.a[part[i]], 1);
-            atomicMax(&w.b[part[i]], s + 1);
+            __stcg(&w.a[part[i]], 0);
+            __stcg(&w.b[part[i]], 0);
         }
     }
+    __threadfence_block();
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (part[i] >= 0) {
+            atomicAdd(&w.a[part[i]], 1);
+            atomicMax(&w.b[part[i]], s0 + i + 1);
+        }
     __threadfence_block();
     __syncthreads();
     const bool bad = s_bad >= 0;
@@ -188,13 +197,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv4_reserve_plan_kernel(const
             }
         }
     }
-    // the scratch goes back to zero
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        if (part[i] >= 0) {
-            w.a[part[i]] = 0;
-            w.b[part[i]] = 0;
-        }
     if (tid == 0) {
         w.header[0] = go ? static_cast<int>(total.y) : 0;
         if (bad) report(st, MOE_DEV_BAD_INDEX, s_bad);

@@ -606,8 +606,9 @@ typedef struct moe_kv4_pool {
  * are free for the next one.  All or nothing: with too few free pages
  * (MOE_DEV_NO_PAGES), or a length beyond the table or a held page outside the
  * pool (MOE_DEV_BAD_INDEX, detail = sequence), nothing changes.
- *   workspace  moe_kv4_pool_workspace(S, n_pages) bytes, 256-byte aligned, zero-filled
- *            before its first use; serves one call at a time.
+ *   workspace  moe_kv4_pool_workspace(S, n_pages) bytes, 256-byte aligned; holds
+ *            nothing between calls, so one buffer serves pools of any sizes in turn;
+ *            serves one call at a time.
  * Limits: S <= 4096.
  */
 moe_status_t moe_kv4_reserve(const moe_kv4_pool* pool, const int32_t* n_new, void* workspace, size_t ws_bytes,
