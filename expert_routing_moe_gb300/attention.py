@@ -42,9 +42,15 @@ def rope_axes(sections, interleaved: bool = False, device="cuda") -> torch.Tenso
 class KvPages:
     """The 4-bit caches of n_layers layers in pages of 64 tokens, for up to
     max_seqs sequences of up to max_len tokens.  page_table, seq_len and ref
-    are views of one int32 tensor, `book`; snapshot() and restore() copy it, so
-    a step that is only tried (drafts, a beam that may be dropped) is undone
-    by one copy."""
+    are views of one int32 tensor, `book`.
+
+    A step that is only tried (drafts, a beam that may be dropped) begins with
+    snapshot() and ends with restore(), which undoes all of its reserves and
+    assigns, or with release(), which keeps them.  In between the snapshot
+    holds a reference on every page that a sequence has: none of them is handed
+    out, and a sequence that grows into a partly filled one gets a copy, so the
+    pool needs a free page for each of those.  Trials may be nested; the last
+    begun ends first.  Pages cannot be packed during one."""
 
     def __init__(self, n_layers: int, n_pages: int, n_kv: int, head_dim: int, max_seqs: int, max_len: int, device="cuda"):
         cols = -(-max_len // abi.MOE_KV4_PAGE)
@@ -58,6 +64,7 @@ class KvPages:
         self.workspace = torch.zeros(max(abi.kv4_pool_workspace(self.pool), 256), dtype=torch.uint8, device=device)
         self.status = torch.zeros(2, dtype=torch.int32, device=device)
         self.n_live = torch.zeros(1, dtype=torch.int32, device=device)
+        self.trials = []                     # the snapshots that live, first to last
 
     def layer(self, i: int, k_scale=None, v_scale=None) -> abi.Kv4Cache:
         return self.pool.layer(i, k_scale, v_scale)
@@ -72,14 +79,41 @@ class KvPages:
 
     def compact(self, stream=None) -> torch.Tensor:
         """Moves the pages in use to the lowest numbers; their count [1] int32."""
+        if self.trials:
+            raise abi.MoeError("pages are not packed while a snapshot lives: restore or release it first")
         abi.moe_kv4_compact(self.pool, self.n_live, self.workspace, self.status, stream)
         return self.n_live
 
+    def _hold(self, saved: torch.Tensor, count: int):
+        """`count` more references on every page for each entry of the saved table that names it."""
+        n = self.ref.numel()
+        pages = saved[:self.page_table.numel()].long()
+        pages = torch.where((pages >= 0) & (pages < n), pages, n)     # one number more for entries without a page
+        held = torch.zeros(n + 1, dtype=torch.int32, device=saved.device)
+        held.index_add_(0, pages, torch.full_like(saved[:pages.numel()], count))
+        self.ref += held[:n]
+
     def snapshot(self) -> torch.Tensor:
-        return self.book.clone()
+        """Begins a step that is only tried, on the current stream."""
+        saved = self.book.clone()
+        self._hold(saved, 1)
+        self.trials.append(saved)
+        return saved
+
+    def _end(self, saved: torch.Tensor):
+        if not self.trials or self.trials[-1] is not saved:
+            raise abi.MoeError("a snapshot is restored or released once, the last one first")
+        self.trials.pop()
 
     def restore(self, saved: torch.Tensor):
+        """Ends the trial that began with `saved`: every sequence has its tokens of then."""
+        self._end(saved)
         self.book.copy_(saved)
+
+    def release(self, saved: torch.Tensor):
+        """Ends the trial that began with `saved` and keeps what it did."""
+        self._end(saved)
+        self._hold(saved, -1)
 
     def device_status(self):
         code, detail = (int(v) for v in self.status.tolist())
