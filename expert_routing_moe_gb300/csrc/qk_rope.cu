@@ -239,8 +239,14 @@ __global__ void __launch_bounds__(TH) qk_norm_rope_kernel(const RopeArgs a) {
         if (col < a.c.max_pages) page = a.c.page_table[static_cast<long long>(seq) * a.c.max_pages + col];
     }
 
+    // The other token of the values' bytes, if it is new too: codes of places 2 j and 2 j + 1 share them.
+    const bool odd = place & 1;
+    const bool other = place >= 0 && (odd ? place - 1 >= first_new && t > 0 : place + 1 < len && t + 1 < a.T);
+    const int step = odd ? -1 : 1;
+
     // (cos, sin) of the thread's eight pairs
     float cs[8], sn[8];
+    bool off = false, other_off = false;        // a position of this or the other token is outside the table
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         cs[i] = 1.f;
@@ -248,15 +254,18 @@ __global__ void __launch_bounds__(TH) qk_norm_rope_kernel(const RopeArgs a) {
     }
     if (turn) {
         const int half = a.rot / 2;
+        auto position = [&](int ax, int d) {    // of token t + d
+            if (a.positions != nullptr) return ax < a.axes ? a.positions[static_cast<long long>(ax) * a.T + t + d] : -1;
+            return max(place + d, 0);           // negative: a row of a padded batch, not appended
+        };
+        auto inside = [&](int p) { return p >= 0 && p < a.n_pos; };
         auto row_of = [&](int ax) {
-            int p = place;
-            if (a.positions != nullptr) p = ax < a.axes ? a.positions[static_cast<long long>(ax) * a.T + t] : -1;
-            else if (p < 0) p = 0;              // a row of a padded batch: not appended
-            if (p < 0 || p >= a.n_pos) {
-                report(a.st, MOE_DEV_BAD_INDEX, p);
-                p = 0;
-            }
-            return p;
+            if (other && h1 > n_qk && !inside(position(ax, step))) other_off = true;
+            const int p = position(ax, 0);
+            if (inside(p)) return p;
+            report(a.st, MOE_DEV_BAD_INDEX, p);
+            off = true;
+            return 0;
         };
         if (a.axis == nullptr) {
             const float4* src = reinterpret_cast<const float4*>(a.table + static_cast<long long>(row_of(0)) * half + 8 * j);
@@ -279,6 +288,10 @@ __global__ void __launch_bounds__(TH) qk_norm_rope_kernel(const RopeArgs a) {
             }
         }
     }
+
+    // nothing is written of a token with a position outside the table (a warp holds all pairs of its rows)
+    if (__any_sync(kFull, off)) return;
+    other_off = __any_sync(kFull, other_off);
 
     // ---- rows of the plain path: queries, and keys that are not cached ----
     // y_u = inv (u (w_u cos) - v (w_v sin)),  y_v = inv (v (w_v cos) + u (w_u sin)): the products in
@@ -458,11 +471,10 @@ __global__ void __launch_bounds__(TH) qk_norm_rope_kernel(const RopeArgs a) {
         }
         if (!is_v) continue;
         // Codes of two neighbouring tokens share a byte.  The even token's row also writes
-        // the odd one's if that is new too; an odd token whose partner is
-        // older puts its half beside the codes that are there.
-        const bool odd = place & 1;
-        if (odd && place - 1 >= first_new && place - 1 >= 0) continue;
-        const bool partner = !odd && place + 1 < len && t + 1 < a.T;
+        // the odd one's if that is new too; a token whose partner is older, or is
+        // not written, puts its half beside the codes that are there.
+        const bool partner = other && !other_off;
+        if (odd && partner) continue;
         float z[16];
         float rz = 0.f;
         uint32_t sz = 0;
@@ -490,6 +502,10 @@ __global__ void __launch_bounds__(TH) qk_norm_rope_kernel(const RopeArgs a) {
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) c[i / 4] |= f32_to_e2m1x2(__fmul_rn(x[i], ra), __fmul_rn(z[i], rz)) << (8 * (i % 4));
+            if (other && !partner) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[i] |= (i < 2 ? codes0[i] : codes1[i - 2]) & 0xf0f0f0f0u;
+            }
         }
         *reinterpret_cast<uint2*>(codes0) = make_uint2(c[0], c[1]);
         *reinterpret_cast<uint2*>(codes1) = make_uint2(c[2], c[3]);

@@ -524,8 +524,10 @@ typedef struct moe_rope_params {
  * Arithmetic is fp32, rounded once to the outputs' type; the sum of a key's
  * squares is carried in two fp32 words, so that a key's code does not depend
  * on the order of the sum.  A NaN or infinite k or v is stored as zero and
- * reported (MOE_DEV_NONFINITE, detail = row); a position outside the table or
- * a page outside the pool is reported (MOE_DEV_BAD_INDEX) and not written.
+ * reported (MOE_DEV_NONFINITE, detail = row).  A token with a position outside
+ * the table is reported (MOE_DEV_BAD_INDEX, detail = the position, -1 for an
+ * axis that has none) and nothing of it is written, neither outputs nor cache;
+ * a page outside the pool is reported (detail = page) and not written.
  * Limits: D is 64 or 128; n_q >= 0, n_kv >= 1, n_q + 2 n_kv <= 1024.
  */
 moe_status_t moe_qk_norm_rope(const void* qkv, int dtype, long long ld, int T, int n_q, int n_kv, int head_dim,
