@@ -21,8 +21,11 @@
 // last CTA to arrive, in the order of the pages: nothing waits, and
 // results do not depend on timing.
 //
-// P is rounded to fp16 (2^-11 of each probability, below the bf16 output's
-// rounding); m, l and O are fp32.
+// P is rounded to fp16; m, l and O are fp32.  The maximum's P is 2^14, so that
+// fp16 holds 11 bits of probabilities down to 2^-28 of the maximum (each is off by 2^-11
+// of itself, an eighth of the bf16 output's half step) and those below by 2^-39 of
+// the maximum each, which a million of them make 2^-19.  With the maximum at 1
+// and the last bits at 2^-24, 100,000 keys at 2^-25 of the first lost the 0.3% that was theirs.
 //
 // What bounds it: the bytes of the pages for long contexts, which stream at
 // 6.4 TB/s (one sequence of 131071 tokens, 32 heads on 4: 75.5 MB in 24.8 us,
@@ -49,6 +52,8 @@ constexpr int kStages = 2;
 constexpr int kMaxCtas = 160;       // one for each SM
 constexpr int kAhead = 16;          // pieces in flight when a tile's are joined
 constexpr int kSiteKvPage = 21;
+// log2 of the largest P: m is the running maximum less this
+constexpr float kRoom = 14.f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -79,7 +84,7 @@ struct Tile {
     static constexpr int MD = D / 16;     // 16-row tiles of V^T
     uint32_t qf[NT][KS][2];
     float f[NT][2];                       // the scores' factor of row 8 n + 2 t + c, in powers of two
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2];             // m: the scores' maximum less kRoom
     float o[NT][MD][4];
 };
 
@@ -221,7 +226,7 @@ __device__ __forceinline__ void do_page(Tile<D, NT>& w, const AttnArgs& a, const
             top[c] = fmaxf(top[c], __shfl_xor_sync(kFull, top[c], 4));
             top[c] = fmaxf(top[c], __shfl_xor_sync(kFull, top[c], 8));
             top[c] = fmaxf(top[c], __shfl_xor_sync(kFull, top[c], 16));
-            top[c] = fmaxf(top[c], w.m[n][c]);
+            top[c] = fmaxf(top[c] - kRoom, w.m[n][c]);
         }
         if (__any_sync(kFull, top[0] > w.m[n][0] || top[1] > w.m[n][1])) {
 #pragma unroll
@@ -238,15 +243,18 @@ __device__ __forceinline__ void do_page(Tile<D, NT>& w, const AttnArgs& a, const
             }
         }
         const float m0 = w.m[n][0] == -INFINITY ? 0.f : w.m[n][0], m1 = w.m[n][1] == -INFINITY ? 0.f : w.m[n][1];
+        float sum0 = 0.f, sum1 = 0.f;               // of the page first: a large l loses less of small terms
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float& x0 = acc[i >> 1][n][2 * (i & 1)];
             float& x1 = acc[i >> 1][n][2 * (i & 1) + 1];
             x0 = ex2(x0 - m0);
             x1 = ex2(x1 - m1);
-            w.l[n][0] += x0;
-            w.l[n][1] += x1;
+            sum0 += x0;
+            sum1 += x1;
         }
+        w.l[n][0] += sum0;
+        w.l[n][1] += sum1;
     }
 
     // O^T += V^T P^T, 16 tokens at a time

@@ -15,10 +15,11 @@
 // items and copies the next one's queries, which the softmax warps turn to fp16
 // between two items.
 //
-// P is fp16: its rounding (2^-11 of each probability) is below that of the bf16
-// output, and sums of it are taken in fp32 before it is rounded.  O is scaled
-// only when a row's maximum grows by more than 2^kGrow: P stays below 2^14 of
-// fp16's 2^16, and a probability of 2^-25 of the maximum in use or less is lost.
+// P is fp16, and sums of it are taken in fp32 before it is rounded.  O is scaled
+// only when a row's maximum grows by more than 2^kGrow over the one in use, whose P
+// is 2^kRoom: P reaches 2^15 of fp16's 2^16.  A probability down to 2^-20 of the
+// maximum in use is off by 2^-11 of itself (an eighth of the bf16 output's half step),
+// one below by 2^-31 of that maximum: 100,000 of them by 2^-14, a million by 2^-11.
 //
 // The pages of all items form one sequence of units, cut into equal runs for
 // the CTAs.  An item of few pages goes whole to one of them; a longer one that
@@ -31,7 +32,7 @@
 // 700 with the other tile's warp on the same scheduler, store 135) about 1200,
 // and the two meet once a page; an item costs another 11,000 clocks (queries
 // 4000, outputs 5500).  A prompt of 8192 tokens, 32 heads on 4 (550 GFLOP):
-// 441 us, 1247 TFLOP/s.
+// 449 us, 1225 TFLOP/s.
 #include <cuda_bf16.h>
 #include <type_traits>
 
@@ -52,8 +53,13 @@ constexpr int kPfWarps = kPfThreads / 32;
 constexpr int kRaw = 3;             // pages in 4 bits in flight
 constexpr int kBuf = 2;             // pages as fp16 operands
 constexpr int kChunk = 256;         // sequences whose units are held in shared memory
-// log2 of the growth that O waits for (8: 565 us for a prompt of 8192 tokens where 11 took 549 and 14 546)
-constexpr float kGrow = 14.f;
+// log2 of the P of the maximum in use, and of the growth that O waits for: 15 in all.  Room keeps small probabilities, growth saves
+// scalings of O: (0, 14), (5, 10), (6, 9), (7, 8), (10, 5), (12, 3) took 443, 444, 449, 455, 493, 542 us for a prompt of 8192 tokens
+// and 102, 102, 103, 104, 113, 125 us for chunks behind long contexts.  With no room, 100,000 keys at 2^-25 of the first
+// lost the 0.3% of the output that was theirs.
+constexpr float kRoom = 6.f;
+constexpr float kGrow = 9.f;
+static_assert(kRoom + kGrow <= 15.f, "P fits fp16");
 // What an item costs beside its pages (its queries, its outputs, the pipeline's
 // start and end), in pages: the runs are cut by cost, so that a CTA with many
 // short items gets fewer pages.  Costs of 2, 4, 6, 8, 10 took 553, 491, 452, 441, 445 us
@@ -768,6 +774,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                 const int first_key = a.window > 0 ? p_row - a.window + 1 : 0;
                 float mf = -INFINITY;                            // the maximum in use, before the factor
                 float2 l2 = make_float2(0.f, 0.f);
+                auto base_of = [&](float top) { return fmaf(top, f, -kRoom); };
                 uint32_t s0[32], s1[32];                         // a page's scores
                 auto wait_s = [&](uint32_t i) {
                     ok = mbar_wait(bar(B_S + 2 * t + (i & 1)), (i >> 1) & 1, &s_abort, a.st, kSiteS);
@@ -808,7 +815,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                     uint32_t h[32];
                     float2 sum;
                     auto exponentials = [&]() {
-                        const float base = mf == -INFINITY ? 0.f : -mf * f;
+                        const float base = mf == -INFINITY ? 0.f : -base_of(mf);
                         const float2 f2 = make_float2(f, f), b2 = make_float2(base, base);
                         float t0 = -INFINITY, t1 = -INFINITY;
                         sum = make_float2(0.f, 0.f);
@@ -874,7 +881,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                     }
                 }
                 l = l2.x + l2.y;
-                m = mf == -INFINITY ? -INFINITY : mf * f;
+                m = mf == -INFINITY ? -INFINITY : base_of(mf);
             }
             if (ok) prepare(it + 1);
             if (ok && x < y) {
