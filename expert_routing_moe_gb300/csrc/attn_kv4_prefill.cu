@@ -972,8 +972,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_kv4_prefill_kernel(const A
                     float gm = -INFINITY, gl = 0.f;
                     for (int b = w.b0; b <= w.b1; ++b) gm = fmaxf(gm, __ldcg(part(b) + kRows * D + row));
                     for (int b = w.b0; b <= w.b1; ++b) {
-                        const float mk = __ldcg(part(b) + kRows * D + row);
-                        gl += mk == -INFINITY ? 0.f : ex2(mk - gm) * __ldcg(part(b) + kRows * D + kRows + row);
+                        const float mk = __ldcg(part(b) + kRows * D + row), lk = __ldcg(part(b) + kRows * D + kRows + row);
+                        // a piece that has seen nothing has l = 0, or a NaN that stays
+                        gl += mk == -INFINITY ? lk : ex2(mk - gm) * lk;
                     }
                     const float ginv = gl == 0.f ? 0.f : vs / gl;
                     // 32 numbers of a piece at a time, and the next 32 on their way
