@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libmoe_gb300.so")
 FAST = os.path.join(HERE, "_fastcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["abi.cu", "router.cu", "route_dispatch.cu", "dispatch.cu", "dispatch_static.cu", "ffn.cu",
            "ffn_decode.cu", "macs.cu", "calib.cu", "cast.cu", "qk_rope.cu", "attn_kv4.cu", "attn_kv4_prefill.cu", "kv4_pages.cu"]
-HEADERS = ["common.cuh", "launch.h", "routing.cuh", "permute.cuh", "kv4.cuh", "attn_kv4.cuh", "tmap.h", "../../include/moe_gb300.h"]
+HEADERS = ["common.cuh", "launch.h", "routing.cuh", "permute.cuh", "kv4.cuh", "attn_kv4.cuh", "ranges.h", "tmap.h", "../../include/moe_gb300.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

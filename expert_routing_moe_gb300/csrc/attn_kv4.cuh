@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "kv4.cuh"
+#include "ranges.h"
 
 namespace moe {
 
@@ -38,12 +39,11 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int s) {
     Seq r;
     r.q0 = a.q_start[s];
-    r.n = a.q_start[s + 1] - r.q0;
+    const int q1 = a.q_start[s + 1];
     r.len = a.c.seq_len[s];
-    if (r.n < 0 || r.q0 < 0 || r.q0 + r.n > a.T || r.len < 0 || r.len > static_cast<long long>(a.c.max_pages) * kPage) {
-        r.n = 0;
-        r.len = -1;
-    }
+    const bool fit = rows_fit(r.q0, q1, r.len, a.T, a.c.max_pages);
+    r.n = fit ? q1 - r.q0 : 0;
+    if (!fit) r.len = -1;
     return r;
 }
 

@@ -1,0 +1,22 @@
+// ranges.h -- the whole-number rules that keep the attention kernels inside
+// their buffers.  Nothing here needs CUDA, so that a test can run the rules on
+// the host with every overflow trapped.
+#pragma once
+
+#ifdef __CUDACC__
+#define MOE_HOST_DEVICE __host__ __device__ __forceinline__
+#else
+#define MOE_HOST_DEVICE inline
+#endif
+
+namespace moe {
+
+constexpr int kPageTokens = 64;
+
+// Whether rows q0 .. q1-1 of T can be the last ones of a sequence of len
+// tokens whose table has max_pages pages, for any four numbers.
+MOE_HOST_DEVICE bool rows_fit(int q0, int q1, int len, int T, int max_pages) {
+    return 0 <= q0 && q0 <= q1 && q1 <= T && 0 <= len && len <= static_cast<long long>(max_pages) * kPageTokens;
+}
+
+}  // namespace moe

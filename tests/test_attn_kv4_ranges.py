@@ -1,0 +1,41 @@
+"""The whole-number rules of the attention kernels, run on the host with every overflow and division by zero trapped."""
+import os
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "expert_routing_moe_gb300", "csrc")
+PRELUDE = """
+#include <climits>
+#include <cstdio>
+#include <cstdlib>
+#include <initializer_list>
+#include "ranges.h"
+using namespace moe;
+#define CHECK(x) do { if (!(x)) { std::printf("%s fails\\n", #x); std::exit(1); } } while (0)
+"""
+
+
+def _run(tmp_path, body):
+    src, exe = tmp_path / "t.cpp", tmp_path / "t"
+    src.write_text(PRELUDE + "int main() {" + body + "return 0; }\n")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fsanitize-undefined-trap-on-error", "-I", CSRC, str(src), "-o", str(exe)],
+                   check=True, capture_output=True, text=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout or "trapped (%d)" % r.returncode
+
+
+def test_the_traps_work(tmp_path):
+    with pytest.raises(AssertionError, match="trapped"):
+        _run(tmp_path, "volatile int x = INT_MIN; x = x - 5;")
+
+
+def test_rows_of_any_starts(tmp_path):
+    """Starts, lengths and tables of any numbers, the ends of their type among them."""
+    _run(tmp_path, """
+    const int v[] = {INT_MIN, INT_MIN + 1, -100, -1, 0, 1, 5, 63, 64, 100, 101, INT_MAX - 64, INT_MAX - 1, INT_MAX};
+    for (int q0 : v) for (int q1 : v) for (int len : v) for (int T : {0, 1, 100, INT_MAX}) for (int mp : {0, 1, 2, INT_MAX}) {
+        const bool want = q0 >= 0 && q1 >= q0 && q1 <= T && len >= 0 && (long long)len <= 64ll * mp;
+        CHECK(rows_fit(q0, q1, len, T, mp) == want);
+    }
+    """)
