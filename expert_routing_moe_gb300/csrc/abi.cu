@@ -5,6 +5,7 @@
 
 #include "../../include/moe_gb300.h"
 #include "launch.h"
+#include "ranges.h"
 
 namespace {
 
@@ -354,6 +355,7 @@ moe_status_t moe_attention_kv4(const void* q, long long ld_q, int T, int n_q, co
     if (T < 0 || n_q < 1 || n_q % cache->n_kv != 0 || max_new < 0 || window < 0 || q_start == nullptr)
         return MOE_ERR_INVALID_ARG;
     if (!(scale == scale) || scale - scale != 0.f) return MOE_ERR_INVALID_ARG;   // finite
+    if ((window = moe::kernel_window(window, T, cache->max_pages)) < 0) return MOE_ERR_UNSUPPORTED;
     if (n_q > 1024 || static_cast<long long>(T) * (n_q / cache->n_kv) > 0x7ffffff0LL) return MOE_ERR_UNSUPPORTED;
     if (T == 0 || cache->S == 0) return MOE_OK;
     const long long width = static_cast<long long>(n_q) * cache->head_dim;

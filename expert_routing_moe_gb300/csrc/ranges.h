@@ -19,4 +19,12 @@ MOE_HOST_DEVICE bool rows_fit(int q0, int q1, int len, int T, int max_pages) {
     return 0 <= q0 && q0 <= q1 && q1 <= T && 0 <= len && len <= static_cast<long long>(max_pages) * kPageTokens;
 }
 
+// The window that the kernels get for one that a caller gave (0: no window).  One that no table of max_pages pages
+// is longer than hides nothing.  Places start at -T (rows before their sequence), so a place less the window stays
+// above -2^31; -1 for the tables of 2^31 tokens where it would not.
+MOE_HOST_DEVICE int kernel_window(int window, int T, int max_pages) {
+    if (window >= static_cast<long long>(max_pages) * kPageTokens) return 0;
+    return static_cast<long long>(window) + T > 0x7fffffff ? -1 : window;
+}
+
 }  // namespace moe

@@ -39,3 +39,22 @@ def test_rows_of_any_starts(tmp_path):
         CHECK(rows_fit(q0, q1, len, T, mp) == want);
     }
     """)
+
+
+def test_windows_of_any_size(tmp_path):
+    """Rows before their sequence and windows near the largest number among them: what the kernels compute, place - window + 1,
+    neither overflows nor hides what the caller's window shows."""
+    _run(tmp_path, """
+    for (int mp : {0, 1, 2, 40, (1 << 25) - 1, 1 << 25, INT_MAX}) for (int T : {1, 6, 1000, 1 << 20})
+    for (int w : {0, 1, 2, 63, 64, 65, 127, 128, 129, 2560, INT_MAX - 250, INT_MAX - 63, INT_MAX - 1, INT_MAX}) {
+        const int k = kernel_window(w, T, mp);
+        const long long tokens = 64ll * mp;
+        if (k < 0) { CHECK(tokens > w && w + (long long)T > INT_MAX); continue; }
+        for (long long p : {-(long long)T, -1ll, 0ll, 1ll, 62ll, 63ll, 64ll, 200ll, tokens - 1}) {
+            if (p >= tokens || p > INT_MAX) continue;
+            const long long first = w > 0 && p - w + 1 > 0 ? p - w + 1 : 0;
+            const int got = k > 0 && (int)p - k + 1 > 0 ? (int)p - k + 1 : 0;
+            CHECK(got == first);
+        }
+    }
+    """)
