@@ -683,16 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv4_stream_kernel(const Attn
         }
         __syncwarp();                        // the next tile's weights take the same memory
         if (here) continue;
-        // the CTAs that hold pieces of this tile: b0 (slot 1) .. b1 (slots 0); a tile's units are a 32-bit number
-        int b0 = bid - bid % per_item, b1 = b0 + (p.units - 1) / static_cast<int>(share);
-        if (!even) {
-            const unsigned sh = static_cast<unsigned>(share);
-            b0 = p.item >= u0 ? bid : bid - static_cast<int>((static_cast<unsigned>(u0 - p.item) + sh - 1) / sh);
-            b1 = b0 + static_cast<int>((static_cast<unsigned>(p.item - share * b0) + p.units - 1) / sh);
-        }
+        // the CTAs that hold pieces of this tile: the first in its slot 1, the others in their slots 0
+        const CtaRange ctas = tile_ctas(even, bid, per_item, share, u0, p.item, p.units);
         if (g_tid == 0) {
-            s_b0[my_slot] = b0;
-            s_n[my_slot] = b1 - b0 + 1;
+            s_b0[my_slot] = ctas.first;
+            s_n[my_slot] = ctas.last - ctas.first + 1;
             s_piece[my_slot] = p;
         }
     }

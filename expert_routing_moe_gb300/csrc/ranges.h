@@ -27,4 +27,23 @@ MOE_HOST_DEVICE int kernel_window(int window, int T, int max_pages) {
     return static_cast<long long>(window) + T > 0x7fffffff ? -1 : window;
 }
 
+// The CTAs that hold pieces of a tile of `units` units, the first being unit `item`, as CTA bid, which holds one of
+// them and starts with unit u0, finds them.  even: each tile has per_item CTAs with `share` units each; else CTA b holds units b *
+// share on, whatever tile they belong to, and per_item may be 0.  A tile's units are a 32-bit number.
+struct CtaRange {
+    int first, last;
+};
+MOE_HOST_DEVICE CtaRange tile_ctas(bool even, int bid, int per_item, long long share, long long u0, long long item, int units) {
+    CtaRange r;
+    if (even) {
+        r.first = bid - bid % per_item;
+        r.last = r.first + (units - 1) / static_cast<int>(share);
+    } else {
+        const unsigned sh = static_cast<unsigned>(share);
+        r.first = item >= u0 ? bid : bid - static_cast<int>((static_cast<unsigned>(u0 - item) + sh - 1) / sh);
+        r.last = r.first + static_cast<int>((static_cast<unsigned>(item - share * r.first) + units - 1) / sh);
+    }
+    return r;
+}
+
 }  // namespace moe

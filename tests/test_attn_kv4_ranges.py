@@ -58,3 +58,36 @@ def test_windows_of_any_size(tmp_path):
         }
     }
     """)
+
+
+def test_ctas_of_a_tile(tmp_path):
+    """Every CTA that holds a piece of a tile finds the same ones, with more tiles than CTAs (no CTA for each) among the cases."""
+    _run(tmp_path, """
+    unsigned x = 1;
+    for (int round = 0; round < 3000; ++round) {
+        const int grid = 152, tiles = 1 + (x = x * 1664525u + 1013904223u) / 65536 % 400, most = 1 + (x = x * 1664525u + 1013904223u) / 65536 % 300;
+        long long total = 0, begin[400], units[400];
+        for (int i = 0; i < tiles; ++i) { begin[i] = total; total += units[i] = 1 + (x = x * 1664525u + 1013904223u) / 65536 % most; }
+        long long share = (total + grid - 1) / grid;
+        if (share < 8) share = 8;
+        for (int i = 0; i < tiles; ++i) {
+            const int b0 = begin[i] / share, b1 = (begin[i] + units[i] - 1) / share;
+            for (int b = b0; b <= b1; ++b) {
+                const CtaRange r = tile_ctas(false, b, grid / tiles, share, share * b, begin[i], units[i]);
+                CHECK(r.first == b0 && r.last == b1);
+            }
+        }
+        const int per_item = grid / tiles;
+        if (per_item < 16) continue;
+        share = (most + per_item - 1) / per_item;
+        if (share < 8) share = 8;
+        for (int i = 0; i < tiles; ++i)
+            for (int j = 0; j * share < most; ++j) {
+                const CtaRange r = tile_ctas(true, i * per_item + j, per_item, share, (long long)i * most + j * share, (long long)i * most, most);
+                CHECK(r.first == i * per_item && r.last == i * per_item + (most - 1) / share && r.last < (i + 1) * per_item);
+            }
+    }
+    // far into a long sequence of units
+    const CtaRange r = tile_ctas(false, 100, 0, 3000000000ll / 152, 3000000000ll / 152 * 100, 3000000000ll / 152 * 99 + 5, 40000000);
+    CHECK(r.first == 99 && r.last == 101);
+    """)
