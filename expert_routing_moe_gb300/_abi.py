@@ -8,6 +8,7 @@ is no other implementation to fall back to.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -565,7 +566,9 @@ def moe_attention_kv4(q, cache: Kv4Cache, q_start, out, scale: float, max_new: i
         raise MoeError("lse: expected [%d][%d]" % (T, n_q))
     if workspace is None:
         n = attention_kv4_workspace(T, n_q, cache.n_kv, D)
-        workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
+        # cleared, used and given back in the order of the call's own stream
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
     rc = load().moe_attention_kv4(qp, ld_q, T, n_q, cache._ref, _check_starts(q_start, cache.S), max_new, scale, window,
                                   op, ld_o, _addr(lse, torch.float32, "lse"), _addr(workspace, None, "workspace"),
                                   workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
