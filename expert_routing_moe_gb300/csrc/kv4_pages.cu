@@ -27,11 +27,11 @@ constexpr int kCopyVec = 3;           // 16-byte words in flight of a thread
 // Workspace: header, copy list [n_pages], three words a page.  Every call sets what it reads, so that it does not
 // matter what a call on another pool has left.
 struct PoolWs {
-    int* header;     // [0] copies, [1] compact: pages in use
+    int* header;     // [0] copies
     int2* copies;    // (from, to)
     int* a;          // reserve: growing sequences that share a page
     int* b;          // reserve: the last of them + 1
-    int* place;      // reserve: the pages handed out, ascending; compact: new numbers
+    int* place;      // reserve: the pages handed out, ascending; compact: new numbers, -1 for a page not in use
 };
 __host__ __device__ inline PoolWs pool_ws(void* ws, int n_pages) {
     PoolWs w;
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv4_compact_plan_kernel(const
         const bool live = p.ref[g] != 0;
         if (live && g >= n) w.copies[x++].x = g;
         if (!live && g < n) w.copies[y++].y = g;
+        if (!live || g < n) w.place[g] = live ? g : -1;   // the list's are set below
     }
     __threadfence_block();
     __syncthreads();
@@ -310,24 +311,22 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv4_compact_plan_kernel(const
     }
     if (tid == 0) {
         w.header[0] = static_cast<int>(total.x);
-        w.header[1] = n;
         if (n_live != nullptr) *n_live = n;
     }
 }
 
-__global__ void __launch_bounds__(kCopyThreads) kv4_compact_kernel(const moe_kv4_pool p, void* ws) {
+__global__ void __launch_bounds__(kCopyThreads) kv4_compact_kernel(const moe_kv4_pool p, void* ws, moe_dev_status* st) {
     pdl_wait();
     pdl_trigger();
     const PoolWs w = pool_ws(ws, p.n_pages);
-    const int n = w.header[1];
     const long long entries = static_cast<long long>(p.S) * p.max_pages;
     for (long long i = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x; i < entries;
          i += static_cast<long long>(gridDim.x) * kCopyThreads) {
         const int g = p.page_table[i];
-        if (g < n || g >= p.n_pages) continue;
-        // a live page from n on is in the list; an entry that names a free page (no valid table has one) stays
-        const int to = w.place[g];
-        if (to >= 0 && to < n) p.page_table[i] = to;
+        if (g == -1) continue;
+        const int to = g >= 0 && g < p.n_pages ? w.place[g] : -1;
+        if (to < 0) report(st, MOE_DEV_BAD_INDEX, g);     // no page in use: the entry stays
+        else if (to != g) p.page_table[i] = to;
     }
     copy_pages(p, w);
 }
@@ -353,10 +352,10 @@ cudaError_t launch_kv4_assign(const moe_kv4_pool& p, const int32_t* parent, moe_
     return launch_pdl(kv4_assign_kernel, dim3((p.max_pages + kAssignCols - 1) / kAssignCols), dim3(kAssignThreads), smem, s, p, parent, st);
 }
 
-cudaError_t launch_kv4_compact(const moe_kv4_pool& p, int32_t* n_live, void* ws, moe_dev_status*, cudaStream_t s) {
+cudaError_t launch_kv4_compact(const moe_kv4_pool& p, int32_t* n_live, void* ws, moe_dev_status* st, cudaStream_t s) {
     cudaError_t e = launch_pdl(kv4_compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p, n_live, ws);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv4_compact_kernel, dim3(8 * sm_count()), dim3(kCopyThreads), 0, s, p, ws);
+    return launch_pdl(kv4_compact_kernel, dim3(8 * sm_count()), dim3(kCopyThreads), 0, s, p, ws, st);
 }
 
 }  // namespace moe

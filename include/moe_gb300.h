@@ -628,8 +628,12 @@ moe_status_t moe_kv4_assign(const moe_kv4_pool* pool, const int32_t* parent, moe
 
 /*
  * Packs the pool: with n pages in use, those numbered n and above move, in
- * ascending order, to the free pages below n, in every layer; tables and
- * references follow.  n_live [1] out (may be NULL): n.
+ * ascending order, to the free pages below n, in every layer: the k-th of them
+ * to the k-th free one.  Tables and references follow (a caller that holds
+ * pages of its own finds their new numbers by that rule from the references
+ * before the call).  A table entry other than -1 that names no page in use is
+ * reported (MOE_DEV_BAD_INDEX, detail = entry) and stays.
+ * n_live [1] out (may be NULL): n.
  *   workspace  as for moe_kv4_reserve.
  */
 moe_status_t moe_kv4_compact(const moe_kv4_pool* pool, int32_t* n_live, void* workspace, size_t ws_bytes,
