@@ -365,6 +365,13 @@ def _addr(t: Optional[torch.Tensor], dtype=None, what: str = "") -> Optional[int
     raise MoeError("%s: expected a dense tensor" % what)
 
 
+def _status(st: Optional[torch.Tensor]) -> Optional[int]:
+    """A device status's address: two int32 numbers."""
+    if st is not None and st.numel() < 2:
+        raise MoeError("status: expected 2 numbers, got %d" % st.numel())
+    return _addr(st, torch.int32, "status")
+
+
 def _rows(t: torch.Tensor, T: int, width: int, dtype, what: str):
     """(address, leading dimension) of T rows of `width` numbers whose trailing
     dimensions are dense; only the first may have a stride of its own."""
@@ -516,7 +523,7 @@ def moe_qk_norm_rope(qkv, n_q: int, n_kv: int, q_out, k_out=None, q_weight=None,
                                  _addr(k_weight, f32, "k_weight"), eps, None if rope is None else rope._ref, q, ld_q, k,
                                  ld_k, None if cache is None else cache._ref,
                                  None if cache is None else _check_starts(q_start, cache.S),
-                                 _addr(st, torch.int32, "st"), _raw_stream(stream, qkv))
+                                 _status(st), _raw_stream(stream, qkv))
     _check(rc, "moe_qk_norm_rope")
 
 
@@ -538,7 +545,7 @@ def moe_kv4_read(cache: Kv4Cache, q_start, k_out=None, v_out=None, st=None, stre
             T = t.shape[0]
     bf = torch.bfloat16
     rc = load().moe_kv4_read(cache._ref, _check_starts(q_start, cache.S), T, _addr(k_out, bf, "k_out"),
-                             _addr(v_out, bf, "v_out"), _addr(st, torch.int32, "st"), _raw_stream(stream, q_start))
+                             _addr(v_out, bf, "v_out"), _status(st), _raw_stream(stream, q_start))
     _check(rc, "moe_kv4_read")
 
 
@@ -571,7 +578,7 @@ def moe_attention_kv4(q, cache: Kv4Cache, q_start, out, scale: float, max_new: i
             workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
     rc = load().moe_attention_kv4(qp, ld_q, T, n_q, cache._ref, _check_starts(q_start, cache.S), max_new, scale, window,
                                   op, ld_o, _addr(lse, torch.float32, "lse"), _addr(workspace, None, "workspace"),
-                                  workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
+                                  workspace.numel() * workspace.element_size(), _status(st),
                                   _raw_stream(stream, q))
     _check(rc, "moe_attention_kv4")
 
@@ -593,7 +600,7 @@ def moe_kv4_reserve(pool: Kv4Pool, n_new, workspace, st=None, stream=None):
     if rc is not None:
         _check(rc, "moe_kv4_reserve")
     rc = load().moe_kv4_reserve(pool._ref, _pool_vector(n_new, pool, "n_new"), _addr(workspace, None, "workspace"),
-                                workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
+                                workspace.numel() * workspace.element_size(), _status(st),
                                 _raw_stream(stream, n_new))
     _check(rc, "moe_kv4_reserve")
 
@@ -608,7 +615,7 @@ def moe_kv4_assign(pool: Kv4Pool, parent, st=None, stream=None):
         return
     if rc is not None:
         _check(rc, "moe_kv4_assign")
-    rc = load().moe_kv4_assign(pool._ref, _pool_vector(parent, pool, "parent"), _addr(st, torch.int32, "st"),
+    rc = load().moe_kv4_assign(pool._ref, _pool_vector(parent, pool, "parent"), _status(st),
                                _raw_stream(stream, parent))
     _check(rc, "moe_kv4_assign")
 
@@ -624,6 +631,6 @@ def moe_kv4_compact(pool: Kv4Pool, n_live, workspace, st=None, stream=None):
     if rc is not None:
         _check(rc, "moe_kv4_compact")
     rc = load().moe_kv4_compact(pool._ref, _addr(n_live, torch.int32, "n_live"), _addr(workspace, None, "workspace"),
-                                workspace.numel() * workspace.element_size(), _addr(st, torch.int32, "st"),
+                                workspace.numel() * workspace.element_size(), _status(st),
                                 _raw_stream(stream, workspace))
     _check(rc, "moe_kv4_compact")

@@ -70,6 +70,12 @@ static int dense(PyObject* t, PyObject* dtype, long long n, void** out) {
     return address(t, out);
 }
 
+/* A device status: two numbers, or NULL for None. */
+static int status(PyObject* t, void** out) {
+    long long n;
+    return dense(t, t_i32, -1, out) && (t == Py_None || (method_int(t, s_numel, &n) && n >= 2));
+}
+
 /* Rows of numbers whose trailing dimensions are dense: address, rows, numbers of a row, leading dimension. */
 static int rows(PyObject* t, PyObject* dtype, void** out, long long* n_rows, long long* width, long long* ld) {
     int ok = 0;
@@ -154,7 +160,7 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) 
         else if (!as_longlong(rt, &rope_T) || rope_T != T) return decline();
     }
     if (cache != NULL && (!attr_int(a[9], s_S, &S) || a[10] == Py_None || !dense(a[10], t_i32, S + 1, &qs))) return decline();
-    if (!dense(a[11], t_i32, -1, &st) || !current_stream(a[0], &stream)) return decline();
+    if (!status(a[11], &st) || !current_stream(a[0], &stream)) return decline();
     return PyLong_FromLong(p_rope(x, bf ? MOE_DTYPE_BF16 : MOE_DTYPE_F32, ld, (int)T, (int)n_q, (int)n_kv, (int)D, qw, kw, (float)eps, rope,
                                   q, ld_q, k, ld_k, cache, qs, st, stream));
 }
@@ -173,7 +179,7 @@ static PyObject* kv4_read(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         if (!rows(a[2 + i], t_bf16, &out[i], &Tt, &w, &ld) || w != kv * D || (Tt > 1 && ld != w) || (T >= 0 && T != Tt)) return decline();
         T = Tt;
     }
-    if (T < 0 || !fits_int(T) || !dense(a[4], t_i32, -1, &st) || !current_stream(a[1], &stream)) return decline();
+    if (T < 0 || !fits_int(T) || !status(a[4], &st) || !current_stream(a[1], &stream)) return decline();
     return PyLong_FromLong(p_read(cache, qs, (int)T, out[0], out[1], st, stream));
 }
 
@@ -192,7 +198,7 @@ static PyObject* attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     n_q = w / D;
     if (a[2] == Py_None || !dense(a[2], t_i32, S + 1, &qs) || !dense(a[7], t_f32, T * n_q, &lse)) return decline();
     if (a[8] == Py_None || !dense(a[8], t_u8, -1, &ws) || !method_int(a[8], s_numel, &bytes)) return decline();
-    if (!dense(a[9], t_i32, -1, &st) || !current_stream(a[0], &stream)) return decline();
+    if (!status(a[9], &st) || !current_stream(a[0], &stream)) return decline();
     return PyLong_FromLong(p_attention(q, ld, (int)T, (int)n_q, cache, qs, (int)max_new, (float)scale, (int)window, out, ldo, lse, ws,
                                        (size_t)bytes, st, stream));
 }
@@ -205,7 +211,7 @@ static PyObject* pool_call(PyObject* const* a, Py_ssize_t n, int which) {
     if (!dense(a[1], t_i32, which == 2 ? -1 : S, &v)) return decline();
     if (which != 1 && (a[2] == Py_None || !dense(a[2], t_u8, -1, &ws) || !method_int(a[2], s_numel, &bytes))) return decline();
     if (which != 2 && a[1] == Py_None) return decline();
-    if (!dense(a[3], t_i32, -1, &st) || !current_stream(which == 2 ? a[2] : a[1], &stream)) return decline();
+    if (!status(a[3], &st) || !current_stream(which == 2 ? a[2] : a[1], &stream)) return decline();
     if (which == 0) return PyLong_FromLong(p_reserve(pool, v, ws, (size_t)bytes, st, stream));
     if (which == 1) return PyLong_FromLong(p_assign(pool, v, st, stream));
     return PyLong_FromLong(p_compact(pool, v, ws, (size_t)bytes, st, stream));
