@@ -11,6 +11,7 @@
 
 namespace moe {
 
+static_assert(kPageTokens == MOE_KV4_PAGE, "ranges.h has the page's size");
 constexpr float kLog2e = 0x1.715476p+0f;
 constexpr float kLn2f = 0x1.62e430p-1f;
 

@@ -9,6 +9,7 @@
 // the plan of reserve 7 us with the launch of the copies.
 #include "common.cuh"
 #include "launch.h"
+#include "ranges.h"
 #include "tmap.h"
 
 namespace moe {
@@ -67,8 +68,6 @@ __device__ __forceinline__ Sum2 scan2(Sum2 v, Sum2& total, Sum2* s_warp) {
     }
     return {before.x + inc.x - v.x, before.y + inc.y - v.y};
 }
-
-__device__ __forceinline__ int pages_of(int len) { return (len + MOE_KV4_PAGE - 1) / MOE_KV4_PAGE; }
 
 // One CTA.  Thread i takes sequences [i * per, (i+1) * per).  What bounds it is
 // the chain of loads (length, last page, sharers, references): each is done

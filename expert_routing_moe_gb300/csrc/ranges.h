@@ -1,5 +1,5 @@
-// ranges.h -- the whole-number rules that keep the attention kernels inside
-// their buffers.  Nothing here needs CUDA, so that a test can run the rules on
+// ranges.h -- the whole-number rules that keep the attention kernels and the
+// pool's inside their buffers.  Nothing here needs CUDA, so that a test can run the rules on
 // the host with every overflow trapped.
 #pragma once
 
@@ -11,7 +11,10 @@
 
 namespace moe {
 
-constexpr int kPageTokens = 64;
+constexpr int kPageTokens = 64;   // MOE_KV4_PAGE
+
+// Pages of a sequence of len >= 0 tokens, up to the largest number.
+MOE_HOST_DEVICE int pages_of(int len) { return len / kPageTokens + (len % kPageTokens != 0); }
 
 // Whether rows q0 .. q1-1 of T can be the last ones of a sequence of len
 // tokens whose table has max_pages pages, for any four numbers.

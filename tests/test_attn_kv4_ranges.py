@@ -1,4 +1,4 @@
-"""The whole-number rules of the attention kernels, run on the host with every overflow and division by zero trapped."""
+"""The whole-number rules of the attention kernels and the pool's, run on the host with every overflow and division by zero trapped."""
 import os
 import subprocess
 
@@ -28,6 +28,12 @@ def _run(tmp_path, body):
 def test_the_traps_work(tmp_path):
     with pytest.raises(AssertionError, match="trapped"):
         _run(tmp_path, "volatile int x = INT_MIN; x = x - 5;")
+
+
+def test_pages_of_any_length(tmp_path):
+    _run(tmp_path, """
+    for (int len : {0, 1, 63, 64, 65, 1 << 20, INT_MAX - 64, INT_MAX - 63, INT_MAX - 62, INT_MAX}) CHECK(pages_of(len) == (len + 63ll) / 64);
+    """)
 
 
 def test_rows_of_any_starts(tmp_path):
