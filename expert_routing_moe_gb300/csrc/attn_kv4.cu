@@ -27,11 +27,12 @@
 // the maximum each, which a million of them make 2^-19.  With the maximum at 1
 // and the last bits at 2^-24, 100,000 keys at 2^-25 of the first lost the 0.3% that was theirs.
 //
-// What bounds it: the bytes of the pages for long contexts, which stream at
-// 6.4 TB/s (one sequence of 131071 tokens, 32 heads on 4: 75.5 MB in 24.8 us,
-// 12 us of it the launch, the search for a CTA's first page and the joins; 32
-// sequences of up to 8192: 18.6 MB in 16.4 us).  For short ones the chain of
-// dependent steps does: 8.5 us for 333 tokens.  fp32 arithmetic or a wider
+// What bounds it: a warp's pages one after the other and, for short contexts, the
+// chain of dependent steps.  Above 131071 tokens of one sequence (32 heads on 4,
+// other inputs from call to call) another page costs what 6.1 TB/s take, 0.91 of a copy: 26.9,
+// 39.6, 52.4, 89.9 us for 131071, 262144, 400000 and 800000 tokens; some 14 us are the launch, the
+// search for a CTA's first page, the first pages and the joins.  32 sequences of up to 8192
+// (18.6 MB) take 15.8 us, 333 tokens 7.9 us.  fp32 arithmetic or a wider
 // conversion of the codes would take the issue slots that the loads leave: a
 // page costs a warp about 1000 instructions and 42% of the slots are used.
 #include <cuda_bf16.h>

@@ -6,9 +6,9 @@
 // x^2 + eps) of its head, then the rotation of its pair.  The pass has to
 // read the rows once and write q once (the cache takes 4.5 bits a number).  For
 // single tokens the chain of loads (row, position, table) bounds it.  For 8192
-// tokens of 32 + 4 heads without a cache it moves 151 MB in 29.1 us (5.2 TB/s, 0.77
+// tokens of 32 + 4 heads without a cache it moves 151 MB in 30.2 us (5.0 TB/s, 0.75
 // of a copy's rate); with the cache, whose codes cost a third of the
-// instructions, 156 MB in 40.6 us (3.8 TB/s).
+// instructions, 156 MB in 40.5 us (3.9 TB/s; 42.1 with three axes).
 //
 // D/16 threads hold one head's row, sixteen numbers each: the eight pairs
 // 8j..8j+7, i.e. two runs of eight numbers (pairs i, i + rot/2) or one run of

@@ -570,7 +570,8 @@ moe_status_t moe_kv4_read(const moe_kv4_cache* cache, const int32_t* q_start, in
  * table or a bad q_start is reported (MOE_DEV_BAD_INDEX) and nothing is read
  * through it; that sequence's rows of out and lse are then unspecified.
  * After MOE_DEV_TIMEOUT the workspace has to be zero-filled again.
- * Limits: D is 64 or 128; n_q a multiple of n_kv; S <= 16384; window + T below
+ * Rows of no sequence are not written.
+ * Limits: D is 64 or 128; n_q <= 1024, a multiple of n_kv; S <= 16384; window + T below
  * 2^31 where a table is longer than the window.
  */
 moe_status_t moe_attention_kv4(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache* cache,
