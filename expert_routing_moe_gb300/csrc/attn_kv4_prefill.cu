@@ -32,7 +32,7 @@
 // 700 with the other tile's warp on the same scheduler, store 135) about 1200,
 // and the two meet once a page; an item costs another 11,000 clocks (queries
 // 4000, outputs 5500).  A prompt of 8192 tokens, 32 heads on 4 (550 GFLOP):
-// 441-449 us from box to box, 1225-1247 TFLOP/s.
+// 441-449 us from card to card, 1225-1247 TFLOP/s.
 #include <cuda_bf16.h>
 #include <type_traits>
 
