@@ -65,7 +65,7 @@ def draw(rng):
     op = rng.choice(["linear", "linear", "verify", "weigh", "weigh", "evict"])
     if op == "linear":
         t = _spread(rng, 1, 2000)
-        k = _spread(rng, 100, 8000)
+        k = 64 * _spread(rng, 2, 125) if rng.random() < 0.8 else _spread(rng, 100, 8000)
         n = _spread(rng, 100, min(128000, 260_000_000 // k, 20_000_000_000 // (k * t)))
         out = rng.choice(["bf16", "f32"])
         return {"op": op, "t": t, "n": n, "k": k, "out": out, "bias": rng.random() < 0.4, "add": out == "f32" and rng.random() < 0.5}
@@ -190,7 +190,8 @@ def _lut(dev):
 # Weights [n][k] lie in tiles of 128 rows and 128 columns, 9216 bytes each, [tiles of rows][tiles of columns]: the codes of
 # row r, column 32 c + i at byte (r/8)*512 + c*128 + ((r%8) ^ (2c))*16 + i/8*4, where eight codes share a word, the even ones of
 # them in its lower half; then the scales of row r, block b at 8192 + r*8 + b.  What lies beyond n or k is zero.
-_WORD = (0, 2, 4, 6, 1, 3, 5, 7)
+# Bits of a half, of the codes (sign, three bits of magnitude) j = 0 .. 3 in it:
+_BITS = ((15, 8, 7, 6), (12, 5, 4, 3), (9, 2, 1, 0), (14, 13, 11, 10))
 
 
 def _pack_weights(codes, scales):
@@ -199,8 +200,13 @@ def _pack_weights(codes, scales):
     dev = codes.device
     full = torch.zeros(nt * TILE, kt * TILE, dtype=torch.uint8, device=dev)
     full[:n, :k] = codes
-    full = full.view(nt, 16, 8, kt, 4, 4, 8)[..., list(_WORD)]
-    full = (full[..., 0::2] | (full[..., 1::2] << 4)).flatten(-2).permute(0, 3, 1, 4, 2, 5)      # [nt][kt][16][c][8][16 bytes]
+    full = full.view(nt, 16, 8, kt, 4, 4, 4, 2)                                                  # ..., word, j, half
+    low, high = torch.zeros_like(full[..., 0, :]), torch.zeros_like(full[..., 0, :])             # bytes of a half
+    for j, bits in enumerate(_BITS):
+        for i, to in enumerate(bits):
+            bit = (full[..., j, :] >> (3 - i)) & 1
+            low, high = (low, high | (bit << (to - 8))) if to >= 8 else (low | (bit << to), high)
+    full = torch.stack([low, high], -1).flatten(-3).permute(0, 3, 1, 4, 2, 5)                    # [nt][kt][16][c][8][16 bytes]
     place = torch.arange(8, device=dev) ^ (2 * torch.arange(4, device=dev)[:, None])             # [c][place] -> row
     full = torch.gather(full, 4, place[:, :, None].expand(nt, kt, 16, 4, 8, 16))
     s = torch.zeros(nt * TILE, kt * 8, dtype=torch.uint8, device=dev)
@@ -215,8 +221,14 @@ def _unpack_weights(tiles, n, k):
     dev = tiles.device
     place = torch.arange(8, device=dev) ^ (2 * torch.arange(4, device=dev)[:, None])             # [c][row] -> place, its own inverse
     b = torch.gather(tiles[..., :8192].reshape(nt, kt, 16, 4, 8, 16), 4, place[:, :, None].expand(nt, kt, 16, 4, 8, 16))
-    b = b.reshape(nt, kt, 16, 4, 8, 4, 4)
-    b = torch.stack([b & 15, b >> 4], -1).flatten(-2)[..., [0, 4, 1, 5, 2, 6, 3, 7]]
+    b = b.reshape(nt, kt, 16, 4, 8, 4, 2, 2)                                                     # ..., word, half, byte
+    codes = []
+    for bits in _BITS:
+        c = torch.zeros_like(b[..., 0])
+        for i, to in enumerate(bits):
+            c |= ((b[..., to // 8] >> (to % 8)) & 1) << (3 - i)
+        codes.append(c)
+    b = torch.stack(codes, -2).flatten(-2)                                                       # j, half -> eight codes
     b = b.permute(0, 2, 4, 1, 3, 5, 6).reshape(nt * TILE, kt * TILE)[:n, :k]
     s = tiles[..., 8192:].reshape(nt, kt, TILE, 8).permute(0, 2, 1, 3).reshape(nt * TILE, kt * 8).contiguous()
     s = s.view(torch.float8_e4m3fn).float().repeat_interleave(BLOCK, -1)[:n, :k]
@@ -618,9 +630,10 @@ def exact(case, seed):
             tile = s["tiles"].reshape(-1)
             base = ((r // TILE) * s["tiles"].shape[1] + col // TILE) * 9216
             c, i, q = col % TILE // 32, col % 32, r % TILE
-            half = i % 8 // 2 + 4 * (i % 2)           # place of the code among the eight of its word
-            byte = tile[base + q // 8 * 512 + c * 128 + ((q % 8) ^ (2 * c)) * 16 + i // 8 * 4 + half // 2]
-            code = (byte.int() >> (4 * (half % 2)).int()) & 15
+            byte = base + q // 8 * 512 + c * 128 + ((q % 8) ^ (2 * c)) * 16 + i // 8 * 4 + i % 2 * 2
+            half = tile[byte].int() + 256 * tile[byte + 1].int()
+            at = torch.tensor(_BITS, device=dev).int()[i % 8 // 2]                              # [k][4]
+            code = sum(((half >> at[:, b]) & 1) << (3 - b) for b in range(4))
             scale = tile[base + 8192 + q * 8 + col % TILE // BLOCK].contiguous().view(torch.float8_e4m3fn).double()
             y[:, r0:r0 + r.shape[0]] = x @ (value[code] * scale * s["row_scale"][r0:r0 + r.shape[0], None].double()).t()
         if case["bias"]:
