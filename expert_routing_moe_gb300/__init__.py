@@ -10,6 +10,8 @@ from ._abi import (MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_FFN_FUSE_COMBINE, MOE_FFN_
 from ._abi import (MOE_KV4_PAGE, Kv4Cache, Kv4Pool, Rope, attention_kv4_workspace, kv4_page_bytes, kv4_pool_workspace,
                    moe_attention_kv4, moe_kv4_assign, moe_kv4_compact, moe_kv4_read, moe_kv4_reserve,
                    moe_qk_norm_rope)
+from ._abi import (Weight4, kv4_evict_workspace, kv4_weigh_workspace, moe_kv4_evict, moe_kv4_weigh, moe_linear_w4, moe_verify_drafts,
+                   moe_w4_pack, verify_workspace, w4_bytes)
 from .attention import AttentionLayer, KvPages, rope_axes, rope_table
 from .layer import MoELayer
 
@@ -18,4 +20,6 @@ __all__ = ["MoELayer", "SereParams", "MoeError", "load", "moe_route", "moe_route
            "MOE_DTYPE_BF16", "MOE_DTYPE_F32", "MOE_FFN_FUSE_COMBINE", "MOE_FFN_ZERO_Y", "MOE_OP_CALIBRATE", "MOE_OP_DISPATCH", "MOE_OP_FFN", "MOE_OP_ROUTE_DISPATCH", "MOE_ROUTE_FROM_LOGITS",
            "MOE_ROUTE_RENORM_TOPK",
            "AttentionLayer", "KvPages", "rope_axes", "rope_table", "Kv4Cache", "Kv4Pool", "Rope", "MOE_KV4_PAGE", "attention_kv4_workspace", "kv4_page_bytes", "kv4_pool_workspace",
-           "moe_attention_kv4", "moe_kv4_assign", "moe_kv4_compact", "moe_kv4_read", "moe_kv4_reserve", "moe_qk_norm_rope"]
+           "moe_attention_kv4", "moe_kv4_assign", "moe_kv4_compact", "moe_kv4_read", "moe_kv4_reserve", "moe_qk_norm_rope",
+           "Weight4", "kv4_evict_workspace", "kv4_weigh_workspace", "moe_kv4_evict", "moe_kv4_weigh", "moe_linear_w4", "moe_verify_drafts", "moe_w4_pack",
+           "verify_workspace", "w4_bytes"]

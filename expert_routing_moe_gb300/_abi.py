@@ -66,10 +66,16 @@ class _Kv4PoolParams(ctypes.Structure):
                 ("S", ctypes.c_int32)]
 
 
+class _W4Params(ctypes.Structure):
+    _fields_ = [("tiles", ctypes.c_void_p), ("row_scale", ctypes.c_void_p), ("N", ctypes.c_int32), ("K", ctypes.c_int32)]
+
+
 EXPORTS = ["moe_route", "moe_route_dispatch", "moe_decode_layer", "moe_reroute_sere", "moe_dispatch_capacity", "moe_ffn_grouped", "moe_combine",
            "moe_residual_to_bf16", "moe_token_weights", "moe_similarity_calibrate", "moe_workspace_size", "moe_status_string",
            "moe_qk_norm_rope", "moe_attention_kv4", "moe_attention_kv4_workspace", "moe_kv4_read", "moe_kv4_reserve",
-           "moe_kv4_assign", "moe_kv4_compact", "moe_kv4_page_bytes", "moe_kv4_pool_workspace"]
+           "moe_kv4_assign", "moe_kv4_compact", "moe_kv4_page_bytes", "moe_kv4_pool_workspace", "moe_kv4_weigh",
+           "moe_kv4_weigh_workspace", "moe_kv4_evict", "moe_kv4_evict_workspace", "moe_w4_bytes", "moe_w4_pack", "moe_linear_w4",
+           "moe_verify_drafts", "moe_verify_workspace"]
 
 
 def load(path: str = LIB_PATH):
@@ -132,6 +138,24 @@ def load(path: str = LIB_PATH):
             L.moe_kv4_compact.restype = i
             L.moe_kv4_pool_workspace.argtypes = [i, i]
             L.moe_kv4_pool_workspace.restype = sz
+            L.moe_kv4_weigh.argtypes = [p, ll, i, i, p, p, i, p, f, i, i, p, ll, i, p, sz, p, p]
+            L.moe_kv4_weigh.restype = i
+            L.moe_kv4_weigh_workspace.argtypes = [i, i, i, i, i, i]
+            L.moe_kv4_weigh_workspace.restype = sz
+            L.moe_kv4_evict.argtypes = [p, i, p, ll, p, i, i, p, ll, p, sz, p, p]
+            L.moe_kv4_evict.restype = i
+            L.moe_kv4_evict_workspace.argtypes = [i, i, i]
+            L.moe_kv4_evict_workspace.restype = sz
+            L.moe_w4_bytes.argtypes = [i, i]
+            L.moe_w4_bytes.restype = sz
+            L.moe_w4_pack.argtypes = [p, i, ll, p, p, p]
+            L.moe_w4_pack.restype = i
+            L.moe_linear_w4.argtypes = [p, ll, i, p, p, p, i, ll, i, p]
+            L.moe_linear_w4.restype = i
+            L.moe_verify_drafts.argtypes = [p, i, ll, i, i, p, p, p, i, p, ll, p, p, p, p, p, sz, p, p]
+            L.moe_verify_drafts.restype = i
+            L.moe_verify_workspace.argtypes = [i, i, i]
+            L.moe_verify_workspace.restype = sz
             _load_fastcall(L)
             _lib = L
     return _lib
@@ -634,3 +658,168 @@ def moe_kv4_compact(pool: Kv4Pool, n_live, workspace, st=None, stream=None):
                                 workspace.numel() * workspace.element_size(), _status(st),
                                 _raw_stream(stream, workspace))
     _check(rc, "moe_kv4_compact")
+
+
+# ---------------------------------------------------------------------------
+# Eviction from the cache by the attention that its tokens draw
+# ---------------------------------------------------------------------------
+def kv4_weigh_workspace(cache: Kv4Cache, T: int, n_q: int) -> int:
+    return int(load().moe_kv4_weigh_workspace(cache.S, T, n_q, cache.n_kv, cache.head_dim, cache._c.max_pages))
+
+
+def kv4_evict_workspace(pool: Kv4Pool) -> int:
+    return int(load().moe_kv4_evict_workspace(pool.S, pool._c.max_pages, pool.n_pages))
+
+
+def _scores(score, S: int, max_pages: int):
+    """(address, leading dimension) of one fp32 score for every place of the tables."""
+    if score.dim() != 2 or score.shape[0] != S or score.shape[1] < max_pages * MOE_KV4_PAGE:
+        raise MoeError("score: expected [%d][%d or more], got %s" % (S, max_pages * MOE_KV4_PAGE, list(score.shape)))
+    return _rows(score, S, score.shape[1], torch.float32, "score")
+
+
+def _bytes(workspace: Optional[torch.Tensor]) -> int:
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def moe_kv4_weigh(q, cache: Kv4Cache, q_start, lse, score, scale: float, max_new: int, window: int = 0, last: int = 0,
+                  fresh: bool = False, workspace=None, st=None, stream=None):
+    """Adds the attention weight that every cached token draws from the rows
+    (those of moe_attention_kv4, with its lse [T][n_q] fp32) to score [S][max_pages * 64
+    or more] fp32: only of each sequence's last `last` rows where that is not 0.  fresh: the
+    entries of the rows' own tokens are set instead.  workspace:
+    kv4_weigh_workspace(...) bytes, zero-filled before its first use; when omitted a buffer
+    is allocated for this call (not graph-capturable)."""
+    D = cache.head_dim
+    if q.dim() != 3 or q.shape[2] != D:
+        raise MoeError("q: expected [T][n_q][%d], got %s" % (D, list(q.shape)))
+    T, n_q = q.shape[0], q.shape[1]
+    qp, ld_q = _rows(q, T, n_q * D, torch.bfloat16, "q")
+    if lse.numel() != T * n_q:
+        raise MoeError("lse: expected [%d][%d]" % (T, n_q))
+    sp, ld_s = _scores(score, cache.S, cache._c.max_pages)
+    if workspace is None:
+        n = kv4_weigh_workspace(cache, T, n_q)
+        if n:
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                workspace = torch.zeros(n, dtype=torch.uint8, device=q.device)
+    rc = load().moe_kv4_weigh(qp, ld_q, T, n_q, cache._ref, _check_starts(q_start, cache.S), max_new, _addr(lse, torch.float32, "lse"),
+                              scale, window, last, sp, ld_s, 1 if fresh else 0, _addr(workspace, None, "workspace"), _bytes(workspace),
+                              _status(st), _raw_stream(stream, q))
+    _check(rc, "moe_kv4_weigh")
+
+
+def moe_kv4_evict(pool: Kv4Pool, score, budget, sinks: int, recent: int, workspace, kept=None, st=None, stream=None):
+    """Every sequence with more than budget[s] tokens (budget [S] int32, negative: all stay)
+    keeps its first `sinks`, its last `recent` and the best others by score [S][max_pages *
+    64 or more] fp32, moved to its front in every layer with their scores; the pages behind are
+    released.  kept [S][any] int32 out (or None): the place that each token had, -1 behind.
+    workspace: kv4_evict_workspace(pool) bytes."""
+    sp, ld_s = _scores(score, pool.S, pool._c.max_pages)
+    kp, ld_k = None, 0
+    if kept is not None:
+        if kept.dim() != 2 or kept.shape[0] != pool.S:
+            raise MoeError("kept: expected [%d][any], got %s" % (pool.S, list(kept.shape)))
+        kp, ld_k = _addr(kept, torch.int32, "kept"), kept.shape[1]
+    rc = load().moe_kv4_evict(pool._ref, pool.head_dim, sp, ld_s, _pool_vector(budget, pool, "budget"), sinks, recent, kp, ld_k,
+                              _addr(workspace, None, "workspace"), _bytes(workspace), _status(st), _raw_stream(stream, budget))
+    _check(rc, "moe_kv4_evict")
+
+
+# ---------------------------------------------------------------------------
+# Products with weights in 4 bits
+# ---------------------------------------------------------------------------
+def w4_bytes(N: int, K: int) -> int:
+    """Bytes of the tiles of [N][K] weights in 4 bits."""
+    return int(load().moe_w4_bytes(N, K))
+
+
+class Weight4:
+    """Weights [N][K] in 4 bits (moe_w4): tiles uint8 in the layout of the header, of
+    w4_bytes(N, K) in all, and row_scale [N] fp32 (None: 1).  Holds the tensors."""
+
+    def __init__(self, tiles, N: int, K: int, row_scale=None):
+        want = -(-N // 128) * -(-K // 128) * 9216
+        if N < 1 or K < 1 or tiles.numel() != want:
+            raise MoeError("tiles: expected %d bytes for [%d][%d], got %d" % (want, N, K, tiles.numel()))
+        if row_scale is not None and row_scale.numel() != N:
+            raise MoeError("row_scale: expected %d numbers, got %d" % (N, row_scale.numel()))
+        self.tensors, self.N, self.K = (tiles, row_scale), N, K
+        self._c = _W4Params(_addr(tiles, torch.uint8, "tiles"), _addr(row_scale, torch.float32, "row_scale"), N, K)
+        self._ref = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, N: int, K: int, device="cuda") -> "Weight4":
+        """Room for weights that moe_w4_pack writes."""
+        tiles = torch.empty(-(-N // 128), -(-K // 128), 9216, dtype=torch.uint8, device=device)
+        return cls(tiles, N, K, torch.empty(N, dtype=torch.float32, device=device))
+
+    @classmethod
+    def pack(cls, w, st=None, stream=None) -> "Weight4":
+        """w [N][K] bf16 or fp32, rounded to 4 bits."""
+        out = cls.empty(w.shape[0], w.shape[1], w.device)
+        moe_w4_pack(w, out, st, stream)
+        return out
+
+
+def moe_w4_pack(w, out: Weight4, st=None, stream=None):
+    """Rounds w [N][K] bf16 or fp32 (rows may be strided) to 4 bits, with a scale for
+    each row and each 16 columns, into `out`."""
+    code = _dtype_code(w)
+    wp, ld = _rows(w, out.N, out.K, w.dtype, "w")
+    rc = load().moe_w4_pack(wp, code, ld, out._ref, _status(st), _raw_stream(stream, w))
+    _check(rc, "moe_w4_pack")
+
+
+def moe_linear_w4(x, w: Weight4, y, bias=None, accumulate: bool = False, stream=None):
+    """y [T][N] = x [T][K] w^T + bias: x bf16, y bf16 or fp32, bias [N] fp32 or None; rows
+    may be strided.  accumulate: added to y (fp32)."""
+    T = x.shape[0]
+    xp, ld_x = _rows(x, T, w.K, torch.bfloat16, "x")
+    code = _dtype_code(y)
+    yp, ld_y = _rows(y, T, w.N, y.dtype, "y")
+    if bias is not None and bias.numel() != w.N:
+        raise MoeError("bias: expected %d numbers, got %d" % (w.N, bias.numel()))
+    if accumulate and code != MOE_DTYPE_F32:
+        raise MoeError("y: only fp32 is added to")
+    rc = load().moe_linear_w4(xp, ld_x, T, w._ref, _addr(bias, torch.float32, "bias"), yp, code, ld_y, 1 if accumulate else 0,
+                              _raw_stream(stream, x))
+    _check(rc, "moe_linear_w4")
+
+
+# ---------------------------------------------------------------------------
+# Verification of drafted tokens
+# ---------------------------------------------------------------------------
+def verify_workspace(T: int, S: int, V: int) -> int:
+    return int(load().moe_verify_workspace(T, S, V))
+
+
+def moe_verify_drafts(logits, tokens, uniform, q_start, accepted, next_token, n_new=None, draft_logits=None, temperature=None,
+                      workspace=None, st=None, stream=None):
+    """How many drafted tokens the target accepts, and the token that follows.  Rows
+    q_start[s] .. q_start[s+1]-1 are a sequence's newest token and its drafts: logits
+    [T][V] bf16 or fp32 of the target, draft_logits like them (None: drafts without a
+    distribution), tokens [T] int32, uniform [T] fp32 from [0, 1), temperature [S] fp32
+    (None: 1; 0: greedy).  Out, [S] int32: accepted drafts, the token that follows, and n_new =
+    accepted - drafts, which moe_kv4_reserve takes to cut the refused ones.  workspace:
+    verify_workspace(...) bytes; when omitted a buffer is allocated for this call."""
+    if logits.dim() != 2:
+        raise MoeError("logits: expected [T][V], got %s" % list(logits.shape))
+    T, V = logits.shape
+    code = _dtype_code(logits)
+    lp, ld = _rows(logits, T, V, logits.dtype, "logits")
+    dp, ld_d = (None, 0) if draft_logits is None else _rows(draft_logits, T, V, logits.dtype, "draft_logits")
+    S = accepted.numel()
+    i32, f32 = torch.int32, torch.float32
+    for t, n, what in ((tokens, T, "tokens"), (uniform, T, "uniform"), (next_token, S, "next_token"), (n_new, S, "n_new"),
+                       (temperature, S, "temperature")):
+        if t is not None and t.numel() != n:
+            raise MoeError("%s: expected %d numbers, got %d" % (what, n, t.numel()))
+    if workspace is None:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = torch.empty(max(verify_workspace(T, S, V), 256), dtype=torch.uint8, device=logits.device)
+    rc = load().moe_verify_drafts(lp, code, ld, T, V, _addr(tokens, i32, "tokens"), _addr(uniform, f32, "uniform"),
+                                  _check_starts(q_start, S), S, dp, ld_d, _addr(temperature, f32, "temperature"),
+                                  _addr(accepted, i32, "accepted"), _addr(next_token, i32, "next_token"), _addr(n_new, i32, "n_new"),
+                                  _addr(workspace, None, "workspace"), _bytes(workspace), _status(st), _raw_stream(stream, logits))
+    _check(rc, "moe_verify_drafts")

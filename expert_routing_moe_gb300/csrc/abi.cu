@@ -40,6 +40,12 @@ moe_status_t check_pool(const moe_kv4_pool* p) {
     return MOE_OK;
 }
 
+moe_status_t check_w4(const moe_w4* w) {
+    if (w == nullptr || w->N < 1 || w->K < 1 || w->tiles == nullptr || !aligned16(w->tiles)) return MOE_ERR_INVALID_ARG;
+    if (w->N > (1 << 24) || w->K > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -400,13 +406,114 @@ moe_status_t moe_kv4_compact(const moe_kv4_pool* pool, int32_t* n_live, void* wo
     return from_cuda(moe::launch_kv4_compact(*pool, n_live, workspace, st, as_stream(stream)));
 }
 
+size_t moe_kv4_weigh_workspace(int S, int T, int n_q, int n_kv, int head_dim, int max_pages) {
+    if (S < 0 || T < 0 || n_kv < 1 || n_q < 1 || n_q % n_kv != 0 || max_pages < 0 || (head_dim != 64 && head_dim != 128)) return 0;
+    return moe::kv4_weigh_workspace(S, T, n_q, n_kv, head_dim, max_pages);
+}
+
+moe_status_t moe_kv4_weigh(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache* cache, const int32_t* q_start, int max_new,
+                           const float* lse, float scale, int window, int last, float* score, long long ld_score, int fresh,
+                           void* workspace, size_t ws_bytes, moe_dev_status* st, void* stream) {
+    const moe_status_t rc = check_cache(cache);
+    if (rc != MOE_OK) return rc;
+    if (T < 0 || n_q < 1 || n_q % cache->n_kv != 0 || max_new < 0 || window < 0 || last < 0 || q_start == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!(scale == scale) || scale - scale != 0.f) return MOE_ERR_INVALID_ARG;   // finite
+    if ((window = moe::kernel_window(window, T, cache->max_pages)) < 0) return MOE_ERR_UNSUPPORTED;
+    if (n_q > 1024 || static_cast<long long>(T) * (n_q / cache->n_kv) > 0x7ffffff0LL) return MOE_ERR_UNSUPPORTED;
+    if (static_cast<long long>(cache->max_pages) * MOE_KV4_PAGE > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+    if (T == 0 || cache->S == 0) return MOE_OK;
+    const long long width = static_cast<long long>(n_q) * cache->head_dim;
+    if (q == nullptr || !aligned16(q) || ld_q < width || ld_q % 8 != 0) return MOE_ERR_INVALID_ARG;
+    if (lse == nullptr || score == nullptr || ld_score < static_cast<long long>(cache->max_pages) * MOE_KV4_PAGE) return MOE_ERR_INVALID_ARG;
+    const size_t need = moe::kv4_weigh_workspace(cache->S, T, n_q, cache->n_kv, cache->head_dim, cache->max_pages);
+    if (need > 0 && (workspace == nullptr || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+    if (need > 0 && !aligned256(workspace)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_kv4_weigh(q, ld_q, T, n_q, *cache, q_start, max_new, lse, scale, window, last, score, ld_score, fresh != 0,
+                                           workspace, st, as_stream(stream)));
+}
+
+size_t moe_kv4_evict_workspace(int S, int max_pages, int n_pages) {
+    if (S < 0 || max_pages < 0 || n_pages < 0) return 0;
+    return moe::kv4_evict_workspace(S, max_pages, n_pages);
+}
+
+moe_status_t moe_kv4_evict(const moe_kv4_pool* pool, int head_dim, float* score, long long ld_score, const int32_t* budget, int sinks,
+                           int recent, int32_t* kept, long long ld_kept, void* workspace, size_t ws_bytes, moe_dev_status* st, void* stream) {
+    const moe_status_t rc = check_pool(pool);
+    if (rc != MOE_OK) return rc;
+    if (head_dim != 64 && head_dim != 128) return MOE_ERR_UNSUPPORTED;
+    const long long head_bytes = MOE_KV4_PAGE * (head_dim + head_dim / 8);
+    if (pool->page_bytes % head_bytes != 0) return MOE_ERR_INVALID_ARG;
+    if (sinks < 0 || recent < 0) return MOE_ERR_INVALID_ARG;
+    if (static_cast<long long>(pool->max_pages) * MOE_KV4_PAGE > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+    if (pool->S == 0) return MOE_OK;
+    if (score == nullptr || budget == nullptr || ld_score < static_cast<long long>(pool->max_pages) * MOE_KV4_PAGE) return MOE_ERR_INVALID_ARG;
+    if (kept != nullptr && ld_kept < 0) return MOE_ERR_INVALID_ARG;
+    if (workspace == nullptr || ws_bytes < moe::kv4_evict_workspace(pool->S, pool->max_pages, pool->n_pages)) return MOE_ERR_WORKSPACE;
+    if (!aligned256(workspace)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_kv4_evict(*pool, head_dim, static_cast<int>(pool->page_bytes / head_bytes), score, ld_score, budget, sinks,
+                                           recent, kept, ld_kept, workspace, st, as_stream(stream)));
+}
+
+size_t moe_w4_bytes(int N, int K) {
+    if (N < 1 || K < 1) return 0;
+    return static_cast<size_t>((N + 127ll) / 128) * static_cast<size_t>((K + 127ll) / 128) * 9216;
+}
+
+moe_status_t moe_w4_pack(const void* w, int dtype, long long ld, const moe_w4* out, moe_dev_status* st, void* stream) {
+    if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+    const moe_status_t rc = check_w4(out);
+    if (rc != MOE_OK) return rc;
+    if (w == nullptr || ld < out->K || out->row_scale == nullptr) return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_w4_pack(w, dtype, ld, out->N, out->K, out->tiles, out->row_scale, st, as_stream(stream)));
+}
+
+moe_status_t moe_linear_w4(const void* x, long long ld_x, int T, const moe_w4* w, const float* bias, void* y, int y_dtype, long long ld_y,
+                           int add, void* stream) {
+    if (T < 0 || (y_dtype != MOE_DTYPE_F32 && y_dtype != MOE_DTYPE_BF16)) return MOE_ERR_INVALID_ARG;
+    if (add != 0 && y_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+    const moe_status_t rc = check_w4(w);
+    if (rc != MOE_OK) return rc;
+    if (T > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (x == nullptr || y == nullptr || ld_x < w->K || ld_y < w->N) return MOE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(x) & 1u) != 0 || (reinterpret_cast<uintptr_t>(y) & (y_dtype == MOE_DTYPE_BF16 ? 1u : 3u)) != 0)
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_linear_w4(x, ld_x, T, *w, bias, y, y_dtype, ld_y, add != 0, as_stream(stream)));
+}
+
+size_t moe_verify_workspace(int T, int S, int V) {
+    if (T < 0 || S < 0 || V < 1) return 0;
+    return moe::verify_workspace(T);
+}
+
+moe_status_t moe_verify_drafts(const void* logits, int dtype, long long ld, int T, int V, const int32_t* tokens, const float* uniform,
+                               const int32_t* q_start, int S, const void* draft_logits, long long ld_draft, const float* temperature,
+                               int32_t* accepted, int32_t* next, int32_t* n_new, void* workspace, size_t ws_bytes, moe_dev_status* st,
+                               void* stream) {
+    if (T < 0 || S < 0 || V < 1 || (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16)) return MOE_ERR_INVALID_ARG;
+    if (T > moe::kVerifyMaxT || V > moe::kVerifyMaxV || S > moe::kVerifyMaxSeqs) return MOE_ERR_UNSUPPORTED;
+    if (S == 0) return MOE_OK;
+    if (q_start == nullptr || accepted == nullptr || next == nullptr) return MOE_ERR_INVALID_ARG;
+    const uintptr_t part = dtype == MOE_DTYPE_BF16 ? 1u : 3u;
+    if (T > 0) {
+        if (logits == nullptr || tokens == nullptr || uniform == nullptr || ld < V || (reinterpret_cast<uintptr_t>(logits) & part) != 0)
+            return MOE_ERR_INVALID_ARG;
+        if (draft_logits != nullptr && (ld_draft < V || (reinterpret_cast<uintptr_t>(draft_logits) & part) != 0)) return MOE_ERR_INVALID_ARG;
+        if (workspace == nullptr || ws_bytes < moe::verify_workspace(T)) return MOE_ERR_WORKSPACE;
+        if (!aligned256(workspace)) return MOE_ERR_INVALID_ARG;
+    }
+    return from_cuda(moe::launch_verify(logits, dtype, ld, T, V, tokens, uniform, q_start, S, draft_logits, ld_draft, temperature, accepted,
+                                        next, n_new, workspace, st, as_stream(stream)));
+}
+
 const char* moe_status_string(int code, int device) {
     if (device) {
         switch (code) {
             case MOE_DEV_OK: return "ok";
-            case MOE_DEV_NONFINITE: return "non-finite router logit, token weight, key or value";
+            case MOE_DEV_NONFINITE: return "non-finite logit, token weight, key, value, weight or temperature";
             case MOE_DEV_TIMEOUT: return "on-chip wait timed out";
-            case MOE_DEV_BAD_INDEX: return "expert id, row index, position or page out of range";
+            case MOE_DEV_BAD_INDEX: return "expert id, row index, position, page, token, length or budget out of range";
             case MOE_DEV_NO_PAGES: return "too few free pages";
             default: return "unknown device status";
         }

@@ -140,6 +140,27 @@ cudaError_t launch_kv4_reserve(const moe_kv4_pool& p, const int32_t* n_new, void
 cudaError_t launch_kv4_assign(const moe_kv4_pool& p, const int32_t* parent, moe_dev_status* st, cudaStream_t s);
 cudaError_t launch_kv4_compact(const moe_kv4_pool& p, int32_t* n_live, void* ws, moe_dev_status* st, cudaStream_t s);
 
+// ---- eviction from the 4-bit cache (kv4_weigh.cu, kv4_evict.cu) ----
+size_t kv4_weigh_workspace(int S, int T, int n_q, int n_kv, int D, int max_pages);
+cudaError_t launch_kv4_weigh(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache& c, const int32_t* q_start, int max_new,
+                             const float* lse, float scale, int window, int last, float* score, long long ld_score, bool fresh, void* ws,
+                             moe_dev_status* st, cudaStream_t s);
+size_t kv4_evict_workspace(int S, int max_pages, int n_pages);
+cudaError_t launch_kv4_evict(const moe_kv4_pool& p, int head_dim, int n_kv, float* score, long long ld_score, const int32_t* budget, int sinks,
+                             int recent, int32_t* kept, long long ld_kept, void* ws, moe_dev_status* st, cudaStream_t s);
+
+// ---- products with weights in 4 bits (linear_w4.cu) ----
+cudaError_t launch_linear_w4(const void* x, long long ld_x, int T, const moe_w4& w, const float* bias, void* y, int y_dtype, long long ld_y,
+                             bool add, cudaStream_t s);
+cudaError_t launch_w4_pack(const void* w, int dtype, long long ld, int N, int K, void* tiles, float* row_scale, moe_dev_status* st, cudaStream_t s);
+
+// ---- verification of drafted tokens (verify.cu) ----
+constexpr int kVerifyMaxT = 1 << 16, kVerifyMaxV = 1 << 20, kVerifyMaxSeqs = 16384;
+size_t verify_workspace(int T);
+cudaError_t launch_verify(const void* logits, int dtype, long long ld, int T, int V, const int32_t* tokens, const float* uniform,
+                          const int32_t* q_start, int S, const void* draft, long long ld_draft, const float* temperature, int32_t* accepted,
+                          int32_t* next, int32_t* n_new, void* ws, moe_dev_status* st, cudaStream_t s);
+
 cudaError_t launch_combine(const float* rows_out, const int32_t* slot_row, const float* slot_gate, int T, int H,
                            int k, float* y, cudaStream_t s);
 

@@ -1,0 +1,266 @@
+// linear_w4.cu -- products with weights in 4 bits, and their packing.
+//
+//   y[t][n] = r[n] * sum_k x[t][k] c[n][k] s[n][k/16]  (+ bias[n]) (+ y[t][n])
+//
+// c * s has at most six significant bits, so it is exact in bf16, and so are the
+// products of the tensor cores; sums are fp32.
+//
+// Few tokens: the weights are the 16-row operand of mma.sync.m16n8k16, eight
+// tokens the other.  A CTA takes 32 rows; its warps share their columns, 128 at
+// a time, and join their sums in shared memory in a fixed order.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "kv4.cuh"
+#include "launch.h"
+#include "tmap.h"
+#include "w4.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 32;           // of a CTA's step
+constexpr int kRedLd = 36;          // rows of a token's sums, padded: no two lanes of a store share a bank
+
+struct LinearArgs {
+    const uint8_t* tiles;
+    const float* row_scale;
+    const __nv_bfloat16* x;
+    long long ld_x, ld_y;
+    int T, N, K, kt;                // kt: tiles of 128 columns
+    const float* bias;
+    void* y;
+    bool y_bf16, add, wide;         // wide: x's rows start at 16-byte boundaries
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// Eight numbers of token t's row from column k on; what lies outside is zero.
+__device__ __forceinline__ uint4 load_x8(const LinearArgs& a, int t, int k) {
+    if (t >= a.T || k >= a.K) return make_uint4(0u, 0u, 0u, 0u);
+    const __nv_bfloat16* p = a.x + t * a.ld_x + k;
+    if (a.wide && k + 8 <= a.K) return *reinterpret_cast<const uint4*>(p);
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = k + 2 * i < a.K ? __bfloat16_as_ushort(p[2 * i]) : 0u;
+        const uint32_t hi = k + 2 * i + 1 < a.K ? __bfloat16_as_ushort(p[2 * i + 1]) : 0u;
+        v[i] = lo | hi << 16;
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ void store_y(const LinearArgs& a, int t, int n, float v) {
+    v *= a.row_scale == nullptr ? kW4Up : a.row_scale[n] * kW4Up;
+    if (a.bias != nullptr) v += a.bias[n];
+    const long long at = t * a.ld_y + n;
+    if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+    else static_cast<float*>(a.y)[at] = a.add ? static_cast<float*>(a.y)[at] + v : v;
+}
+
+// What a lane holds of 32 rows and 128 columns: rows g + 8 i, columns 32 t .. 32 t + 31.
+struct Piece {
+    uint4 w[4];
+    uint32_t s[4];     // two scales each
+};
+__device__ __forceinline__ void load_piece(Piece& p, const LinearArgs& a, int row0, int c, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t* tile = a.tiles + (static_cast<long long>(row0 / kW4Tile) * a.kt + c) * kW4Bytes;
+    const int r = row0 % kW4Tile + g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        p.w[i] = ldg_stream(tile + w4_run(r + 8 * i, t));
+        p.s[i] = __ldg(reinterpret_cast<const uint16_t*>(tile + w4_scale(r + 8 * i, 2 * t)));
+    }
+}
+
+// NT: groups of eight tokens.  STAGED: x lies in shared memory as operands, else each warp loads it as it goes.
+template <int NT, bool STAGED>
+__global__ void __launch_bounds__(kThreads) linear_w4_kernel(const LinearArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* red = reinterpret_cast<float*>(smem);                       // [2][warps][tokens][kRedLd]
+    constexpr int kRed = kWarps * 8 * NT * kRedLd;
+    uint4* xs = reinterpret_cast<uint4*>(smem + 2 * kRed * sizeof(float));   // [column tile][word][NT][lane]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int t0 = blockIdx.y * 8 * NT;
+    pdl_wait();
+    pdl_trigger();
+    if constexpr (STAGED) {
+        const int per = a.kt * 16;                                     // runs of eight columns of a token
+        for (int i = threadIdx.x; i < per * 8 * NT; i += kThreads) {
+            const int tok = i / per, k8 = i % per;
+            const uint4 v = load_x8(a, t0 + tok, 8 * k8);
+            xs[((k8 / 16 * 4 + k8 % 4) * NT + tok / 8) * 32 + (tok % 8) * 4 + k8 / 4 % 4] = v;
+        }
+        __syncthreads();
+    }
+    int buf = 0;
+    for (int row0 = blockIdx.x * kRows; row0 < a.N; row0 += gridDim.x * kRows, buf ^= 1) {
+        float acc[2][NT][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+        for (int c = warp; c < a.kt; c += kWarps) {
+            Piece p;
+            load_piece(p, a, row0, c, lane);
+            uint32_t s[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w4_scales(p.s[i], s[i][0], s[i][1]);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t f[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w4_values(w == 0 ? p.w[i].x : w == 1 ? p.w[i].y : w == 2 ? p.w[i].z : p.w[i].w, f[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f[i][j] = bmul2(f[i][j], s[i][w / 2]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    uint4 b;
+                    if constexpr (STAGED) b = xs[((c * 4 + w) * NT + n) * 32 + lane];
+                    else b = load_x8(a, t0 + 8 * n + g, c * kW4Tile + 32 * t + 8 * w);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        mma_bf16(acc[m][n], f[2 * m][0], f[2 * m + 1][0], f[2 * m][1], f[2 * m + 1][1], b.x, b.y);
+                        mma_bf16(acc[m][n], f[2 * m][2], f[2 * m + 1][2], f[2 * m][3], f[2 * m + 1][3], b.z, b.w);
+                    }
+                }
+            }
+        }
+        float* mine = red + buf * kRed + warp * 8 * NT * kRedLd;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mine[(8 * n + 2 * t + (i & 1)) * kRedLd + 16 * m + g + 8 * (i >> 1)] = acc[m][n][i];
+        __syncthreads();                 // the other buffer is free: its readers are through before this barrier's next use
+        for (int i = threadIdx.x; i < kRows * 8 * NT; i += kThreads) {
+            const int tok = i / kRows, r = i % kRows;
+            if (t0 + tok >= a.T || row0 + r >= a.N) continue;
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += red[buf * kRed + (w * 8 * NT + tok) * kRedLd + r];
+            store_y(a, t0 + tok, row0 + r, v);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Packing: a warp for each row (of the padded ones too, whose tiles are zero).
+// ---------------------------------------------------------------------------
+template <typename W>
+__device__ __forceinline__ float load_w(const W* w, int k, int K) {
+    return k < K ? static_cast<float>(w[k]) : 0.f;
+}
+__device__ __forceinline__ bool finite(float v) { return v - v == 0.f; }
+
+template <typename W>
+__global__ void __launch_bounds__(kThreads) w4_pack_kernel(const W* w, long long ld, int N, int K, uint8_t* tiles, float* row_scale, moe_dev_status* st) {
+    const int row = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int kt = (K + kW4Tile - 1) / kW4Tile, rows = (N + kW4Tile - 1) / kW4Tile * kW4Tile;
+    pdl_wait();       // no early trigger: who reads weights may do so before its own wait
+    if (row >= rows) return;
+    const bool live = row < N;
+    const W* p = w + row * ld;
+    float top = 0.f;
+    bool bad = false;
+    if (live)
+        for (int k = lane; k < K; k += 32) {
+            const float v = load_w(p, k, K);
+            if (finite(v)) top = fmaxf(top, fabsf(v));
+            else bad = true;
+        }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+    if (__any_sync(kFull, bad) && lane == 0) report(st, MOE_DEV_NONFINITE, row);
+    float hs = __fmul_rn(top, 1.f / 2688.f);
+    if (!(hs >= 0x1p-100f)) hs = 1.f;
+    const float inv = __fdiv_rn(1.f, hs);
+    if (live && lane == 0) row_scale[row] = hs;
+    for (int run = lane; run < kt * 4; run += 32) {                    // runs of 32 columns
+        uint8_t* tile = tiles + (static_cast<long long>(row / kW4Tile) * kt + run / 4) * kW4Bytes;
+        const int r = row % kW4Tile, c = run % 4;
+        uint32_t words[4] = {0u, 0u, 0u, 0u}, scales = 0u;
+        if (live)
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                float z[16], most = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float v = load_w(p, run * 32 + b * 16 + i, K);
+                    z[i] = finite(v) ? __fmul_rn(v, inv) : 0.f;
+                    most = fmaxf(most, fabsf(z[i]));
+                }
+                const uint32_t s = f32_to_e4m3(__fmul_rn(most, 1.f / 6.f));
+                const float sv = e4m3_to_f32(s), up = sv > 0.f ? __fdiv_rn(1.f, sv) : 0.f;
+                scales |= s << (8 * b);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const uint32_t two = f32_to_e2m1x2(__fmul_rn(z[i], up), __fmul_rn(z[i + 1], up));
+                    const int j = i % 8 / 2;
+                    const uint32_t bits = w4_half_bits(two & 15u, j) | w4_half_bits(two >> 4 & 15u, j) << 16;
+                    words[2 * b + i / 8] |= bits;
+                }
+            }
+        *reinterpret_cast<uint4*>(tile + w4_run(r, c)) = make_uint4(words[0], words[1], words[2], words[3]);
+        *reinterpret_cast<uint16_t*>(tile + w4_scale(r, 2 * c)) = static_cast<uint16_t>(scales);
+    }
+}
+
+template <int NT, bool STAGED>
+cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
+    const size_t smem = 2 * kWarps * 8 * NT * kRedLd * sizeof(float) + (STAGED ? static_cast<size_t>(a.kt) * kW4Tile * 16 * NT : 0);
+    cudaError_t e = cudaFuncSetAttribute(linear_w4_kernel<NT, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int steps = (a.N + kRows - 1) / kRows, most = 2 * sm_count();
+    return launch_pdl(linear_w4_kernel<NT, STAGED>, dim3(steps < most ? steps : most, (a.T + 8 * NT - 1) / (8 * NT)), dim3(kThreads), smem, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_w4(const void* x, long long ld_x, int T, const moe_w4& w, const float* bias, void* y, int y_dtype, long long ld_y,
+                             bool add, cudaStream_t s) {
+    LinearArgs a;
+    a.tiles = static_cast<const uint8_t*>(w.tiles);
+    a.row_scale = w.row_scale;
+    a.x = static_cast<const __nv_bfloat16*>(x);
+    a.ld_x = ld_x;
+    a.ld_y = ld_y;
+    a.T = T;
+    a.N = w.N;
+    a.K = w.K;
+    a.kt = (w.K + kW4Tile - 1) / kW4Tile;
+    a.bias = bias;
+    a.y = y;
+    a.y_bf16 = y_dtype == MOE_DTYPE_BF16;
+    a.add = add;
+    a.wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ld_x % 8 == 0;
+    if (T <= 8) return a.kt <= 64 ? launch_few<1, true>(a, s) : launch_few<1, false>(a, s);
+    return a.kt <= 32 ? launch_few<2, true>(a, s) : launch_few<2, false>(a, s);
+}
+
+cudaError_t launch_w4_pack(const void* w, int dtype, long long ld, int N, int K, void* tiles, float* row_scale, moe_dev_status* st, cudaStream_t s) {
+    const dim3 grid((N + kW4Tile - 1) / kW4Tile * (kW4Tile / kWarps));
+    if (dtype == MOE_DTYPE_BF16)
+        return launch_pdl(w4_pack_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, static_cast<const __nv_bfloat16*>(w), ld, N, K, static_cast<uint8_t*>(tiles), row_scale, st);
+    return launch_pdl(w4_pack_kernel<float>, grid, dim3(kThreads), 0, s, static_cast<const float*>(w), ld, N, K, static_cast<uint8_t*>(tiles), row_scale, st);
+}
+
+}  // namespace moe

@@ -642,6 +642,182 @@ moe_status_t moe_kv4_compact(const moe_kv4_pool* pool, int32_t* n_live, void* wo
 size_t moe_kv4_pool_workspace(int S, int n_pages);
 
 /* ---------------------------------------------------------------- */
+/* Eviction from the cache by the attention that its tokens draw      */
+/* ---------------------------------------------------------------- */
+/*
+ * The attention weight that cached tokens draw: for every token j of sequence s
+ *     score[s][j] += sum over rows i and heads h of exp(scale * q_i . k_j - lse[i][h])
+ * over the rows q_start[s] + i that see token j, as moe_attention_kv4 lets them
+ * (places, window, key heads); with that call's lse the exponentials are its
+ * probabilities.  A row whose lse is -inf sees nothing and adds nothing.
+ *
+ *   q, ld_q, q_start, max_new, scale, window  as for moe_attention_kv4
+ *   last     count only the last `last` rows of each sequence; 0 = all
+ *   lse      [T][n_q] fp32
+ *   score    [S][ld_score] fp32, ld_score >= max_pages * 64; entries beyond a
+ *            sequence's tokens are not touched
+ *   fresh    nonzero: the entries of the rows' own tokens (the last of the
+ *            sequence) are set instead of added to.  With one score for all
+ *            layers the first layer's call is fresh and the others add.
+ *   workspace  moe_kv4_weigh_workspace() bytes, 256-byte aligned, ZERO-FILLED
+ *            before its first use (every call leaves its counters at zero, at places
+ *            that no size changes); serves one call at a time; may be NULL where that is 0
+ * The cache's values are not read.  Products run on the tensor cores in fp16 (q
+ * scaled by a power of two of its row, keys exact) with fp32 sums;
+ * exponentials and their sums are fp32, added in an order that depends on
+ * sizes alone, so results are reproducible bit for bit.  A page outside the pool, a
+ * length beyond the table or a bad q_start is reported (MOE_DEV_BAD_INDEX)
+ * and adds nothing.
+ * Limits: those of moe_attention_kv4.
+ */
+moe_status_t moe_kv4_weigh(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache* cache,
+                           const int32_t* q_start, int max_new, const float* lse, float scale, int window,
+                           int last, float* score, long long ld_score, int fresh, void* workspace,
+                           size_t ws_bytes, moe_dev_status* st, void* stream);
+size_t moe_kv4_weigh_workspace(int S, int T, int n_q, int n_kv, int head_dim, int max_pages);
+
+/*
+ * Eviction: every sequence with more than budget[s] tokens keeps that many --
+ * its first `sinks`, its last `recent`, and of the others those with the
+ * highest scores (equal ones: the earlier first; a NaN counts as lowest) -- in
+ * their order, moved to its front in every layer.  Keys and values are moved as
+ * they are (a rotated key keeps the position that it was turned to).  The
+ * pages behind are released.  budget[s] < 0, or at least the sequence's tokens:
+ * the sequence stays as it is.
+ *
+ *   head_dim  D of the pool's caches (64 or 128; page_bytes is n_kv * 64 * (D + D/8))
+ *   score    [S][ld_score] fp32, ld_score >= max_pages * 64: the kept tokens'
+ *            entries move with them, those behind are set to 0 up to the old length
+ *   budget   [S] int32; at least sinks + recent where the sequence has more tokens
+ *   kept     [S][ld_kept] int32 out, or NULL: the place that each token had
+ *            before (of every sequence), -1 from its new length on
+ * Pages in front of the first evicted token's stay as they are.  Of the others
+ * a page that only one table entry holds is rewritten in place; one that
+ * others hold too is left, and a free one taken for it (ascending, in the order
+ * of sequences and places).  In a rewritten page the codes and scales behind the last
+ * token are zero.  Pages freed by the call are free for the next one.  All or
+ * nothing: with too few free pages (MOE_DEV_NO_PAGES, detail = how many more), or a
+ * length beyond the table, a held page outside the pool or a budget below
+ * sinks + recent (MOE_DEV_BAD_INDEX, detail = sequence), nothing changes and
+ * nothing is written, kept included.
+ *   workspace  moe_kv4_evict_workspace() bytes, 256-byte aligned; holds nothing
+ *            between calls, so one buffer serves pools of any sizes in turn; serves one call
+ *            at a time.
+ * Limits: S <= 4096; tables of at most 2^31 - 1 tokens a sequence.
+ */
+moe_status_t moe_kv4_evict(const moe_kv4_pool* pool, int head_dim, float* score, long long ld_score,
+                           const int32_t* budget, int sinks, int recent, int32_t* kept, long long ld_kept,
+                           void* workspace, size_t ws_bytes, moe_dev_status* st, void* stream);
+size_t moe_kv4_evict_workspace(int S, int max_pages, int n_pages);
+
+/* ---------------------------------------------------------------- */
+/* Products with weights in 4 bits                                    */
+/* ---------------------------------------------------------------- */
+/*
+ * Weights [N][K] in 4 bits: number (n, k) stands for c * s * row_scale[n], c an
+ * e2m1 code and s the e4m3 scale of columns 16 (k/16) .. + 15 of its row.
+ *
+ * tiles  [ceil(N/128)][ceil(K/128)][9216] bytes, 16-byte aligned.  In a tile
+ *        (r, k = row and column in it, c = k / 32): the code of (r, k) is in the
+ *        16-byte run at
+ *            (r/8)*512 + c*128 + ((r%8) ^ (2c))*16,
+ *        eight columns to a 32-bit word, the even ones in its lower half, the
+ *        j-th two (j = k%8/2) in bits 15 8 7 6, 12 5 4 3, 9 2 1 0 or
+ *        14 13 11 10 of a half (sign, then magnitude from its high bit); the
+ *        scale of (r, k) is byte 8192 + r*8 + k/16.  Codes and scales beyond N or K are zero.
+ *        (Three of four codes then become bf16 with a shift and a mask.)
+ */
+typedef struct moe_w4 {
+    void* tiles;
+    float* row_scale;   /* [N], or NULL: 1 */
+    int32_t N;
+    int32_t K;
+} moe_w4;
+
+/* Bytes of the tiles; 0 for sizes below 1. */
+size_t moe_w4_bytes(int N, int K);
+
+/*
+ * Packs weights: row_scale[n] = max|w[n]| / 2688 (1 where that is below 2^-100),
+ * z = w * (1/row_scale), and codes and scales of z as in the cache (above): s =
+ * e4m3(max|z| * (1/6)), c = e2m1(z * (1/s)), every operation one fp32 operation.
+ *   w   [N][ld] BF16 or F32
+ *   out tiles and row_scale (not NULL) are written
+ * A NaN or infinite weight is packed as zero and reported (MOE_DEV_NONFINITE,
+ * detail = row).
+ */
+moe_status_t moe_w4_pack(const void* w, int dtype, long long ld, const moe_w4* out, moe_dev_status* st, void* stream);
+
+/*
+ * y[t][n] = row_scale[n] * sum_k x[t][k] c[n][k] s[n][k/16] + bias[n]  (+ y[t][n])
+ *
+ *   x     [T][ld_x] bf16, K numbers a row (any alignment; rows that start at
+ *         16-byte boundaries are read faster)
+ *   bias  [N] fp32, or NULL
+ *   y     [T][ld_y] BF16 or F32, N numbers a row; must not overlap x
+ *   add   nonzero: added to what y holds (F32 only), e.g. a residual
+ * Products are exact, sums fp32, results rounded once to y's type.  Sums are added
+ * in an order that depends on sizes alone, so results are reproducible bit
+ * for bit.
+ * Limits: N, K <= 2^24, T <= 2^20.
+ */
+moe_status_t moe_linear_w4(const void* x, long long ld_x, int T, const moe_w4* w, const float* bias, void* y,
+                           int y_dtype, long long ld_y, int add, void* stream);
+
+/* ---------------------------------------------------------------- */
+/* Verification of drafted tokens                                     */
+/* ---------------------------------------------------------------- */
+/*
+ * How many of each sequence's drafted tokens the target accepts, and the token
+ * that follows them; tokens are then distributed as the target's.
+ *
+ * Rows q_start[s] .. q_start[s+1]-1 of a step are a sequence's newest known
+ * token and its n drafts behind it.  logits of a row are the target's for the
+ * place behind it, so row r judges the draft tokens[r+1].  With p the
+ * target's and q the drafting model's distribution at a row, the draft x is
+ * accepted if uniform[r+1] * q(x) < p(x); the first one that is not ends
+ * the run, and the next token is drawn from max(p - q, 0); with all accepted it
+ * is drawn from the last row's p.  uniform[q_start[s]] draws it: of the tokens
+ * in order, the first whose cumulated weight exceeds uniform * the sum.
+ *
+ *   logits        [T][ld] BF16 or F32, V numbers a row (any alignment)
+ *   draft_logits  [T][ld_draft], same type: row r's distribution is the one that
+ *                 tokens[r+1] was drawn from (a sequence's last row is not read);
+ *                 NULL: drafts without a distribution, q = 1 at the draft
+ *   tokens        [T] int32; uniform [T] fp32 from [0, 1)
+ *   temperature   [S] fp32, or NULL: 1.  Below 2^-60 (0 among it): greedy -- a draft
+ *                 is accepted if it is the target's strongest (of equal ones the lowest
+ *                 number), and so is the next token
+ *   accepted      [S] int32 out: accepted drafts
+ *   next          [S] int32 out: the token that follows; -1 for a sequence without rows
+ *   n_new         [S] int32 out, or NULL: accepted - n, what moe_kv4_reserve takes to
+ *                 cut the refused drafts' tokens from the cache
+ *   workspace     moe_verify_workspace() bytes, 256-byte aligned; holds nothing between calls; serves
+ *                 one call at a time
+ * A logit of -inf is a token that cannot be.  A row with a NaN, with +inf or
+ * without a finite logit is reported (MOE_DEV_NONFINITE, detail = row; T + row for
+ * draft_logits), and so is a temperature that is NaN, negative or infinite
+ * (detail = -1 - sequence) and a draft outside [0, V) (MOE_DEV_BAD_INDEX, detail = row):
+ * such a sequence has accepted 0 and next -1.  A bad q_start is reported (MOE_DEV_BAD_INDEX, detail = sequence)
+ * and its sequence counts as without rows.
+ *
+ * Whole numbers decide, so that results do not depend on the order of a sum:
+ * with m the row's maximum, it = log2(e) / temperature,
+ *     t = max((logit - m) * it, -60),  n = rint(t),  f = t - n
+ *     w = 2^n * (((((c6 f + c5) f + c4) f + c3) f + c2) f + c1) f + c0,  c_i = ln(2)^i / i!
+ * each operation one fp32 operation (the series' steps fused), W = rint(w 2^42), Z the sum
+ * of a row's W, p(x) = W/Z in fp64; max(p - q, 0) is rint(max(w_p i_p - w_q i_q, 0) 2^42) with i =
+ * 2^42/Z rounded to fp32, or p's W with the draft's set to 0 when draft_logits is NULL; where all of
+ * it is 0, p's W.  The cumulated weight is compared with floor(uniform * sum) in fp64, at most sum - 1.
+ * Limits: V <= 2^20, T <= 2^16, S <= 16384.
+ */
+moe_status_t moe_verify_drafts(const void* logits, int dtype, long long ld, int T, int V, const int32_t* tokens,
+                               const float* uniform, const int32_t* q_start, int S, const void* draft_logits,
+                               long long ld_draft, const float* temperature, int32_t* accepted, int32_t* next,
+                               int32_t* n_new, void* workspace, size_t ws_bytes, moe_dev_status* st, void* stream);
+size_t moe_verify_workspace(int T, int S, int V);
+
+/* ---------------------------------------------------------------- */
 /* Workspace sizes and status strings                                 */
 /* ---------------------------------------------------------------- */
 #define MOE_OP_DISPATCH 1
