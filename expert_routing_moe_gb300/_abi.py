@@ -150,7 +150,7 @@ def load(path: str = LIB_PATH):
             L.moe_w4_bytes.restype = sz
             L.moe_w4_pack.argtypes = [p, i, ll, p, p, p]
             L.moe_w4_pack.restype = i
-            L.moe_linear_w4.argtypes = [p, ll, i, p, p, p, i, ll, i, p]
+            L.moe_linear_w4.argtypes = [p, ll, i, p, p, p, i, ll, i, p, p]
             L.moe_linear_w4.restype = i
             L.moe_verify_drafts.argtypes = [p, i, ll, i, i, p, p, p, i, p, ll, p, p, p, p, p, sz, p, p]
             L.moe_verify_drafts.restype = i
@@ -771,7 +771,7 @@ def moe_w4_pack(w, out: Weight4, st=None, stream=None):
     _check(rc, "moe_w4_pack")
 
 
-def moe_linear_w4(x, w: Weight4, y, bias=None, accumulate: bool = False, stream=None):
+def moe_linear_w4(x, w: Weight4, y, bias=None, accumulate: bool = False, st=None, stream=None):
     """y [T][N] = x [T][K] w^T + bias: x bf16, y bf16 or fp32, bias [N] fp32 or None; rows
     may be strided.  accumulate: added to y (fp32)."""
     T = x.shape[0]
@@ -783,7 +783,7 @@ def moe_linear_w4(x, w: Weight4, y, bias=None, accumulate: bool = False, stream=
     if accumulate and code != MOE_DTYPE_F32:
         raise MoeError("y: only fp32 is added to")
     rc = load().moe_linear_w4(xp, ld_x, T, w._ref, _addr(bias, torch.float32, "bias"), yp, code, ld_y, 1 if accumulate else 0,
-                              _raw_stream(stream, x))
+                              _status(st), _raw_stream(stream, x))
     _check(rc, "moe_linear_w4")
 
 

@@ -469,7 +469,7 @@ moe_status_t moe_w4_pack(const void* w, int dtype, long long ld, const moe_w4* o
 }
 
 moe_status_t moe_linear_w4(const void* x, long long ld_x, int T, const moe_w4* w, const float* bias, void* y, int y_dtype, long long ld_y,
-                           int add, void* stream) {
+                           int add, moe_dev_status* st, void* stream) {
     if (T < 0 || (y_dtype != MOE_DTYPE_F32 && y_dtype != MOE_DTYPE_BF16)) return MOE_ERR_INVALID_ARG;
     if (add != 0 && y_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
     const moe_status_t rc = check_w4(w);
@@ -479,7 +479,7 @@ moe_status_t moe_linear_w4(const void* x, long long ld_x, int T, const moe_w4* w
     if (x == nullptr || y == nullptr || ld_x < w->K || ld_y < w->N) return MOE_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(x) & 1u) != 0 || (reinterpret_cast<uintptr_t>(y) & (y_dtype == MOE_DTYPE_BF16 ? 1u : 3u)) != 0)
         return MOE_ERR_INVALID_ARG;
-    return from_cuda(moe::launch_linear_w4(x, ld_x, T, *w, bias, y, y_dtype, ld_y, add != 0, as_stream(stream)));
+    return from_cuda(moe::launch_linear_w4(x, ld_x, T, *w, bias, y, y_dtype, ld_y, add != 0, st, as_stream(stream)));
 }
 
 size_t moe_verify_workspace(int T, int S, int V) {

@@ -151,7 +151,7 @@ cudaError_t launch_kv4_evict(const moe_kv4_pool& p, int head_dim, int n_kv, floa
 
 // ---- products with weights in 4 bits (linear_w4.cu) ----
 cudaError_t launch_linear_w4(const void* x, long long ld_x, int T, const moe_w4& w, const float* bias, void* y, int y_dtype, long long ld_y,
-                             bool add, cudaStream_t s);
+                             bool add, moe_dev_status* st, cudaStream_t s);
 cudaError_t launch_w4_pack(const void* w, int dtype, long long ld, int N, int K, void* tiles, float* row_scale, moe_dev_status* st, cudaStream_t s);
 
 // ---- verification of drafted tokens (verify.cu) ----

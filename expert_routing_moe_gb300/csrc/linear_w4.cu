@@ -13,6 +13,7 @@
 #include "common.cuh"
 #include "kv4.cuh"
 #include "launch.h"
+#include "linear_w4.cuh"
 #include "tmap.h"
 #include "w4.cuh"
 
@@ -25,17 +26,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 32;           // of a CTA's step
 constexpr int kRedLd = 36;          // rows of a token's sums, padded: no two lanes of a store share a bank
 
-struct LinearArgs {
-    const uint8_t* tiles;
-    const float* row_scale;
-    const __nv_bfloat16* x;
-    long long ld_x, ld_y;
-    int T, N, K, kt;                // kt: tiles of 128 columns
-    const float* bias;
-    void* y;
-    bool y_bf16, add, wide;         // wide: x's rows start at 16-byte boundaries
-};
-
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -47,27 +37,9 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
     return v;
 }
 
-// Eight numbers of token t's row from column k on; what lies outside is zero.
-__device__ __forceinline__ uint4 load_x8(const LinearArgs& a, int t, int k) {
-    if (t >= a.T || k >= a.K) return make_uint4(0u, 0u, 0u, 0u);
-    const __nv_bfloat16* p = a.x + t * a.ld_x + k;
-    if (a.wide && k + 8 <= a.K) return *reinterpret_cast<const uint4*>(p);
-    uint32_t v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = k + 2 * i < a.K ? __bfloat16_as_ushort(p[2 * i]) : 0u;
-        const uint32_t hi = k + 2 * i + 1 < a.K ? __bfloat16_as_ushort(p[2 * i + 1]) : 0u;
-        v[i] = lo | hi << 16;
-    }
-    return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
 __device__ __forceinline__ void store_y(const LinearArgs& a, int t, int n, float v) {
     v *= a.row_scale == nullptr ? kW4Up : a.row_scale[n] * kW4Up;
-    if (a.bias != nullptr) v += a.bias[n];
-    const long long at = t * a.ld_y + n;
-    if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
-    else static_cast<float*>(a.y)[at] = a.add ? static_cast<float*>(a.y)[at] + v : v;
+    put_y(a, t, n, a.bias != nullptr ? v + a.bias[n] : v);
 }
 
 // What a lane holds of 32 rows and 128 columns: rows g + 8 i, columns 32 t .. 32 t + 31.
@@ -175,7 +147,8 @@ template <typename W>
 __global__ void __launch_bounds__(kThreads) w4_pack_kernel(const W* w, long long ld, int N, int K, uint8_t* tiles, float* row_scale, moe_dev_status* st) {
     const int row = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int kt = (K + kW4Tile - 1) / kW4Tile, rows = (N + kW4Tile - 1) / kW4Tile * kW4Tile;
-    pdl_wait();       // no early trigger: who reads weights may do so before its own wait
+    pdl_wait();
+    pdl_trigger();
     if (row >= rows) return;
     const bool live = row < N;
     const W* p = w + row * ld;
@@ -236,8 +209,9 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_linear_w4(const void* x, long long ld_x, int T, const moe_w4& w, const float* bias, void* y, int y_dtype, long long ld_y,
-                             bool add, cudaStream_t s) {
+                             bool add, moe_dev_status* st, cudaStream_t s) {
     LinearArgs a;
+    a.st = st;
     a.tiles = static_cast<const uint8_t*>(w.tiles);
     a.row_scale = w.row_scale;
     a.x = static_cast<const __nv_bfloat16*>(x);
@@ -252,6 +226,7 @@ cudaError_t launch_linear_w4(const void* x, long long ld_x, int T, const moe_w4&
     a.y_bf16 = y_dtype == MOE_DTYPE_BF16;
     a.add = add;
     a.wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ld_x % 8 == 0;
+    if (T > 64 || a.kt > 64) return launch_linear_w4_tc(a, s);
     if (T <= 8) return a.kt <= 64 ? launch_few<1, true>(a, s) : launch_few<1, false>(a, s);
     return a.kt <= 32 ? launch_few<2, true>(a, s) : launch_few<2, false>(a, s);
 }

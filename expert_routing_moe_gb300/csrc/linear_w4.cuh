@@ -1,0 +1,47 @@
+// linear_w4.cuh -- what the two kernels of the products with weights in 4 bits
+// share: their arguments, the tokens' numbers and the outputs.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "w4.cuh"
+
+namespace moe {
+
+struct LinearArgs {
+    const uint8_t* tiles;
+    const float* row_scale;
+    const __nv_bfloat16* x;
+    long long ld_x, ld_y;
+    int T, N, K, kt;                // kt: tiles of 128 columns
+    const float* bias;
+    void* y;
+    bool y_bf16, add, wide;         // wide: x's rows start at 16-byte boundaries
+    moe_dev_status* st;
+};
+
+// Eight numbers of token t's row from column k on; what lies outside is zero.
+__device__ __forceinline__ uint4 load_x8(const LinearArgs& a, int t, int k) {
+    if (t >= a.T || k >= a.K) return make_uint4(0u, 0u, 0u, 0u);
+    const __nv_bfloat16* p = a.x + t * a.ld_x + k;
+    if (a.wide && k + 8 <= a.K) return *reinterpret_cast<const uint4*>(p);
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = k + 2 * i < a.K ? __bfloat16_as_ushort(p[2 * i]) : 0u;
+        const uint32_t hi = k + 2 * i + 1 < a.K ? __bfloat16_as_ushort(p[2 * i + 1]) : 0u;
+        v[i] = lo | hi << 16;
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ void put_y(const LinearArgs& a, int t, int n, float v) {
+    const long long at = t * a.ld_y + n;
+    if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+    else static_cast<float*>(a.y)[at] = a.add ? static_cast<float*>(a.y)[at] + v : v;
+}
+
+cudaError_t launch_linear_w4_tc(const LinearArgs& a, cudaStream_t s);
+
+}  // namespace moe

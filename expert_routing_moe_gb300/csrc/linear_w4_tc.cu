@@ -1,0 +1,329 @@
+// linear_w4_tc.cu -- products with weights in 4 bits for many tokens: tcgen05.
+//
+// A tile of the output is 256 weight rows (two halves of 128 TMEM lanes) and up
+// to 192 tokens.  For 64 columns at a time, four warps turn each half's codes
+// to bf16 in TMEM (a thread is a row), where they are the products' A
+// operand, and the tokens' numbers come to shared memory by TMA as the B operand:
+//     D[row][token] += A[row][64] B[token][64]^T      (fp32 in TMEM)
+//
+// Warps: 0-3 and 4-7 convert the halves and write the outputs, 8 issues the
+// products, 9 copies the weights' tiles, 10 the tokens (or 10-13, with plain loads, where
+// rows of x do not start at 16-byte boundaries).
+// TMEM columns: D 2 x 192, A 2 halves x 2 buffers x 32.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "linear_w4.cuh"
+#include "tmap.h"
+#include "w4.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kHalves = 2;
+constexpr int kTileRows = kHalves * kW4Tile;
+constexpr int kStep = 64;                 // columns of a step
+constexpr int kMaxTok = 192;
+constexpr int kRaw = 3;                   // weights' tiles in flight, of a half
+constexpr int kB = 6;                     // steps of tokens in flight
+constexpr int kBBytes = kMaxTok * kStep * 2;
+constexpr int kRawOff = kB * kBBytes;
+constexpr int kSmem = kRawOff + kHalves * kRaw * kW4Bytes + 1024;   // slack for 1024-byte alignment
+constexpr int kColA = kHalves * kMaxTok;  // TMEM column of the A buffers
+constexpr int kLoaders = 4;               // warps that load x where TMA cannot
+
+enum Bar : int { B_WF = 0, B_WE = B_WF + kHalves * kRaw, B_AF = B_WE + kHalves * kRaw, B_AE = B_AF + 4, B_BF = B_AE + 4, B_BE = B_BF + kB,
+                 B_DF = B_BE + kB, B_DE, B_DRAIN, B_N };
+enum Site : int { kSiteWFull = 41, kSiteWEmpty, kSiteAFull, kSiteAEmpty, kSiteBFull, kSiteBEmpty, kSiteDFull, kSiteDEmpty };
+
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16 (bf16 inputs, fp32 accumulate).
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// The tiles of a CTA: row tile and first token.
+struct Tiles {
+    int tok_tiles, total, tok;
+    __device__ int row(int i) const { return i / tok_tiles; }
+    __device__ int t0(int i) const { return i % tok_tiles * tok; }
+};
+
+template <bool TMA>
+__global__ void __launch_bounds__((TMA ? 11 : 10 + kLoaders) * 32, 1) linear_w4_tc_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_x, int tok) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ __align__(8) uint64_t bars[B_N];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kHalves * kRaw; ++i) { mbar_init(bar(B_WF + i), 1); mbar_init(bar(B_WE + i), 4); }
+        for (int i = 0; i < 4; ++i) { mbar_init(bar(B_AF + i), 4); mbar_init(bar(B_AE + i), 1); }
+        for (int i = 0; i < kB; ++i) { mbar_init(bar(B_BF + i), TMA ? 1 : kLoaders); mbar_init(bar(B_BE + i), 1); }
+        mbar_init(bar(B_DF), 1);
+        mbar_init(bar(B_DE), 8);
+        mbar_init(bar(B_DRAIN), 1);
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_u32(&s_tmem), 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    Tiles w;
+    w.tok = tok;
+    w.tok_tiles = (a.T + tok - 1) / tok;
+    const int halves = (a.N + kW4Tile - 1) / kW4Tile;
+    w.total = (halves + kHalves - 1) / kHalves * w.tok_tiles;
+    const int steps = 2 * a.kt;
+    const int first = blockIdx.x, by = gridDim.x;
+    bool ok = true;
+
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 9) {
+        // ---------------- weights ----------------
+        if (lane == 0) {
+            uint32_t n = 0;            // tiles of a half copied
+            for (int i = first; i < w.total && ok; i += by)
+                for (int c = 0; c < a.kt && ok; ++c, ++n) {
+                    const int st = n % kRaw;
+                    for (int m = 0; m < kHalves && ok; ++m) {
+                        ok = mbar_wait(bar(B_WE + m * kRaw + st), ((n / kRaw) & 1) ^ 1, &s_abort, a.st, kSiteWEmpty);
+                        if (!ok) break;
+                        // the last tile's second half may be none: its rows are not written
+                        const int half = min(w.row(i) * kHalves + m, halves - 1);
+                        mbar_arrive_expect_tx(bar(B_WF + m * kRaw + st), kW4Bytes);
+                        bulk_copy_g2s(smem_u32(smem + kRawOff + (m * kRaw + st) * kW4Bytes), a.tiles + (static_cast<long long>(half) * a.kt + c) * kW4Bytes, kW4Bytes,
+                                      bar(B_WF + m * kRaw + st));
+                    }
+                }
+            if (!ok)                   // what is in flight lands before the CTA ends
+                for (int i = 0; i < kHalves * kRaw; ++i) {
+                    mbar_drain(bar(B_WF + i), 0);
+                    mbar_drain(bar(B_WF + i), 1);
+                }
+        }
+    } else if (warp >= 10) {
+        // ---------------- tokens ----------------
+        uint32_t n = 0;
+        if (TMA) {
+            if (lane == 0) {
+                tma_prefetch_desc(&map_x);
+                const uint64_t policy = l2_policy_evict_last();
+                for (int i = first; i < w.total && ok; i += by)
+                    for (int k = 0; k < steps && ok; ++k, ++n) {
+                        const int st = n % kB;
+                        ok = mbar_wait(bar(B_BE + st), ((n / kB) & 1) ^ 1, &s_abort, a.st, kSiteBEmpty);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(bar(B_BF + st), tok * kStep * 2);
+                        tma_load_2d(smem_u32(smem + st * kBBytes), &map_x, k * kStep, w.t0(i), bar(B_BF + st), policy);
+                    }
+                if (!ok)
+                    for (int i = 0; i < kB; ++i) {
+                        mbar_drain(bar(B_BF + i), 0);
+                        mbar_drain(bar(B_BF + i), 1);
+                    }
+            }
+        } else {
+            for (int i = first; i < w.total && ok; i += by)
+                for (int k = 0; k < steps && ok; ++k, ++n) {
+                    const int st = n % kB;
+                    ok = mbar_wait(bar(B_BE + st), ((n / kB) & 1) ^ 1, &s_abort, a.st, kSiteBEmpty);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    uint8_t* dst = smem + st * kBBytes;
+                    for (int u = threadIdx.x - 320; u < tok * 8; u += kLoaders * 32) {
+                        const int r = u >> 3, seg = u & 7;
+                        *reinterpret_cast<uint4*>(dst + r * 128 + ((seg ^ (r & 7)) * 16)) = load_x8(a, w.t0(i) + r, k * kStep + seg * 8);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_BF + st));
+                }
+        }
+    } else if (warp == 8) {
+        // ---------------- products ----------------
+        const uint32_t idesc = idesc_bf16_f32(kW4Tile, tok);
+        uint32_t n = 0, done = 0;
+        bool issued = false;
+        for (int i = first; i < w.total && ok; i += by, ++done) {
+            ok = mbar_wait(bar(B_DE), (done & 1) ^ 1, &s_abort, a.st, kSiteDEmpty);
+            ok = __all_sync(kFull, ok);
+            for (int k = 0; k < steps && ok; ++k, ++n) {
+                const int st = n % kB, buf = n & 1;
+                ok = mbar_wait(bar(B_BF + st), (n / kB) & 1, &s_abort, a.st, kSiteBFull);
+                ok = __all_sync(kFull, ok);
+                for (int m = 0; m < kHalves && ok; ++m) {
+                    ok = mbar_wait(bar(B_AF + m * 2 + buf), (n >> 1) & 1, &s_abort, a.st, kSiteAFull);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t b = sw128_desc(smem_u32(smem + st * kBBytes));
+                        const uint32_t at = tmem + kColA + (m * 2 + buf) * 32;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) mma_ts(tmem + m * kMaxTok, at + x * 8, b + x * 2, idesc, k > 0 || x > 0);
+                        tc_commit(bar(B_AE + m * 2 + buf));
+                        if (m == kHalves - 1) tc_commit(bar(B_BE + st));
+                    }
+                    issued = true;
+                    __syncwarp();
+                }
+            }
+            if (ok && elect_one()) tc_commit(bar(B_DF));
+            __syncwarp();
+        }
+        if (!ok && issued) {           // the products in flight end before TMEM is freed
+            if (elect_one()) tc_commit(bar(B_DRAIN));
+            __syncwarp();
+            mbar_drain(bar(B_DRAIN), 0);
+        }
+    } else {
+        // ---------------- weights to bf16, and the outputs ----------------
+        const int m = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        uint32_t n = 0, raw = 0, done = 0;
+        for (int i = first; i < w.total && ok; i += by, ++done) {
+            for (int c = 0; c < a.kt && ok; ++c, ++raw) {
+                const int st = raw % kRaw;
+                ok = mbar_wait(bar(B_WF + m * kRaw + st), (raw / kRaw) & 1, &s_abort, a.st, kSiteWFull);
+                if (!ok) break;
+                const uint8_t* tile = smem + kRawOff + (m * kRaw + st) * kW4Bytes;
+                const uint2 scales = *reinterpret_cast<const uint2*>(tile + w4_scale(r, 0));
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h, ++n) {
+                    const int buf = n & 1;
+                    uint32_t v[32];
+                    const uint32_t four = h == 0 ? scales.x : scales.y;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint4 run = *reinterpret_cast<const uint4*>(tile + w4_run(r, 2 * h + x));
+                        uint32_t s[2];
+                        w4_scales(x == 0 ? four & 0xffffu : four >> 16, s[0], s[1]);
+                        const uint32_t words[4] = {run.x, run.y, run.z, run.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            uint32_t f[4];
+                            w4_values(words[y], f);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) v[x * 16 + y * 4 + j] = bmul2(f[j], s[y / 2]);
+                        }
+                    }
+                    ok = mbar_wait(bar(B_AE + m * 2 + buf), ((n >> 1) & 1) ^ 1, &s_abort, a.st, kSiteAEmpty);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    st32(tmem + kColA + (m * 2 + buf) * 32 + lanes, v);
+                    st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_AF + m * 2 + buf));
+                }
+                if (lane == 0 && ok) mbar_arrive(bar(B_WE + m * kRaw + st));
+            }
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            ok = mbar_wait(bar(B_DF), done & 1, &s_abort, a.st, kSiteDFull);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const int row = w.row(i) * kTileRows + m * kW4Tile + r, t0 = w.t0(i);
+            const bool live = row < a.N;
+            const float scale = (live && a.row_scale != nullptr ? a.row_scale[row] : 1.f) * kW4Up;
+            const float bias = live && a.bias != nullptr ? a.bias[row] : 0.f;
+            for (int c = 0; c < tok; c += 16) {
+                uint32_t d[16];
+                tmem_ld16(tmem + m * kMaxTok + lanes + c, d);
+                tmem_ld_wait();
+                if (c + 16 >= tok) {   // D is read: the next tile's products may begin
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_DE));
+                }
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const int t = t0 + c + x;
+                    if (!live || t >= a.T) continue;
+                    put_y(a, t, row, __uint_as_float(d[x]) * scale + bias);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// [T][K] bf16 with rows `ld` numbers apart, boxes of 64 columns and `tok` rows with the 128-byte swizzle.
+bool map_tokens(CUtensorMap* m, const LinearArgs& a, int tok) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.T)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.ld_x) * 2};
+    cuuint32_t box[2] = {kStep, static_cast<cuuint32_t>(tok)};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<__nv_bfloat16*>(a.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool TMA>
+cudaError_t launch(const LinearArgs& a, int tok, cudaStream_t s) {
+    CUtensorMap map = {};
+    if (TMA && !map_tokens(&map, a, tok)) return cudaErrorInvalidValue;
+    auto* k = linear_w4_tc_kernel<TMA>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    const long long tiles = static_cast<long long>((a.N + kTileRows - 1) / kTileRows) * ((a.T + tok - 1) / tok);
+    return launch_pdl(k, dim3(static_cast<unsigned>(tiles < sm_count() ? tiles : sm_count())), dim3((TMA ? 11 : 10 + kLoaders) * 32), kSmem, s, a, map, tok);
+}
+
+}  // namespace
+
+// Tokens of a tile: as many as make the longest CTA's time shortest.  A step of 64 columns takes 4 clocks a
+// token of the products, or some 380 for the conversion of its weights, and a tile its outputs.
+cudaError_t launch_linear_w4_tc(const LinearArgs& a, cudaStream_t s) {
+    const long long rows = (a.N + kTileRows - 1) / kTileRows;
+    int best = 16;
+    double least = 1e300;
+    for (int tok = 16; tok <= kMaxTok; tok += 16) {
+        const long long tiles = rows * ((a.T + tok - 1) / tok), waves = (tiles + sm_count() - 1) / sm_count();
+        const double step = 4.0 * tok > 380.0 ? 4.0 * tok : 380.0;
+        const double time = static_cast<double>(waves) * (2.0 * a.kt * step + 1500.0 + 12.0 * tok);
+        if (time < least) { least = time; best = tok; }
+    }
+    return a.wide ? launch<true>(a, best, s) : launch<false>(a, best, s);
+}
+
+}  // namespace moe

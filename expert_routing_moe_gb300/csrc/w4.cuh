@@ -52,11 +52,11 @@ __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
 
 // Two e4m3 scales (low, high byte), each as a pair of bf16 equal to it times 2^119.
 __device__ __forceinline__ void w4_scales(uint32_t two, uint32_t& lo, uint32_t& hi) {
-    uint32_t h, b;
+    uint32_t b;
     float x, y;
-    asm("{\n\t.reg .b16 s, p, q;\n\tcvt.u16.u32 s, %3;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t"
-        "mov.b32 {p, q}, %0;\n\tcvt.f32.f16 %1, p;\n\tcvt.f32.f16 %2, q;\n\t}"
-        : "=r"(h), "=f"(x), "=f"(y)
+    asm("{\n\t.reg .b16 s, p, q;\n\t.reg .b32 h;\n\tcvt.u16.u32 s, %2;\n\tcvt.rn.f16x2.e4m3x2 h, s;\n\t"
+        "mov.b32 {p, q}, h;\n\tcvt.f32.f16 %0, p;\n\tcvt.f32.f16 %1, q;\n\t}"
+        : "=f"(x), "=f"(y)
         : "r"(two));
     x *= 0x1p119f;
     y *= 0x1p119f;

@@ -762,7 +762,7 @@ moe_status_t moe_w4_pack(const void* w, int dtype, long long ld, const moe_w4* o
  * Limits: N, K <= 2^24, T <= 2^20.
  */
 moe_status_t moe_linear_w4(const void* x, long long ld_x, int T, const moe_w4* w, const float* bias, void* y,
-                           int y_dtype, long long ld_y, int add, void* stream);
+                           int y_dtype, long long ld_y, int add, moe_dev_status* st, void* stream);
 
 /* ---------------------------------------------------------------- */
 /* Verification of drafted tokens                                     */

@@ -187,7 +187,7 @@ def _linear(lib, w=None, **kw):
     a = dict(x=FAKE, ld_x=64, T=2, bias=None, y=FAKE, dtype=0, ld_y=64, add=0)
     a.update(kw)
     p = _w4p() if w is None else w
-    return lib.moe_linear_w4(a["x"], a["ld_x"], a["T"], ctypes.byref(p), a["bias"], a["y"], a["dtype"], a["ld_y"], a["add"], None)
+    return lib.moe_linear_w4(a["x"], a["ld_x"], a["T"], ctypes.byref(p), a["bias"], a["y"], a["dtype"], a["ld_y"], a["add"], None, None)
 
 
 @pytest.mark.parametrize("want,kw", [
