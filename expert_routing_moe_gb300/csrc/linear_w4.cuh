@@ -26,12 +26,24 @@ __device__ __forceinline__ uint4 load_x8(const LinearArgs& a, int t, int k) {
     if (t >= a.T || k >= a.K) return make_uint4(0u, 0u, 0u, 0u);
     const __nv_bfloat16* p = a.x + t * a.ld_x + k;
     if (a.wide && k + 8 <= a.K) return *reinterpret_cast<const uint4*>(p);
+    // the one or two 16-byte words that hold the eight numbers (each holds one of the row at least), shifted into place
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint4* words = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+    const int off = static_cast<int>(at & 15), left = min(8, a.K - k);
+    const uint4 lo = words[0], hi = off + 2 * left > 16 ? words[1] : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     uint32_t v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = k + 2 * i < a.K ? __bfloat16_as_ushort(p[2 * i]) : 0u;
-        const uint32_t hi = k + 2 * i + 1 < a.K ? __bfloat16_as_ushort(p[2 * i + 1]) : 0u;
-        v[i] = lo | hi << 16;
+        const int q = off >> 2;
+        // (selected, so that the words stay in registers)
+        uint32_t x = w[i], y = w[i + 1];
+        if (q == 1) { x = w[i + 1]; y = w[i + 2]; }
+        if (q == 2) { x = w[i + 2]; y = w[i + 3]; }
+        if (q == 3) { x = w[i + 3]; y = w[i + 4 < 8 ? i + 4 : 7]; }
+        x = __funnelshift_r(x, y, (off & 2) * 8);
+        const int n = left - 2 * i;       // numbers of the pair that are the row's
+        v[i] = n >= 2 ? x : n == 1 ? x & 0xffffu : 0u;
     }
     return make_uint4(v[0], v[1], v[2], v[3]);
 }

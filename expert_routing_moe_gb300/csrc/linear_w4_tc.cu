@@ -6,11 +6,12 @@
 // operand, and the tokens' numbers come to shared memory by TMA as the B operand:
 //     D[row][token] += A[row][64] B[token][64]^T      (fp32 in TMEM)
 //
-// Warps: 0-3 and 4-7 convert the halves and write the outputs, 8 issues the
-// products, 9 copies the weights' tiles, 10 the tokens (or 10-13, with plain loads, where
-// rows of x do not start at 16-byte boundaries).
+// Warps: 0-15 convert (eight for each half, in two groups that take the steps in
+// turn) and write the outputs, 16 and 17 issue a half's products each, 18 copies the
+// weights' tiles, 19 the tokens (or 19-22, with plain loads, where rows of x do not start at 16-byte boundaries).
 // TMEM columns: D 2 x 192, A 2 halves x 2 buffers x 32.
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -33,9 +34,11 @@ constexpr int kRawOff = kB * kBBytes;
 constexpr int kSmem = kRawOff + kHalves * kRaw * kW4Bytes + 1024;   // slack for 1024-byte alignment
 constexpr int kColA = kHalves * kMaxTok;  // TMEM column of the A buffers
 constexpr int kLoaders = 4;               // warps that load x where TMA cannot
+constexpr int kConv = 16;                 // warps that convert
+constexpr int kWarpMma = kConv, kWarpW = kConv + 2, kWarpX = kConv + 3;
 
 enum Bar : int { B_WF = 0, B_WE = B_WF + kHalves * kRaw, B_AF = B_WE + kHalves * kRaw, B_AE = B_AF + 4, B_BF = B_AE + 4, B_BE = B_BF + kB,
-                 B_DF = B_BE + kB, B_DE, B_DRAIN, B_N };
+                 B_DF = B_BE + kB, B_DE, B_DRAIN, B_N = B_DRAIN + kHalves };
 enum Site : int { kSiteWFull = 41, kSiteWEmpty, kSiteAFull, kSiteAEmpty, kSiteBFull, kSiteBEmpty, kSiteDFull, kSiteDEmpty };
 
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&v)[32]) {
@@ -65,6 +68,15 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
+// A wait that is mostly over when it begins: the loop with the time limit stays out of the way.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag, moe_dev_status* st, int site) {
+    return mbar_wait(bar, parity, abort_flag, st, site);
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, moe_dev_status* st, int site) {
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(kFull, wait_long(bar, parity, abort_flag, st, site));
+}
+
 // The tiles of a CTA: row tile and first token.
 struct Tiles {
     int tok_tiles, total, tok;
@@ -73,7 +85,7 @@ struct Tiles {
 };
 
 template <bool TMA>
-__global__ void __launch_bounds__((TMA ? 11 : 10 + kLoaders) * 32, 1) linear_w4_tc_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_x, int tok) {
+__global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linear_w4_tc_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_x, int tok) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ __align__(8) uint64_t bars[B_N];
@@ -82,23 +94,23 @@ __global__ void __launch_bounds__((TMA ? 11 : 10 + kLoaders) * 32, 1) linear_w4_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kHalves * kRaw; ++i) { mbar_init(bar(B_WF + i), 1); mbar_init(bar(B_WE + i), 4); }
+        for (int i = 0; i < kHalves * kRaw; ++i) { mbar_init(bar(B_WF + i), 1); mbar_init(bar(B_WE + i), 8); }
         for (int i = 0; i < 4; ++i) { mbar_init(bar(B_AF + i), 4); mbar_init(bar(B_AE + i), 1); }
-        for (int i = 0; i < kB; ++i) { mbar_init(bar(B_BF + i), TMA ? 1 : kLoaders); mbar_init(bar(B_BE + i), 1); }
-        mbar_init(bar(B_DF), 1);
-        mbar_init(bar(B_DE), 8);
-        mbar_init(bar(B_DRAIN), 1);
+        for (int i = 0; i < kB; ++i) { mbar_init(bar(B_BF + i), TMA ? 1 : kLoaders); mbar_init(bar(B_BE + i), kHalves); }
+        mbar_init(bar(B_DF), kHalves);
+        mbar_init(bar(B_DE), kConv);
+        for (int i = 0; i < kHalves; ++i) mbar_init(bar(B_DRAIN + i), 1);
         fence_mbar_init();
         s_abort = 0;
     }
-    if (warp == 8) {
+    if (warp == kWarpMma) {
         tmem_alloc(smem_u32(&s_tmem), 512);
         tmem_relinquish();
         tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = s_tmem;             // all 512 columns are taken, so it is 0
     Tiles w;
     w.tok = tok;
     w.tok_tiles = (a.T + tok - 1) / tok;
@@ -110,7 +122,7 @@ __global__ void __launch_bounds__((TMA ? 11 : 10 + kLoaders) * 32, 1) linear_w4_
 
     pdl_wait();
     pdl_trigger();
-    if (warp == 9) {
+    if (warp == kWarpW) {
         // ---------------- weights ----------------
         if (lane == 0) {
             uint32_t n = 0;            // tiles of a half copied
@@ -133,7 +145,7 @@ __global__ void __launch_bounds__((TMA ? 11 : 10 + kLoaders) * 32, 1) linear_w4_
                     mbar_drain(bar(B_WF + i), 1);
                 }
         }
-    } else if (warp >= 10) {
+    } else if (warp >= kWarpX) {
         // ---------------- tokens ----------------
         uint32_t n = 0;
         if (TMA) {
@@ -162,7 +174,7 @@ __global__ void __launch_bounds__((TMA ? 11 : 10 + kLoaders) * 32, 1) linear_w4_
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
                     uint8_t* dst = smem + st * kBBytes;
-                    for (int u = threadIdx.x - 320; u < tok * 8; u += kLoaders * 32) {
+                    for (int u = threadIdx.x - kWarpX * 32; u < tok * 8; u += kLoaders * 32) {
                         const int r = u >> 3, seg = u & 7;
                         *reinterpret_cast<uint4*>(dst + r * 128 + ((seg ^ (r & 7)) * 16)) = load_x8(a, w.t0(i) + r, k * kStep + seg * 8);
                     }
@@ -171,116 +183,115 @@ __global__ void __launch_bounds__((TMA ? 11 : 10 + kLoaders) * 32, 1) linear_w4_
                     if (lane == 0) mbar_arrive(bar(B_BF + st));
                 }
         }
-    } else if (warp == 8) {
-        // ---------------- products ----------------
+    } else if (warp >= kWarpMma && warp < kWarpMma + kHalves) {
+        // ---------------- products: a warp for each half ----------------
+        const int m = warp - kWarpMma;
         const uint32_t idesc = idesc_bf16_f32(kW4Tile, tok);
+        const uint64_t b0 = sw128_desc(smem_u32(smem));
         uint32_t n = 0, done = 0;
-        bool issued = false;
         for (int i = first; i < w.total && ok; i += by, ++done) {
-            ok = mbar_wait(bar(B_DE), (done & 1) ^ 1, &s_abort, a.st, kSiteDEmpty);
-            ok = __all_sync(kFull, ok);
+            ok = wait_warp(bar(B_DE), (done & 1) ^ 1, &s_abort, a.st, kSiteDEmpty);
             for (int k = 0; k < steps && ok; ++k, ++n) {
                 const int st = n % kB, buf = n & 1;
-                ok = mbar_wait(bar(B_BF + st), (n / kB) & 1, &s_abort, a.st, kSiteBFull);
-                ok = __all_sync(kFull, ok);
-                for (int m = 0; m < kHalves && ok; ++m) {
-                    ok = mbar_wait(bar(B_AF + m * 2 + buf), (n >> 1) & 1, &s_abort, a.st, kSiteAFull);
-                    ok = __all_sync(kFull, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t b = sw128_desc(smem_u32(smem + st * kBBytes));
-                        const uint32_t at = tmem + kColA + (m * 2 + buf) * 32;
+                ok = wait_warp(bar(B_BF + st), (n / kB) & 1, &s_abort, a.st, kSiteBFull) &&
+                     wait_warp(bar(B_AF + m * 2 + buf), (n >> 1) & 1, &s_abort, a.st, kSiteAFull);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t b = b0 + static_cast<uint64_t>(st * (kBBytes >> 4));
+                    const uint32_t at = kColA + (m * 2 + buf) * 32;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) mma_ts(tmem + m * kMaxTok, at + x * 8, b + x * 2, idesc, k > 0 || x > 0);
-                        tc_commit(bar(B_AE + m * 2 + buf));
-                        if (m == kHalves - 1) tc_commit(bar(B_BE + st));
-                    }
-                    issued = true;
-                    __syncwarp();
+                    for (int x = 0; x < 4; ++x) mma_ts(m * kMaxTok, at + x * 8, b + x * 2, idesc, k > 0 || x > 0);
+                    tc_commit(bar(B_AE + m * 2 + buf));
+                    tc_commit(bar(B_BE + st));
                 }
+                __syncwarp();
             }
             if (ok && elect_one()) tc_commit(bar(B_DF));
             __syncwarp();
         }
-        if (!ok && issued) {           // the products in flight end before TMEM is freed
-            if (elect_one()) tc_commit(bar(B_DRAIN));
+        if (!ok && n > 0) {            // the products in flight end before TMEM is freed
+            if (elect_one()) tc_commit(bar(B_DRAIN + m));
             __syncwarp();
-            mbar_drain(bar(B_DRAIN), 0);
+            mbar_drain(bar(B_DRAIN + m), 0);
         }
     } else {
         // ---------------- weights to bf16, and the outputs ----------------
-        const int m = warp >> 2, r = (warp & 3) * 32 + lane;
+        // A group takes every other step, so its own half of the columns of each tile of weights.
+        const int m = warp >> 3, g = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        uint32_t n = 0, raw = 0, done = 0;
+        uint32_t raw = 0, done = 0;
         for (int i = first; i < w.total && ok; i += by, ++done) {
             for (int c = 0; c < a.kt && ok; ++c, ++raw) {
                 const int st = raw % kRaw;
-                ok = mbar_wait(bar(B_WF + m * kRaw + st), (raw / kRaw) & 1, &s_abort, a.st, kSiteWFull);
+                ok = wait_warp(bar(B_WF + m * kRaw + st), (raw / kRaw) & 1, &s_abort, a.st, kSiteWFull);
                 if (!ok) break;
                 const uint8_t* tile = smem + kRawOff + (m * kRaw + st) * kW4Bytes;
-                const uint2 scales = *reinterpret_cast<const uint2*>(tile + w4_scale(r, 0));
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h, ++n) {
-                    const int buf = n & 1;
-                    uint32_t v[32];
-                    const uint32_t four = h == 0 ? scales.x : scales.y;
+                const uint32_t four = *reinterpret_cast<const uint32_t*>(tile + w4_scale(r, 4 * g));
+                const uint4 run[2] = {*reinterpret_cast<const uint4*>(tile + w4_run(r, 2 * g)), *reinterpret_cast<const uint4*>(tile + w4_run(r, 2 * g + 1))};
+                uint32_t v[32];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint4 run = *reinterpret_cast<const uint4*>(tile + w4_run(r, 2 * h + x));
-                        uint32_t s[2];
-                        w4_scales(x == 0 ? four & 0xffffu : four >> 16, s[0], s[1]);
-                        const uint32_t words[4] = {run.x, run.y, run.z, run.w};
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t s[2];
+                    w4_scales(x == 0 ? four & 0xffffu : four >> 16, s[0], s[1]);
+                    const uint32_t words[4] = {run[x].x, run[x].y, run[x].z, run[x].w};
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            uint32_t f[4];
-                            w4_values(words[y], f);
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t f[4];
+                        w4_values(words[y], f);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) v[x * 16 + y * 4 + j] = bmul2(f[j], s[y / 2]);
-                        }
+                        for (int j = 0; j < 4; ++j) v[x * 16 + y * 4 + j] = bmul2(f[j], s[y / 2]);
                     }
-                    ok = mbar_wait(bar(B_AE + m * 2 + buf), ((n >> 1) & 1) ^ 1, &s_abort, a.st, kSiteAEmpty);
-                    ok = __all_sync(kFull, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                    st32(tmem + kColA + (m * 2 + buf) * 32 + lanes, v);
-                    st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_AF + m * 2 + buf));
                 }
-                if (lane == 0 && ok) mbar_arrive(bar(B_WE + m * kRaw + st));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_WE + m * kRaw + st));
+                ok = wait_warp(bar(B_AE + m * 2 + g), (raw & 1) ^ 1, &s_abort, a.st, kSiteAEmpty);
+                if (!ok) break;
+                tc_fence_after();
+                st32(kColA + (m * 2 + g) * 32 + lanes, v);
+                st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_AF + m * 2 + g));
             }
-            ok = __all_sync(kFull, ok);
             if (!ok) break;
-            ok = mbar_wait(bar(B_DF), done & 1, &s_abort, a.st, kSiteDFull);
-            ok = __all_sync(kFull, ok);
+            ok = wait_warp(bar(B_DF), done & 1, &s_abort, a.st, kSiteDFull);
             if (!ok) break;
             tc_fence_after();
             const int row = w.row(i) * kTileRows + m * kW4Tile + r, t0 = w.t0(i);
             const bool live = row < a.N;
             const float scale = (live && a.row_scale != nullptr ? a.row_scale[row] : 1.f) * kW4Up;
             const float bias = live && a.bias != nullptr ? a.bias[row] : 0.f;
-            for (int c = 0; c < tok; c += 16) {
-                uint32_t d[16];
-                tmem_ld16(tmem + m * kMaxTok + lanes + c, d);
-                tmem_ld_wait();
-                if (c + 16 >= tok) {   // D is read: the next tile's products may begin
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_DE));
-                }
+            // the groups share the tokens, 16 at a time
+            auto put = [&](auto* y, auto add) {
+                auto* p = y + static_cast<long long>(t0 + 16 * g) * a.ld_y + row;
+                for (int c = 16 * g; c < tok; c += 32, p += 32 * a.ld_y) {
+                    uint32_t d[16];
+                    tmem_ld16(m * kMaxTok + lanes + c, d);
+                    tmem_ld_wait();
+                    const int left = live ? a.T - (t0 + c) : 0;      // tokens of the 16 that there are
+                    auto* q = p;
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const int t = t0 + c + x;
-                    if (!live || t >= a.T) continue;
-                    put_y(a, t, row, __uint_as_float(d[x]) * scale + bias);
+                    for (int x = 0; x < 16; ++x, q += a.ld_y) {
+                        float v = fmaf(__uint_as_float(d[x]), scale, bias);
+                        if (x < left) {
+                            if constexpr (decltype(add)::value) v += *q;
+                            if constexpr (sizeof(*q) == 2) *q = __float2bfloat16_rn(v);
+                            else *q = v;
+                        }
+                    }
                 }
-            }
+            };
+            if (a.y_bf16) put(static_cast<__nv_bfloat16*>(a.y), std::false_type());
+            else if (a.add) put(static_cast<float*>(a.y), std::true_type());
+            else put(static_cast<float*>(a.y), std::false_type());
+            tc_fence_before();         // D is read: the next tile's products may begin
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_DE));
         }
     }
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -306,20 +317,21 @@ cudaError_t launch(const LinearArgs& a, int tok, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const long long tiles = static_cast<long long>((a.N + kTileRows - 1) / kTileRows) * ((a.T + tok - 1) / tok);
-    return launch_pdl(k, dim3(static_cast<unsigned>(tiles < sm_count() ? tiles : sm_count())), dim3((TMA ? 11 : 10 + kLoaders) * 32), kSmem, s, a, map, tok);
+    return launch_pdl(k, dim3(static_cast<unsigned>(tiles < sm_count() ? tiles : sm_count())), dim3((kWarpX + (TMA ? 1 : kLoaders)) * 32), kSmem, s, a, map, tok);
 }
 
 }  // namespace
 
-// Tokens of a tile: as many as make the longest CTA's time shortest.  A step of 64 columns takes 4 clocks a
-// token of the products, or some 380 for the conversion of its weights, and a tile its outputs.
+// Tokens of a tile: as many as make the longest CTA's time shortest.  A step of 64 columns takes 4 clocks a token and
+// some 100 more, or 630 for the conversion of its weights, whichever is longer, and a tile its outputs.  (2001 tokens through 5120 x
+// 2048 with 64, 96, 128, 144, 160 tokens a tile: 58.0, 37.6, 39.2, 28.1, 29.8 us; 8192 tokens with 128, 144, 160: 112, 104, 98 us.)
 cudaError_t launch_linear_w4_tc(const LinearArgs& a, cudaStream_t s) {
     const long long rows = (a.N + kTileRows - 1) / kTileRows;
     int best = 16;
     double least = 1e300;
     for (int tok = 16; tok <= kMaxTok; tok += 16) {
         const long long tiles = rows * ((a.T + tok - 1) / tok), waves = (tiles + sm_count() - 1) / sm_count();
-        const double step = 4.0 * tok > 380.0 ? 4.0 * tok : 380.0;
+        const double step = 4.0 * tok + 100.0 > 630.0 ? 4.0 * tok + 100.0 : 630.0;
         const double time = static_cast<double>(waves) * (2.0 * a.kt * step + 1500.0 + 12.0 * tok);
         if (time < least) { least = time; best = tok; }
     }

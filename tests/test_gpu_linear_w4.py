@@ -37,7 +37,8 @@ def _check(y, ref, dtype):
 
 SIZES = [(1, 1, 1), (1, 31, 16), (1, 128, 128), (2, 33, 17), (7, 200, 129), (8, 1000, 500), (9, 130, 2048), (16, 515, 640), (17, 96, 1000), (5, 5000, 384),
          (31, 257, 256), (32, 64, 1100), (33, 300, 130), (64, 129, 512), (65, 1027, 200), (100, 40, 3001), (129, 260, 448), (257, 385, 320), (300, 700, 96),
-         (3, 40, 9000), (12, 40, 5000), (40, 40, 9000), (1, 20, 20011), (1500, 130, 72)]
+         (3, 40, 9000), (12, 40, 5000), (40, 40, 9000), (1, 20, 20011), (1500, 130, 72),
+         (2001, 5000, 128), (700, 20000, 200), (800, 9001, 75)]
 
 
 @pytest.mark.parametrize("T,N,K", SIZES)
