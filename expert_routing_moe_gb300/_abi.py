@@ -162,7 +162,7 @@ def load(path: str = LIB_PATH):
 
 
 def _load_fastcall(L):
-    """The C module that makes the attention operators' calls; built beside
+    """The C module that makes the calls of a decoder's step; built beside
     the library, so it is there when the library is."""
     global _fast
     from . import _fastcall
@@ -170,7 +170,8 @@ def _load_fastcall(L):
     # (a torch built without CUDA has no raw stream to read: every tensor is refused before it is asked for)
     _fastcall.setup(torch.bfloat16, torch.float32, torch.int32, torch.uint8, getattr(torch._C, "_cuda_getCurrentRawStream", None),
                     *(addr(f) for f in (L.moe_qk_norm_rope, L.moe_kv4_read, L.moe_attention_kv4, L.moe_kv4_reserve,
-                                        L.moe_kv4_assign, L.moe_kv4_compact)))
+                                        L.moe_kv4_assign, L.moe_kv4_compact, L.moe_kv4_weigh, L.moe_kv4_evict, L.moe_linear_w4,
+                                        L.moe_verify_drafts)))
     _fast = _fastcall
 
 
@@ -430,7 +431,7 @@ class Kv4Cache:
         for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t is not None and t.numel() != self.n_kv:
                 raise MoeError("%s: expected %d numbers" % (what, self.n_kv))
-        self.head_dim, self.S = head_dim, seq_len.shape[0]
+        self.head_dim, self.S, self.max_pages = head_dim, seq_len.shape[0], page_table.shape[1]
         self.tensors = (pages, page_table, seq_len, k_scale, v_scale)
         i32, f32 = torch.int32, torch.float32
         self._c = _Kv4CacheParams(_addr(pages, torch.uint8, "pages"), _addr(page_table, i32, "page_table"),
@@ -474,6 +475,7 @@ class Kv4Pool:
             raise MoeError("page_table is [S][max_pages], seq_len [S] and ref [n_pages]")
         self.tensors = (pages, page_table, seq_len, ref)
         self.head_dim, self.n_layers, self.n_pages, self.S = head_dim, pages.shape[0], pages.shape[1], seq_len.numel()
+        self.max_pages = page_table.shape[1]
         i32 = torch.int32
         page_bytes = pages.shape[2] * pages.shape[3]
         self._c = _Kv4PoolParams(_addr(pages, torch.uint8, "pages"), self.n_pages * page_bytes, page_bytes,
@@ -664,11 +666,11 @@ def moe_kv4_compact(pool: Kv4Pool, n_live, workspace, st=None, stream=None):
 # Eviction from the cache by the attention that its tokens draw
 # ---------------------------------------------------------------------------
 def kv4_weigh_workspace(cache: Kv4Cache, T: int, n_q: int) -> int:
-    return int(load().moe_kv4_weigh_workspace(cache.S, T, n_q, cache.n_kv, cache.head_dim, cache._c.max_pages))
+    return int(load().moe_kv4_weigh_workspace(cache.S, T, n_q, cache.n_kv, cache.head_dim, cache.max_pages))
 
 
 def kv4_evict_workspace(pool: Kv4Pool) -> int:
-    return int(load().moe_kv4_evict_workspace(pool.S, pool._c.max_pages, pool.n_pages))
+    return int(load().moe_kv4_evict_workspace(pool.S, pool.max_pages, pool.n_pages))
 
 
 def _scores(score, S: int, max_pages: int):
@@ -690,6 +692,13 @@ def moe_kv4_weigh(q, cache: Kv4Cache, q_start, lse, score, scale: float, max_new
     entries of the rows' own tokens are set instead.  workspace:
     kv4_weigh_workspace(...) bytes, zero-filled before its first use; when omitted a buffer
     is allocated for this call (not graph-capturable)."""
+    if _fast is None:
+        load()
+    rc = _fast.weigh(q, cache, q_start, lse, score, scale, max_new, window, last, fresh, workspace, st) if stream is None else None
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        _check(rc, "moe_kv4_weigh")
     D = cache.head_dim
     if q.dim() != 3 or q.shape[2] != D:
         raise MoeError("q: expected [T][n_q][%d], got %s" % (D, list(q.shape)))
@@ -697,7 +706,7 @@ def moe_kv4_weigh(q, cache: Kv4Cache, q_start, lse, score, scale: float, max_new
     qp, ld_q = _rows(q, T, n_q * D, torch.bfloat16, "q")
     if lse.numel() != T * n_q:
         raise MoeError("lse: expected [%d][%d]" % (T, n_q))
-    sp, ld_s = _scores(score, cache.S, cache._c.max_pages)
+    sp, ld_s = _scores(score, cache.S, cache.max_pages)
     if workspace is None:
         n = kv4_weigh_workspace(cache, T, n_q)
         if n:
@@ -715,7 +724,14 @@ def moe_kv4_evict(pool: Kv4Pool, score, budget, sinks: int, recent: int, workspa
     64 or more] fp32, moved to its front in every layer with their scores; the pages behind are
     released.  kept [S][any] int32 out (or None): the place that each token had, -1 behind.
     workspace: kv4_evict_workspace(pool) bytes."""
-    sp, ld_s = _scores(score, pool.S, pool._c.max_pages)
+    if _fast is None:
+        load()
+    rc = _fast.evict(pool, score, budget, sinks, recent, workspace, kept, st) if stream is None else None
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        _check(rc, "moe_kv4_evict")
+    sp, ld_s = _scores(score, pool.S, pool.max_pages)
     kp, ld_k = None, 0
     if kept is not None:
         if kept.dim() != 2 or kept.shape[0] != pool.S:
@@ -774,6 +790,13 @@ def moe_w4_pack(w, out: Weight4, st=None, stream=None):
 def moe_linear_w4(x, w: Weight4, y, bias=None, accumulate: bool = False, st=None, stream=None):
     """y [T][N] = x [T][K] w^T + bias: x bf16, y bf16 or fp32, bias [N] fp32 or None; rows
     may be strided.  accumulate: added to y (fp32)."""
+    if _fast is None:
+        load()
+    rc = _fast.linear(x, w, y, bias, accumulate, st) if stream is None else None
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        _check(rc, "moe_linear_w4")
     T = x.shape[0]
     xp, ld_x = _rows(x, T, w.K, torch.bfloat16, "x")
     code = _dtype_code(y)
@@ -803,6 +826,13 @@ def moe_verify_drafts(logits, tokens, uniform, q_start, accepted, next_token, n_
     (None: 1; 0: greedy).  Out, [S] int32: accepted drafts, the token that follows, and n_new =
     accepted - drafts, which moe_kv4_reserve takes to cut the refused ones.  workspace:
     verify_workspace(...) bytes; when omitted a buffer is allocated for this call."""
+    if _fast is None:
+        load()
+    rc = _fast.verify(logits, tokens, uniform, q_start, accepted, next_token, n_new, draft_logits, temperature, workspace, st) if stream is None else None
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        _check(rc, "moe_verify_drafts")
     if logits.dim() != 2:
         raise MoeError("logits: expected [T][V], got %s" % list(logits.shape))
     T, V = logits.shape

@@ -1,5 +1,5 @@
-/* fastcall.c -- a CPython module that makes the attention operators' calls
- * from PyTorch tensors without ctypes.
+/* fastcall.c -- a CPython module that makes the calls of the operators that run
+ * at every step of a decoder from PyTorch tensors without ctypes.
  *
  * At decode sizes a call's kernels take a few microseconds, and reading the
  * tensors' attributes in Python and converting twenty arguments through ctypes
@@ -17,7 +17,7 @@
 #include "../../include/moe_gb300.h"
 
 static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_numel, *s_get_device, *s_ref, *s_S,
-    *s_n_kv, *s_head_dim, *s_T;
+    *s_n_kv, *s_head_dim, *s_T, *s_N, *s_K, *s_max_pages;
 static PyObject *t_bf16, *t_f32, *t_i32, *t_u8, *f_stream; /* torch.bfloat16, ..., torch._C._cuda_getCurrentRawStream */
 
 /* The entry points, as addresses that setup() is given. */
@@ -29,6 +29,14 @@ static moe_status_t (*p_attention)(const void*, long long, int, int, const moe_k
 static moe_status_t (*p_reserve)(const moe_kv4_pool*, const int32_t*, void*, size_t, moe_dev_status*, void*);
 static moe_status_t (*p_assign)(const moe_kv4_pool*, const int32_t*, moe_dev_status*, void*);
 static moe_status_t (*p_compact)(const moe_kv4_pool*, int32_t*, void*, size_t, moe_dev_status*, void*);
+
+static moe_status_t (*p_weigh)(const void*, long long, int, int, const moe_kv4_cache*, const int32_t*, int, const float*, float, int, int, float*,
+                               long long, int, void*, size_t, moe_dev_status*, void*);
+static moe_status_t (*p_evict)(const moe_kv4_pool*, int, float*, long long, const int32_t*, int, int, int32_t*, long long, void*, size_t,
+                               moe_dev_status*, void*);
+static moe_status_t (*p_linear)(const void*, long long, int, const moe_w4*, const float*, void*, int, long long, int, moe_dev_status*, void*);
+static moe_status_t (*p_verify)(const void*, int, long long, int, int, const int32_t*, const float*, const int32_t*, int, const void*, long long,
+                                const float*, int32_t*, int32_t*, int32_t*, void*, size_t, moe_dev_status*, void*);
 
 /* Whether an attribute is that very object. */
 static int attr_is(PyObject* o, PyObject* name, PyObject* want) {
@@ -220,16 +228,101 @@ static PyObject* reserve(PyObject* s, PyObject* const* a, Py_ssize_t n) { (void)
 static PyObject* assign(PyObject* s, PyObject* const* a, Py_ssize_t n) { (void)s; return pool_call(a, n, 1); }
 static PyObject* compact(PyObject* s, PyObject* const* a, Py_ssize_t n) { (void)s; return pool_call(a, n, 2); }
 
-/* setup(torch.bfloat16, torch.float32, torch.int32, torch.uint8, raw-stream function, six addresses) */
+/* A score for every place of the tables: rows of max_pages * 64 numbers or more. */
+static int scores(PyObject* t, long long S, long long max_pages, void** out, long long* ld) {
+    long long n, w;
+    return rows(t, t_f32, out, &n, &w, ld) && n == S && w >= max_pages * MOE_KV4_PAGE;
+}
+
+/* q, cache, q_start, lse, score, scale, max_new, window, last, fresh, workspace, st */
+static PyObject* weigh(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    void *q, *cache, *qs, *lse, *score, *ws, *st, *stream;
+    long long T, w, ld, ld_s, S, D, mp, bytes, n_q;
+    (void)self;
+    if (n != 12) return decline();
+    const double scale = PyFloat_AsDouble(a[5]);
+    const long long max_new = PyLong_AsLongLong(a[6]), window = PyLong_AsLongLong(a[7]), last = PyLong_AsLongLong(a[8]);
+    const int fresh = PyObject_IsTrue(a[9]);
+    if (PyErr_Occurred() || fresh < 0 || !fits_int(max_new) || !fits_int(window) || !fits_int(last)) return decline();
+    if (!handle(a[1], &cache) || cache == NULL || !attr_int(a[1], s_S, &S) || !attr_int(a[1], s_head_dim, &D) || !attr_int(a[1], s_max_pages, &mp))
+        return decline();
+    if (!rows(a[0], t_bf16, &q, &T, &w, &ld) || D < 1 || w % D != 0 || !fits_int(T) || !fits_int(w)) return decline();
+    n_q = w / D;
+    if (a[2] == Py_None || !dense(a[2], t_i32, S + 1, &qs) || a[3] == Py_None || !dense(a[3], t_f32, T * n_q, &lse)) return decline();
+    if (!scores(a[4], S, mp, &score, &ld_s)) return decline();
+    if (a[10] == Py_None || !dense(a[10], t_u8, -1, &ws) || !method_int(a[10], s_numel, &bytes)) return decline();
+    if (!status(a[11], &st) || !current_stream(a[0], &stream)) return decline();
+    return PyLong_FromLong(p_weigh(q, ld, (int)T, (int)n_q, cache, qs, (int)max_new, lse, (float)scale, (int)window, (int)last, score, ld_s, fresh,
+                                   ws, (size_t)bytes, st, stream));
+}
+
+/* pool, score, budget, sinks, recent, workspace, kept, st */
+static PyObject* evict(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    void *pool, *score, *budget, *ws, *kept = NULL, *st, *stream;
+    long long S, D, mp, ld_s, bytes, nk, wk, ld_k = 0;
+    (void)self;
+    if (n != 8) return decline();
+    const long long sinks = PyLong_AsLongLong(a[3]), recent = PyLong_AsLongLong(a[4]);
+    if (PyErr_Occurred() || !fits_int(sinks) || !fits_int(recent)) return decline();
+    if (!handle(a[0], &pool) || pool == NULL || !attr_int(a[0], s_S, &S) || !attr_int(a[0], s_head_dim, &D) || !attr_int(a[0], s_max_pages, &mp))
+        return decline();
+    if (!scores(a[1], S, mp, &score, &ld_s) || a[2] == Py_None || !dense(a[2], t_i32, S, &budget)) return decline();
+    if (a[5] == Py_None || !dense(a[5], t_u8, -1, &ws) || !method_int(a[5], s_numel, &bytes)) return decline();
+    if (a[6] != Py_None && (!rows(a[6], t_i32, &kept, &nk, &wk, &ld_k) || nk != S || (nk > 1 && ld_k != wk))) return decline();
+    if (kept != NULL) ld_k = wk;
+    if (!status(a[7], &st) || !current_stream(a[2], &stream)) return decline();
+    return PyLong_FromLong(p_evict(pool, (int)D, score, ld_s, budget, (int)sinks, (int)recent, kept, ld_k, ws, (size_t)bytes, st, stream));
+}
+
+/* x, w, y, bias, accumulate, st */
+static PyObject* linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    void *x, *w, *y, *bias, *st, *stream;
+    long long N, K, T, wx, ld_x, Ty, wy, ld_y;
+    (void)self;
+    if (n != 6 || !handle(a[1], &w) || w == NULL || !attr_int(a[1], s_N, &N) || !attr_int(a[1], s_K, &K)) return decline();
+    const int add = PyObject_IsTrue(a[4]), bf = attr_is(a[2], s_dtype, t_bf16);
+    if (add < 0 || (add && bf)) return decline();
+    if (!rows(a[0], t_bf16, &x, &T, &wx, &ld_x) || wx != K || !fits_int(T)) return decline();
+    if (!rows(a[2], bf ? t_bf16 : t_f32, &y, &Ty, &wy, &ld_y) || Ty != T || wy != N) return decline();
+    if (!dense(a[3], t_f32, N, &bias) || !status(a[5], &st) || !current_stream(a[0], &stream)) return decline();
+    return PyLong_FromLong(p_linear(x, ld_x, (int)T, w, bias, y, bf ? MOE_DTYPE_BF16 : MOE_DTYPE_F32, ld_y, add, st, stream));
+}
+
+/* logits, tokens, uniform, q_start, accepted, next, n_new, draft_logits, temperature, workspace, st */
+static PyObject* verify(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    void *l, *d = NULL, *tokens, *uniform, *qs, *acc, *next, *n_new, *temp, *ws, *st, *stream;
+    long long T, V, ld, Td, Vd, ld_d = 0, S, bytes;
+    (void)self;
+    if (n != 11) return decline();
+    const int bf = attr_is(a[0], s_dtype, t_bf16);
+    PyObject* dt = bf ? t_bf16 : t_f32;
+    if (!rows(a[0], dt, &l, &T, &V, &ld) || !fits_int(T) || !fits_int(V)) return decline();
+    PyObject* shape = PyObject_GetAttr(a[0], s_shape);
+    if (shape == NULL) return decline();
+    const Py_ssize_t dims = PyTuple_Check(shape) ? PyTuple_GET_SIZE(shape) : 0;
+    Py_DECREF(shape);
+    if (dims != 2) return decline();
+    if (a[7] != Py_None && (!rows(a[7], dt, &d, &Td, &Vd, &ld_d) || Td != T || Vd != V)) return decline();
+    if (a[4] == Py_None || !method_int(a[4], s_numel, &S) || !fits_int(S)) return decline();
+    if (a[1] == Py_None || !dense(a[1], t_i32, T, &tokens) || a[2] == Py_None || !dense(a[2], t_f32, T, &uniform)) return decline();
+    if (a[3] == Py_None || !dense(a[3], t_i32, S + 1, &qs) || !dense(a[4], t_i32, S, &acc) || a[5] == Py_None || !dense(a[5], t_i32, S, &next)) return decline();
+    if (!dense(a[6], t_i32, S, &n_new) || !dense(a[8], t_f32, S, &temp)) return decline();
+    if (a[9] == Py_None || !dense(a[9], t_u8, -1, &ws) || !method_int(a[9], s_numel, &bytes)) return decline();
+    if (!status(a[10], &st) || !current_stream(a[0], &stream)) return decline();
+    return PyLong_FromLong(p_verify(l, bf ? MOE_DTYPE_BF16 : MOE_DTYPE_F32, ld, (int)T, (int)V, tokens, uniform, qs, (int)S, d, ld_d, temp, acc, next,
+                                    n_new, ws, (size_t)bytes, st, stream));
+}
+
+/* setup(torch.bfloat16, torch.float32, torch.int32, torch.uint8, raw-stream function, ten addresses) */
 static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    uintptr_t p[6];
+    uintptr_t p[10];
     int i;
     (void)self;
-    if (n != 11) {
-        PyErr_SetString(PyExc_TypeError, "setup takes eleven arguments");
+    if (n != 15) {
+        PyErr_SetString(PyExc_TypeError, "setup takes fifteen arguments");
         return NULL;
     }
-    for (i = 0; i < 6; ++i) p[i] = (uintptr_t)PyLong_AsUnsignedLongLong(a[5 + i]);
+    for (i = 0; i < 10; ++i) p[i] = (uintptr_t)PyLong_AsUnsignedLongLong(a[5 + i]);
     if (PyErr_Occurred()) return NULL;
     t_bf16 = Py_NewRef(a[0]);
     t_f32 = Py_NewRef(a[1]);
@@ -242,6 +335,10 @@ static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     memcpy(&p_reserve, &p[3], sizeof p[0]);
     memcpy(&p_assign, &p[4], sizeof p[0]);
     memcpy(&p_compact, &p[5], sizeof p[0]);
+    memcpy(&p_weigh, &p[6], sizeof p[0]);
+    memcpy(&p_evict, &p[7], sizeof p[0]);
+    memcpy(&p_linear, &p[8], sizeof p[0]);
+    memcpy(&p_verify, &p[9], sizeof p[0]);
     Py_RETURN_NONE;
 }
 
@@ -253,6 +350,10 @@ static PyMethodDef methods[] = {
     {"reserve", (PyCFunction)(void (*)(void))reserve, METH_FASTCALL, NULL},
     {"assign", (PyCFunction)(void (*)(void))assign, METH_FASTCALL, NULL},
     {"compact", (PyCFunction)(void (*)(void))compact, METH_FASTCALL, NULL},
+    {"weigh", (PyCFunction)(void (*)(void))weigh, METH_FASTCALL, NULL},
+    {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, NULL},
+    {"linear", (PyCFunction)(void (*)(void))linear, METH_FASTCALL, NULL},
+    {"verify", (PyCFunction)(void (*)(void))verify, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
@@ -266,7 +367,8 @@ PyMODINIT_FUNC PyInit__fastcall(void) {
                  {&s_numel, "numel"},       {&s_get_device, "get_device"},
                  {&s_ref, "_ref"},          {&s_S, "S"},
                  {&s_n_kv, "n_kv"},         {&s_head_dim, "head_dim"},
-                 {&s_T, "T"}};
+                 {&s_T, "T"},               {&s_N, "N"},
+                 {&s_K, "K"},               {&s_max_pages, "max_pages"}};
     size_t i;
     for (i = 0; i < sizeof names / sizeof names[0]; ++i) {
         *names[i].to = PyUnicode_InternFromString(names[i].name);

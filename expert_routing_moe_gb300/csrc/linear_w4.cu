@@ -23,8 +23,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 32;           // of a CTA's step
-constexpr int kRedLd = 36;          // rows of a token's sums, padded: no two lanes of a store share a bank
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -42,33 +40,50 @@ __device__ __forceinline__ void store_y(const LinearArgs& a, int t, int n, float
     put_y(a, t, n, a.bias != nullptr ? v + a.bias[n] : v);
 }
 
-// What a lane holds of 32 rows and 128 columns: rows g + 8 i, columns 32 t .. 32 t + 31.
+// What a lane holds of 16 MT rows and 128 columns: rows g + 8 i, columns 32 t .. 32 t + 31.
+template <int MT>
 struct Piece {
-    uint4 w[4];
-    uint32_t s[4];     // two scales each
+    uint4 w[2 * MT];
+    uint32_t s[2 * MT];     // two scales each
 };
-__device__ __forceinline__ void load_piece(Piece& p, const LinearArgs& a, int row0, int c, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    const uint8_t* tile = a.tiles + (static_cast<long long>(row0 / kW4Tile) * a.kt + c) * kW4Bytes;
-    const int r = row0 % kW4Tile + g;
+template <int MT>
+__device__ __forceinline__ const uint8_t* piece_at(const LinearArgs& a, int row0, int c) {
+    return a.tiles + (static_cast<long long>(row0 / kW4Tile) * a.kt + c) * kW4Bytes;
+}
+template <int MT>
+__device__ __forceinline__ void load_piece(Piece<MT>& p, const LinearArgs& a, int row0, int c, int lane) {
+    const int g = lane >> 2, t = lane & 3, r = row0 % kW4Tile + g;
+    const uint8_t* tile = piece_at<MT>(a, row0, c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * MT; ++i) {
         p.w[i] = ldg_stream(tile + w4_run(r + 8 * i, t));
         p.s[i] = __ldg(reinterpret_cast<const uint16_t*>(tile + w4_scale(r + 8 * i, 2 * t)));
     }
 }
 
-// NT: groups of eight tokens.  STAGED: x lies in shared memory as operands, else each warp loads it as it goes.
-template <int NT, bool STAGED>
+// NT: groups of eight tokens.  MT: groups of 16 rows of a step.  STAGED: x lies in shared memory as operands (a CTA with more
+// than one step), else each warp loads its columns as it goes.
+template <int NT, int MT, bool STAGED>
 __global__ void __launch_bounds__(kThreads) linear_w4_kernel(const LinearArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    float* red = reinterpret_cast<float*>(smem);                       // [2][warps][tokens][kRedLd]
+    constexpr int kRows = 16 * MT, kRedLd = kRows + 4;                 // padded: no two lanes of a store share a bank
     constexpr int kRed = kWarps * 8 * NT * kRedLd;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* red = reinterpret_cast<float*>(smem);                       // [STAGED ? 2 : 1][warps][tokens][kRedLd]
     uint4* xs = reinterpret_cast<uint4*>(smem + 2 * kRed * sizeof(float));   // [column tile][word][NT][lane]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int t0 = blockIdx.y * 8 * NT;
+    const int stride = gridDim.x * kRows;
+    int row = blockIdx.x * kRows, c = warp;                            // the next piece
+    // weights on their way to L2 while the kernel before ends (L2 is where everybody's writes meet, so nothing stale is kept)
+    for (int k = warp; k < a.kt; k += kWarps) {
+        const uint8_t* tile = piece_at<MT>(a, row, k) + row % kW4Tile / 8 * 512;
+        for (int i = lane * 128; i < 2 * MT * 512; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(tile + i));
+        if (lane == 31) asm volatile("prefetch.global.L2 [%0];" ::"l"(piece_at<MT>(a, row, k) + w4_scale(row % kW4Tile, 0)));
+    }
     pdl_wait();
     pdl_trigger();
+    Piece<MT> next;
+    if (c < a.kt) load_piece<MT>(next, a, row, c, lane);
     if constexpr (STAGED) {
         const int per = a.kt * 16;                                     // runs of eight columns of a token
         for (int i = threadIdx.x; i < per * 8 * NT; i += kThreads) {
@@ -79,36 +94,49 @@ __global__ void __launch_bounds__(kThreads) linear_w4_kernel(const LinearArgs a)
         __syncthreads();
     }
     int buf = 0;
-    for (int row0 = blockIdx.x * kRows; row0 < a.N; row0 += gridDim.x * kRows, buf ^= 1) {
-        float acc[2][NT][4];
+    for (int row0 = row; row0 < a.N; row0 += stride, buf ^= 1) {
+        float acc[MT][NT][4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-        for (int c = warp; c < a.kt; c += kWarps) {
-            Piece p;
-            load_piece(p, a, row0, c, lane);
-            uint32_t s[4][2];
+        for (int cc = warp; cc < a.kt; cc += kWarps) {
+            const Piece<MT> p = next;
+            c += kWarps;
+            if (c >= a.kt) { c = warp; row += stride; }
+            if (row < a.N) load_piece<MT>(next, a, row, c, lane);
+            uint4 x[STAGED ? 1 : 4][NT];
+            if constexpr (!STAGED) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w4_scales(p.s[i], s[i][0], s[i][1]);
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int k = cc * kW4Tile + 32 * t + 8 * w, tok = t0 + 8 * n + g;
+                        if (a.wide && (cc + 1) * kW4Tile <= a.K)
+                            x[w][n] = tok < a.T ? __ldg(reinterpret_cast<const uint4*>(a.x + tok * a.ld_x + k)) : make_uint4(0u, 0u, 0u, 0u);
+                        else
+                            x[w][n] = load_x8(a, tok, k);
+                    }
+            }
+            uint32_t s[2 * MT][2];
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) w4_scales(p.s[i], s[i][0], s[i][1]);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                uint32_t f[4][4];
+                uint32_t f[2 * MT][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2 * MT; ++i) {
                     w4_values(w == 0 ? p.w[i].x : w == 1 ? p.w[i].y : w == 2 ? p.w[i].z : p.w[i].w, f[i]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) f[i][j] = bmul2(f[i][j], s[i][w / 2]);
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    uint4 b;
-                    if constexpr (STAGED) b = xs[((c * 4 + w) * NT + n) * 32 + lane];
-                    else b = load_x8(a, t0 + 8 * n + g, c * kW4Tile + 32 * t + 8 * w);
+                    const uint4 b = STAGED ? xs[((cc * 4 + w) * NT + n) * 32 + lane] : x[STAGED ? 0 : w][n];
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
+                    for (int m = 0; m < MT; ++m) {
                         mma_bf16(acc[m][n], f[2 * m][0], f[2 * m + 1][0], f[2 * m][1], f[2 * m + 1][1], b.x, b.y);
                         mma_bf16(acc[m][n], f[2 * m][2], f[2 * m + 1][2], f[2 * m][3], f[2 * m + 1][3], b.z, b.w);
                     }
@@ -117,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) linear_w4_kernel(const LinearArgs a)
         }
         float* mine = red + buf * kRed + warp * 8 * NT * kRedLd;
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -197,13 +225,25 @@ __global__ void __launch_bounds__(kThreads) w4_pack_kernel(const W* w, long long
     }
 }
 
-template <int NT, bool STAGED>
+template <int NT, int MT, bool STAGED>
 cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
-    const size_t smem = 2 * kWarps * 8 * NT * kRedLd * sizeof(float) + (STAGED ? static_cast<size_t>(a.kt) * kW4Tile * 16 * NT : 0);
-    cudaError_t e = cudaFuncSetAttribute(linear_w4_kernel<NT, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    constexpr int rows = 16 * MT;
+    const size_t red = kWarps * 8 * NT * (rows + 4) * sizeof(float);
+    const size_t smem = 2 * red + (STAGED ? static_cast<size_t>(a.kt) * kW4Tile * 16 * NT : 0);
+    cudaError_t e = cudaFuncSetAttribute(linear_w4_kernel<NT, MT, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    const int steps = (a.N + kRows - 1) / kRows, most = 2 * sm_count();
-    return launch_pdl(linear_w4_kernel<NT, STAGED>, dim3(steps < most ? steps : most, (a.T + 8 * NT - 1) / (8 * NT)), dim3(kThreads), smem, s, a);
+    const int steps = (a.N + rows - 1) / rows, fit = static_cast<int>((227 * 1024) / (smem + 1024));
+    const int most = STAGED ? (fit < 3 ? fit : 3) * sm_count() : steps;
+    return launch_pdl(linear_w4_kernel<NT, MT, STAGED>, dim3(steps < most ? steps : most, (a.T + 8 * NT - 1) / (8 * NT)), dim3(kThreads), smem, s, a);
+}
+
+template <int NT>
+cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
+    // few rows: every CTA has one step, of 16 rows where 32 would leave SMs without any
+    const int sms = sm_count();
+    if (a.N <= 16 * sms * 2) return launch_few<NT, 1, false>(a, s);
+    if (a.N <= 32 * sms * 3 || static_cast<size_t>(a.kt) * kW4Tile * 16 * NT > 128 * 1024) return launch_few<NT, 2, false>(a, s);
+    return launch_few<NT, 2, true>(a, s);
 }
 
 }  // namespace
@@ -226,9 +266,9 @@ cudaError_t launch_linear_w4(const void* x, long long ld_x, int T, const moe_w4&
     a.y_bf16 = y_dtype == MOE_DTYPE_BF16;
     a.add = add;
     a.wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ld_x % 8 == 0;
-    if (T > 64 || a.kt > 64) return launch_linear_w4_tc(a, s);
-    if (T <= 8) return a.kt <= 64 ? launch_few<1, true>(a, s) : launch_few<1, false>(a, s);
-    return a.kt <= 32 ? launch_few<2, true>(a, s) : launch_few<2, false>(a, s);
+    if (T > 64) return launch_linear_w4_tc(a, s);
+    if (T <= 8) return launch_few<1>(a, s);
+    return T <= 16 ? launch_few<2>(a, s) : launch_few<4>(a, s);
 }
 
 cudaError_t launch_w4_pack(const void* w, int dtype, long long ld, int N, int K, void* tiles, float* row_scale, moe_dev_status* st, cudaStream_t s) {
