@@ -690,8 +690,8 @@ def moe_kv4_weigh(q, cache: Kv4Cache, q_start, lse, score, scale: float, max_new
     (those of moe_attention_kv4, with its lse [T][n_q] fp32) to score [S][max_pages * 64
     or more] fp32: only of each sequence's last `last` rows where that is not 0.  fresh: the
     entries of the rows' own tokens are set instead.  workspace:
-    kv4_weigh_workspace(...) bytes, zero-filled before its first use; when omitted a buffer
-    is allocated for this call (not graph-capturable)."""
+    kv4_weigh_workspace(...) bytes; when omitted a buffer is allocated for this call (not
+    graph-capturable)."""
     if _fast is None:
         load()
     rc = _fast.weigh(q, cache, q_start, lse, score, scale, max_new, window, last, fresh, workspace, st) if stream is None else None
@@ -711,7 +711,7 @@ def moe_kv4_weigh(q, cache: Kv4Cache, q_start, lse, score, scale: float, max_new
         n = kv4_weigh_workspace(cache, T, n_q)
         if n:
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-                workspace = torch.zeros(n, dtype=torch.uint8, device=q.device)
+                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     rc = load().moe_kv4_weigh(qp, ld_q, T, n_q, cache._ref, _check_starts(q_start, cache.S), max_new, _addr(lse, torch.float32, "lse"),
                               scale, window, last, sp, ld_s, 1 if fresh else 0, _addr(workspace, None, "workspace"), _bytes(workspace),
                               _status(st), _raw_stream(stream, q))

@@ -8,9 +8,8 @@
 // sum a token is left to add across lanes and warps, in a fixed order.
 #include <cuda_bf16.h>
 
-#include "attn_kv4.cuh"
 #include "common.cuh"
-#include "kv4.cuh"
+#include "kv4_weigh.cuh"
 #include "launch.h"
 #include "tmap.h"
 
@@ -20,21 +19,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-
-struct WeighArgs {
-    const __nv_bfloat16* q;
-    long long ld_q;
-    int T, n_q, group;
-    moe_kv4_cache c;
-    const int32_t* q_start;
-    const float* lse;
-    float scale;
-    int window, last;
-    float* score;
-    long long ld_score;
-    bool fresh;
-    moe_dev_status* st;
-};
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -50,7 +34,7 @@ struct Queries {
     float up, z;                 // the scores' factor and the row's log-sum-exp, in powers of two; of row g
 };
 template <int D>
-__device__ __forceinline__ void load_rows(Queries<D>& w, const WeighArgs& a, const Seq& s, int h, int r0, int lane, float k_scale) {
+__device__ __forceinline__ void load_rows(Queries<D>& w, const WeighArgs& a, const WeighSeq& s, int h, int r0, int lane, float k_scale) {
     const int g = lane >> 2, t = lane & 3, r = r0 + g;
     const bool live = r < s.n * a.group;
     uint32_t raw[D / 8];
@@ -95,20 +79,10 @@ __global__ void __launch_bounds__(kThreads) kv4_weigh_kernel(const WeighArgs a) 
     pdl_wait();
     pdl_trigger();
     for (int s = blockIdx.y; s < a.c.S; s += gridDim.y) {
-        Seq q;
-        q.q0 = a.q_start[s];
-        const int q1 = a.q_start[s + 1];
-        q.len = a.c.seq_len[s];
-        if (!rows_fit(q.q0, q1, q.len, a.T, a.c.max_pages)) {
-            if (blockIdx.x == 0 && threadIdx.x == 0) report(a.st, MOE_DEV_BAD_INDEX, s);
-            continue;
-        }
-        q.n = q1 - q.q0;
-        if (q.n == 0 || q.len == 0) continue;
-        const int i0 = a.last > 0 && a.last < q.n ? q.n - a.last : 0;      // the first row that counts
-        const int p0 = q.len - q.n + i0, first_new = max(0, q.len - q.n);
-        int lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-        if (a.fresh) lo = min(lo, first_new);
+        const WeighSeq q = weigh_seq(a, s);
+        if (!q.fit && blockIdx.x == 0 && threadIdx.x == 0) report(a.st, MOE_DEV_BAD_INDEX, s);
+        if (q.n == 0 || q.len == 0 || (q.n - q.i0) * a.group >= a.many) continue;
+        const int lo = weigh_first(a, q);
         for (int page = lo / kPage + blockIdx.x; page < pages_of(q.len); page += gridDim.x) {
             const int id = a.c.page_table[static_cast<long long>(s) * a.c.max_pages + page];
             const bool ok = id >= 0 && id < a.c.n_pages;
@@ -117,10 +91,9 @@ __global__ void __launch_bounds__(kThreads) kv4_weigh_kernel(const WeighArgs a) 
                 continue;
             }
             const int key0 = page * kPage;
-            // rows that see something of the page: places key0 .. (window after the page's end)
-            int ia = max(i0, key0 - (q.len - q.n)), ib = q.n;
-            if (a.window > 0) ib = static_cast<int>(min(static_cast<long long>(ib), static_cast<long long>(key0) + kPage - 1 + a.window - (q.len - q.n)));
-            const int r_begin = ia * a.group, r_end = max(r_begin, ib * a.group);
+            int ia, ib;
+            weigh_rows(a, q, key0, kPage, ia, ib);
+            const int r_begin = ia * a.group, r_end = ib * a.group;
             const int tiles = (r_end - r_begin + 7) / 8;
             float sum[8];
 #pragma unroll
@@ -196,12 +169,10 @@ __global__ void __launch_bounds__(kThreads) kv4_weigh_kernel(const WeighArgs a) 
             }
             __syncthreads();
             if (threadIdx.x < kPage && key0 + static_cast<int>(threadIdx.x) < q.len) {
-                const int key = key0 + threadIdx.x;
-                float* out = a.score + s * a.ld_score + key;
                 float v = 0.f;
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) v += s_sum[i][threadIdx.x];
-                *out = a.fresh && key >= first_new ? v : *out + v;
+                weigh_add(a, q, s, key0 + threadIdx.x, v);
             }
             __syncthreads();
         }
@@ -217,17 +188,25 @@ cudaError_t launch(const WeighArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t kv4_weigh_workspace(int S, int T, int n_q, int n_kv, int D, int max_pages) {
-    (void)S; (void)T; (void)n_q; (void)n_kv; (void)D; (void)max_pages;
-    return 0;
+    (void)D;
+    const int group = n_q / n_kv;
+    return static_cast<long long>(T) * group >= kWeighMany && weigh_tc_fits(group) ? kv4_weigh_tc_workspace(S, max_pages) : 0;
 }
 
 cudaError_t launch_kv4_weigh(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache& c, const int32_t* q_start, int max_new,
                              const float* lse, float scale, int window, int last, float* score, long long ld_score, bool fresh, void* ws,
                              moe_dev_status* st, cudaStream_t s) {
-    (void)max_new;
-    (void)ws;
     if (c.max_pages < 1) return cudaSuccess;
-    const WeighArgs a = {static_cast<const __nv_bfloat16*>(q), ld_q, T, n_q, n_q / c.n_kv, c, q_start, lse, scale, window, last, score, ld_score, fresh, st};
+    const int group = n_q / c.n_kv;
+    long long most = max_new < T ? max_new : T;        // rows of a sequence that count
+    if (last > 0 && last < most) most = last;
+    const bool prompts = most * group >= kWeighMany && weigh_tc_fits(group);
+    const WeighArgs a = {static_cast<const __nv_bfloat16*>(q), ld_q, T, n_q, group, c, q_start, lse, scale, window, last, score, ld_score, fresh,
+                         prompts ? kWeighMany : 0x7fffffff, st};
+    if (prompts) {
+        const cudaError_t e = launch_kv4_weigh_tc(a, ws, s);
+        if (e != cudaSuccess) return e;
+    }
     return c.head_dim == 64 ? launch<64>(a, s) : launch<128>(a, s);
 }
 

@@ -651,7 +651,7 @@ size_t moe_kv4_pool_workspace(int S, int n_pages);
  * (places, window, key heads); with that call's lse the exponentials are its
  * probabilities.  A row whose lse is -inf sees nothing and adds nothing.
  *
- *   q, ld_q, q_start, max_new, scale, window  as for moe_attention_kv4
+ *   q, ld_q, q_start, scale, window  as for moe_attention_kv4
  *   last     count only the last `last` rows of each sequence; 0 = all
  *   lse      [T][n_q] fp32
  *   score    [S][ld_score] fp32, ld_score >= max_pages * 64; entries beyond a
@@ -659,9 +659,10 @@ size_t moe_kv4_pool_workspace(int S, int n_pages);
  *   fresh    nonzero: the entries of the rows' own tokens (the last of the
  *            sequence) are set instead of added to.  With one score for all
  *            layers the first layer's call is fresh and the others add.
- *   workspace  moe_kv4_weigh_workspace() bytes, 256-byte aligned, ZERO-FILLED
- *            before its first use (every call leaves its counters at zero, at places
- *            that no size changes); serves one call at a time; may be NULL where that is 0
+ *   max_new  an upper bound of the rows of a sequence; it only chooses the kernels
+ *   workspace  moe_kv4_weigh_workspace() bytes, 256-byte aligned; holds nothing between
+ *            calls, so one buffer serves calls of any sizes in turn; serves one call at a
+ *            time; may be NULL where that is 0
  * The cache's values are not read.  Products run on the tensor cores in fp16 (q
  * scaled by a power of two of its row, keys exact) with fp32 sums;
  * exponentials and their sums are fp32, added in an order that depends on

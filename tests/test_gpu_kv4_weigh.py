@@ -69,7 +69,7 @@ class Case:
         wide = torch.zeros(T, n_q * D + stride, dtype=torch.bfloat16, device=DEV)
         self.q_dev = wide[:, :n_q * D].unflatten(1, (n_q, D))
         self.q_dev.copy_(self.q)
-        self.ws = torch.zeros(max(moe.kv4_weigh_workspace(self.cache, T, n_q), 256), dtype=torch.uint8, device=DEV)
+        self.ws = torch.full((max(moe.kv4_weigh_workspace(self.cache, T, n_q), 256),), 255, dtype=torch.uint8, device=DEV)
 
     def run(self, window=0, last=0, fresh=False, lse=None, st=None, score=None):
         out = dev(self.score) if score is None else score
