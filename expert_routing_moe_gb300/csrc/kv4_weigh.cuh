@@ -19,7 +19,7 @@ struct WeighArgs {
     const int32_t* q_start;
     const float* lse;
     float scale;
-    int window, last;
+    int window, last, max_new;
     float* score;
     long long ld_score;
     bool fresh;
@@ -40,7 +40,7 @@ __device__ __forceinline__ WeighSeq weigh_seq(const WeighArgs& a, int s) {
     q.q0 = a.q_start[s];
     const int q1 = a.q_start[s + 1];
     q.len = a.c.seq_len[s];
-    q.fit = rows_fit(q.q0, q1, q.len, a.T, a.c.max_pages);
+    q.fit = rows_fit(q.q0, q1, q.len, a.T, a.c.max_pages) && q1 - q.q0 <= a.max_new;
     q.n = q.fit ? q1 - q.q0 : 0;
     if (!q.fit) q.len = 0;
     q.i0 = a.last > 0 && a.last < q.n ? q.n - a.last : 0;

@@ -659,7 +659,8 @@ size_t moe_kv4_pool_workspace(int S, int n_pages);
  *   fresh    nonzero: the entries of the rows' own tokens (the last of the
  *            sequence) are set instead of added to.  With one score for all
  *            layers the first layer's call is fresh and the others add.
- *   max_new  an upper bound of the rows of a sequence; it only chooses the kernels
+ *   max_new  an upper bound of the rows of a sequence; one with more is reported
+ *            (MOE_DEV_BAD_INDEX, detail = sequence) and adds nothing
  *   workspace  moe_kv4_weigh_workspace() bytes, 256-byte aligned; holds nothing between
  *            calls, so one buffer serves calls of any sizes in turn; serves one call at a
  *            time; may be NULL where that is 0
