@@ -6,12 +6,14 @@
 //          tokens in order
 //  plan    one CTA gives every sequence its free pages, all or nothing
 //  move    tables, references, lengths and scores, a CTA for each sequence; and
-//          the kept tokens' codes and scales, a CTA for each (layer, head,
+//          the kept tokens' codes and scales, a cluster for each (layer, head,
 //          sequence)
 //
 // Moving in place: the k-th kept token comes from a place >= k, so a page is read
-// only for itself and for pages before it.  A CTA reads the sources of
-// eight pages, then writes them: whatever it writes has been read by then.
+// only for itself and for pages before it.  A cluster reads the sources of
+// up to 32 pages into registers, meets, then writes them: whatever it writes has been read by then.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "kv4.cuh"
 #include "launch.h"
@@ -20,12 +22,15 @@
 
 namespace moe {
 
+namespace cg = cooperative_groups;
+
 namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kMoveThreads = 256;
-constexpr int kMoveWarps = kMoveThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMovePages = 4;             // pages of a CTA at a time, three warps each: keys, and two halves of the values
+constexpr int kMoveThreads = kMovePages * 96;
 
 // What is known of a sequence.
 struct SeqPlan {
@@ -76,6 +81,25 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 
 // Exclusive prefix sum over the CTA, and the total.
+__device__ __forceinline__ long long scan_pair(long long v, long long& total, long long* s_warp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long inc = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long x = __shfl_up_sync(kFull, inc, off);
+        if (lane >= off) inc += x;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+    for (int i = 0; i < kSelWarps; ++i) {
+        if (i < warp) before += s_warp[i];
+        total += s_warp[i];
+    }
+    return before + inc - v;
+}
 __device__ __forceinline__ int scan(int v, int& total, int* s_warp) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int inc = v;
@@ -98,12 +122,19 @@ __device__ __forceinline__ int scan(int v, int& total, int* s_warp) {
     return (warp > 0 ? before : 0) + inc - v;
 }
 
+// A sequence's places are shared by the CTAs of a cluster, and a CTA's by its threads, in neighbouring runs: so one prefix sum
+// gives every kept token its place.
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictArgs a) {
-    __shared__ int s_hist[256], s_warp[kSelWarps], s_pick[2], s_first, s_bad;
-    const int s = blockIdx.x, tid = threadIdx.x;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int parts = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
+    __shared__ __align__(16) int s_hist[kBins];
+    __shared__ int s_warp[kSelWarps], s_pick[2], s_bad, s_first;
+    __shared__ long long s_warp2[kSelWarps], s_count;
+    const int s = blockIdx.x / parts, tid = threadIdx.x;
     const EvictWs w = evict_ws(a.ws, a.p.S, a.p.max_pages, a.p.n_pages);
     if (tid == 0) { s_first = 0x7fffffff; s_bad = 0; }
-    __syncthreads();
+    for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
+    cluster.sync();
     pdl_wait();
     pdl_trigger();
     const int len = a.p.seq_len[s], budget = a.budget[s];
@@ -116,70 +147,106 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     const int32_t* row = a.p.page_table + static_cast<long long>(s) * a.p.max_pages;
     int* old_page = w.old_page + static_cast<long long>(s) * a.p.max_pages;
     if (cut)
-        for (int c = tid; c < pages; c += kSelThreads) {
+        for (int c = tid; c < pages; c += kSelThreads) {       // every CTA looks at all of them: all know whether one is bad
             const int id = row[c];
             if (id < 0 || id >= a.p.n_pages) s_bad = 1;
-            old_page[c] = id;
+            if (part == 0) old_page[c] = id;
         }
     __syncthreads();
     bad = bad || s_bad;
     if (bad || !cut) {
         r.bad = bad;
-        if (tid == 0) w.seqs[s] = r;
-        return;
+        if (part == 0 && tid == 0) w.seqs[s] = r;
+        return;                                                // the whole cluster
     }
     // the best k of the places between the first and the last ones
     const int lo = a.sinks, hi = len - a.recent, k = budget - a.sinks - a.recent;
     const float* score = a.score + s * a.ld_score;
+    const int c0 = static_cast<int>(static_cast<long long>(len) * part / parts), c1 = static_cast<int>(static_cast<long long>(len) * (part + 1) / parts);
+    const int m0 = max(c0, lo), m1 = min(c1, hi);
     uint32_t prefix = 0u;
     int want = k;                       // of those whose higher bits are the prefix's
-    for (int shift = 24; shift >= 0 && k > 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelThreads) s_hist[i] = 0;
-        __syncthreads();
-        for (int j = lo + tid; j < hi; j += kSelThreads) {
+    for (int pass = 0; pass < 3 && k > 0; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        for (int j = m0 + tid; j < m1; j += kSelThreads) {
             const uint32_t o = order_of(score[j]);
-            if (shift == 24 || (o >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_hist[(o >> shift) & 255u], 1);
+            if (pass == 0 || (o >> (shift + bits)) == (prefix >> (shift + bits))) atomicAdd(&s_hist[o >> shift & ((1u << bits) - 1)], 1);
         }
-        __syncthreads();
+        cluster.sync();
+        // two bins a thread, from the highest down
+        const int b1 = (1 << bits) - 1 - 2 * tid;
+        int n[2] = {0, 0};
+        if (b1 > 0)
+            for (int i = 0; i < parts; ++i) {
+                const int2 v = *reinterpret_cast<const int2*>(cluster.map_shared_rank(s_hist, i) + b1 - 1);
+                n[0] += v.y;
+                n[1] += v.x;
+            }
         int total;
-        const int mine = tid < 256 ? s_hist[255 - tid] : 0;      // from the highest down
-        const int before = scan(mine, total, s_warp);
-        if (tid < 256 && before < want && before + mine >= want) {
-            s_pick[0] = 255 - tid;
-            s_pick[1] = before;
+        int before = scan(n[0] + n[1], total, s_warp);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (before < want && before + n[i] >= want) {
+                s_pick[0] = b1 - i;
+                s_pick[1] = before;
+            }
+            before += n[i];
         }
-        __syncthreads();
+        cluster.sync();                 // every CTA has read the counts
         prefix |= static_cast<uint32_t>(s_pick[0]) << shift;
         want -= s_pick[1];
+        for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
         __syncthreads();
     }
     // prefix: the score of the last one that is kept; `want` of those that have it are, the first ones
-    int* kept = w.kept + static_cast<long long>(s) * a.p.max_pages * kPage;
-    int n_kept = 0, n_equal = 0;
-    for (int j0 = 0; j0 < len; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        bool keep = j < len && (j < lo || j >= hi), equal = false;
-        if (j >= lo && j < hi && k > 0) {
-            const uint32_t o = order_of(score[j]);
-            keep = o > prefix;
-            equal = o == prefix;
-        }
-        int total;
-        const int e = scan(equal, total, s_warp);
-        if (equal && n_equal + e < want) keep = true;
-        n_equal += total;
-        const int at = n_kept + scan(keep, total, s_warp);
-        n_kept += total;
-        if (keep) kept[at] = j;
-        else if (j < len && j < s_first) atomicMin(&s_first, j);
+    const int each = (c1 - c0 + kSelThreads - 1) / kSelThreads, j0 = min(c1, c0 + tid * each), j1 = min(c1, j0 + each);
+    // 1: kept, 2: kept if it is among the first `want`, 0: not
+    auto judge = [&](int j) {
+        if (j < lo || j >= hi) return 1;
+        if (k == 0) return 0;
+        const uint32_t o = order_of(score[j]);
+        return o > prefix ? 1 : o == prefix ? 2 : 0;
+    };
+    long long mine = 0;                 // kept ones, and in the upper half those that may be
+    for (int j = j0; j < j1; ++j) {
+        const int v = judge(j);
+        mine += v == 1 ? 1ll : v == 2 ? 1ll << 32 : 0ll;
     }
-    __syncthreads();
-    r.now = n_kept;
-    r.first = s_first / kPage;
+    long long total2;
+    long long at2 = scan_pair(mine, total2, s_warp2);
+    if (tid == 0) s_count = total2;
+    cluster.sync();
+    long long all = 0;
+    for (int i = 0; i < parts; ++i) {
+        const long long c = *cluster.map_shared_rank(&s_count, i);
+        if (i < part) at2 += c;
+        all += c;
+    }
+    int* kept = w.kept + static_cast<long long>(s) * a.p.max_pages * kPage;
+    int sure = static_cast<int>(at2), equal = static_cast<int>(at2 >> 32);
+    int first = 0x7fffffff;
+    for (int j = j0; j < j1; ++j) {
+        const int v = judge(j);
+        if (v == 1 || (v == 2 && equal < want)) kept[sure + min(equal, want)] = j;
+        else first = min(first, j);
+        sure += v == 1;
+        equal += v == 2;
+    }
+    first = __reduce_min_sync(kFull, first);
+    if ((tid & 31) == 0 && first != 0x7fffffff) atomicMin(&s_first, first);
+    cluster.sync();
+    if (part == 0) {
+        first = 0x7fffffff;
+        for (int i = 0; i < parts; ++i) first = min(first, *cluster.map_shared_rank(&s_first, i));
+    }
+    cluster.sync();                     // no CTA leaves while its shared memory is read
+    if (part != 0) return;
+    r.now = static_cast<int>(all) + min(static_cast<int>(all >> 32), want);
+    r.first = first / kPage;
     // pages that others hold too are written elsewhere
     int* rank = w.rank + static_cast<long long>(s) * a.p.max_pages;
-    for (int c0 = r.first; c0 < pages_of(r.now); c0 += kSelThreads) {
-        const int c = c0 + tid;
+    for (int x0 = r.first; x0 < pages_of(r.now); x0 += kSelThreads) {
+        const int c = x0 + tid;
         const bool in = c < pages_of(r.now);
         const bool shared = in && a.p.ref[row[c]] > 1;
         int total;
@@ -238,20 +305,26 @@ __device__ __forceinline__ void move_book(const EvictArgs& a, const EvictWs& w, 
     if (!cut) return;
     float* score = a.score + s * a.ld_score;
     // a score moves to a place at or before its own: what is written has been read
-    for (int i0 = 0; i0 < r.len; i0 += kMoveThreads * 4) {
-        float v[4];
+    constexpr int kEach = 12;
+    for (int i0 = 0; i0 < r.now; i0 += kMoveThreads * kEach) {
+        int from[kEach];
+        float v[kEach];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kEach; ++u) {
             const int i = i0 + u * kMoveThreads + tid;
-            v[u] = i < r.now ? score[kept[i]] : 0.f;
+            from[u] = i < r.now ? kept[i] : -1;
         }
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) v[u] = from[u] >= 0 ? score[from[u]] : 0.f;
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kEach; ++u) {
             const int i = i0 + u * kMoveThreads + tid;
-            if (i < r.len) score[i] = v[u];
+            if (i < r.now) score[i] = v[u];
         }
     }
+    __syncthreads();
+    for (int i = r.now + tid; i < r.len; i += kMoveThreads) score[i] = 0.f;
     int32_t* row = a.p.page_table + static_cast<long long>(s) * a.p.max_pages;
     const int* old_page = w.old_page + static_cast<long long>(s) * a.p.max_pages;
     const int* rank = w.rank + static_cast<long long>(s) * a.p.max_pages;
@@ -270,149 +343,145 @@ __device__ __forceinline__ void move_book(const EvictArgs& a, const EvictWs& w, 
     if (tid == 0) a.p.seq_len[s] = r.now;
 }
 
-// The kept tokens of page c of (layer, head, sequence), read by one warp into registers and written from them.
-// A lane reads and writes 16-byte runs of the page that it makes, but for the scales' sources.
+// The CTAs of a cluster, or the threads of one.
+__device__ __forceinline__ void meet(cg::cluster_group& cluster, int parts) {
+    if (parts > 1) cluster.sync();
+    else __syncthreads();
+}
+
+// Where a token of a page that is made comes from, in shared memory: its keys' codes and its values' codes (NULL: no token,
+// zeros), and what leads from there to the scales.  A lane's place is added by whoever reads.
+struct __align__(16) Source {
+    const uint8_t* codes;
+    int scales;
+    int shift;                       // values: 4 where the token's codes are in the high halves
+};
 template <int D>
-struct Page {
-    using L = Kv4Layout<D>;
-    static constexpr int KC = kPage * D / 2 / 512;       // 16-byte runs of key codes of a lane
-    static constexpr int VC = KC;                        // and of value codes
-    uint4 k[KC], va[VC];
-    uint32_t ks[L::R == 2 ? 4 : 2], vs[4];
+struct Sources {
+    Source k[kPage], v[kPage];
+    __device__ __forceinline__ void set(int tok, const uint8_t* head, int t) {     // head: the head's part of the page, t: the token in it
+        using L = Kv4Layout<D>;
+        Source x = {nullptr, 0, 0}, y = {nullptr, 0, 0};
+        if (head != nullptr) {
+            const int j = t >> 1;
+            x.codes = head + t * (D / 2);
+            x.scales = L::kScales + ((t % 8) * 8 + t / 8) * L::R - t * (D / 2);
+            const int vc = L::vCodes + ((j / 4 * 8) * 4 + j % 4) * L::U;
+            y.codes = head + vc;
+            y.scales = L::vScales + ((j % 4) * 8 + j / 4) * 2 + (t & 1) - vc;
+            y.shift = 4 * (t & 1);
+        }
+        k[tok] = x;
+        v[tok] = y;
+    }
 };
 
+// The keys of a page: lane (part, g) = (lane / 8, lane % 8) has 16-byte runs of tokens g + 8 x -- for D = 64, where a token has
+// two, parts 0 and 1 of tokens 16 x + g and parts 2 and 3 of 8 further -- and the scales of blocks part*R .. of tokens g + 8 i.
 template <int D>
-__device__ __forceinline__ void read_page(Page<D>& g, const uint8_t* head, long long page_bytes, const int* kept, const int* old_page, int c, int now, int lane) {
+struct KeyPart {
     using L = Kv4Layout<D>;
-    // lane's two tokens of the page and the pages that hold them
-    int src[2];
-    const uint8_t* from[2];
+    static constexpr int runs = kPage * D / 2 / 512, per = D / 32;
+    uint4 c[runs];
+    uint32_t s[2 * L::R];
+    __device__ __forceinline__ int token(int x, int lane) const { return per == 4 ? 8 * x + (lane & 7) : 16 * x + (lane & 7) + 8 * (lane >> 4); }
+    __device__ __forceinline__ int run(int lane) const { return per == 4 ? lane >> 3 : lane >> 3 & 1; }
+    __device__ __forceinline__ void read(const Sources<D>& src, int lane) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int i = c * kPage + 2 * lane + u;
-        src[u] = i < now ? kept[i] : -1;
-        from[u] = src[u] < 0 ? nullptr : head + old_page[src[u] / kPage] * page_bytes;
-    }
-    auto token = [&](int tok, const uint8_t*& base, int& t) {       // of another lane
-        const int l = tok >> 1;
-        const int s0 = __shfl_sync(kFull, src[0], l), s1 = __shfl_sync(kFull, src[1], l);
-        const unsigned long long b0 = __shfl_sync(kFull, reinterpret_cast<unsigned long long>(from[0]), l);
-        const unsigned long long b1 = __shfl_sync(kFull, reinterpret_cast<unsigned long long>(from[1]), l);
-        const int v = tok & 1 ? s1 : s0;
-        base = reinterpret_cast<const uint8_t*>(tok & 1 ? b1 : b0);
-        t = v & (kPage - 1);
-    };
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    // key codes: D/32 runs a token
-    constexpr int per = D / 32;
+        for (int x = 0; x < 2 * L::R; ++x) s[x] = 0u;
 #pragma unroll
-    for (int x = 0; x < Page<D>::KC; ++x) {
-        const int run = x * 32 + lane;
-        const uint8_t* b;
-        int t;
-        token(run / per, b, t);
-        g.k[x] = b == nullptr ? zero : *reinterpret_cast<const uint4*>(b + t * (D / 2) + run % per * 16);
-    }
-    // key scales: R bytes of tokens g + 8 i (i < 8), block t: place (t*8 + g)*8 + i
-    {
-#pragma unroll
-        for (int x = 0; x < (L::R == 2 ? 4 : 2); ++x) g.ks[x] = 0u;
-        const int gg = lane & 7, tt = lane >> 3;
+        for (int x = 0; x < runs; ++x) {
+            const Source a = src.k[token(x, lane)];
+            c[x] = make_uint4(0u, 0u, 0u, 0u);
+            if (a.codes != nullptr) c[x] = *reinterpret_cast<const uint4*>(a.codes + run(lane) * 16);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint8_t* b;
-            int t;
-            token(gg + 8 * i, b, t);
-            if (L::R == 2) {
-                const uint32_t v = b == nullptr ? 0u : *reinterpret_cast<const uint16_t*>(b + L::kScales + ((tt * 8 + t % 8) * 8 + t / 8) * 2);
-                g.ks[i / 2] |= v << (16 * (i & 1));
-            } else {
-                const uint32_t v = b == nullptr ? 0u : b[L::kScales + (tt * 8 + t % 8) * 8 + t / 8];
-                g.ks[i / 4] |= v << (8 * (i & 3));
-            }
+            const Source a = src.k[8 * i + (lane & 7)];
+            if (a.codes == nullptr) continue;
+            const uint8_t* p = a.codes + a.scales + (lane >> 3) * 64 * L::R;
+            if constexpr (L::R == 2) s[i / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) << (16 * (i & 1));
+            else s[i / 4] |= static_cast<uint32_t>(*p) << (8 * (i & 3));
         }
     }
-    // value codes: two tokens share a byte; run z of the page: tokens 2j, 2j+1, numbers 16-byte runs
-    constexpr int U = L::U;                              // bytes of a pair's run: 16 or 8
+    __device__ __forceinline__ void write(uint8_t* to, int lane) const {
 #pragma unroll
-    for (int x = 0; x < Page<D>::VC; ++x) {
-        const int at = (x * 32 + lane) * 16;             // byte of the value codes
-        uint32_t out[4];
+        for (int x = 0; x < runs; ++x) *reinterpret_cast<uint4*>(to + token(x, lane) * (D / 2) + run(lane) * 16) = c[x];
+        uint8_t* p = to + L::kScales + lane * 8 * L::R;
+        if constexpr (L::R == 2) *reinterpret_cast<uint4*>(p) = make_uint4(s[0], s[1], s[2], s[3]);
+        else *reinterpret_cast<uint2*>(p) = make_uint2(s[0], s[1]);
+    }
+};
+// The values of 32 tokens of a page: lane (g', j) = (lane / 4, lane % 4) has the runs of tokens 8 x + 2 j and + 1, which share
+// bytes, and numbers g' (D/8) .., and the scales of the same tokens, block g'.
+template <int D>
+struct ValuePart {
+    using L = Kv4Layout<D>;
+    static constexpr int U = L::U, W = U / 4;            // U: bytes of two tokens' run, 16 or 8
+    uint32_t c[4][W];
+    uint32_t s[2];
+    __device__ __forceinline__ void read(const Sources<D>& src, int half, int lane) {
+        const int gp = lane >> 2, j = lane & 3;
+        s[0] = s[1] = 0u;
 #pragma unroll
-        for (int half = 0; half < 16 / U; ++half) {
-            const int run = (at + half * U) / U;         // ((j/4)*8 + g')*4 + j%4
-            const int j = run / 32 * 4 + run % 4, gp = run / 4 % 8;
-            uint32_t v[2][U / 4];
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint8_t* b;
-                int t;
-                token(2 * j + u, b, t);
-                const int js = t >> 1;
+                const Source a = src.v[32 * half + 8 * x + 2 * j + u];
+                uint32_t v[W];
+                uint32_t sc = 0u;
 #pragma unroll
-                for (int y = 0; y < U / 4; ++y) v[u][y] = 0u;
-                if (b != nullptr) {
-                    const uint8_t* p = b + L::vCodes + ((js / 4 * 8 + gp) * 4 + js % 4) * U;
+                for (int y = 0; y < W; ++y) v[y] = 0u;
+                if (a.codes != nullptr) {
+                    const uint8_t* p = a.codes + gp * 4 * U;
                     if constexpr (U == 16) {
                         const uint4 q = *reinterpret_cast<const uint4*>(p);
-                        v[u][0] = q.x; v[u][1] = q.y; v[u][2] = q.z; v[u][3] = q.w;
+                        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
                     } else {
                         const uint2 q = *reinterpret_cast<const uint2*>(p);
-                        v[u][0] = q.x; v[u][1] = q.y;
+                        v[0] = q.x; v[1] = q.y;
                     }
-                    const int sh = 4 * (t & 1);
-#pragma unroll
-                    for (int y = 0; y < U / 4; ++y) v[u][y] = v[u][y] >> sh & 0x0f0f0f0fu;
+                    if (gp < D / 16) sc = a.codes[a.scales + gp * 64];
                 }
+#pragma unroll
+                for (int y = 0; y < W; ++y) {
+                    v[y] = v[y] >> a.shift & 0x0f0f0f0fu;
+                    c[x][y] = u == 0 ? v[y] : c[x][y] | v[y] << 4;
+                }
+                s[x / 2] |= sc << (8 * (2 * (x & 1) + u));
             }
-#pragma unroll
-            for (int y = 0; y < U / 4; ++y) out[half * (U / 4) + y] = v[0][y] | v[1][y] << 4;
-        }
-        g.va[x] = make_uint4(out[0], out[1], out[2], out[3]);
     }
-    // value scales: block b, pair j, token parity: byte ((b*4 + j%4)*8 + j/4)*2 + parity
-    {
+    __device__ __forceinline__ void write(uint8_t* to, int half, int lane) const {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) g.vs[x] = 0u;
-        const int blk = lane >> 2, j4 = lane & 3;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint8_t* b;
-            int t;
-            token(2 * (j4 + 4 * (i >> 1)) + (i & 1), b, t);
-            const int js = t >> 1;
-            const uint32_t v = b == nullptr || blk >= D / 16 ? 0u : b[L::vScales + ((blk * 4 + js % 4) * 8 + js / 4) * 2 + (t & 1)];
-            g.vs[i / 4] |= v << (8 * (i & 3));
+        for (int x = 0; x < 4; ++x) {
+            uint8_t* p = to + L::vCodes + (half * 4 + x) * 32 * U + lane * U;
+            if constexpr (U == 16) *reinterpret_cast<uint4*>(p) = make_uint4(c[x][0], c[x][1], c[x][2], c[x][3]);
+            else *reinterpret_cast<uint2*>(p) = make_uint2(c[x][0], c[x][1]);
         }
+        if ((lane >> 2) < D / 16) *reinterpret_cast<uint2*>(to + L::vScales + lane * 16 + half * 8) = make_uint2(s[0], s[1]);
     }
-}
+};
 
+// The first S CTAs keep the books; then a cluster for each (layer, head, sequence) moves its pages.
 template <int D>
-__device__ __forceinline__ void write_page(const Page<D>& g, uint8_t* to, int lane) {
+__global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const EvictArgs a) {
     using L = Kv4Layout<D>;
-#pragma unroll
-    for (int x = 0; x < Page<D>::KC; ++x) *reinterpret_cast<uint4*>(to + (x * 32 + lane) * 16) = g.k[x];
-    if constexpr (L::R == 2) *reinterpret_cast<uint4*>(to + L::kScales + ((lane >> 3) * 8 + (lane & 7)) * 16) = make_uint4(g.ks[0], g.ks[1], g.ks[2], g.ks[3]);
-    else *reinterpret_cast<uint2*>(to + L::kScales + ((lane >> 3) * 8 + (lane & 7)) * 8) = make_uint2(g.ks[0], g.ks[1]);
-#pragma unroll
-    for (int x = 0; x < Page<D>::VC; ++x) *reinterpret_cast<uint4*>(to + L::vCodes + (x * 32 + lane) * 16) = g.va[x];
-    if ((lane >> 2) < D / 16) *reinterpret_cast<uint4*>(to + L::vScales + lane * 16) = make_uint4(g.vs[0], g.vs[1], g.vs[2], g.vs[3]);
-}
-
-template <int D>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
-    using L = Kv4Layout<D>;
+    __shared__ Sources<D> s_src[kMovePages];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int parts = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
     const EvictWs w = evict_ws(a.ws, a.p.S, a.p.max_pages, a.p.n_pages);
     pdl_wait();
     pdl_trigger();
     if (w.header[0] == 0) return;
-    if (static_cast<int>(blockIdx.x) < a.p.S) {
-        move_book(a, w, blockIdx.x);
+    const int books = (a.p.S + parts - 1) / parts;         // clusters that keep them
+    if (static_cast<int>(blockIdx.x) / parts < books) {
+        if (static_cast<int>(blockIdx.x) < a.p.S) move_book(a, w, blockIdx.x);
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tid = threadIdx.x, lane = tid & 31, mine = tid / 96, role = tid % 96 / 32;
     const long long items = static_cast<long long>(a.p.n_layers) * a.n_kv * a.p.S;
-    for (long long item = blockIdx.x - a.p.S; item < items; item += gridDim.x - a.p.S) {
+    const int clusters = static_cast<int>(gridDim.x) / parts - books;
+    for (long long item = static_cast<int>(blockIdx.x) / parts - books; item < items; item += clusters) {
         const int s = static_cast<int>(item % a.p.S);
         const long long rest = item / a.p.S;
         const int h = static_cast<int>(rest % a.n_kv);
@@ -424,18 +493,59 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
         const int* old_page = w.old_page + static_cast<long long>(s) * a.p.max_pages;
         const int* rank = w.rank + static_cast<long long>(s) * a.p.max_pages;
         const int end = pages_of(r.now);
-        for (int c0 = r.first; c0 < end; c0 += kMoveWarps) {
-            const int c = c0 + warp;
-            Page<D> g;
-            if (c < end) read_page<D>(g, head, a.p.page_bytes, kept, old_page, c, r.now, lane);
+        for (int c0 = r.first + part * kMovePages; c0 - part * kMovePages < end; c0 += parts * kMovePages) {
+            __syncthreads();                               // the sources before have been read
+            if (tid < kMovePages * kPage) {
+                const int i = c0 * kPage + tid, src = i < r.now ? kept[i] : -1;
+                s_src[tid / kPage].set(tid % kPage, src < 0 ? nullptr : head + old_page[src / kPage] * a.p.page_bytes, src & (kPage - 1));
+            }
+            const int c = c0 + mine;
+            const bool live = c < end;
+            uint8_t* to = nullptr;
+            if (live) to = head + (rank[c] >= 0 ? w.free_pages[r.base + rank[c]] : old_page[c]) * a.p.page_bytes;
             __syncthreads();
-            if (c < end) {
-                const int to = rank[c] >= 0 ? w.free_pages[r.base + rank[c]] : old_page[c];
-                write_page<D>(g, head + to * a.p.page_bytes, lane);
+            // what is written has been read by then (pages that come later read neither)
+            if (role == 0) {
+                KeyPart<D> g;
+                if (live) g.read(s_src[mine], lane);
+                meet(cluster, parts);
+                if (live) g.write(to, lane);
+            } else {
+                ValuePart<D> g;
+                if (live) g.read(s_src[mine], role - 1, lane);
+                meet(cluster, parts);
+                if (live) g.write(to, role - 1, lane);
             }
         }
-        __syncthreads();
     }
+}
+
+cudaError_t launch_clusters(void (*kernel)(EvictArgs), int ctas, int parts, int threads, cudaStream_t s, const EvictArgs& a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int D>
+cudaError_t launch_move(const EvictArgs& a, cudaStream_t s) {
+    // enough CTAs for every SM four times over, by clusters of up to eight, but no more than a table has pages for
+    const long long items = static_cast<long long>(a.p.n_layers) * a.n_kv * a.p.S;
+    int parts = 1;
+    while (parts < 8 && items * parts < 4ll * sm_count() && parts * kMovePages < a.p.max_pages) parts *= 2;
+    const long long most = 8ll * sm_count() / parts > 0 ? 8ll * sm_count() / parts : 1;
+    const long long n = ((a.p.S + parts - 1) / parts + (items < most ? items : most)) * parts;
+    return launch_clusters(evict_move_kernel<D>, static_cast<int>(n), parts, kMoveThreads, s, a);
 }
 
 }  // namespace
@@ -448,14 +558,14 @@ size_t kv4_evict_workspace(int S, int max_pages, int n_pages) {
 cudaError_t launch_kv4_evict(const moe_kv4_pool& p, int head_dim, int n_kv, float* score, long long ld_score, const int32_t* budget, int sinks,
                              int recent, int32_t* kept, long long ld_kept, void* ws, moe_dev_status* st, cudaStream_t s) {
     const EvictArgs a = {p, n_kv, score, ld_score, budget, sinks, recent, kept, ld_kept, ws, st};
-    cudaError_t e = launch_pdl(evict_select_kernel, dim3(p.S), dim3(kSelThreads), 0, s, a);
+    // a CTA for about 4096 places of the longest sequence that there can be, up to eight
+    int parts = 1;
+    while (parts < 8 && parts * 64 < p.max_pages) parts *= 2;
+    cudaError_t e = launch_clusters(evict_select_kernel, p.S * parts, parts, kSelThreads, s, a);
     if (e != cudaSuccess) return e;
     e = launch_pdl(evict_plan_kernel, dim3(1), dim3(kSelThreads), 0, s, a);
     if (e != cudaSuccess) return e;
-    const long long items = static_cast<long long>(p.n_layers) * n_kv * p.S;
-    const int grid = p.S + static_cast<int>(items < 16 * sm_count() ? items : 16 * sm_count());
-    return head_dim == 64 ? launch_pdl(evict_move_kernel<64>, dim3(grid), dim3(kMoveThreads), 0, s, a)
-                          : launch_pdl(evict_move_kernel<128>, dim3(grid), dim3(kMoveThreads), 0, s, a);
+    return head_dim == 64 ? launch_move<64>(a, s) : launch_move<128>(a, s);
 }
 
 }  // namespace moe
