@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
         const int* old_page = w.old_page + static_cast<long long>(s) * a.p.max_pages;
         const int* rank = w.rank + static_cast<long long>(s) * a.p.max_pages;
         const int end = pages_of(r.now);
+        const bool apart = r.fresh == end - r.first;       // every page is written to a free one: nothing is read that is written
         for (int c0 = r.first + part * kMovePages; c0 - part * kMovePages < end; c0 += parts * kMovePages) {
             __syncthreads();                               // the sources before have been read
             if (tid < kMovePages * kPage) {
@@ -508,12 +509,12 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
             if (role == 0) {
                 KeyPart<D> g;
                 if (live) g.read(s_src[mine], lane);
-                meet(cluster, parts);
+                if (!apart) meet(cluster, parts);
                 if (live) g.write(to, lane);
             } else {
                 ValuePart<D> g;
                 if (live) g.read(s_src[mine], role - 1, lane);
-                meet(cluster, parts);
+                if (!apart) meet(cluster, parts);
                 if (live) g.write(to, role - 1, lane);
             }
         }
