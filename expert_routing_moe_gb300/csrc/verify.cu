@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "kv4.cuh"
 #include "launch.h"
 #include "ranges.h"
 #include "tmap.h"
@@ -79,42 +80,102 @@ struct Row {
     __device__ bool whole(int v) const { return first(v) >= 0 && first(v) + Run<L>::E <= V; }
 };
 
+// The run with -inf in the places outside the row, which then weigh nothing.
+template <typename L>
+__device__ __forceinline__ uint4 mask_run(const Row<L>& r, uint4 x, int v) {
+    if (r.whole(v)) return x;
+    const int e = r.first(v);
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(L) == 4) {
+            if (e + i < 0 || e + i >= r.V) w[i] = 0xff800000u;
+        } else {
+            if (e + 2 * i < 0 || e + 2 * i >= r.V) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
+            if (e + 2 * i + 1 < 0 || e + 2 * i + 1 >= r.V) w[i] = (w[i] & 0xffffu) | 0xff800000u;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The largest of the run's numbers, or a NaN.
+template <typename L>
+__device__ __forceinline__ float max_run(uint4 x);
+
 __device__ __forceinline__ float max_nan(float x, float y) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
 
-// A token's weight relative to the row's strongest: 2^t, t = n + f, the series of 2^f by Horner.
-__device__ __forceinline__ float weight(float l, float m, float it) {
-    const float t = fmaxf(__fmul_rn(__fsub_rn(l, m), it), -60.f);
-    const float y = __fadd_rn(t, 0x1.8p23f);              // rounds t to a whole number, ties to even
-    const float f = __fsub_rn(t, __fsub_rn(y, 0x1.8p23f));
-    float p = 0x1.430912p-13f;                            // ln(2)^i / i!, i = 6 .. 0, nearest fp32
-    p = __fmaf_rn(p, f, 0x1.5d87fep-10f);
-    p = __fmaf_rn(p, f, 0x1.3b2ab6p-7f);
-    p = __fmaf_rn(p, f, 0x1.c6b08ep-5f);
-    p = __fmaf_rn(p, f, 0x1.ebfbe0p-3f);
-    p = __fmaf_rn(p, f, 0x1.62e430p-1f);
-    p = __fmaf_rn(p, f, 1.f);
-    return __uint_as_float(__float_as_uint(p) + (__float_as_uint(y) << 23));   // y's low bits are n
+template <>
+__device__ __forceinline__ float max_run<float>(uint4 x) {
+    return max_nan(max_nan(__uint_as_float(x.x), __uint_as_float(x.y)), max_nan(__uint_as_float(x.z), __uint_as_float(x.w)));
+}
+__device__ __forceinline__ uint32_t max_nan_bf2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+template <>
+__device__ __forceinline__ float max_run<__nv_bfloat16>(uint4 x) {
+    const uint32_t m = max_nan_bf2(max_nan_bf2(x.x, x.y), max_nan_bf2(x.z, x.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
 }
 
+// What two tokens weigh relative to the row's strongest: 2^t, t = n + f, the series of 2^f by Horner.  Every operation is
+// rounded as the definition has it (a product by -1 is exact, so t - n may be a fused product).
+struct Scale {
+    float2 minus_m, it;
+    __device__ Scale(float m, float it_) : minus_m(make_float2(-m, -m)), it(make_float2(it_, it_)) {}
+};
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 weight2(float2 l, const Scale& s) {
+    float2 t = mul2(add2(l, s.minus_m), s.it);
+    t = make_float2(fmaxf(t.x, -60.f), fmaxf(t.y, -60.f));
+    const float2 y = add2(t, both(0x1.8p23f));            // rounds t to a whole number, ties to even
+    const float2 f = fma2(add2(y, both(-0x1.8p23f)), both(-1.f), t);
+    float2 p = both(0x1.430912p-13f);                     // ln(2)^i / i!, i = 6 .. 0, nearest fp32
+    p = fma2(p, f, both(0x1.5d87fep-10f));
+    p = fma2(p, f, both(0x1.3b2ab6p-7f));
+    p = fma2(p, f, both(0x1.c6b08ep-5f));
+    p = fma2(p, f, both(0x1.ebfbe0p-3f));
+    p = fma2(p, f, both(0x1.62e430p-1f));
+    p = fma2(p, f, both(1.f));
+    // y's low bits are n
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(y.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(y.y) << 23)));
+}
+__device__ __forceinline__ float weight(float l, const Scale& s) { return weight2(both(l), s).x; }
+
 // rint(w * 2^42) for 0 <= w < 4 as hi * 2^22 + lo (a conversion to 64 bits runs at 1/64 of an addition's rate): hi counts
-// units of 2^-20, what is left of w is exact and counts units of 2^-42.
-__device__ __forceinline__ void add_units(float w, int& hi, int& lo) {
-    const float y = __fadd_rn(w, 12.f);                   // 12: its neighbours are 2^-20 apart
-    const float r = __fsub_rn(w, __fsub_rn(y, 12.f));
-    const float z = __fmaf_rn(r, 0x1p42f, 0x1.8p23f);
-    hi += __float_as_int(y) - __float_as_int(12.f);
-    lo += __float_as_int(z) - __float_as_int(0x1.8p23f);
+// units of 2^-20, what is left of w is exact and counts units of 2^-42.  The bits of two fp32 numbers count them, from those
+// of 12 (whose neighbours are 2^-20 apart) and of 1.5 * 2^23.
+constexpr uint32_t kHi0 = 0x41400000u, kLo0 = 0x4b400000u;
+__device__ __forceinline__ void split2(float2 w, float2& hi, float2& lo) {
+    hi = add2(w, both(12.f));
+    const float2 r = fma2(add2(hi, both(-12.f)), both(-1.f), w);
+    lo = fma2(r, both(0x1p42f), both(0x1.8p23f));
 }
-__device__ __forceinline__ long long units(int hi, int lo) { return static_cast<long long>(hi) * (1 << 22) + lo; }
+__device__ __forceinline__ long long units(uint32_t hi, uint32_t lo) {     // of the bits less kHi0 and kLo0
+    return static_cast<long long>(static_cast<int>(hi)) * (1 << 22) + static_cast<int>(lo);
+}
 __device__ __forceinline__ long long units_of(float w) {
-    int hi = 0, lo = 0;
-    add_units(w, hi, lo);
-    return units(hi, lo);
+    float2 hi, lo;
+    split2(both(w), hi, lo);
+    return units(__float_as_uint(hi.x) - kHi0, __float_as_uint(lo.x) - kLo0);
 }
+// Sums of them, for up to 2^10 numbers.
+struct Units {
+    uint32_t hi = 0u, lo = 0u, n = 0u;
+    __device__ __forceinline__ void add(float2 w) {
+        float2 h, l;
+        split2(w, h, l);
+        hi += __float_as_uint(h.x) + __float_as_uint(h.y);
+        lo += __float_as_uint(l.x) + __float_as_uint(l.y);
+        n += 2;
+    }
+    __device__ __forceinline__ long long sum() const { return units(hi - n * kHi0, lo - n * kLo0); }
+};
 
 // The sequence's temperature: 1 / it, greedy or bad.
 struct Temp {
@@ -176,24 +237,16 @@ __global__ void __launch_bounds__(kThreads) verify_rows_kernel(const VerifyArgs 
     const int v0 = static_cast<int>(static_cast<long long>(rw.n) * part / parts), v1 = static_cast<int>(static_cast<long long>(rw.n) * (part + 1) / parts);
     uint4 held[kHeld];
     float m = -INFINITY;
-    auto top = [&](uint4 x, int v) {
-        if (rw.whole(v)) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) m = max_nan(m, as_float<L>(x, i));
-        } else {
-            const int e = rw.first(v);
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (e + i >= 0 && e + i < rw.V) m = max_nan(m, as_float<L>(x, i));
-        }
-    };
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
         if (v0 + tid + i * kThreads < v1) held[i] = __ldg(rw.runs + v0 + tid + i * kThreads);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
-        if (v0 + tid + i * kThreads < v1) top(held[i], v0 + tid + i * kThreads);
-    for (int v = v0 + tid + kHeld * kThreads; v < v1; v += kThreads) top(__ldg(rw.runs + v), v);
+        if (v0 + tid + i * kThreads < v1) {
+            held[i] = mask_run(rw, held[i], v0 + tid + i * kThreads);
+            m = max_nan(m, max_run<L>(held[i]));
+        }
+    for (int v = v0 + tid + kHeld * kThreads; v < v1; v += kThreads) m = max_nan(m, max_run<L>(mask_run(rw, __ldg(rw.runs + v), v)));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, off));
     if (lane == 0) s_max[warp] = m;
@@ -209,28 +262,27 @@ __global__ void __launch_bounds__(kThreads) verify_rows_kernel(const VerifyArgs 
     const bool bad = !(m - m == 0.f);
     if (bad && part == 0 && tid == 0) report(a.st, MOE_DEV_NONFINITE, item);
 
-    int hi = 0, lo = 0, best = 0x7fffffff;
+    int best = 0x7fffffff;
+    Units u;
     if (!bad) {
+        const Scale scale(m, temp.it);
         auto add = [&](uint4 x, int v) {
-            const int e = rw.first(v);
-            const bool whole = rw.whole(v);
+            if (temp.greedy) {
+                const int e = rw.first(v);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                if (!whole && !(e + i >= 0 && e + i < rw.V)) continue;
-                const float l = as_float<L>(x, i);
-                if (temp.greedy) {
-                    if (l == m) best = min(best, e + i);
-                } else {
-                    add_units(weight(l, m, temp.it), hi, lo);
-                }
+                for (int i = 0; i < E; ++i)
+                    if (as_float<L>(x, i) == m) best = min(best, e + i);       // (the places outside the row are -inf)
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; i += 2) u.add(weight2(make_float2(as_float<L>(x, i), as_float<L>(x, i + 1)), scale));
             }
         };
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
             if (v0 + tid + i * kThreads < v1) add(held[i], v0 + tid + i * kThreads);
-        for (int v = v0 + tid + kHeld * kThreads; v < v1; v += kThreads) add(__ldg(rw.runs + v), v);
+        for (int v = v0 + tid + kHeld * kThreads; v < v1; v += kThreads) add(mask_run(rw, __ldg(rw.runs + v), v), v);
     }
-    const long long sum = warp_sum(units(hi, lo));
+    const long long sum = warp_sum(u.sum());
     best = __reduce_min_sync(kFull, best);
     if (lane == 0) { s_sum[warp] = sum; s_best[warp] = best; }
     __syncthreads();
@@ -258,28 +310,43 @@ __global__ void __launch_bounds__(kThreads) verify_rows_kernel(const VerifyArgs 
 template <typename L>
 struct Draw {
     Row<L> p, q;
-    float mp, mq, ip, iq, it;
+    Scale sp, sq;
+    float ip, iq;
     int mode, without;               // mode 0: the target's weights, 1: those but for one token, 2: max(p - q, 0)
     static constexpr int E = Run<L>::E;
-    // the weights of a run's numbers, in units of 2^-42; 0 outside the row
-    __device__ __forceinline__ void run(int v, long long (&u)[E]) const {
+    // the weights of a run's numbers two by two; 0 (or less than half a unit) outside the row
+    template <typename F>
+    __device__ __forceinline__ void run(int v, F use) const {
         const int e = p.first(v);
-        const bool whole = p.whole(v);
-        const uint4 x = __ldg(p.runs + v);
+        const uint4 x = mask_run(p, __ldg(p.runs + v), v);
         uint4 y = make_uint4(0u, 0u, 0u, 0u);
-        const bool same = q.off == p.off;
-        if (mode == 2 && same) y = __ldg(q.runs + v);
+        if (mode == 2) {
+            if (q.off == p.off) {
+                y = mask_run(q, __ldg(q.runs + v), v);
+            } else {
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            u[i] = 0;
-            if (!whole && !(e + i >= 0 && e + i < p.V)) continue;
-            float w = weight(as_float<L>(x, i), mp, it);
-            if (mode == 2) {
-                const float l = same ? as_float<L>(y, i) : load_one<L>(q.runs, q.off + e + i);
-                w = fmaxf(__fsub_rn(__fmul_rn(w, ip), __fmul_rn(weight(l, mq, it), iq)), 0.f);
+                for (int i = 0; i < E; ++i) {
+                    if (e + i < 0 || e + i >= p.V) continue;
+                    if constexpr (sizeof(L) == 4) w[i] = __float_as_uint(load_one<L>(q.runs, q.off + e + i));
+                    else w[i / 2] |= (__float_as_uint(load_one<L>(q.runs, q.off + e + i)) >> 16) << (16 * (i & 1));
+                }
+                y = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (mode == 1 && e + i == without) continue;
-            u[i] = units_of(w);
+        }
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            float2 w = weight2(make_float2(as_float<L>(x, i), as_float<L>(x, i + 1)), sp);
+            if (mode == 2) {
+                const float2 o = mul2(weight2(make_float2(as_float<L>(y, i), as_float<L>(y, i + 1)), sq), both(iq));
+                w = fma2(o, both(-1.f), mul2(w, both(ip)));
+                w = make_float2(fmaxf(w.x, 0.f), fmaxf(w.y, 0.f));
+            }
+            if (mode == 1) {
+                if (e + i == without) w.x = 0.f;
+                if (e + i + 1 == without) w.y = 0.f;
+            }
+            use(i, w);
         }
     }
 };
@@ -333,11 +400,11 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
                 const RowInfo rq = a.rows[a.T + r0 + j];
                 if (rq.bad) { s_bad = 1; continue; }
                 const float l = load_one<L>(a.draft, (r0 + j) * a.ld_draft + x);
-                q = __ll2double_rn(units_of(weight(l, rq.m, temp.it))) / __ll2double_rn(static_cast<long long>(rq.z));
+                q = __ll2double_rn(units_of(weight(l, Scale(rq.m, temp.it)))) / __ll2double_rn(static_cast<long long>(rq.z));
             }
             if (ri.bad) continue;
             const float l = load_one<L>(a.logits, (r0 + j) * a.ld + x);
-            const double p = __ll2double_rn(units_of(weight(l, ri.m, temp.it))) / __ll2double_rn(static_cast<long long>(ri.z));
+            const double p = __ll2double_rn(units_of(weight(l, Scale(ri.m, temp.it)))) / __ll2double_rn(static_cast<long long>(ri.z));
             ok = __dmul_rn(static_cast<double>(a.uniform[r0 + j + 1]), q) < p;
         }
         if (!ok) atomicMin(&s_stop, j);
@@ -354,7 +421,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
         if (lead) answer(stop, ri.best);
         return;
     }
-    Draw<L> d = {Row<L>(a.logits, a.ld, row, a.V), Row<L>(a.logits, a.ld, row, a.V), ri.m, 0.f, 0.f, 0.f, temp.it, 0, -1};
+    Draw<L> d = {Row<L>(a.logits, a.ld, row, a.V), Row<L>(a.logits, a.ld, row, a.V), Scale(ri.m, temp.it), Scale(0.f, temp.it), 0.f, 0.f, 0, -1};
     if (stop < n - 1) {
         d.mode = 1;
         d.without = a.tokens[row + 1];
@@ -362,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
             const RowInfo rq = a.rows[a.T + row];
             d.mode = 2;
             d.q = Row<L>(a.draft, a.ld_draft, row, a.V);
-            d.mq = rq.m;
+            d.sq = Scale(rq.m, temp.it);
             d.ip = __double2float_rn(0x1p42 / __ll2double_rn(static_cast<long long>(ri.z)));
             d.iq = __double2float_rn(0x1p42 / __ll2double_rn(static_cast<long long>(rq.z)));
         }
@@ -370,39 +437,42 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
     // a warp's runs are neighbours, so that the warps' sums are the cumulated weight in order
     const int warps = parts * kWarps, w = part * kWarps + warp;
     const int v0 = static_cast<int>(static_cast<long long>(d.p.n) * w / warps), v1 = static_cast<int>(static_cast<long long>(d.p.n) * (w + 1) / warps);
-    long long total = 0;
-    int at = 0;
+    long long total = 0, before = 0, own = 0;
     for (int turn = 0; turn < 2; ++turn) {
-        long long sum = 0;
-        for (int v = v0 + lane; v < v1; v += 32) {
-            long long u[E];
-            d.run(v, u);
-#pragma unroll
-            for (int i = 0; i < E; ++i) sum += u[i];
-        }
-        sum = warp_sum(sum);
-        if (lane < parts) cluster.map_shared_rank(s_sums[turn], lane)[w] = sum;
+        Units u;
+        for (int v = v0 + lane; v < v1; v += 32) d.run(v, [&](int, float2 x) { u.add(x); });
+        own = warp_sum(u.sum());
+        if (lane < parts) cluster.map_shared_rank(s_sums[turn], lane)[w] = own;
         cluster.sync();
-        total = 0;
-        for (int i = 0; i < warps; ++i) total += s_sums[turn][i];
-        at = turn;
+        // all of them, and those of the warps before
+        total = before = 0;
+        for (int i = lane; i < warps; i += 32) {
+            const long long v = s_sums[turn][i];
+            total += v;
+            if (i < w) before += v;
+        }
+        total = warp_sum(total);
+        before = warp_sum(before);
         if (total > 0) break;        // the same in every CTA
         d.mode = 0;                  // nothing of the target is beyond the draft
     }
     long long target = __double2ll_rd(__dmul_rn(static_cast<double>(a.uniform[r0]), __ll2double_rn(total)));
     target = max(0ll, min(target, total - 1));
-    long long before = 0;
-    for (int i = 0; i < w; ++i) before += s_sums[at][i];
     if (lead) {
         a.accepted[s] = stop;
         if (a.n_new != nullptr) a.n_new[s] = stop - (n - 1);
     }
-    if (target < before || target >= before + s_sums[at][w]) return;
+    if (target < before || target >= before + own) return;
     // this warp's runs hold the token
     for (int v = v0; v < v1; v += 32) {
         long long u[E], mine = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) u[i] = 0;
         if (v + lane < v1) {
-            d.run(v + lane, u);
+            d.run(v + lane, [&](int i, float2 x) {
+                u[i] = units_of(x.x);
+                u[i + 1] = units_of(x.y);
+            });
 #pragma unroll
             for (int i = 0; i < E; ++i) mine += u[i];
         }
