@@ -483,8 +483,8 @@ moe_status_t moe_linear_w4(const void* x, long long ld_x, int T, const moe_w4* w
 }
 
 size_t moe_verify_workspace(int T, int S, int V) {
-    if (T < 0 || S < 0 || V < 1) return 0;
-    return moe::verify_workspace(T);
+    if (T < 0 || S < 0 || V < 1 || T > moe::kVerifyMaxT || V > moe::kVerifyMaxV) return 0;
+    return moe::verify_workspace(T, V);
 }
 
 moe_status_t moe_verify_drafts(const void* logits, int dtype, long long ld, int T, int V, const int32_t* tokens, const float* uniform,
@@ -500,7 +500,7 @@ moe_status_t moe_verify_drafts(const void* logits, int dtype, long long ld, int 
         if (logits == nullptr || tokens == nullptr || uniform == nullptr || ld < V || (reinterpret_cast<uintptr_t>(logits) & part) != 0)
             return MOE_ERR_INVALID_ARG;
         if (draft_logits != nullptr && (ld_draft < V || (reinterpret_cast<uintptr_t>(draft_logits) & part) != 0)) return MOE_ERR_INVALID_ARG;
-        if (workspace == nullptr || ws_bytes < moe::verify_workspace(T)) return MOE_ERR_WORKSPACE;
+        if (workspace == nullptr || ws_bytes < moe::verify_workspace(T, V)) return MOE_ERR_WORKSPACE;
         if (!aligned256(workspace)) return MOE_ERR_INVALID_ARG;
     }
     return from_cuda(moe::launch_verify(logits, dtype, ld, T, V, tokens, uniform, q_start, S, draft_logits, ld_draft, temperature, accepted,

@@ -156,7 +156,7 @@ cudaError_t launch_w4_pack(const void* w, int dtype, long long ld, int N, int K,
 
 // ---- verification of drafted tokens (verify.cu) ----
 constexpr int kVerifyMaxT = 1 << 16, kVerifyMaxV = 1 << 20, kVerifyMaxSeqs = 16384;
-size_t verify_workspace(int T);
+size_t verify_workspace(int T, int V);
 cudaError_t launch_verify(const void* logits, int dtype, long long ld, int T, int V, const int32_t* tokens, const float* uniform,
                           const int32_t* q_start, int S, const void* draft, long long ld_draft, const float* temperature, int32_t* accepted,
                           int32_t* next, int32_t* n_new, void* ws, moe_dev_status* st, cudaStream_t s);

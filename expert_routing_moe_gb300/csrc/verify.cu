@@ -1,13 +1,16 @@
 // verify.cu -- verification of drafted tokens against the target's
 // distribution (moe_verify_drafts).
 //
-// First a cluster for every row finds its maximum and the sum of its tokens'
-// weights; then a cluster for every sequence judges its drafts and draws the
-// token that follows.  Weights are whole multiples of 2^-42 made from fp32
-// numbers whose every operation is rounded in a known way, so that sums of
-// them do not depend on their order and a draw not on the grid.
+// First the rows' maxima and the sums of their tokens' weights: a cluster a row
+// where there are few, and otherwise a kernel for the maxima and one for the
+// sums, a warp a chunk of a row.  Then a cluster for every sequence judges its
+// drafts and draws the token that follows.  Weights are whole multiples of 2^-42
+// made from fp32 numbers whose every operation is rounded in a known way, so
+// that sums of them do not depend on their order and a draw not on the grid.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "kv4.cuh"
@@ -21,19 +24,22 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;        // of the clusters
 constexpr int kWarps = kThreads / 32;
-constexpr int kHeld = 4;             // 16-byte runs of a row that a thread keeps in registers
+constexpr int kHeld = 4;             // 16-byte runs of a row that a thread of a cluster loads at once
 constexpr int kMaxCluster = 8;
+constexpr int kRowCtas = 304;        // a wave of clusters, two CTAs an SM
+constexpr int kMaxThreads = 256;     // of the kernel for the maxima; a CTA's chunk has kChunkHeld runs a thread
+constexpr int kSumThreads = 128;     // of the sums; a warp's chunk has kChunkHeld runs a lane
+constexpr int kChunkHeld = 8;        // 16-byte runs of a chunk that a thread has
 constexpr float kLog2eF = 0x1.715476p+0f;
 constexpr float kGreedyBelow = 0x1p-60f;
 
-struct RowInfo {
-    unsigned long long z;            // sum of the weights
-    float m;                         // largest logit
-    int32_t best;                    // greedy: its place
-    int32_t bad;
-    int32_t pad[3];
+// What a row's tokens weigh, of a chunk of it.
+struct ChunkSum {
+    long long z;                     // sum of the weights
+    int32_t best;                    // greedy: place of the row's largest logit
+    int32_t pad;
 };
 
 struct VerifyArgs {
@@ -43,7 +49,12 @@ struct VerifyArgs {
     const int32_t *tokens, *q_start;
     const float *uniform, *temperature;
     int32_t *accepted, *next, *n_new;
-    RowInfo* rows;                   // [T] of the target, then [T] of the drafting model
+    int items;                       // rows of the target, then of the drafting model
+    int max_chunks, max_per;         // chunks of a row and their 16-byte runs, for the maxima
+    int chunks, per;                 // for the sums
+    float* scale;                    // [items]: 1 / temperature, 0: greedy, below: not needed
+    float* maxima;                   // [items][max_chunks]
+    ChunkSum* sums;                  // [items][chunks]
     moe_dev_status* st;
 };
 
@@ -82,20 +93,22 @@ struct Row {
 
 // The run with -inf in the places outside the row, which then weigh nothing.
 template <typename L>
-__device__ __forceinline__ uint4 mask_run(const Row<L>& r, uint4 x, int v) {
-    if (r.whole(v)) return x;
-    const int e = r.first(v);
+__device__ __noinline__ uint4 mask_ends(uint4 x, int e, int V) {
     uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(L) == 4) {
-            if (e + i < 0 || e + i >= r.V) w[i] = 0xff800000u;
+            if (e + i < 0 || e + i >= V) w[i] = 0xff800000u;
         } else {
-            if (e + 2 * i < 0 || e + 2 * i >= r.V) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
-            if (e + 2 * i + 1 < 0 || e + 2 * i + 1 >= r.V) w[i] = (w[i] & 0xffffu) | 0xff800000u;
+            if (e + 2 * i < 0 || e + 2 * i >= V) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
+            if (e + 2 * i + 1 < 0 || e + 2 * i + 1 >= V) w[i] = (w[i] & 0xffffu) | 0xff800000u;
         }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename L>
+__device__ __forceinline__ uint4 mask_run(const Row<L>& r, uint4 x, int v) {
+    return r.whole(v) ? x : mask_ends<L>(x, r.first(v), r.V);
 }
 // The largest of the run's numbers, or a NaN.
 template <typename L>
@@ -175,6 +188,12 @@ struct Units {
         n += 2;
     }
     __device__ __forceinline__ long long sum() const { return units(hi - n * kHi0, lo - n * kLo0); }
+    // Of a warp, up to 2^6 numbers a lane.
+    __device__ __forceinline__ long long warp_sum() const {
+        const int l = static_cast<int>(lo - n * kLo0);
+        const long long h = __reduce_add_sync(kFull, hi - n * kHi0);
+        return (h << 22) + (static_cast<long long>(__reduce_add_sync(kFull, l >> 16)) << 16) + __reduce_add_sync(kFull, l & 0xffff);
+    }
 };
 
 // The sequence's temperature: 1 / it, greedy or bad.
@@ -205,8 +224,33 @@ __device__ __forceinline__ long long warp_sum(long long v) {
     return v;
 }
 
+// What the judge needs of a row: the sum of its weights, its largest logit, the weight of the draft behind it and 2^42 / z.
+struct Judge {
+    long long z, u;
+    float m, inv;
+};
+
+__device__ __noinline__ double ratio(double x, long long z) { return x / __ll2double_rn(z); }
+// 2^42 / z in fp64, rounded to fp32, for 2^42 <= z <= 2^62.  An SM has two fp64 lanes and a division takes a microsecond there:
+// with z = zh + zl and r = 1 / zh in fp32, r + r (1 - (zh + zl) r) is within 2^-45 of the quotient, and the division
+// is only needed where numbers that close to it round differently.
+__device__ __forceinline__ float inverse(long long z) {
+    const float top = __ll2float_rn(z), zh = top * 0x1p-42f, zl = __ll2float_rn(z - __float2ll_rn(top)) * 0x1p-42f;
+    const float r = __frcp_rn(zh), c = r * fmaf(-zl, r, fmaf(-zh, r, 1.f)), d = r * 0x1p-43f;
+    const float lo = r + (c - d), hi = r + (c + d);
+    return lo == hi ? lo : __double2float_rn(ratio(0x1p42, z));
+}
+// uniform * q < p, each p of a token u / z in fp64: again fp32 decides unless both sides are close.
+__device__ __forceinline__ bool accepts(float uniform, const Judge& p, const Judge& q, bool model) {
+    const float pr = __ll2float_rn(p.u) * 0x1p-42f * p.inv, other = uniform * (model ? __ll2float_rn(q.u) * 0x1p-42f * q.inv : 1.f);
+    if (fabsf(pr - other) > 0x1p-20f * pr) return other < pr;
+    const double exact = model ? ratio(__ll2double_rn(q.u), q.z) : 1.0;
+    return __dmul_rn(static_cast<double>(uniform), exact) < ratio(__ll2double_rn(p.u), p.z);
+}
+
+// A row by a cluster.
 template <typename L>
-__global__ void __launch_bounds__(kThreads) verify_rows_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) verify_rows_kernel(const VerifyArgs a) {
     constexpr int E = Run<L>::E;
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
@@ -219,27 +263,29 @@ __global__ void __launch_bounds__(kThreads) verify_rows_kernel(const VerifyArgs 
     const bool draft = item >= a.T;
     const int row = draft ? item - a.T : item;
     if (tid == 0) s_seq = -1;
-    cluster.sync();                  // every CTA of the cluster runs: its shared memory can be written
+    cluster.barrier_arrive();        // waited for before the cluster's shared memory is written
+    const Row<L> rw(draft ? a.draft : a.logits, draft ? a.ld_draft : a.ld, row, a.V);
+    const int v0 = static_cast<int>(static_cast<long long>(rw.n) * part / parts), v1 = static_cast<int>(static_cast<long long>(rw.n) * (part + 1) / parts);
+    uint4 held[kHeld];
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
+    // the row is on its way while its sequence is looked for
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (v0 + tid + i * kThreads < v1) held[i] = __ldg(rw.runs + v0 + tid + i * kThreads);
     for (int s = tid; s < a.S; s += kThreads) {
         const int r0 = a.q_start[s], r1 = a.q_start[s + 1];
         // a drafting model's row is read for the draft behind it
         if (r0 >= 0 && r0 <= row && row + (draft ? 1 : 0) < r1 && r1 <= a.T) s_seq = s;
     }
     __syncthreads();
+    cluster.barrier_wait();
     const int s = s_seq;
     if (s < 0) return;               // the whole cluster
     const Temp temp = temp_of(a, s);
     if (temp.bad || (draft && temp.greedy)) return;
-
-    const Row<L> rw(draft ? a.draft : a.logits, draft ? a.ld_draft : a.ld, row, a.V);
-    const int v0 = static_cast<int>(static_cast<long long>(rw.n) * part / parts), v1 = static_cast<int>(static_cast<long long>(rw.n) * (part + 1) / parts);
-    uint4 held[kHeld];
     float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-        if (v0 + tid + i * kThreads < v1) held[i] = __ldg(rw.runs + v0 + tid + i * kThreads);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
         if (v0 + tid + i * kThreads < v1) {
@@ -294,16 +340,145 @@ __global__ void __launch_bounds__(kThreads) verify_rows_kernel(const VerifyArgs 
     }
     cluster.sync();
     if (part == 0 && tid == 0) {
-        RowInfo r;
-        long long z = 0;
-        for (int i = 0; i < parts; ++i) { z += s_part_sum[i]; best = min(best, s_part_best[i]); }
-        r.z = static_cast<unsigned long long>(z);
-        r.m = m;
-        r.best = best;
-        r.bad = bad;
-        r.pad[0] = r.pad[1] = r.pad[2] = 0;
-        a.rows[item] = r;
+        ChunkSum c = {0, best, 0};
+        for (int i = 0; i < parts; ++i) { c.z += s_part_sum[i]; c.best = min(c.best, s_part_best[i]); }
+        a.maxima[item] = m;
+        a.sums[item] = c;
     }
+}
+
+// Sequence of an item's row, -1 without one.
+__device__ __forceinline__ int find_seq(const VerifyArgs& a, int row, bool draft, int* s_seq) {
+    if (threadIdx.x == 0) *s_seq = -1;
+    __syncthreads();
+    for (int s = threadIdx.x; s < a.S; s += kMaxThreads) {
+        const int r0 = __ldg(a.q_start + s), r1 = __ldg(a.q_start + s + 1);
+        // a drafting model's row is read for the draft behind it
+        if (r0 >= 0 && r0 <= row && row + (draft ? 1 : 0) < r1 && r1 <= a.T) *s_seq = s;
+    }
+    __syncthreads();
+    const int s = *s_seq;
+    if (s < 0) return -1;
+    return s;
+}
+
+template <typename L>
+__global__ void __launch_bounds__(kMaxThreads) verify_max_kernel(const VerifyArgs a) {
+    __shared__ int s_seq;
+    __shared__ float s_max[kMaxThreads / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int item = blockIdx.x / a.max_chunks, chunk = blockIdx.x % a.max_chunks;
+    const bool draft = item >= a.T;
+    const int row = draft ? item - a.T : item;
+    pdl_wait();
+    pdl_trigger();
+    const int s = find_seq(a, row, draft, &s_seq);
+    const Temp temp = s < 0 ? Temp{-1.f, false, true} : temp_of(a, s);
+    const bool needed = !temp.bad && !(draft && temp.greedy);
+    if (chunk == 0 && tid == 0) a.scale[item] = !needed ? -1.f : temp.greedy ? 0.f : temp.it;
+    if (!needed) return;
+    const Row<L> rw(draft ? a.draft : a.logits, draft ? a.ld_draft : a.ld, row, a.V);
+    const int v0 = chunk * a.max_per + tid, v1 = min(rw.n, (chunk + 1) * a.max_per);
+    uint4 held[kChunkHeld];
+#pragma unroll
+    for (int i = 0; i < kChunkHeld; ++i)
+        if (v0 + i * kMaxThreads < v1) held[i] = __ldg(rw.runs + v0 + i * kMaxThreads);
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kChunkHeld; ++i)
+        if (v0 + i * kMaxThreads < v1) m = max_nan(m, max_run<L>(mask_run(rw, held[i], v0 + i * kMaxThreads)));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, off));
+    if (lane == 0) s_max[warp] = m;
+    __syncthreads();
+    if (tid == 0) {
+        for (int i = 1; i < kMaxThreads / 32; ++i) m = max_nan(m, s_max[i]);
+        a.maxima[blockIdx.x] = m;
+    }
+}
+
+// The row's largest logit, or what is not finite.
+__device__ __forceinline__ float row_max(const VerifyArgs& a, int item, int lane) {
+    float m = -INFINITY;
+    for (int i = lane; i < a.max_chunks; i += 32) m = max_nan(m, __ldcg(a.maxima + static_cast<size_t>(item) * a.max_chunks + i));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, off));
+    return m;
+}
+
+template <typename L>
+__global__ void __launch_bounds__(kSumThreads, 8) verify_sum_kernel(const VerifyArgs a) {
+    constexpr int E = Run<L>::E;
+    const int lane = threadIdx.x & 31;
+    const int unit = blockIdx.x * (kSumThreads / 32) + (threadIdx.x >> 5);
+    const int item = unit / a.chunks, chunk = unit - item * a.chunks;
+    if (item >= a.items) return;
+    const bool draft = item >= a.T;
+    const int row = draft ? item - a.T : item;
+    const Row<L> rw(draft ? a.draft : a.logits, draft ? a.ld_draft : a.ld, row, a.V);
+    const int v0 = chunk * a.per + lane, v1 = min(rw.n, (chunk + 1) * a.per);
+    pdl_wait();
+    pdl_trigger();
+    const float it = __ldcg(a.scale + item);
+    const float m = row_max(a, item, lane);
+    if (it < 0.f) return;
+    uint4 held[kChunkHeld];
+#pragma unroll
+    for (int i = 0; i < kChunkHeld; ++i)
+        if (v0 + i * 32 < v1) held[i] = __ldg(rw.runs + v0 + i * 32);
+    if (!(m - m == 0.f)) {
+        if (chunk == 0 && lane == 0) report(a.st, MOE_DEV_NONFINITE, item);
+        return;
+    }
+    if (it == 0.f) {
+        int best = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < kChunkHeld; ++i) {
+            const int v = v0 + i * 32;
+            if (v >= v1) continue;
+            const uint4 x = mask_run(rw, held[i], v);
+            const int e = rw.first(v);
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (as_float<L>(x, j) == m) best = min(best, e + j);   // (the places outside the row are -inf)
+        }
+        best = __reduce_min_sync(kFull, best);
+        if (lane == 0) a.sums[unit] = {0, best, 0};
+        return;
+    }
+    Units u;
+    const Scale scale(m, it);
+#pragma unroll
+    for (int i = 0; i < kChunkHeld; ++i) {
+        const int v = v0 + i * 32;
+        if (v >= v1) continue;
+        const uint4 x = mask_run(rw, held[i], v);
+#pragma unroll
+        for (int j = 0; j < E; j += 2) u.add(weight2(make_float2(as_float<L>(x, j), as_float<L>(x, j + 1)), scale));
+    }
+    const long long sum = u.warp_sum();
+    if (lane == 0) a.sums[unit] = {sum, 0x7fffffff, 0};
+}
+
+// A row's maximum and sum, by a warp.
+struct RowInfo {
+    float m;
+    bool bad;
+    long long z;
+    int best;
+};
+__device__ __forceinline__ RowInfo row_info(const VerifyArgs& a, int item, int lane) {
+    RowInfo r = {row_max(a, item, lane), false, 0, 0x7fffffff};
+    r.bad = !(r.m - r.m == 0.f);
+    if (r.bad) return r;
+    for (int i = lane; i < a.chunks; i += 32) {
+        const int4 c = __ldcg(reinterpret_cast<const int4*>(a.sums + static_cast<size_t>(item) * a.chunks + i));
+        r.z += static_cast<long long>(static_cast<unsigned long long>(static_cast<uint32_t>(c.y)) << 32 | static_cast<uint32_t>(c.x));
+        r.best = min(r.best, c.z);
+    }
+    r.z = warp_sum(r.z);
+    r.best = __reduce_min_sync(kFull, r.best);
+    return r;
 }
 
 // What the tokens of the row behind the last accepted draft weigh for the draw.
@@ -314,30 +489,30 @@ struct Draw {
     float ip, iq;
     int mode, without;               // mode 0: the target's weights, 1: those but for one token, 2: max(p - q, 0)
     static constexpr int E = Run<L>::E;
-    // the weights of a run's numbers two by two; 0 (or less than half a unit) outside the row
-    template <typename F>
-    __device__ __forceinline__ void run(int v, F use) const {
-        const int e = p.first(v);
-        const uint4 x = mask_run(p, __ldg(p.runs + v), v);
-        uint4 y = make_uint4(0u, 0u, 0u, 0u);
-        if (mode == 2) {
-            if (q.off == p.off) {
-                y = mask_run(q, __ldg(q.runs + v), v);
-            } else {
-                uint32_t w[4] = {0u, 0u, 0u, 0u};
+    // the drafting model's logits beside the target's run
+    __device__ __forceinline__ uint4 beside(int v) const {
+        return q.off == p.off ? __ldg(q.runs + v) : gather(q.runs, q.off + p.first(v), p.first(v), p.V);
+    }
+    __device__ static __noinline__ uint4 gather(const uint4* runs, int at, int e, int V) {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    if (e + i < 0 || e + i >= p.V) continue;
-                    if constexpr (sizeof(L) == 4) w[i] = __float_as_uint(load_one<L>(q.runs, q.off + e + i));
-                    else w[i / 2] |= (__float_as_uint(load_one<L>(q.runs, q.off + e + i)) >> 16) << (16 * (i & 1));
-                }
-                y = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+        for (int i = 0; i < E; ++i) {
+            if (e + i < 0 || e + i >= V) continue;
+            if constexpr (sizeof(L) == 4) w[i] = __float_as_uint(load_one<L>(runs, at + i));
+            else w[i / 2] |= (__float_as_uint(load_one<L>(runs, at + i)) >> 16) << (16 * (i & 1));
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // the weights of a run's numbers two by two; less than half a unit outside the row
+    template <typename F>
+    __device__ __forceinline__ void run(int v, uint4 x, uint4 y, F use) const {
+        const int e = p.first(v);
+        x = mask_run(p, x, v);
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
             float2 w = weight2(make_float2(as_float<L>(x, i), as_float<L>(x, i + 1)), sp);
             if (mode == 2) {
+                // (p is nothing outside the row, and what is negative then is nothing too)
                 const float2 o = mul2(weight2(make_float2(as_float<L>(y, i), as_float<L>(y, i + 1)), sq), both(iq));
                 w = fma2(o, both(-1.f), mul2(w, both(ip)));
                 w = make_float2(fmaxf(w.x, 0.f), fmaxf(w.y, 0.f));
@@ -351,16 +526,26 @@ struct Draw {
     }
 };
 
+// Rows of a sequence that a turn of the judge looks at, and what it found at the row that ends the accepted drafts.
+struct Judged {
+    long long z[kWarps][2], u[kWarps][2];          // of the target and of the drafting model: sum, the draft's weight
+    float m[kWarps][2];
+    int best[kWarps];
+    int stop, bad, stop_best;
+    float stop_m[2], stop_inv[2];
+    long long target;
+};
+
 template <typename L>
-__global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyArgs a) {
     constexpr int E = Run<L>::E;
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    __shared__ int s_stop, s_bad;
+    __shared__ Judged s_j;
     __shared__ long long s_sums[2][kMaxCluster * kWarps];
     const int s = blockIdx.x / parts;
-    if (tid == 0) { s_stop = 0x7fffffff; s_bad = 0; }
+    if (tid == 0) { s_j.stop = -1; s_j.bad = 0; }
     cluster.sync();
     pdl_wait();
     pdl_trigger();
@@ -380,120 +565,159 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
         if (lead) answer(0, -1);
         return;                      // the whole cluster
     }
-    // every CTA judges the drafts for itself
-    for (int j = tid; j < n; j += kThreads) {
-        const RowInfo ri = a.rows[r0 + j];
-        if (ri.bad) s_bad = 1;
-        if (j == n - 1) continue;
-        const int x = a.tokens[r0 + j + 1];
-        if (x < 0 || x >= a.V) {
-            s_bad = 1;
-            if (part == 0) report(a.st, MOE_DEV_BAD_INDEX, r0 + j + 1);
-            continue;
-        }
-        bool ok;
-        if (temp.greedy) {
-            ok = x == ri.best;
-        } else {
-            double q = 1.0;
-            if (a.draft != nullptr) {
-                const RowInfo rq = a.rows[a.T + r0 + j];
-                if (rq.bad) { s_bad = 1; continue; }
-                const float l = load_one<L>(a.draft, (r0 + j) * a.ld_draft + x);
-                q = __ll2double_rn(units_of(weight(l, Scale(rq.m, temp.it)))) / __ll2double_rn(static_cast<long long>(rq.z));
+    // every CTA judges the drafts for itself: a warp gathers what is known of a row, then the first warp looks at them
+    for (int base = 0; base < n; base += kWarps) {
+        const int j = base + warp;
+        if (j < n) {
+            const bool last = j == n - 1, with = a.draft != nullptr && !temp.greedy && !last;
+            const int x = last ? 0 : a.tokens[r0 + j + 1];
+            const bool in = x >= 0 && x < a.V;
+            int best = 0;
+            bool bad = !in;
+#pragma unroll 1
+            for (int q = 0; q <= with; ++q) {
+                const float l = in ? load_one<L>(q ? a.draft : a.logits, (r0 + j) * (q ? a.ld_draft : a.ld) + x) : 0.f;
+                const RowInfo r = row_info(a, r0 + j + q * a.T, lane);
+                bad = bad || r.bad;
+                if (q == 0) best = r.best;
+                if (lane == 0) {
+                    s_j.z[warp][q] = r.z;
+                    s_j.m[warp][q] = r.m;
+                    s_j.u[warp][q] = units_of(weight(l, Scale(r.m, temp.it)));
+                }
             }
-            if (ri.bad) continue;
-            const float l = load_one<L>(a.logits, (r0 + j) * a.ld + x);
-            const double p = __ll2double_rn(units_of(weight(l, Scale(ri.m, temp.it)))) / __ll2double_rn(static_cast<long long>(ri.z));
-            ok = __dmul_rn(static_cast<double>(a.uniform[r0 + j + 1]), q) < p;
+            if (lane == 0) {
+                s_j.best[warp] = temp.greedy && !last && x != best ? -1 - best : best;
+                if (bad) s_j.bad = 1;
+                if (!in && part == 0) report(a.st, MOE_DEV_BAD_INDEX, r0 + j + 1);
+            }
         }
-        if (!ok) atomicMin(&s_stop, j);
+        __syncthreads();
+        if (warp == 0 && s_j.stop < 0) {
+            const int row = base + lane;
+            const bool in = lane < kWarps && row < n;
+            bool ends = in && row == n - 1;
+            Judge p = {}, q = {};
+            if (in && temp.greedy) {
+                ends = ends || s_j.best[lane] < 0;
+            } else if (in) {
+                const bool with = a.draft != nullptr && !ends;
+#pragma unroll 1
+                for (int i = 0; i <= with; ++i) {
+                    q = p;
+                    p = {s_j.z[lane][with - i], s_j.u[lane][with - i], s_j.m[lane][with - i], inverse(s_j.z[lane][with - i])};
+                }
+                ends = ends || !accepts(a.uniform[r0 + row + 1], p, q, with);
+            }
+            const unsigned mask = __ballot_sync(kFull, ends);
+            if (mask != 0 && lane == __ffs(mask) - 1) {
+                s_j.stop = row;
+                s_j.stop_m[0] = p.m;
+                s_j.stop_m[1] = q.m;
+                s_j.stop_inv[0] = p.inv;
+                s_j.stop_inv[1] = q.inv;
+                s_j.stop_best = s_j.best[lane] < 0 ? -1 - s_j.best[lane] : s_j.best[lane];
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    if (s_bad) {
+    if (s_j.bad) {
         if (lead) answer(0, -1);
         return;
     }
-    const int stop = min(s_stop, n - 1);
+    const int stop = s_j.stop;
     const int row = r0 + stop;
-    const RowInfo ri = a.rows[row];
     if (temp.greedy) {
-        if (lead) answer(stop, ri.best);
+        if (lead) answer(stop, s_j.stop_best);
         return;
     }
-    Draw<L> d = {Row<L>(a.logits, a.ld, row, a.V), Row<L>(a.logits, a.ld, row, a.V), Scale(ri.m, temp.it), Scale(0.f, temp.it), 0.f, 0.f, 0, -1};
+    Draw<L> d = {Row<L>(a.logits, a.ld, row, a.V), Row<L>(a.logits, a.ld, row, a.V), Scale(s_j.stop_m[0], temp.it), Scale(s_j.stop_m[1], temp.it), s_j.stop_inv[0], s_j.stop_inv[1], 0, -1};
     if (stop < n - 1) {
         d.mode = 1;
         d.without = a.tokens[row + 1];
         if (a.draft != nullptr) {
-            const RowInfo rq = a.rows[a.T + row];
             d.mode = 2;
             d.q = Row<L>(a.draft, a.ld_draft, row, a.V);
-            d.sq = Scale(rq.m, temp.it);
-            d.ip = __double2float_rn(0x1p42 / __ll2double_rn(static_cast<long long>(ri.z)));
-            d.iq = __double2float_rn(0x1p42 / __ll2double_rn(static_cast<long long>(rq.z)));
         }
     }
     // a warp's runs are neighbours, so that the warps' sums are the cumulated weight in order
     const int warps = parts * kWarps, w = part * kWarps + warp;
     const int v0 = static_cast<int>(static_cast<long long>(d.p.n) * w / warps), v1 = static_cast<int>(static_cast<long long>(d.p.n) * (w + 1) / warps);
-    long long total = 0, before = 0, own = 0;
-    for (int turn = 0; turn < 2; ++turn) {
-        Units u;
-        for (int v = v0 + lane; v < v1; v += 32) d.run(v, [&](int, float2 x) { u.add(x); });
-        own = warp_sum(u.sum());
+    long long before = 0, target = 0;
+    bool search = false;
+    // once or twice for the sums, then by the warp whose runs hold the token (one loop: the code is fetched once)
+#pragma unroll 1
+    for (int turn = 0;;) {
+        long long own = 0;
+        uint4 x = {}, y = {};
+        auto load = [&](int v) {
+            if (v >= v1) return;
+            x = __ldg(d.p.runs + v);
+            if (d.mode == 2) y = d.beside(v);
+        };
+        load(v0 + lane);
+#pragma unroll 1
+        for (int v = v0 + lane; v - lane < v1; v += 32) {
+            const uint4 xv = x, yv = y;
+            load(v + 32);
+            long long u[E], mine = 0;
+#pragma unroll
+            for (int i = 0; i < E; ++i) u[i] = 0;
+            if (v < v1)
+                d.run(v, xv, yv, [&](int i, float2 f) {
+                    u[i] = units_of(f.x);
+                    u[i + 1] = units_of(f.y);
+                });
+#pragma unroll
+            for (int i = 0; i < E; ++i) mine += u[i];
+            own += mine;
+            if (!search) continue;
+            long long inc = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long o = __shfl_up_sync(kFull, inc, off);
+                if (lane >= off) inc += o;
+            }
+            long long c = before + inc - mine;
+            if (target >= c && target < c + mine) {
+                int at = 0;
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    c += u[i];
+                    at += target >= c;
+                }
+                answer(stop, d.p.first(v) + at);
+            }
+            before += __shfl_sync(kFull, inc, 31);
+            if (target < before) break;
+        }
+        if (search) return;
+        own = warp_sum(own);
         if (lane < parts) cluster.map_shared_rank(s_sums[turn], lane)[w] = own;
         cluster.sync();
         // all of them, and those of the warps before
-        total = before = 0;
+        long long total = 0;
+        before = 0;
         for (int i = lane; i < warps; i += 32) {
-            const long long v = s_sums[turn][i];
-            total += v;
-            if (i < w) before += v;
+            const long long o = s_sums[turn][i];
+            total += o;
+            if (i < w) before += o;
         }
         total = warp_sum(total);
         before = warp_sum(before);
-        if (total > 0) break;        // the same in every CTA
-        d.mode = 0;                  // nothing of the target is beyond the draft
-    }
-    long long target = __double2ll_rd(__dmul_rn(static_cast<double>(a.uniform[r0]), __ll2double_rn(total)));
-    target = max(0ll, min(target, total - 1));
-    if (lead) {
-        a.accepted[s] = stop;
-        if (a.n_new != nullptr) a.n_new[s] = stop - (n - 1);
-    }
-    if (target < before || target >= before + own) return;
-    // this warp's runs hold the token
-    for (int v = v0; v < v1; v += 32) {
-        long long u[E], mine = 0;
-#pragma unroll
-        for (int i = 0; i < E; ++i) u[i] = 0;
-        if (v + lane < v1) {
-            d.run(v + lane, [&](int i, float2 x) {
-                u[i] = units_of(x.x);
-                u[i + 1] = units_of(x.y);
-            });
-#pragma unroll
-            for (int i = 0; i < E; ++i) mine += u[i];
+        if (total == 0) {            // nothing of the target is beyond the draft; the same in every CTA
+            d.mode = 0;
+            ++turn;
+            continue;
         }
-        long long inc = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long o = __shfl_up_sync(kFull, inc, off);
-            if (lane >= off) inc += o;
+        if (tid == 0) {
+            const long long t = __double2ll_rd(__dmul_rn(static_cast<double>(a.uniform[r0]), __ll2double_rn(total)));
+            s_j.target = max(0ll, min(t, total - 1));
         }
-        const long long all = __shfl_sync(kFull, inc, 31);
-        if (target < before + all) {
-            long long c = before + inc - mine;
-            if (target >= c && target < c + mine)
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    if (target >= c && target < c + u[i]) a.next[s] = d.p.first(v + lane) + i;
-                    c += u[i];
-                }
-            return;
-        }
-        before += all;
+        __syncthreads();
+        target = s_j.target;
+        if (target < before || target >= before + own) return;
+        search = true;
     }
 }
 
@@ -515,13 +739,30 @@ cudaError_t launch_clusters(K kernel, int items, int parts, cudaStream_t s, cons
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+int cdiv(int n, int d) { return (n + d - 1) / d; }
 template <typename L>
-cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
+cudaError_t launch(VerifyArgs a, void* ws, cudaStream_t s) {
     const int runs = a.V / Run<L>::E + 2;
     int parts = 1;
-    while (parts < kMaxCluster && runs > parts * kThreads * kHeld / 2) parts *= 2;
+    while (parts < kMaxCluster && runs > parts * kThreads) parts *= 2;
     if (a.T > 0) {
-        const cudaError_t e = launch_clusters(verify_rows_kernel<L>, a.draft != nullptr ? 2 * a.T : a.T, parts, s, a);
+        a.items = a.draft != nullptr ? 2 * a.T : a.T;
+        const bool few = static_cast<long long>(a.items) * parts <= kRowCtas;
+        a.max_per = few ? runs : kMaxThreads * kChunkHeld;
+        a.max_chunks = cdiv(runs, a.max_per);
+        a.per = few ? runs : 32 * kChunkHeld;
+        a.chunks = cdiv(runs, a.per);
+        const size_t units = static_cast<size_t>(a.items) * a.chunks;
+        a.sums = static_cast<ChunkSum*>(ws);
+        a.maxima = reinterpret_cast<float*>(a.sums + units);
+        a.scale = a.maxima + static_cast<size_t>(a.items) * a.max_chunks;
+        cudaError_t e;
+        if (few) {
+            e = launch_clusters(verify_rows_kernel<L>, a.items, parts, s, a);
+        } else {
+            e = launch_pdl(verify_max_kernel<L>, dim3(a.items * a.max_chunks), dim3(kMaxThreads), 0, s, a);
+            if (e == cudaSuccess) e = launch_pdl(verify_sum_kernel<L>, dim3((units + kSumThreads / 32 - 1) / (kSumThreads / 32)), dim3(kSumThreads), 0, s, a);
+        }
         if (e != cudaSuccess) return e;
     }
     return launch_clusters(verify_draw_kernel<L>, a.S, parts, s, a);
@@ -529,13 +770,20 @@ cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t verify_workspace(int T) { return 2 * static_cast<size_t>(T) * sizeof(RowInfo); }
+size_t verify_workspace(int T, int V) {
+    if (T == 0) return 0;
+    const int runs = V / Run<float>::E + 2;
+    const long long items = 2ll * T;
+    return static_cast<size_t>(items * cdiv(runs, 32 * kChunkHeld)) * sizeof(ChunkSum) +
+           static_cast<size_t>(items * (cdiv(runs, kMaxThreads * kChunkHeld) + 1)) * sizeof(float);
+}
 
 cudaError_t launch_verify(const void* logits, int dtype, long long ld, int T, int V, const int32_t* tokens, const float* uniform,
                           const int32_t* q_start, int S, const void* draft, long long ld_draft, const float* temperature, int32_t* accepted,
                           int32_t* next, int32_t* n_new, void* ws, moe_dev_status* st, cudaStream_t s) {
-    const VerifyArgs a = {logits, draft, ld, ld_draft, T, V, S, tokens, q_start, uniform, temperature, accepted, next, n_new, static_cast<RowInfo*>(ws), st};
-    return dtype == MOE_DTYPE_BF16 ? launch<__nv_bfloat16>(a, s) : launch<float>(a, s);
+    VerifyArgs a = {logits, draft, ld, ld_draft, T, V, S, tokens, q_start, uniform, temperature, accepted, next, n_new};
+    a.st = st;
+    return dtype == MOE_DTYPE_BF16 ? launch<__nv_bfloat16>(a, ws, s) : launch<float>(a, ws, s);
 }
 
 }  // namespace moe
