@@ -266,16 +266,23 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
             auto put = [&](auto* y, auto add) {
                 auto* p = y + static_cast<long long>(t0 + 16 * g) * a.ld_y + row;
                 for (int c = 16 * g; c < tok; c += 32, p += 32 * a.ld_y) {
+                    const int left = live ? a.T - (t0 + c) : 0;      // tokens of the 16 that there are
+                    auto* q = p;
+                    // (all on their way at once: a store could be to what a later load reads)
+                    float old[16];
+                    if constexpr (decltype(add)::value) {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x, q += a.ld_y) old[x] = x < left ? *q : 0.f;
+                        q = p;
+                    }
                     uint32_t d[16];
                     tmem_ld16(m * kMaxTok + lanes + c, d);
                     tmem_ld_wait();
-                    const int left = live ? a.T - (t0 + c) : 0;      // tokens of the 16 that there are
-                    auto* q = p;
 #pragma unroll
                     for (int x = 0; x < 16; ++x, q += a.ld_y) {
                         float v = fmaf(__uint_as_float(d[x]), scale, bias);
                         if (x < left) {
-                            if constexpr (decltype(add)::value) v += *q;
+                            if constexpr (decltype(add)::value) v += old[x];
                             if constexpr (sizeof(*q) == 2) *q = __float2bfloat16_rn(v);
                             else *q = v;
                         }
