@@ -27,7 +27,7 @@ constexpr int kHalves = 2;
 constexpr int kKeys = 256;                // places of an item
 constexpr int kMaxRows = 96;              // of a tile
 constexpr int kPart = kMaxRows / 2;       // columns that a thread takes at a time
-constexpr int kEpi = 8;                   // warps that convert keys and add up
+constexpr int kEpi = 16;                  // warps that convert keys and add up
 constexpr int kWarpMma = kEpi, kWarpQ = kEpi + kHalves;
 constexpr int kThreads = (kWarpQ + 1) * 32;
 constexpr int kPlanThreads = 1024;
@@ -203,13 +203,13 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
     if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
     return __all_sync(kFull, wait_long(bar, parity, abort_flag, st, site));
 }
-// Barrier of a half's four warps; the AND of what they bring.
+// Barrier of a half's warps; the AND of what they bring.
 __device__ __forceinline__ bool half_sync_and(int m, bool v) {
     uint32_t r;
     if (m == 0)
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(v ? 1u : 0u) : "memory");
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(v ? 1u : 0u) : "memory");
     else
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 3, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(v ? 1u : 0u) : "memory");
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 3, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(v ? 1u : 0u) : "memory");
     return r != 0;
 }
 // 4-d box of query numbers: numbers, query heads of a key head, key head, tokens.
@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const WeighArgs a
     __shared__ __align__(16) float s_z[C::stages][kMaxRows];   // -lse in powers of two
     __shared__ __align__(16) int s_p[C::stages][kMaxRows];     // the rows' places, -1 for one that adds nothing
     __shared__ int s_slow[C::stages];
+    __shared__ float s_sum[kKeys];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const WeighArgs a
             }
         } else {
             // ---------------- keys to bf16, and the sums ----------------
-            const int m = warp >> 2, r = (warp & 3) * 32 + lane;
+            const int m = warp >> 3, part = warp >> 2 & 1, r = (warp & 3) * 32 + lane;     // half, half of the columns, place
             const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
             uint32_t n = 0, seg = 0;
             bool more = true;
@@ -437,18 +438,21 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const WeighArgs a
                     const int tiles = k.head_tiles();
                     if (tiles == 0) continue;              // (goes on with the next head)
                     const uint8_t* base = static_cast<const uint8_t*>(a.c.pages) + (static_cast<long long>(page) * a.c.n_kv + k.head) * L::bytes;
-                    uint4 run[D / 32];
-                    uint32_t sc[D / 32];                   // two scales each
+                    // (the two warps of a place convert half of its numbers each)
+                    constexpr int kRuns = D / 64;
+                    uint4 run[kRuns];
+                    uint32_t sc[kRuns];                    // two scales each
 #pragma unroll
-                    for (int x = 0; x < D / 32; ++x) { run[x] = make_uint4(0u, 0u, 0u, 0u); sc[x] = 0u; }
+                    for (int x = 0; x < kRuns; ++x) { run[x] = make_uint4(0u, 0u, 0u, 0u); sc[x] = 0u; }
                     if (good) {
                         const int tok = key % kPage;
 #pragma unroll
-                        for (int x = 0; x < D / 32; ++x) run[x] = __ldg(reinterpret_cast<const uint4*>(base + L::k_code(tok, 32 * x)));
+                        for (int x = 0; x < kRuns; ++x) run[x] = __ldg(reinterpret_cast<const uint4*>(base + L::k_code(tok, 32 * (part * kRuns + x))));
 #pragma unroll
-                        for (int x = 0; x < D / 32; ++x) {
-                            if constexpr (L::R == 2) sc[x] = __ldg(reinterpret_cast<const uint16_t*>(base + L::k_scale(tok, 2 * x)));
-                            else sc[x] = __ldg(base + L::k_scale(tok, 2 * x)) | static_cast<uint32_t>(__ldg(base + L::k_scale(tok, 2 * x + 1))) << 8;
+                        for (int x = 0; x < kRuns; ++x) {
+                            const int y = 2 * (part * kRuns + x);
+                            if constexpr (L::R == 2) sc[x] = __ldg(reinterpret_cast<const uint16_t*>(base + L::k_scale(tok, y)));
+                            else sc[x] = __ldg(base + L::k_scale(tok, y)) | static_cast<uint32_t>(__ldg(base + L::k_scale(tok, y + 1))) << 8;
                         }
                     }
                     ok = wait_warp(bar(B_SEG + m), (seg & 1) ^ 1, &s_abort, a.st, kSiteSeg);     // the products with the keys before are over
@@ -456,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const WeighArgs a
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int x = 0; x < D / 32; ++x) {
+                    for (int x = 0; x < kRuns; ++x) {
                         const uint32_t two = e4m3x2_to_f16(sc[x]);
                         const uint32_t s2[2] = {__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232)};
                         const uint32_t words[4] = {run[x].x, run[x].y, run[x].z, run[x].w};
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const WeighArgs a
                                 memcpy(&v[y * 4 + j], &o, 4);
                             }
                         }
-                        st_cols(C::c_a + m * (D / 2) + x * 16 + lanes, v);
+                        st_cols(C::c_a + m * (D / 2) + (part * kRuns + x) * 16 + lanes, v);
                     }
                     st_wait();
                     tc_fence_before();
@@ -484,9 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const WeighArgs a
                     const float f = a.scale * kLog2e * (a.c.k_scale != nullptr ? a.c.k_scale[k.head] : 1.f);
                     const unsigned span = a.window > 0 ? a.window : 0x7fffffff;    // places from a key's own on that see it
                     float head_sum = 0.f;
-                    // Half a tile's columns at a time, the next ones on their way while the sums of these are taken.
-                    uint32_t d[2][kPart];
-                    auto at = [&](uint32_t u, int part) { return (m * 2 + (u & 1)) * kMaxRows + part * kPart + lanes; };
+                    auto at = [&](uint32_t u) { return (m * 2 + (u & 1)) * kMaxRows + part * kPart + lanes; };
                     auto wait_d = [&](uint32_t u) {
                         const uint32_t df = bar(B_DF + m * 2 + (u & 1)), qf = bar(B_QF + u % C::stages), pd = (u >> 1) & 1, pq = (u / C::stages) & 1;
                         if (!__all_sync(kFull, mbar_try_wait(qf, pq) && mbar_try_wait(df, pd)))
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const WeighArgs a
                         tc_fence_after();
                         return ok;
                     };
-                    auto add = [&](const uint32_t (&v)[kPart], int st, int part, bool slow) {
+                    auto add = [&](const uint32_t (&v)[kPart], int st, bool slow) {
                         float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                         if (!slow) {
 #pragma unroll
@@ -520,44 +522,38 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const WeighArgs a
                         }
                         head_sum += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
                     };
-                    int next_slow = 0;
-                    if (wait_d(n)) {
-                        ld_cols(at(n, 0), d[0]);
-                        next_slow = s_slow[n % C::stages];
-                    }
-                    for (int x = 0; x < tiles && ok; ++x, ++n) {
+                    for (int x = 0; x < tiles && wait_d(n); ++x, ++n) {
                         const int st = n % C::stages;
-                        const bool slow = next_slow != 0;
-                        tmem_ld_wait();
-                        ld_cols(at(n, 1), d[1]);
-                        add(d[0], st, 0, slow);
+                        uint32_t d[kPart];
+                        ld_cols(at(n), d);
+                        const bool slow = s_slow[st] != 0;
                         tmem_ld_wait();
                         tc_fence_before();                     // D is read: it may be written again
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(B_DE + m * 2 + (n & 1)));
-                        if (x + 1 < tiles && wait_d(n + 1)) {
-                            ld_cols(at(n + 1, 0), d[0]);
-                            next_slow = s_slow[(n + 1) % C::stages];
-                        }
-                        add(d[1], st, 1, slow);
+                        add(d, st, slow);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(B_QE + st));
                     }
-                    tmem_ld_wait();
                     sum += head_sum;
                 } while (ok && k.next_head());
                 // the warps of a half leave together where a wait has failed
+                if (part == 1) s_sum[m * 128 + r] = sum;
                 ok = half_sync_and(m, ok);
                 if (!ok) break;
-                if (starts && ends) {
-                    WeighSeq q;
-                    q.len = k.it.len;
-                    q.n = k.it.len - k.it.base;
-                    if (there && good) weigh_add(a, q, k.it.s, key, sum);
-                } else {
-                    w.part[(blockIdx.x * 2 + (starts ? 1 : 0)) * kKeys + m * 128 + r] = sum;
+                if (part == 0) {
+                    sum += s_sum[m * 128 + r];
+                    if (starts && ends) {
+                        WeighSeq q;
+                        q.len = k.it.len;
+                        q.n = k.it.len - k.it.base;
+                        if (there && good) weigh_add(a, q, k.it.s, key, sum);
+                    } else {
+                        w.part[(blockIdx.x * 2 + (starts ? 1 : 0)) * kKeys + m * 128 + r] = sum;
+                    }
                 }
                 more = k.next_item();
+                if (more) ok = half_sync_and(m, ok);           // the sums are read
             }
         }
     }
