@@ -1,0 +1,179 @@
+"""Calls at the edges between variants of the products in 4 bits, the weighing, the
+verification and the eviction: many rows, many sequences, other streams."""
+import numpy as np
+import pytest
+import torch
+
+import _kv4
+import _verify
+import _w4
+import expert_routing_moe_gb300 as moe
+from _gpu import DEV, dev, host, status_tensor
+from test_gpu_kv4_evict import Gpu, Host
+from test_gpu_kv4_weigh import Case
+from test_gpu_linear_w4 import EPS, Weights, _bf16, _check
+from test_gpu_verify import _case
+
+pytestmark = pytest.mark.gpu
+
+
+def _place(a, dtype, shift, ld):
+    """Rows `ld` numbers apart that start `shift` numbers into their memory, NaN between them."""
+    T, V = a.shape
+    buf = torch.full((T * ld + shift + 8,), float("nan"), dtype=dtype, device=DEV)
+    out = buf[shift:shift + T * ld].view(T, ld)[:, :V]
+    out.copy_(dev(a))
+    return out
+
+
+@pytest.mark.parametrize("S,V", [(70, 20003), (33, 50001)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("by_model", [False, True])
+def test_verification_of_many_rows(S, V, dtype, by_model):
+    """Rows in many chunks; the drafting model's rows lie otherwise between 16-byte boundaries than the target's."""
+    rng = np.random.default_rng(S)
+    logits, tokens, uniform, q_start, draft, temp = _case(rng, S, 3, V, by_model, dtype)
+    T = len(tokens)
+    bad = {1: np.nan, 5: np.inf}                       # rows of sequences that then have no answer
+    for s, v in bad.items():
+        if q_start[s + 1] > q_start[s]:
+            logits[q_start[s], V - 1] = v
+    nothing = q_start[9]
+    logits[nothing] = -np.inf
+    st = status_tensor()
+    acc, nxt, n_new = (torch.full((S,), -77, dtype=torch.int32, device=DEV) for _ in range(3))
+    ws = torch.full((moe.verify_workspace(T, S, V),), 255, dtype=torch.uint8, device=DEV)
+    moe.moe_verify_drafts(_place(logits, dtype, 1, V + 2), dev(tokens), dev(uniform), dev(q_start.astype(np.int32)), acc, nxt, n_new,
+                          draft_logits=None if draft is None else _place(draft, dtype, 3, V + 5), temperature=dev(temp), workspace=ws, st=st)
+    with np.errstate(invalid="ignore"):
+        want = _verify.verify(logits, tokens, uniform, q_start, draft, temp)
+    for g, w in zip((acc, nxt, n_new), want):
+        assert np.array_equal(host(g), w)
+    assert st.tolist()[0] == 1                         # not finite
+
+
+@pytest.mark.parametrize("S", [303, 304, 305])
+def test_verification_between_its_variants(S):
+    rng = np.random.default_rng(S)
+    V = 300
+    c = [rng.normal(size=(S, V)).astype(np.float32) * 3, np.zeros(S, np.int32), rng.random(S).astype(np.float32), np.arange(S + 1), None, None]
+    acc, nxt, n_new = (torch.full((S,), -77, dtype=torch.int32, device=DEV) for _ in range(3))
+    moe.moe_verify_drafts(dev(c[0]), dev(c[1]), dev(c[2]), dev(c[3].astype(np.int32)), acc, nxt, n_new)
+    for g, w in zip((acc, nxt, n_new), _verify.verify(*c)):
+        assert np.array_equal(host(g), w)
+
+
+def test_more_rows_than_a_sequence_may_have():
+    c = Case(31, [100, 90], [5, 2], 8, 2, 64)
+    good = host(c.run())
+    for n, q_start in ((3, [0, 5, 7]), (200, [0, 300, 302])):
+        c = Case(31, [400, 90], [q_start[1], 2], 8, 2, 64) if n > 3 else c
+        good = host(c.run())
+        c.max_new = n
+        st = status_tensor()
+        got = host(c.run(st=st))
+        assert st.tolist() == [3, 0]
+        assert np.array_equal(got[0], c.score[0]) and np.array_equal(got[1], good[1])
+
+
+@pytest.mark.parametrize("lengths,rows,n_q,n_kv,D", [
+    ([150], [3], 32, 16, 64), ([90, 200], [20, 4], 100, 1, 64), ([200], [30], 97, 1, 128), ([130], [3], 96, 1, 64), ([70] * 40, [1] * 40, 4, 2, 64), (list(range(300)), [1] * 300, 2, 1, 64),
+    ([300] * 5, [32] * 5, 8, 1, 64), ([300] * 5, [31] * 5, 8, 1, 64)])
+def test_weighing_of_other_shapes(lengths, rows, n_q, n_kv, D):
+    """More key heads than one pass holds, groups beyond a tile, many sequences, rows at the limit of a variant."""
+    rows = [min(r, n) for r, n in zip(rows, lengths)]
+    Case(32, lengths, rows, n_q, n_kv, D).check()
+
+
+@pytest.mark.parametrize("T,N,K", [
+    (8, 4864, 130), (8, 4865, 130), (9, 14592, 130), (9, 14593, 130), (40, 14593, 200), (63, 257, 200), (64, 257, 200), (65, 257, 200), (66, 130, 137), (5, 14600, 8200),
+    (96, 600, 72), (97, 600, 72), (191, 300, 130), (192, 300, 130), (193, 300, 130), (385, 129, 140)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_products_between_their_variants(T, N, K, dtype):
+    rng = np.random.default_rng(T + N)
+    w = Weights(rng, N, K)
+    x = _bf16(rng.normal(size=(T, K)))
+    y = torch.full((T, N), float("nan"), dtype=dtype, device=DEV)
+    moe.moe_linear_w4(x.to(DEV), w.w, y)
+    _check(y, _w4.linear(x.double().numpy(), w.ref, out_eps=EPS[dtype]), dtype)
+    if dtype == torch.float32:
+        before = y.double()
+        moe.moe_linear_w4(x.to(DEV), w.w, y, accumulate=True)
+        # twice the first sum, rounded once
+        assert torch.equal(y, (2 * before).float())
+
+
+def test_through_another_stream():
+    """Each operator with `stream=`, while the current stream is another one and busy with something else."""
+    rng = np.random.default_rng(33)
+    side = torch.cuda.Stream()
+    w = Weights(rng, 300, 200)
+    x = _bf16(rng.normal(size=(70, 200))).to(DEV)
+    want_y, got_y = (torch.empty(70, 300, device=DEV) for _ in range(2))
+    moe.moe_linear_w4(x, w.w, want_y)
+    c = Case(34, [500, 90], [70, 3], 8, 2, 64)
+    q_start, lse, score = dev(c.q_start), dev(c.lse), dev(c.score)
+    want_s = c.run()
+    v = _case(rng, 7, 3, 2001, True, torch.float32)
+    args = [dev(v[0]), dev(v[1]), dev(v[2]), dev(v[3].astype(np.int32))]
+    outs = [torch.full((7,), -77, dtype=torch.int32, device=DEV) for _ in range(3)]
+    draft, temp = dev(v[4]), dev(v[5])
+    h = Host(rng, [300, 200], 2, 1, 64)
+    g = Gpu(h)
+    budget = dev(np.array([100, 150], np.int32))
+    tiles = moe.Weight4.empty(300, 200, DEV)
+    dense = torch.randn(300, 200, device=DEV)
+    want_w = moe.Weight4.pack(dense)
+    torch.cuda.synchronize()
+    busy = torch.randn(2048, 2048, device=DEV)
+    for _ in range(5):
+        busy = busy @ busy
+    moe.moe_linear_w4(x, w.w, got_y, stream=side)
+    moe.moe_kv4_weigh(c.q_dev, c.cache, q_start, lse, score, c.scale, c.max_new, stream=side)
+    moe.moe_verify_drafts(*args, *outs, draft_logits=draft, temperature=temp, stream=side)
+    moe.moe_kv4_evict(g.pool, g.score, budget, 2, 3, g.ws, None, g.st, stream=side)
+    moe.moe_w4_pack(dense, tiles, stream=side)
+    side.synchronize()
+    assert torch.equal(want_y, got_y) and torch.equal(want_s, score)
+    for a, b in zip(outs, _verify.verify(*v)):
+        assert np.array_equal(host(a), b)
+    assert h.evict(host(budget), 2, 3) == (0, 0)
+    g.same(h)
+    assert torch.equal(tiles.tensors[0], want_w.tensors[0]) and torch.equal(tiles.tensors[1], want_w.tensors[1])
+
+
+def test_two_evictions_at_once():
+    """Pools of their own, each with its workspace, on two streams."""
+    rng = np.random.default_rng(35)
+    hosts = [Host(rng, [3000, 100, 900], 4, 2, 64, shared=[2], spare=30), Host(rng, [2500, 1800], 4, 2, 128)]
+    gpus, streams = [Gpu(h) for h in hosts], [torch.cuda.Stream() for _ in hosts]
+    for turn in range(3):
+        budgets = [np.array([1500 - 400 * turn, 50, 300], np.int32), np.array([2000 - 500 * turn, 1000], np.int32)]
+        on = [dev(b) for b in budgets]
+        torch.cuda.synchronize()
+        for g, b, s in zip(gpus, on, streams):
+            moe.moe_kv4_evict(g.pool, g.score, b, 4, 20, g.ws, None, g.st, stream=s)
+        torch.cuda.synchronize()
+        for g, b, h in zip(gpus, budgets, hosts):
+            assert h.evict(b, 4, 20) == (0, 0)
+            g.same(h)
+
+
+def test_a_short_status_is_refused():
+    short = torch.zeros(1, dtype=torch.int32, device=DEV)
+    w = Weights(np.random.default_rng(36), 20, 16)
+    x, y = torch.zeros(1, 16, dtype=torch.bfloat16, device=DEV), torch.zeros(1, 20, device=DEV)
+    c = Case(36, [70], [1], 2, 1, 64)
+    q_start, lse, score = dev(c.q_start), dev(c.lse), dev(c.score)
+    one, f = torch.zeros(1, dtype=torch.int32, device=DEV), torch.zeros(1, device=DEV)
+    g = Gpu(Host(np.random.default_rng(36), [70], 1, 1, 64))
+    before = g.len.clone()
+    for stream in (None, torch.cuda.current_stream()):
+        for call in (lambda: moe.moe_linear_w4(x, w.w, y, st=short, stream=stream),
+                     lambda: moe.moe_w4_pack(torch.zeros(20, 16, device=DEV), w.w, st=short, stream=stream),
+                     lambda: moe.moe_kv4_weigh(c.q_dev, c.cache, q_start, lse, score, 1.0, 1, st=short, stream=stream),
+                     lambda: moe.moe_verify_drafts(torch.zeros(1, 9, device=DEV), one, f, q_start, one, one, st=short, stream=stream),
+                     lambda: moe.moe_kv4_evict(g.pool, g.score, one, 0, 0, g.ws, st=short, stream=stream)):
+            with pytest.raises(moe.MoeError, match="status"):
+                call()
+    assert torch.equal(g.len, before) and np.array_equal(host(score), c.score)
