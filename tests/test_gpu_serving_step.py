@@ -1,5 +1,9 @@
 """The products with weights in 4 bits, the scores of cached tokens, the verification
 of drafts and the eviction together, as a server runs them."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -305,3 +309,12 @@ def test_what_was_not_asked_for_is_refused():
     pages.reserve(_i32([4]))
     with pytest.raises(moe.MoeError):
         layer.forward(torch.zeros(4, H, dtype=torch.bfloat16, device=DEV), pages.layer(0), _i32([0, 4]), 4, score=torch.zeros(1, 128, device=DEV))
+
+
+def test_the_example_drafts_and_evicts():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "decode_kv4.py"), "--layers", "2", "--batch", "8", "--prompt", "170", "--steps", "4", "--hidden", "256",
+                        "--experts", "16", "--intermediate", "128", "--vocabulary", "1001", "--drafts", "3", "--budget", "100", "--four-bit"],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert "evicted: 100 tokens a sequence were 174" in r.stdout and "with drafts" in r.stdout and "after forking and packing" in r.stdout
