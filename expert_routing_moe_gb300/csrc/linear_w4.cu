@@ -248,6 +248,12 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// Clocks that the kernel for few tokens should take, for 9 to 64 of them.
+static double few_clocks(const LinearArgs& a) {
+    const double rows = a.N * 1e-3 * a.kt;
+    return 1000.0 + rows * (a.T <= 16 ? 53.0 : a.T <= 32 ? 142.0 : 285.0);
+}
+
 cudaError_t launch_linear_w4(const void* x, long long ld_x, int T, const moe_w4& w, const float* bias, void* y, int y_dtype, long long ld_y,
                              bool add, moe_dev_status* st, cudaStream_t s) {
     LinearArgs a;
@@ -266,7 +272,10 @@ cudaError_t launch_linear_w4(const void* x, long long ld_x, int T, const moe_w4&
     a.y_bf16 = y_dtype == MOE_DTYPE_BF16;
     a.add = add;
     a.wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ld_x % 8 == 0;
-    if (T > 64) return launch_linear_w4_tc(a, s);
+    if (T > 8) {
+        const LinearTile t = linear_w4_tile(a);
+        if (T > 64 || t.clocks < few_clocks(a)) return launch_linear_w4_tc(a, t, s);
+    }
     if (T <= 8) return launch_few<1>(a, s);
     return T <= 16 ? launch_few<2>(a, s) : launch_few<4>(a, s);
 }

@@ -54,6 +54,12 @@ __device__ __forceinline__ void put_y(const LinearArgs& a, int t, int n, float v
     else static_cast<float*>(a.y)[at] = a.add ? static_cast<float*>(a.y)[at] + v : v;
 }
 
-cudaError_t launch_linear_w4_tc(const LinearArgs& a, cudaStream_t s);
+// How the kernel for many tokens cuts a call: tokens of a tile, CTAs that share one, and the clocks that it should take.
+struct LinearTile {
+    int tok, split;
+    double clocks;
+};
+LinearTile linear_w4_tile(const LinearArgs& a);
+cudaError_t launch_linear_w4_tc(const LinearArgs& a, const LinearTile& t, cudaStream_t s);
 
 }  // namespace moe

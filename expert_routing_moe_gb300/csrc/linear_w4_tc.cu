@@ -10,6 +10,7 @@
 // turn) and write the outputs, 16 and 17 issue a half's products each, 18 copies the
 // weights' tiles, 19 the tokens (or 19-22, with plain loads, where rows of x do not start at 16-byte boundaries).
 // TMEM columns: D 2 x 192, A 2 halves x 2 buffers x 32.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <type_traits>
 
@@ -20,6 +21,8 @@
 #include "w4.cuh"
 
 namespace moe {
+
+namespace cg = cooperative_groups;
 
 namespace {
 
@@ -36,6 +39,10 @@ constexpr int kColA = kHalves * kMaxTok;  // TMEM column of the A buffers
 constexpr int kLoaders = 4;               // warps that load x where TMA cannot
 constexpr int kConv = 16;                 // warps that convert
 constexpr int kWarpMma = kConv, kWarpW = kConv + 2, kWarpX = kConv + 3;
+
+constexpr int kMaxSplit = 8;              // CTAs that share a tile
+// Clusters of that many CTAs that run at a time: some groups of SMs have too few left for another one.
+int clusters_of(int split) { return sm_count() / split - (split == 8 ? 4 : split == 4 ? 2 : 0); }
 
 enum Bar : int { B_WF = 0, B_WE = B_WF + kHalves * kRaw, B_AF = B_WE + kHalves * kRaw, B_AE = B_AF + 4, B_BF = B_AE + 4, B_BE = B_BF + kB,
                  B_DF = B_BE + kB, B_DE, B_DRAIN, B_N = B_DRAIN + kHalves };
@@ -77,6 +84,8 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
     return __all_sync(kFull, wait_long(bar, parity, abort_flag, st, site));
 }
 
+long long tiles_of(const LinearArgs& a, int tok) { return static_cast<long long>((a.N + kTileRows - 1) / kTileRows) * ((a.T + tok - 1) / tok); }
+
 // The tiles of a CTA: row tile and first token.
 struct Tiles {
     int tok_tiles, total, tok;
@@ -85,7 +94,7 @@ struct Tiles {
 };
 
 template <bool TMA>
-__global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linear_w4_tc_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_x, int tok) {
+__global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linear_w4_tc_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_x, int tok, int split) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ __align__(8) uint64_t bars[B_N];
@@ -116,8 +125,10 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
     w.tok_tiles = (a.T + tok - 1) / tok;
     const int halves = (a.N + kW4Tile - 1) / kW4Tile;
     w.total = (halves + kHalves - 1) / kHalves * w.tok_tiles;
-    const int steps = 2 * a.kt;
-    const int first = blockIdx.x, by = gridDim.x;
+    // a cluster of `split` CTAs has a tile, each a part of its columns; without one a CTA has every gridDim.x-th tile
+    const int part = split > 1 ? static_cast<int>(blockIdx.x) % split : 0;
+    const int first = blockIdx.x / split, by = gridDim.x / split;
+    const int c0 = a.kt * part / split, c1 = a.kt * (part + 1) / split;
     bool ok = true;
 
     pdl_wait();
@@ -127,7 +138,7 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
         if (lane == 0) {
             uint32_t n = 0;            // tiles of a half copied
             for (int i = first; i < w.total && ok; i += by)
-                for (int c = 0; c < a.kt && ok; ++c, ++n) {
+                for (int c = c0; c < c1 && ok; ++c, ++n) {
                     const int st = n % kRaw;
                     for (int m = 0; m < kHalves && ok; ++m) {
                         ok = mbar_wait(bar(B_WE + m * kRaw + st), ((n / kRaw) & 1) ^ 1, &s_abort, a.st, kSiteWEmpty);
@@ -153,7 +164,7 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
                 tma_prefetch_desc(&map_x);
                 const uint64_t policy = l2_policy_evict_last();
                 for (int i = first; i < w.total && ok; i += by)
-                    for (int k = 0; k < steps && ok; ++k, ++n) {
+                    for (int k = 2 * c0; k < 2 * c1 && ok; ++k, ++n) {
                         const int st = n % kB;
                         ok = mbar_wait(bar(B_BE + st), ((n / kB) & 1) ^ 1, &s_abort, a.st, kSiteBEmpty);
                         if (!ok) break;
@@ -168,7 +179,7 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
             }
         } else {
             for (int i = first; i < w.total && ok; i += by)
-                for (int k = 0; k < steps && ok; ++k, ++n) {
+                for (int k = 2 * c0; k < 2 * c1 && ok; ++k, ++n) {
                     const int st = n % kB;
                     ok = mbar_wait(bar(B_BE + st), ((n / kB) & 1) ^ 1, &s_abort, a.st, kSiteBEmpty);
                     ok = __all_sync(kFull, ok);
@@ -191,7 +202,7 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
         uint32_t n = 0, done = 0;
         for (int i = first; i < w.total && ok; i += by, ++done) {
             ok = wait_warp(bar(B_DE), (done & 1) ^ 1, &s_abort, a.st, kSiteDEmpty);
-            for (int k = 0; k < steps && ok; ++k, ++n) {
+            for (int k = 2 * c0; k < 2 * c1 && ok; ++k, ++n) {
                 const int st = n % kB, buf = n & 1;
                 ok = wait_warp(bar(B_BF + st), (n / kB) & 1, &s_abort, a.st, kSiteBFull) &&
                      wait_warp(bar(B_AF + m * 2 + buf), (n >> 1) & 1, &s_abort, a.st, kSiteAFull);
@@ -201,7 +212,7 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
                     const uint64_t b = b0 + static_cast<uint64_t>(st * (kBBytes >> 4));
                     const uint32_t at = kColA + (m * 2 + buf) * 32;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) mma_ts(m * kMaxTok, at + x * 8, b + x * 2, idesc, k > 0 || x > 0);
+                    for (int x = 0; x < 4; ++x) mma_ts(m * kMaxTok, at + x * 8, b + x * 2, idesc, k > 2 * c0 || x > 0);
                     tc_commit(bar(B_AE + m * 2 + buf));
                     tc_commit(bar(B_BE + st));
                 }
@@ -222,7 +233,7 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         uint32_t raw = 0, done = 0;
         for (int i = first; i < w.total && ok; i += by, ++done) {
-            for (int c = 0; c < a.kt && ok; ++c, ++raw) {
+            for (int c = c0; c < c1 && ok; ++c, ++raw) {
                 const int st = raw % kRaw;
                 ok = wait_warp(bar(B_WF + m * kRaw + st), (raw / kRaw) & 1, &s_abort, a.st, kSiteWFull);
                 if (!ok) break;
@@ -258,6 +269,17 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
             ok = wait_warp(bar(B_DF), done & 1, &s_abort, a.st, kSiteDFull);
             if (!ok) break;
             tc_fence_after();
+            if (split > 1) {
+                // what is not yet the whole sum waits in shared memory, whose operands are used up: [token][row]
+                for (int c = 16 * g; c < tok; c += 32) {
+                    uint32_t d[16];
+                    tmem_ld16(m * kMaxTok + lanes + c, d);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) reinterpret_cast<float*>(smem)[(c + x) * kTileRows + m * kW4Tile + r] = __uint_as_float(d[x]);
+                }
+                break;                 // (the CTA's only tile)
+            }
             const int row = w.row(i) * kTileRows + m * kW4Tile + r, t0 = w.t0(i);
             const bool live = row < a.N;
             const float scale = (live && a.row_scale != nullptr ? a.row_scale[row] : 1.f) * kW4Up;
@@ -302,6 +324,33 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (split > 1) {
+        // each CTA adds up the parts of some of the tile's tokens, in the order of the columns
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        const float* parts[kMaxSplit];
+#pragma unroll
+        for (int i = 0; i < kMaxSplit; ++i) parts[i] = cluster.map_shared_rank(reinterpret_cast<const float*>(smem), i < split ? i : 0);
+        const int x0 = tok * part / split, x1 = min(tok * (part + 1) / split, a.T - w.t0(first));
+        for (int u = warp; u < (x1 - x0) * kHalves; u += blockDim.x / 32) {
+            const int x = x0 + u / kHalves, r = u % kHalves * kW4Tile + lane * 4, row = w.row(first) * kTileRows + r;
+            float4 v[kMaxSplit], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kMaxSplit; ++i)
+                if (i < split) v[i] = *reinterpret_cast<const float4*>(parts[i] + x * kTileRows + r);
+#pragma unroll
+            for (int i = 0; i < kMaxSplit; ++i)
+                if (i < split) { sum.x += v[i].x; sum.y += v[i].y; sum.z += v[i].z; sum.w += v[i].w; }
+            const float of[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (row + i >= a.N) break;
+                const float scale = (a.row_scale != nullptr ? a.row_scale[row + i] : 1.f) * kW4Up;
+                put_y(a, w.t0(first) + x, row + i, fmaf(of[i], scale, a.bias != nullptr ? a.bias[row + i] : 0.f));
+            }
+        }
+        cluster.sync();                // no CTA leaves while its shared memory is read
+    }
 }
 
 // [T][K] bf16 with rows `ld` numbers apart, boxes of 64 columns and `tok` rows with the 128-byte swizzle.
@@ -317,32 +366,50 @@ bool map_tokens(CUtensorMap* m, const LinearArgs& a, int tok) {
 }
 
 template <bool TMA>
-cudaError_t launch(const LinearArgs& a, int tok, cudaStream_t s) {
+cudaError_t launch(const LinearArgs& a, const LinearTile& t, cudaStream_t s) {
     CUtensorMap map = {};
-    if (TMA && !map_tokens(&map, a, tok)) return cudaErrorInvalidValue;
+    if (TMA && !map_tokens(&map, a, t.tok)) return cudaErrorInvalidValue;
     auto* k = linear_w4_tc_kernel<TMA>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    const long long tiles = static_cast<long long>((a.N + kTileRows - 1) / kTileRows) * ((a.T + tok - 1) / tok);
-    return launch_pdl(k, dim3(static_cast<unsigned>(tiles < sm_count() ? tiles : sm_count())), dim3((kWarpX + (TMA ? 1 : kLoaders)) * 32), kSmem, s, a, map, tok);
+    const long long ctas = tiles_of(a, t.tok) * t.split;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(t.split > 1 || ctas < sm_count() ? ctas : sm_count()));
+    cfg.blockDim = dim3((kWarpX + (TMA ? 1 : kLoaders)) * 32);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = t.split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = t.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, a, static_cast<const CUtensorMap>(map), t.tok, t.split);
 }
 
 }  // namespace
 
-// Tokens of a tile: as many as make the longest CTA's time shortest.  A step of 64 columns takes 4 clocks a token and
-// some 100 more, or 630 for the conversion of its weights, whichever is longer, and a tile its outputs.  (2001 tokens through 5120 x
-// 2048 with 64, 96, 128, 144, 160 tokens a tile: 58.0, 37.6, 39.2, 28.1, 29.8 us; 8192 tokens with 128, 144, 160: 112, 104, 98 us.)
-cudaError_t launch_linear_w4_tc(const LinearArgs& a, cudaStream_t s) {
-    const long long rows = (a.N + kTileRows - 1) / kTileRows;
-    int best = 16;
-    double least = 1e300;
-    for (int tok = 16; tok <= kMaxTok; tok += 16) {
-        const long long tiles = rows * ((a.T + tok - 1) / tok), waves = (tiles + sm_count() - 1) / sm_count();
+// Tokens of a tile, and CTAs that share one: those that make the longest CTA's time shortest.  A step of 64 columns takes 4 clocks
+// a token and some 100 more, or 630 for the conversion of its weights, whichever is longer, and a tile its outputs; parts
+// meet in 2000 clocks more, and clusters of 8 leave some SMs without work.
+LinearTile linear_w4_tile(const LinearArgs& a) {
+    LinearTile best = {16, 1, 1e300};
+    for (int tok = 16; tok <= kMaxTok && tok < a.T + 16; tok += 16) {
+        const long long tiles = tiles_of(a, tok);
         const double step = 4.0 * tok + 100.0 > 630.0 ? 4.0 * tok + 100.0 : 630.0;
-        const double time = static_cast<double>(waves) * (2.0 * a.kt * step + 1500.0 + 12.0 * tok);
-        if (time < least) { least = time; best = tok; }
+        for (int split = 1; split <= kMaxSplit && split <= a.kt; split *= 2) {
+            if (split > 1 && tiles > clusters_of(split)) break;
+            const long long waves = split > 1 ? 1 : (tiles + sm_count() - 1) / sm_count();
+            const double clocks = static_cast<double>(waves) * (2.0 * ((a.kt + split - 1) / split) * step + 1500.0 + 12.0 * tok) + (split > 1 ? 2000.0 + 8.0 * tok : 0.0);
+            if (clocks < best.clocks) best = {tok, split, clocks};
+        }
     }
-    return a.wide ? launch<true>(a, best, s) : launch<false>(a, best, s);
+    return best;
 }
+
+cudaError_t launch_linear_w4_tc(const LinearArgs& a, const LinearTile& t, cudaStream_t s) { return a.wide ? launch<true>(a, t, s) : launch<false>(a, t, s); }
 
 }  // namespace moe
