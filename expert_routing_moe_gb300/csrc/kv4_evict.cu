@@ -1,9 +1,9 @@
 // kv4_evict.cu -- eviction from the 4-bit cache by the tokens' scores
 // (moe_kv4_evict): three launches.
 //
-//  select  a CTA for each sequence finds the score that a token needs (a radix
-//          select over the scores' bits, eight at a time) and lists the kept
-//          tokens in order
+//  select  a cluster for each sequence finds the score that a token needs (a
+//          radix select over the scores' 32 bits, 11, 11 and 10 at a time) and
+//          lists the kept tokens in order
 //  plan    one CTA gives every sequence its free pages, all or nothing
 //  move    tables, references, lengths and scores, a CTA for each sequence; and
 //          the kept tokens' codes and scales, a cluster for each (layer, head,
@@ -11,7 +11,17 @@
 //
 // Moving in place: the k-th kept token comes from a place >= k, so a page is read
 // only for itself and for pages before it.  A cluster reads the sources of
-// up to 32 pages into registers, meets, then writes them: whatever it writes has been read by then.
+// up to 32 pages into registers, meets, then writes them: whatever it writes has
+// been read by then.  A sequence whose pages all go to free ones needs no meeting.
+//
+// 32001 tokens of 48 layers (4 heads of 128) cut to 8192: 200 us onto free pages,
+// 243 in place, of which the selection takes 23; 32 sequences of 8 layers 167.
+// 453 MB are to be moved, which is 67 us at the rate of a copy; kept tokens lie
+// scattered, 64 bytes of keys and as many of values that they share with a
+// neighbour, so that whole sectors of others come with them.  (A CTA a page, whose
+// threads look for their sources in the list: 353 us; sources of a page's tokens in
+// shared memory, three warps a page: 238; the next pages' sources looked for ahead: 207
+// against 200.)
 #include <cooperative_groups.h>
 
 #include "common.cuh"

@@ -64,8 +64,10 @@ __device__ __forceinline__ void weigh_add(const WeighArgs& a, const WeighSeq& q,
     *out = a.fresh && key >= q.first_new() ? v : *out + v;
 }
 
-// The kernel for prompts takes sequences of that many counted rows (times query heads of a key head).
-constexpr int kWeighMany = 256;
+// The kernel for prompts takes sequences of that many counted rows (times query heads of a key head).  9001 tokens, 32 + 4 heads:
+// 64 rows 14.6 us without it and 20.5 with it (it is three launches), 128 rows 23.6 and 18.0, 256 rows 42 and 19, 1024 rows
+// 154 and 27; six such sequences 14.4 / 21.4, 23.8 / 22.1, 42 / 24, 154 / 34; 128 rows of 500 tokens 23.2 / 17.0.
+constexpr int kWeighMany = 128;
 bool weigh_tc_fits(int group);
 size_t kv4_weigh_tc_workspace(int S, int max_pages);
 cudaError_t launch_kv4_weigh_tc(const WeighArgs& a, void* ws, cudaStream_t s);

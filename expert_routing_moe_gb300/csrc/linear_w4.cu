@@ -5,9 +5,19 @@
 // c * s has at most six significant bits, so it is exact in bf16, and so are the
 // products of the tensor cores; sums are fp32.
 //
-// Few tokens: the weights are the 16-row operand of mma.sync.m16n8k16, eight
-// tokens the other.  A CTA takes 32 rows; its warps share their columns, 128 at
-// a time, and join their sums in shared memory in a fixed order.
+// Few tokens (more: linear_w4_tc.cu): the weights are the 16-row operand of
+// mma.sync.m16n8k16, eight tokens the other.  A CTA takes 16 or 32 rows a step;
+// its warps share their columns, 128 at a time, and join their sums in shared
+// memory in a fixed order.  A piece of weights is on its way while the one
+// before is multiplied, the first one's bytes before the kernel before has ended.
+//
+// What bounds it: one token through 5120 x 2048 takes 3.7 us (the call's host
+// time), a head of 128001 x 2048 for five tokens 36.6 us for 148 MB (4.0 TB/s;
+// 22 us at the rate of a copy): 15 instructions turn eight codes into bf16,
+// 25 codes a clock and SM, and 443 go with a piece of 32 x 128 in all, at
+// 63% of the issue slots.  (Two pieces ahead: 41.5 us, a CTA less fits; four
+// CTAs an SM: 39.5 with spills; sums of two steps joined at a time: 38.4;
+// pieces of all steps in equal runs for the warps, without a join a step: 43.7.)
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -239,7 +249,10 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
 
 template <int NT>
 cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
-    // few rows: every CTA has one step, of 16 rows where 32 would leave SMs without any
+    // Few rows: every CTA has one step, of 16 rows where 32 would leave SMs without any; many: persistent CTAs with x in
+    // shared memory.  Through 2048 x N, 16 rows / 32 rows / persistent, 1 token: N = 2048 2.7 / 2.9 / 3.5 us, 8192 5.3 / 3.9 /
+    // 6.4, 14000 7.0 / 6.4 / 6.8, 32000 14.2 / 12.1 / 11.9; 16 tokens: 3.7 / 4.3 / 7.0, 9.0 / 6.2 / 8.6, 12.9 / 11.3 / 11.5,
+    // 26.4 / 18.4 / 16.8.
     const int sms = sm_count();
     if (a.N <= 16 * sms * 2) return launch_few<NT, 1, false>(a, s);
     if (a.N <= 32 * sms * 3 || static_cast<size_t>(a.kt) * kW4Tile * 16 * NT > 128 * 1024) return launch_few<NT, 2, false>(a, s);
@@ -248,7 +261,9 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Clocks that the kernel for few tokens should take, for 9 to 64 of them.
+// Clocks that the kernel for few tokens should take, for 9 to 64 of them.  (Both sides, few / many: through 2048 x 2048 16
+// tokens 3.7 / 6.2 us, 32 5.1 / 6.8, 48 8.6 / 7.4, 64 9.6 / 8.1; 8192 x 2048: 9.6 / 10.3, 15.2 / 10.9, 25.6 / 11.5, 29.5 / 12.2; 2048 x
+// 5120: 6.0 / 7.5, 11.4 / 8.2, 15.6 / 8.8, 17.0 / 9.3; 2048 x 32000: 16.9 / 13.9, 28.4 / 14.2, 51 / 14.6, 55 / 15.0.)
 static double few_clocks(const LinearArgs& a) {
     const double rows = a.N * 1e-3 * a.kt;
     return 1000.0 + rows * (a.T <= 16 ? 53.0 : a.T <= 32 ? 142.0 : 285.0);

@@ -7,6 +7,14 @@
 // drafts and draws the token that follows.  Weights are whole multiples of 2^-42
 // made from fp32 numbers whose every operation is rounded in a known way, so
 // that sums of them do not depend on their order and a draw not on the grid.
+//
+// 32 sequences of up to five rows of 128001 bf16 logits and as many of a drafting
+// model's: 54 MB, 8 us at the rate of a copy; 41 us, about 10 for the maxima, 16 for the sums (24 instructions for two
+// weights, half of the issue slots) and 15 for the draw, a chain of loads and
+// meetings.  One sequence of five rows of 32000: 9.8 us, all of it such a chain.
+// Tried: a row's cluster that finds the maximum and the sum at once for all sizes
+// (53 us), one kernel with a cluster a sequence for everything (56 us, one
+// sequence 14.9), the draw by a warp a chunk and the last one (44 us, 12.8).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -747,6 +755,8 @@ cudaError_t launch(VerifyArgs a, void* ws, cudaStream_t s) {
     while (parts < kMaxCluster && runs > parts * kThreads) parts *= 2;
     if (a.T > 0) {
         a.items = a.draft != nullptr ? 2 * a.T : a.T;
+        // (clusters / chunks, five rows of 32000 fp32 logits a sequence: 1 sequence 10.0 / 10.9 us, 8 12.5 / 12.3, 16 17.4 /
+        // 15.3, 64 48.9 / 27.2; of 2000, with a drafting model's: 1 11.1 / 11.9, 32 11.8 / 12.7, 64 15.3 / 13.9)
         const bool few = static_cast<long long>(a.items) * parts <= kRowCtas;
         a.max_per = few ? runs : kMaxThreads * kChunkHeld;
         a.max_chunks = cdiv(runs, a.max_per);

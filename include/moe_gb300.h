@@ -36,6 +36,15 @@
  *               moe_kv4_reserve, moe_kv4_assign, moe_kv4_compact
  *                                the cache's pages: growing, copying on write,
  *                                forking, reordering, freeing and packing
+ *               moe_kv4_weigh, moe_kv4_evict
+ *                                the attention weight that cached tokens draw,
+ *                                and eviction of those that drew least
+ *               moe_linear_w4, moe_w4_pack
+ *                                products with weights in 4 bits (projections,
+ *                                heads), and their rounding
+ *               moe_verify_drafts
+ *                                how many drafted tokens the target's logits
+ *                                accept, and the token that follows
  *
  * Conventions for every entry point
  *  - Pointers named "host" are host memory; every other pointer is device
@@ -664,12 +673,12 @@ size_t moe_kv4_pool_workspace(int S, int n_pages);
  *   workspace  moe_kv4_weigh_workspace() bytes, 256-byte aligned; holds nothing between
  *            calls, so one buffer serves calls of any sizes in turn; serves one call at a
  *            time; may be NULL where that is 0
- * The cache's values are not read.  Products run on the tensor cores in fp16 (q
- * scaled by a power of two of its row, keys exact) with fp32 sums;
- * exponentials and their sums are fp32, added in an order that depends on
- * sizes alone, so results are reproducible bit for bit.  A page outside the pool, a
- * length beyond the table or a bad q_start is reported (MOE_DEV_BAD_INDEX)
- * and adds nothing.
+ * The cache's values are not read.  Products run on the tensor cores with fp32
+ * sums, keys exact: in fp16 with q scaled by a power of two of its row, or, where a
+ * sequence has many rows, in bf16 (q as it is).  Exponentials and their sums are
+ * fp32, added in an order that depends on sizes alone, so results are
+ * reproducible bit for bit.  A page outside the pool, a length beyond the table
+ * or a bad q_start is reported (MOE_DEV_BAD_INDEX) and adds nothing.
  * Limits: those of moe_attention_kv4.
  */
 moe_status_t moe_kv4_weigh(const void* q, long long ld_q, int T, int n_q, const moe_kv4_cache* cache,
@@ -758,6 +767,7 @@ moe_status_t moe_w4_pack(const void* w, int dtype, long long ld, const moe_w4* o
  *   bias  [N] fp32, or NULL
  *   y     [T][ld_y] BF16 or F32, N numbers a row; must not overlap x
  *   add   nonzero: added to what y holds (F32 only), e.g. a residual
+ *   st    an internal wait that gave up (MOE_DEV_TIMEOUT); no number of x or w is reported
  * Products are exact, sums fp32, results rounded once to y's type.  Sums are added
  * in an order that depends on sizes alone, so results are reproducible bit
  * for bit.

@@ -78,7 +78,7 @@ def test_more_rows_than_a_sequence_may_have():
 
 @pytest.mark.parametrize("lengths,rows,n_q,n_kv,D", [
     ([150], [3], 32, 16, 64), ([90, 200], [20, 4], 100, 1, 64), ([200], [30], 97, 1, 128), ([130], [3], 96, 1, 64), ([70] * 40, [1] * 40, 4, 2, 64), (list(range(300)), [1] * 300, 2, 1, 64),
-    ([300] * 5, [32] * 5, 8, 1, 64), ([300] * 5, [31] * 5, 8, 1, 64)])
+    ([300] * 5, [32] * 5, 8, 1, 64), ([300] * 5, [31] * 5, 8, 1, 64), ([300] * 5, [16] * 5, 8, 1, 64), ([300] * 5, [15] * 5, 8, 1, 64), ([200, 70], [16, 15], 8, 1, 128)])
 def test_weighing_of_other_shapes(lengths, rows, n_q, n_kv, D):
     """More key heads than one pass holds, groups beyond a tile, many sequences, rows at the limit of a variant."""
     rows = [min(r, n) for r, n in zip(rows, lengths)]
