@@ -102,8 +102,8 @@ struct Tiles {
     __device__ int t0(int i) const { return i % tok_tiles * tok; }
 };
 
-template <bool TMA>
-__global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linear_w4_tc_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_x, int tok, int split) {
+template <bool TMA, bool SPLIT>
+__global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linear_w4_tc_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_x, int tok, int ctas) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ __align__(8) uint64_t bars[B_N];
@@ -135,7 +135,8 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
     const int halves = (a.N + kW4Tile - 1) / kW4Tile;
     w.total = (halves + kHalves - 1) / kHalves * w.tok_tiles;
     // a cluster of `split` CTAs has a tile, each a part of its columns; without one a CTA has every gridDim.x-th tile
-    const int part = split > 1 ? static_cast<int>(blockIdx.x) % split : 0;
+    const int split = SPLIT ? ctas : 1;
+    const int part = SPLIT ? static_cast<int>(blockIdx.x) % split : 0;
     const int first = blockIdx.x / split, by = gridDim.x / split;
     const int c0 = a.kt * part / split, c1 = a.kt * (part + 1) / split;
     bool ok = true;
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
             ok = wait_warp(bar(B_DF), done & 1, &s_abort, a.st, kSiteDFull);
             if (!ok) break;
             tc_fence_after();
-            if (split > 1) {
+            if constexpr (SPLIT) {
                 // what is not yet the whole sum waits in shared memory, whose operands are used up: [token][row]
                 for (int c = 16 * g; c < tok; c += 32) {
                     uint32_t d[16];
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (split > 1) {
+    if constexpr (SPLIT) {
         // each CTA adds up the parts of some of the tile's tokens, in the order of the columns
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
@@ -374,16 +375,16 @@ bool map_tokens(CUtensorMap* m, const LinearArgs& a, int tok) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool TMA>
+template <bool TMA, bool SPLIT>
 cudaError_t launch(const LinearArgs& a, const LinearTile& t, cudaStream_t s) {
     CUtensorMap map = {};
     if (TMA && !map_tokens(&map, a, t.tok)) return cudaErrorInvalidValue;
-    auto* k = linear_w4_tc_kernel<TMA>;
+    auto* k = linear_w4_tc_kernel<TMA, SPLIT>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const long long ctas = tiles_of(a, t.tok) * t.split;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(t.split > 1 || ctas < sm_count() ? ctas : sm_count()));
+    cfg.gridDim = dim3(static_cast<unsigned>(SPLIT || ctas < sm_count() ? ctas : sm_count()));
     cfg.blockDim = dim3((kWarpX + (TMA ? 1 : kLoaders)) * 32);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
@@ -395,7 +396,7 @@ cudaError_t launch(const LinearArgs& a, const LinearTile& t, cudaStream_t s) {
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = t.split > 1 ? 2 : 1;
+    cfg.numAttrs = SPLIT ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k, a, static_cast<const CUtensorMap>(map), t.tok, t.split);
 }
 
@@ -420,6 +421,9 @@ LinearTile linear_w4_tile(const LinearArgs& a) {
     return best;
 }
 
-cudaError_t launch_linear_w4_tc(const LinearArgs& a, const LinearTile& t, cudaStream_t s) { return a.wide ? launch<true>(a, t, s) : launch<false>(a, t, s); }
+cudaError_t launch_linear_w4_tc(const LinearArgs& a, const LinearTile& t, cudaStream_t s) {
+    if (t.split > 1) return a.wide ? launch<true, true>(a, t, s) : launch<false, true>(a, t, s);
+    return a.wide ? launch<true, false>(a, t, s) : launch<false, false>(a, t, s);
+}
 
 }  // namespace moe
