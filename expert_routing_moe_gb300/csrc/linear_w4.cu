@@ -255,8 +255,10 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
     // 26.4 / 18.4 / 16.8.
     const int sms = sm_count();
     if (a.N <= 16 * sms * 2) return launch_few<NT, 1, false>(a, s);
-    if (a.N <= 32 * sms * 3 || static_cast<size_t>(a.kt) * kW4Tile * 16 * NT > 128 * 1024) return launch_few<NT, 2, false>(a, s);
-    return launch_few<NT, 2, true>(a, s);
+    // (more than 16 tokens through that many rows go to the kernel for many)
+    if constexpr (NT < 4)
+        if (a.N > 32 * sms * 3 && static_cast<size_t>(a.kt) * kW4Tile * 16 * NT <= 128 * 1024) return launch_few<NT, 2, true>(a, s);
+    return launch_few<NT, 2, false>(a, s);
 }
 
 }  // namespace

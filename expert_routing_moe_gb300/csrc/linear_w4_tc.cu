@@ -6,7 +6,7 @@
 // operand, and the tokens' numbers come to shared memory by TMA as the B operand:
 //     D[row][token] += A[row][64] B[token][64]^T      (fp32 in TMEM)
 //
-// 2001 tokens through 5120 x 2048 take 28.1 us (1490 TFLOP/s of the 1910 that a
+// 2001 tokens through 5120 x 2048 take 29.3 us (1430 TFLOP/s of the 1910 that a
 // large bf16 product of the library reaches), 8192 tokens 98 us (1750): the
 // products are fed without a pause but for the first and last step of a tile.  Few
 // tokens are bound by the conversion, 630 clocks for 256 rows of 64 columns.

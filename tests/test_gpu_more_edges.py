@@ -177,3 +177,115 @@ def test_a_short_status_is_refused():
             with pytest.raises(moe.MoeError, match="status"):
                 call()
     assert torch.equal(g.len, before) and np.array_equal(host(score), c.score)
+
+
+@pytest.mark.parametrize("T,N,K", [(9, 30000, 1024), (16, 40001, 600), (17, 9000, 1100), (33, 2049, 2100), (70, 300, 513), (24, 3000, 2047), (130, 2048, 4096), (64, 4000, 8000), (300, 515, 1290)])
+def test_products_whose_tiles_are_shared(T, N, K):
+    """Few tiles: a tile's columns in parts; with a bias and added to y, rows of x at any boundary."""
+    rng = np.random.default_rng(T + N)
+    w = Weights(rng, N, K)
+    wide = torch.full((T, K + 3), float("nan"), dtype=torch.bfloat16, device=DEV)
+    for shift in (0, 1):
+        x = _bf16(rng.normal(size=(T, K)))
+        if shift:
+            on = wide[:, 1:K + 1]
+            on.copy_(x)
+        else:
+            on = x.to(DEV)
+        bias, y0 = rng.normal(size=N).astype(np.float32), rng.normal(size=(T, N)).astype(np.float32)
+        y = dev(y0)
+        moe.moe_linear_w4(on, w.w, y, bias=dev(bias), accumulate=True)
+        _check(y, _w4.linear(x.double().numpy(), w.ref, bias.astype(np.float64), y0.astype(np.float64), 0.0), torch.float32)
+
+
+def test_no_tokens():
+    w = Weights(np.random.default_rng(37), 20, 16)
+    y = torch.full((1, 20), 7.0, device=DEV)
+    moe.moe_linear_w4(torch.zeros(0, 16, dtype=torch.bfloat16, device=DEV), w.w, y[:0])
+    assert (y == 7).all()
+
+
+def test_captured_calls_share_workspaces():
+    """Two graphs of other sizes use one workspace in turn: verification of few and many rows, prompts weighed."""
+    rng = np.random.default_rng(38)
+    cases = [_case(rng, 3, 4, 5003, True, torch.float32), _case(rng, 200, 3, 401, False, torch.float32)]
+    ws = torch.empty(max(moe.verify_workspace(len(c[1]), len(c[3]) - 1, c[0].shape[1]) for c in cases), dtype=torch.uint8, device=DEV)
+    graphs = []
+    for c in cases:
+        S = len(c[3]) - 1
+        on = [dev(c[0]), dev(c[1]), dev(c[2]), dev(c[3].astype(np.int32))]
+        outs = [torch.zeros(S, dtype=torch.int32, device=DEV) for _ in range(3)]
+        draft, temp = None if c[4] is None else dev(c[4]), dev(c[5])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_verify_drafts(*on, *outs, draft_logits=draft, temperature=temp, workspace=ws)
+        graphs.append((graph, on, outs, draft, temp))
+    weighed = [Case(39, [500, 90], [70, 30], 8, 2, 64), Case(40, [1100], [300], 4, 1, 128)]
+    shared = max((c.ws for c in weighed), key=lambda t: t.numel())
+    wanted, replays = [], []
+    for c in weighed:
+        wanted.append(c.run())
+        c.ws = shared
+        on = dev(c.score), dev(c.q_start), dev(c.lse)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_kv4_weigh(c.q_dev, c.cache, on[1], on[2], on[0], c.scale, c.max_new, workspace=c.ws)
+        replays.append((graph, on))
+    for turn in range(3):
+        for c, (graph, on, outs, _, _) in zip(cases, graphs):
+            u = rng.random(len(c[2])).astype(np.float32)
+            on[2].copy_(dev(u))
+            graph.replay()
+            for g, want in zip(outs, _verify.verify(c[0], c[1], u, *c[3:])):
+                assert np.array_equal(host(g), want)
+        for c, want, (graph, on) in zip(weighed, wanted, replays):
+            on[0].copy_(dev(c.score))
+            graph.replay()
+            assert torch.equal(on[0], want)
+
+
+def test_a_page_twice_in_a_table():
+    """A sequence whose table names a page twice (held twice): both are read before either place is made anew."""
+    rng = np.random.default_rng(41)
+    h = Host(rng, [256, 100], 2, 1, 64, spare=9)
+    freed = h.table[0, 1]
+    h.table[0, 1] = h.table[0, 0]
+    h.ref[h.table[0, 0]], h.ref[freed] = 2, 0
+    g = Gpu(h)
+    g.evict([100, 50], 2, 3)
+    assert h.evict([100, 50], 2, 3) == (0, 0) and g.st.tolist() == [0, 0]
+    g.same(h)
+
+
+@pytest.mark.parametrize("first", [59000, 118000])
+def test_pages_far_into_a_large_pool(first):
+    """Bytes beyond 2^31 and 2^32 of a pool: the same numbers as in a small one."""
+    rng = np.random.default_rng(42)
+    c = Case(43, [700, 90], [130, 2], 8, 4, 128)
+    small = c.run()
+    n, ids = int(c.pages.shape[0]), c.table.clone()
+    page = c.pages[0].numel()
+    big = torch.zeros(first + n, page, dtype=torch.uint8, device=DEV)
+    assert (first + n) * page > 2 ** 31 * (1 if first < 100000 else 2)
+    big[first:] = c.pages.view(n, page)
+    table = torch.where(ids >= 0, ids + first, ids)
+    c.cache = moe.Kv4Cache(big.view(first + n, *c.pages.shape[1:]), table, c.lens, 128, None if c.ref.k_scale is None else dev(c.ref.k_scale), None)
+    assert torch.equal(c.run(), small)
+    # eviction: the first pages are held by nobody, so free ones are low
+    h = Host(rng, [300, 200], 1, 4, 128, spare=0)
+    low = Gpu(h)
+    held = h.table.copy()
+    pages, ref = len(h.ref), np.zeros(first + len(h.ref), np.int32)
+    far = Gpu(h)
+    data = torch.zeros(1, first + pages, *h.data.shape[2:], dtype=torch.uint8, device=DEV)
+    data[:, first:] = dev(h.data)
+    ref[first:] = h.ref
+    ref[:first] = 1
+    far.pages, far.ref, far.table = data, dev(ref), dev(np.where(held >= 0, held + first, held).astype(np.int32))
+    far.pool = moe.Kv4Pool(far.pages, far.table, far.len, far.ref, 128)
+    far.ws = torch.empty(moe.kv4_evict_workspace(far.pool), dtype=torch.uint8, device=DEV)
+    for g in (low, far):
+        g.evict([130, 64], 2, 3)
+        assert g.st.tolist() == [0, 0]
+    assert torch.equal(low.len, far.len) and torch.equal(low.score, far.score) and torch.equal(low.pages, far.pages[:, first:])
+    assert torch.equal(torch.where(low.table >= 0, low.table + first, low.table), far.table)
