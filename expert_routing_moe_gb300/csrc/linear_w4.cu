@@ -236,14 +236,16 @@ __global__ void __launch_bounds__(kThreads) w4_pack_kernel(const W* w, long long
 }
 
 template <int NT, int MT, bool STAGED>
-cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
+cudaError_t launch_few(const LinearArgs& a, int sms, cudaStream_t s) {
     constexpr int rows = 16 * MT;
     const size_t red = kWarps * 8 * NT * (rows + 4) * sizeof(float);
     const size_t smem = 2 * red + (STAGED ? static_cast<size_t>(a.kt) * kW4Tile * 16 * NT : 0);
-    cudaError_t e = cudaFuncSetAttribute(linear_w4_kernel<NT, MT, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {          // (a call of some 0.3 us that a short product can do without)
+        const cudaError_t e = cudaFuncSetAttribute(linear_w4_kernel<NT, MT, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
     const int steps = (a.N + rows - 1) / rows, fit = static_cast<int>((227 * 1024) / (smem + 1024));
-    const int most = STAGED ? (fit < 3 ? fit : 3) * sm_count() : steps;
+    const int most = STAGED ? (fit < 3 ? fit : 3) * sms : steps;
     return launch_pdl(linear_w4_kernel<NT, MT, STAGED>, dim3(steps < most ? steps : most, (a.T + 8 * NT - 1) / (8 * NT)), dim3(kThreads), smem, s, a);
 }
 
@@ -254,11 +256,11 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
     // 6.4, 14000 7.0 / 6.4 / 6.8, 32000 14.2 / 12.1 / 11.9; 16 tokens: 3.7 / 4.3 / 7.0, 9.0 / 6.2 / 8.6, 12.9 / 11.3 / 11.5,
     // 26.4 / 18.4 / 16.8.
     const int sms = sm_count();
-    if (a.N <= 16 * sms * 2) return launch_few<NT, 1, false>(a, s);
+    if (a.N <= 16 * sms * 2) return launch_few<NT, 1, false>(a, sms, s);
     // (more than 16 tokens through that many rows go to the kernel for many)
     if constexpr (NT < 4)
-        if (a.N > 32 * sms * 3 && static_cast<size_t>(a.kt) * kW4Tile * 16 * NT <= 128 * 1024) return launch_few<NT, 2, true>(a, s);
-    return launch_few<NT, 2, false>(a, s);
+        if (a.N > 32 * sms * 3 && static_cast<size_t>(a.kt) * kW4Tile * 16 * NT <= 128 * 1024) return launch_few<NT, 2, true>(a, sms, s);
+    return launch_few<NT, 2, false>(a, sms, s);
 }
 
 }  // namespace
