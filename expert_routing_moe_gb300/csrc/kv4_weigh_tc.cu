@@ -56,7 +56,6 @@ __device__ __forceinline__ int head_cost(int tiles, int ntok) { return tiles > 0
 // Workspace: header, the runs' first items, their pieces, then the items and the tiles before each.
 struct WeighWs {
     long long* total;
-    int* n_items;
     int* start;                           // [kMaxCtas]
     float* part;                          // [kMaxCtas][2][kKeys]: of the item that the run starts in and of the one that it ends in
     Item* items;
@@ -65,7 +64,6 @@ struct WeighWs {
 __host__ __device__ inline WeighWs weigh_ws(void* ws, size_t items) {
     WeighWs w;
     w.total = static_cast<long long*>(ws);
-    w.n_items = reinterpret_cast<int*>(w.total + 1);
     w.start = reinterpret_cast<int*>(w.total) + 64;
     w.part = reinterpret_cast<float*>(w.start + kMaxCtas);
     w.items = reinterpret_cast<Item*>(w.part + kMaxCtas * 2 * kKeys);
@@ -104,57 +102,86 @@ __device__ __forceinline__ long long scan_long(long long v, long long& total, lo
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) weigh_plan_kernel(const WeighArgs a, void* ws, int ntok, int grid) {
-    __shared__ long long s_warp[kPlanThreads / 32];
+    constexpr int kSeqs = kPlanThreads / 32;
+    __shared__ long long s_warp[kSeqs];
+    __shared__ WeighSeq s_seq[kSeqs];
+    __shared__ int s_b0[kSeqs], s_n[kSeqs], s_first[kSeqs + 1];
     const WeighWs w = weigh_ws(ws, max_items(a.c.S, a.c.max_pages));
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
     pdl_trigger();
-    long long items = 0, tiles = 0;
-    for (int s0 = 0; s0 < a.c.S; s0 += kPlanThreads / 32) {
-        // a warp for each sequence
-        const int s = s0 + (tid >> 5), lane = tid & 31;
+    long long items = 0, tiles = 0, own = -1, own_u0 = 0, own_u1 = 0;
+    for (int s0 = 0; s0 < a.c.S; s0 += kSeqs) {
+        // a warp for each sequence, then a thread for each item
+        const int s = s0 + warp;
         WeighSeq q = {0, 0, 0, 0, true};
         if (s < a.c.S) q = weigh_seq(a, s);
         const bool mine = s < a.c.S && q.fit && (q.n - q.i0) * a.group >= a.many && q.len > 0;
-        const int b0 = mine ? weigh_first(a, q) / kKeys : 0, b1 = mine ? (q.len + kKeys - 1) / kKeys : 0;
-        long long all;
-        const long long at = items + scan_long(lane == 0 ? b1 - b0 : 0, all, s_warp);
-        const long long first = __shfl_sync(kFull, at, 0);
-        for (int b = b0 + lane; b < b1; b += 32) {
-            Item it;
-            it.s = s;
-            it.key0 = b * kKeys;
-            weigh_rows(a, q, it.key0, kKeys, it.ia, it.ib);
-            it.tiles = (it.ib - it.ia + ntok - 1) / ntok;
-            it.q0 = q.q0;
-            it.len = q.len;
-            it.base = q.base();
-            w.items[first + b - b0] = it;
+        if (lane == 0) {
+            s_seq[warp] = q;
+            s_b0[warp] = mine ? weigh_first(a, q) / kKeys : 0;
+            s_n[warp] = mine ? (q.len + kKeys - 1) / kKeys - s_b0[warp] : 0;
         }
-        items += all;
+        __syncthreads();
+        if (warp == 0) {
+            int inc = s_n[lane];
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int x = __shfl_up_sync(kFull, inc, off);
+                if (lane >= off) inc += x;
+            }
+            s_first[lane + 1] = inc;
+            if (lane == 0) s_first[0] = 0;
+        }
+        __syncthreads();
+        const int n = s_first[kSeqs];
+        for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+            const int i = i0 + tid;
+            long long cost = 0, all;
+            if (i < n) {
+                int j = 0;
+#pragma unroll
+                for (int step = kSeqs / 2; step > 0; step >>= 1)
+                    if (s_first[j + step] <= i) j += step;
+                const WeighSeq x = s_seq[j];
+                Item it;
+                it.s = s0 + j;
+                it.key0 = (s_b0[j] + i - s_first[j]) * kKeys;
+                weigh_rows(a, x, it.key0, kKeys, it.ia, it.ib);
+                it.tiles = (it.ib - it.ia + ntok - 1) / ntok;
+                it.q0 = x.q0;
+                it.len = x.len;
+                it.base = x.base();
+                w.items[items + i] = it;
+                // an item without rows has one unit all the same: its new tokens' scores may have to be set
+                cost = max(1ll, static_cast<long long>(it.tiles + head_cost(it.tiles, ntok)) * a.c.n_kv);
+            }
+            const long long at = tiles + scan_long(cost, all, s_warp);
+            if (i < n) {
+                w.before[items + i] = at;
+                own = items + i;
+                own_u0 = at;
+                own_u1 = at + cost;
+            }
+            tiles += all;
+        }
+        items += n;
+        __syncthreads();
     }
-    __threadfence_block();
-    __syncthreads();
-    for (long long i0 = 0; i0 < items; i0 += kPlanThreads) {
-        const long long i = i0 + tid;
-        long long all;
-        // an item without rows has one unit all the same: its new tokens' scores may have to be set
-        const long long mine = i < items ? max(1ll, static_cast<long long>(w.items[i].tiles + head_cost(w.items[i].tiles, ntok)) * a.c.n_kv) : 0;
-        const long long at = tiles + scan_long(mine, all, s_warp);
-        if (i < items) w.before[i] = at;
-        tiles += all;
-    }
-    __threadfence_block();
-    __syncthreads();
     const long long share = run_share(tiles, grid);
-    for (long long i = tid; i < items; i += kPlanThreads) {
-        const long long u0 = w.before[i], u1 = i + 1 < items ? w.before[i + 1] : tiles;
+    auto starts = [&](long long i, long long u0, long long u1) {
         for (long long b = (u0 + share - 1) / share; b * share < u1 && b < grid; ++b) w.start[b] = static_cast<int>(i);
+    };
+    if (a.c.S <= kSeqs && items <= kPlanThreads) {
+        if (own >= 0) starts(own, own_u0, own_u1);
+    } else {
+        __threadfence_block();
+        __syncthreads();
+        for (long long i = tid; i < items; i += kPlanThreads) starts(i, w.before[i], i + 1 < items ? w.before[i + 1] : tiles);
     }
     if (tid == 0) {
         w.before[items] = tiles;
         *w.total = tiles;
-        *w.n_items = static_cast<int>(items);
     }
 }
 
@@ -581,21 +608,21 @@ __global__ void __launch_bounds__(kKeys) weigh_join_kernel(const WeighArgs a, vo
     const WeighWs w = weigh_ws(ws, max_items(a.c.S, a.c.max_pages));
     pdl_wait();
     pdl_trigger();
+    // (loads that do not wait for one another are made together; the last run's next one is none)
+    const int b = blockIdx.x, idx = b + 1 < grid ? w.start[b + 1] : 0;
     const long long total = *w.total, share = run_share(total, grid);
-    const int b = blockIdx.x;
     const long long u1 = min(total, share * (b + 1));
     if (share * b >= total || u1 >= total) return;
     // the item of the next run's first unit, if it starts in this one
-    const int idx = w.start[b + 1];
     const long long begin = w.before[idx], end = w.before[idx + 1];
-    if (begin >= u1 || begin < share * b) return;
     const Item it = w.items[idx];
+    float v = w.part[(b * 2 + 1) * kKeys + threadIdx.x];
+    if (begin >= u1 || begin < share * b) return;
     const int key = it.key0 + threadIdx.x;
     if (key >= it.len) return;
     const int page = a.c.page_table[static_cast<long long>(it.s) * a.c.max_pages + key / kPage];
-    if (page < 0 || page >= a.c.n_pages) return;
-    float v = w.part[(b * 2 + 1) * kKeys + threadIdx.x];
     for (int i = b + 1; share * i < end; ++i) v += w.part[i * 2 * kKeys + threadIdx.x];
+    if (page < 0 || page >= a.c.n_pages) return;
     WeighSeq q;
     q.len = it.len;
     q.n = it.len - it.base;
