@@ -23,7 +23,7 @@ struct WeighArgs {
     float* score;
     long long ld_score;
     bool fresh;
-    int many;                   // sequences with that many counted rows or more go to the kernel for prompts
+    int many;                   // sequences with that many counted rows or more go to the kernel for prompts (1: all that have any)
     moe_dev_status* st;
 };
 

@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) weigh_plan_kernel(const Weigh
         if (s < a.c.S) q = weigh_seq(a, s);
         const bool mine = s < a.c.S && q.fit && (q.n - q.i0) * a.group >= a.many && q.len > 0;
         if (lane == 0) {
+            if (!q.fit && a.many == 1) report(a.st, MOE_DEV_BAD_INDEX, s);     // (the other kernel does it otherwise)
             s_seq[warp] = q;
             s_b0[warp] = mine ? weigh_first(a, q) / kKeys : 0;
             s_n[warp] = mine ? (q.len + kKeys - 1) / kKeys - s_b0[warp] : 0;

@@ -289,3 +289,16 @@ def test_pages_far_into_a_large_pool(first):
         assert g.st.tolist() == [0, 0]
     assert torch.equal(low.len, far.len) and torch.equal(low.score, far.score) and torch.equal(low.pages, far.pages[:, first:])
     assert torch.equal(torch.where(low.table >= 0, low.table + first, low.table), far.table)
+
+
+@pytest.mark.parametrize("lengths,rows", [([400, 300, 90], [200, 0, 2]), ([400, 300, 90, 70], [40, 1, 1, 1]), ([300] * 20, [100] + [1] * 19), ([300] * 20, [1] * 19 + [290])])
+def test_prompts_and_single_tokens_in_one_call(lengths, rows):
+    """Sequences of many and of few rows, where the many decide the kernel and where they do not; one that does not fit is reported."""
+    c = Case(44, lengths, rows, 8, 2, 64)
+    c.check()
+    c.check(last=3, fresh=True)
+    good = host(c.run())
+    c.lens[0] = -1
+    st = status_tensor()
+    got = host(c.run(st=st))
+    assert st.tolist() == [3, 0] and np.array_equal(got[0], c.score[0]) and np.array_equal(got[1:], good[1:])
