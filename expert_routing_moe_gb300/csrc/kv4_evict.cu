@@ -11,17 +11,18 @@
 //
 // Moving in place: the k-th kept token comes from a place >= k, so a page is read
 // only for itself and for pages before it.  A cluster reads the sources of
-// up to 32 pages into registers, meets, then writes them: whatever it writes has
+// up to 16 pages into registers, meets, then writes them: whatever it writes has
 // been read by then.  A sequence whose pages all go to free ones needs no meeting.
 //
-// 32001 tokens of 48 layers (4 heads of 128) cut to 8192: 200 us onto free pages,
-// 243 in place, of which the selection takes 23; 32 sequences of 8 layers 167.
+// 32001 tokens of 48 layers (4 heads of 128) cut to 8192: 182 us onto free pages,
+// 221 in place, of which the selection takes 23; 32 sequences of 8 layers 155.
 // 453 MB are to be moved, which is 67 us at the rate of a copy; kept tokens lie
 // scattered, 64 bytes of keys and as many of values that they share with a
 // neighbour, so that whole sectors of others come with them.  (A CTA a page, whose
 // threads look for their sources in the list: 353 us; sources of a page's tokens in
 // shared memory, three warps a page: 238; the next pages' sources looked for ahead: 207
-// against 200.)
+// against 200; four pages a CTA in three warps each 200, two pages 185, in six warps each 182;
+// sources made out of line, so that nothing spills: 197.)
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -39,8 +40,8 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMovePages = 4;             // pages of a CTA at a time, three warps each: keys, and two halves of the values
-constexpr int kMoveThreads = kMovePages * 96;
+constexpr int kMovePages = 2;             // pages of a CTA at a time, six warps each: two halves of the keys, four quarters of the values
+constexpr int kMoveThreads = kMovePages * 192;
 
 // What is known of a sequence.
 struct SeqPlan {
@@ -386,58 +387,59 @@ struct Sources {
     }
 };
 
-// The keys of a page: lane (part, g) = (lane / 8, lane % 8) has 16-byte runs of tokens g + 8 x -- for D = 64, where a token has
-// two, parts 0 and 1 of tokens 16 x + g and parts 2 and 3 of 8 further -- and the scales of blocks part*R .. of tokens g + 8 i.
+// The keys of 32 tokens of a page: lane (part, g) = (lane / 8, lane % 8) has 16-byte runs of tokens g + 8 x -- for D = 64, where a
+// token has two, parts 0 and 1 of tokens 16 x + g and parts 2 and 3 of 8 further -- and the scales of blocks part*R .. of
+// tokens g + 8 i.
 template <int D>
 struct KeyPart {
     using L = Kv4Layout<D>;
-    static constexpr int runs = kPage * D / 2 / 512, per = D / 32;
+    static constexpr int runs = kPage * D / 4 / 512, per = D / 32;
     uint4 c[runs];
-    uint32_t s[2 * L::R];
+    uint32_t s[L::R];
     __device__ __forceinline__ int token(int x, int lane) const { return per == 4 ? 8 * x + (lane & 7) : 16 * x + (lane & 7) + 8 * (lane >> 4); }
     __device__ __forceinline__ int run(int lane) const { return per == 4 ? lane >> 3 : lane >> 3 & 1; }
-    __device__ __forceinline__ void read(const Sources<D>& src, int lane) {
+    __device__ __forceinline__ void read(const Sources<D>& src, int half, int lane) {
 #pragma unroll
-        for (int x = 0; x < 2 * L::R; ++x) s[x] = 0u;
+        for (int x = 0; x < L::R; ++x) s[x] = 0u;
 #pragma unroll
         for (int x = 0; x < runs; ++x) {
-            const Source a = src.k[token(x, lane)];
+            const Source a = src.k[32 * half + token(x, lane)];
             c[x] = make_uint4(0u, 0u, 0u, 0u);
             if (a.codes != nullptr) c[x] = *reinterpret_cast<const uint4*>(a.codes + run(lane) * 16);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const Source a = src.k[8 * i + (lane & 7)];
+        for (int i = 0; i < 4; ++i) {
+            const Source a = src.k[32 * half + 8 * i + (lane & 7)];
             if (a.codes == nullptr) continue;
             const uint8_t* p = a.codes + a.scales + (lane >> 3) * 64 * L::R;
             if constexpr (L::R == 2) s[i / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) << (16 * (i & 1));
-            else s[i / 4] |= static_cast<uint32_t>(*p) << (8 * (i & 3));
+            else s[0] |= static_cast<uint32_t>(*p) << (8 * i);
         }
     }
-    __device__ __forceinline__ void write(uint8_t* to, int lane) const {
+    __device__ __forceinline__ void write(uint8_t* to, int half, int lane) const {
 #pragma unroll
-        for (int x = 0; x < runs; ++x) *reinterpret_cast<uint4*>(to + token(x, lane) * (D / 2) + run(lane) * 16) = c[x];
-        uint8_t* p = to + L::kScales + lane * 8 * L::R;
-        if constexpr (L::R == 2) *reinterpret_cast<uint4*>(p) = make_uint4(s[0], s[1], s[2], s[3]);
-        else *reinterpret_cast<uint2*>(p) = make_uint2(s[0], s[1]);
+        for (int x = 0; x < runs; ++x) *reinterpret_cast<uint4*>(to + (32 * half + token(x, lane)) * (D / 2) + run(lane) * 16) = c[x];
+        uint8_t* p = to + L::kScales + (lane * 8 + 4 * half) * L::R;
+        if constexpr (L::R == 2) *reinterpret_cast<uint2*>(p) = make_uint2(s[0], s[1]);
+        else *reinterpret_cast<uint32_t*>(p) = s[0];
     }
 };
-// The values of 32 tokens of a page: lane (g', j) = (lane / 4, lane % 4) has the runs of tokens 8 x + 2 j and + 1, which share
+// The values of 16 tokens of a page: lane (g', j) = (lane / 4, lane % 4) has the runs of tokens 8 x + 2 j and + 1, which share
 // bytes, and numbers g' (D/8) .., and the scales of the same tokens, block g'.
 template <int D>
 struct ValuePart {
     using L = Kv4Layout<D>;
     static constexpr int U = L::U, W = U / 4;            // U: bytes of two tokens' run, 16 or 8
-    uint32_t c[4][W];
-    uint32_t s[2];
-    __device__ __forceinline__ void read(const Sources<D>& src, int half, int lane) {
+    uint32_t c[2][W];
+    uint32_t s;
+    __device__ __forceinline__ void read(const Sources<D>& src, int quarter, int lane) {
         const int gp = lane >> 2, j = lane & 3;
-        s[0] = s[1] = 0u;
+        s = 0u;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const Source a = src.v[32 * half + 8 * x + 2 * j + u];
+                const Source a = src.v[16 * quarter + 8 * x + 2 * j + u];
                 uint32_t v[W];
                 uint32_t sc = 0u;
 #pragma unroll
@@ -458,23 +460,23 @@ struct ValuePart {
                     v[y] = v[y] >> a.shift & 0x0f0f0f0fu;
                     c[x][y] = u == 0 ? v[y] : c[x][y] | v[y] << 4;
                 }
-                s[x / 2] |= sc << (8 * (2 * (x & 1) + u));
+                s |= sc << (8 * (2 * x + u));
             }
     }
-    __device__ __forceinline__ void write(uint8_t* to, int half, int lane) const {
+    __device__ __forceinline__ void write(uint8_t* to, int quarter, int lane) const {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            uint8_t* p = to + L::vCodes + (half * 4 + x) * 32 * U + lane * U;
+        for (int x = 0; x < 2; ++x) {
+            uint8_t* p = to + L::vCodes + (quarter * 2 + x) * 32 * U + lane * U;
             if constexpr (U == 16) *reinterpret_cast<uint4*>(p) = make_uint4(c[x][0], c[x][1], c[x][2], c[x][3]);
             else *reinterpret_cast<uint2*>(p) = make_uint2(c[x][0], c[x][1]);
         }
-        if ((lane >> 2) < D / 16) *reinterpret_cast<uint2*>(to + L::vScales + lane * 16 + half * 8) = make_uint2(s[0], s[1]);
+        if ((lane >> 2) < D / 16) *reinterpret_cast<uint32_t*>(to + L::vScales + lane * 16 + quarter * 4) = s;
     }
 };
 
 // The first S CTAs keep the books; then a cluster for each (layer, head, sequence) moves its pages.
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const EvictArgs a) {
     using L = Kv4Layout<D>;
     __shared__ Sources<D> s_src[kMovePages];
     cg::cluster_group cluster = cg::this_cluster();
@@ -488,7 +490,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
         if (static_cast<int>(blockIdx.x) < a.p.S) move_book(a, w, blockIdx.x);
         return;
     }
-    const int tid = threadIdx.x, lane = tid & 31, mine = tid / 96, role = tid % 96 / 32;
+    const int tid = threadIdx.x, lane = tid & 31, mine = tid / 192, role = tid % 192 / 32;
     const long long items = static_cast<long long>(a.p.n_layers) * a.n_kv * a.p.S;
     const int clusters = static_cast<int>(gridDim.x) / parts - books;
     for (long long item = static_cast<int>(blockIdx.x) / parts - books; item < items; item += clusters) {
@@ -516,16 +518,16 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
             if (live) to = head + (rank[c] >= 0 ? w.free_pages[r.base + rank[c]] : old_page[c]) * a.p.page_bytes;
             __syncthreads();
             // what is written has been read by then (pages that come later read neither)
-            if (role == 0) {
+            if (role < 2) {
                 KeyPart<D> g;
-                if (live) g.read(s_src[mine], lane);
+                if (live) g.read(s_src[mine], role, lane);
                 if (!apart) meet(cluster, parts);
-                if (live) g.write(to, lane);
+                if (live) g.write(to, role, lane);
             } else {
                 ValuePart<D> g;
-                if (live) g.read(s_src[mine], role - 1, lane);
+                if (live) g.read(s_src[mine], role - 2, lane);
                 if (!apart) meet(cluster, parts);
-                if (live) g.write(to, role - 1, lane);
+                if (live) g.write(to, role - 2, lane);
             }
         }
     }
@@ -550,11 +552,11 @@ cudaError_t launch_clusters(void (*kernel)(EvictArgs), int ctas, int parts, int 
 
 template <int D>
 cudaError_t launch_move(const EvictArgs& a, cudaStream_t s) {
-    // enough CTAs for every SM four times over, by clusters of up to eight, but no more than a table has pages for
+    // enough CTAs for every SM eight times over (four times: 221 us for 185), by clusters of up to eight, but no more than a table has pages for
     const long long items = static_cast<long long>(a.p.n_layers) * a.n_kv * a.p.S;
     int parts = 1;
-    while (parts < 8 && items * parts < 4ll * sm_count() && parts * kMovePages < a.p.max_pages) parts *= 2;
-    const long long most = 8ll * sm_count() / parts > 0 ? 8ll * sm_count() / parts : 1;
+    while (parts < 8 && items * parts < 8ll * sm_count() && parts * kMovePages < a.p.max_pages) parts *= 2;
+    const long long most = 16ll * sm_count() / parts > 0 ? 16ll * sm_count() / parts : 1;
     const long long n = ((a.p.S + parts - 1) / parts + (items < most ? items : most)) * parts;
     return launch_clusters(evict_move_kernel<D>, static_cast<int>(n), parts, kMoveThreads, s, a);
 }
