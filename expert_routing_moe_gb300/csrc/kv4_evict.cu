@@ -552,10 +552,10 @@ cudaError_t launch_clusters(void (*kernel)(EvictArgs), int ctas, int parts, int 
 
 template <int D>
 cudaError_t launch_move(const EvictArgs& a, cudaStream_t s) {
-    // enough CTAs for every SM eight times over (four times: 221 us for 185), by clusters of up to eight, but no more than a table has pages for
+    // enough CTAs for every SM eight times over (four times: 221 us for 185), by clusters of up to eight, but none wider than a quarter of a table
     const long long items = static_cast<long long>(a.p.n_layers) * a.n_kv * a.p.S;
     int parts = 1;
-    while (parts < 8 && items * parts < 8ll * sm_count() && parts * kMovePages < a.p.max_pages) parts *= 2;
+    while (parts < 8 && items * parts < 8ll * sm_count() && parts * kMovePages * 4 < a.p.max_pages) parts *= 2;
     const long long most = 16ll * sm_count() / parts > 0 ? 16ll * sm_count() / parts : 1;
     const long long n = ((a.p.S + parts - 1) / parts + (items < most ? items : most)) * parts;
     return launch_clusters(evict_move_kernel<D>, static_cast<int>(n), parts, kMoveThreads, s, a);
