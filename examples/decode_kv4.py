@@ -3,7 +3,7 @@ steps replayed from one CUDA graph, a prompt forked into beams, and the pool
 packed.  Random weights; prints tokens/s and the cache's size.
 
 With --drafts n the decode goes on with n drafted tokens a sequence and step: a
-4-bit head's logits judge them, and the refused ones leave the cache.  With
+4-bit head's logits accept or refuse them, and the refused ones leave the cache.  With
 --budget b the layers weigh their cached tokens, and the caches are then cut
 to the b tokens that drew most.  --four-bit: the projections in 4 bits too.
 

@@ -22,7 +22,7 @@ FAST = os.path.join(HERE, "_fastcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["abi.cu", "router.cu", "route_dispatch.cu", "dispatch.cu", "dispatch_static.cu", "ffn.cu",
            "ffn_decode.cu", "macs.cu", "calib.cu", "cast.cu", "qk_rope.cu", "attn_kv4.cu", "attn_kv4_prefill.cu", "kv4_pages.cu",
            "kv4_weigh.cu", "kv4_weigh_tc.cu", "kv4_evict.cu", "linear_w4.cu", "linear_w4_tc.cu", "verify.cu"]
-HEADERS = ["common.cuh", "launch.h", "routing.cuh", "permute.cuh", "kv4.cuh", "attn_kv4.cuh", "w4.cuh", "linear_w4.cuh", "kv4_weigh.cuh", "ranges.h", "tmap.h", "../../include/moe_gb300.h"]
+HEADERS = ["common.cuh", "launch.h", "routing.cuh", "permute.cuh", "kv4.cuh", "attn_kv4.cuh", "w4.cuh", "linear_w4.cuh", "kv4_weigh.cuh", "tc_ts.cuh", "ranges.h", "tmap.h", "../../include/moe_gb300.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     // prefix: the score of the last one that is kept; `want` of those that have it are, the first ones
     const int each = (c1 - c0 + kSelThreads - 1) / kSelThreads, j0 = min(c1, c0 + tid * each), j1 = min(c1, j0 + each);
     // 1: kept, 2: kept if it is among the first `want`, 0: not
-    auto judge = [&](int j) {
+    auto kind = [&](int j) {
         if (j < lo || j >= hi) return 1;
         if (k == 0) return 0;
         const uint32_t o = order_of(score[j]);
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     };
     long long mine = 0;                 // kept ones, and in the upper half those that may be
     for (int j = j0; j < j1; ++j) {
-        const int v = judge(j);
+        const int v = kind(j);
         mine += v == 1 ? 1ll : v == 2 ? 1ll << 32 : 0ll;
     }
     long long total2;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     int sure = static_cast<int>(at2), equal = static_cast<int>(at2 >> 32);
     int first = 0x7fffffff;
     for (int j = j0; j < j1; ++j) {
-        const int v = judge(j);
+        const int v = kind(j);
         if (v == 1 || (v == 2 && equal < want)) kept[sure + min(equal, want)] = j;
         else first = min(first, j);
         sure += v == 1;

@@ -29,6 +29,7 @@
 #include "common.cuh"
 #include "kv4_weigh.cuh"
 #include "launch.h"
+#include "tc_ts.cuh"
 #include "tmap.h"
 
 namespace moe {
@@ -220,28 +221,6 @@ __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&v)[48]) {
           "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47])
         : "r"(taddr + 32)
         : "memory");
-}
-__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-// A wait that is mostly over when it begins: the loop with the time limit stays out of the way.
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag, moe_dev_status* st, int site) {
-    return mbar_wait(bar, parity, abort_flag, st, site);
-}
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, moe_dev_status* st, int site) {
-    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(kFull, wait_long(bar, parity, abort_flag, st, site));
 }
 // Barrier of a half's warps; the AND of what they bring.
 __device__ __forceinline__ bool half_sync_and(int m, bool v) {

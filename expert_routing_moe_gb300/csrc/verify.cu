@@ -3,8 +3,8 @@
 //
 // First the rows' maxima and the sums of their tokens' weights: a cluster a row
 // where there are few, and otherwise a kernel for the maxima and one for the
-// sums, a warp a chunk of a row.  Then a cluster for every sequence judges its
-// drafts and draws the token that follows.  Weights are whole multiples of 2^-42
+// sums, a warp a chunk of a row.  Then a cluster for every sequence accepts its
+// drafts or not and draws the token that follows.  Weights are whole multiples of 2^-42
 // made from fp32 numbers whose every operation is rounded in a known way, so
 // that sums of them do not depend on their order and a draw not on the grid.
 //
@@ -232,8 +232,8 @@ __device__ __forceinline__ long long warp_sum(long long v) {
     return v;
 }
 
-// What the judge needs of a row: the sum of its weights, its largest logit, the weight of the draft behind it and 2^42 / z.
-struct Judge {
+// What acceptance needs of a row: the sum of its weights, its largest logit, the weight of the draft behind it and 2^42 / z.
+struct Weighed {
     long long z, u;
     float m, inv;
 };
@@ -249,7 +249,7 @@ __device__ __forceinline__ float inverse(long long z) {
     return lo == hi ? lo : __double2float_rn(ratio(0x1p42, z));
 }
 // uniform * q < p, each p of a token u / z in fp64: again fp32 decides unless both sides are close.
-__device__ __forceinline__ bool accepts(float uniform, const Judge& p, const Judge& q, bool model) {
+__device__ __forceinline__ bool accepts(float uniform, const Weighed& p, const Weighed& q, bool model) {
     const float pr = __ll2float_rn(p.u) * 0x1p-42f * p.inv, other = uniform * (model ? __ll2float_rn(q.u) * 0x1p-42f * q.inv : 1.f);
     if (fabsf(pr - other) > 0x1p-20f * pr) return other < pr;
     const double exact = model ? ratio(__ll2double_rn(q.u), q.z) : 1.0;
@@ -534,8 +534,8 @@ struct Draw {
     }
 };
 
-// Rows of a sequence that a turn of the judge looks at, and what it found at the row that ends the accepted drafts.
-struct Judged {
+// Rows of a sequence that are looked at in a turn, and what was found at the row that ends the accepted drafts.
+struct Looked {
     long long z[kWarps][2], u[kWarps][2];          // of the target and of the drafting model: sum, the draft's weight
     float m[kWarps][2];
     int best[kWarps];
@@ -550,10 +550,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyAr
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    __shared__ Judged s_j;
+    __shared__ Looked s_l;
     __shared__ long long s_sums[2][kMaxCluster * kWarps];
     const int s = blockIdx.x / parts;
-    if (tid == 0) { s_j.stop = -1; s_j.bad = 0; }
+    if (tid == 0) { s_l.stop = -1; s_l.bad = 0; }
     cluster.sync();
     pdl_wait();
     pdl_trigger();
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyAr
         if (lead) answer(0, -1);
         return;                      // the whole cluster
     }
-    // every CTA judges the drafts for itself: a warp gathers what is known of a row, then the first warp looks at them
+    // every CTA looks at all drafts for itself: a warp gathers what is known of a row, then the first warp looks at them
     for (int base = 0; base < n; base += kWarps) {
         const int j = base + warp;
         if (j < n) {
@@ -589,57 +589,57 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyAr
                 bad = bad || r.bad;
                 if (q == 0) best = r.best;
                 if (lane == 0) {
-                    s_j.z[warp][q] = r.z;
-                    s_j.m[warp][q] = r.m;
-                    s_j.u[warp][q] = units_of(weight(l, Scale(r.m, temp.it)));
+                    s_l.z[warp][q] = r.z;
+                    s_l.m[warp][q] = r.m;
+                    s_l.u[warp][q] = units_of(weight(l, Scale(r.m, temp.it)));
                 }
             }
             if (lane == 0) {
-                s_j.best[warp] = temp.greedy && !last && x != best ? -1 - best : best;
-                if (bad) s_j.bad = 1;
+                s_l.best[warp] = temp.greedy && !last && x != best ? -1 - best : best;
+                if (bad) s_l.bad = 1;
                 if (!in && part == 0) report(a.st, MOE_DEV_BAD_INDEX, r0 + j + 1);
             }
         }
         __syncthreads();
-        if (warp == 0 && s_j.stop < 0) {
+        if (warp == 0 && s_l.stop < 0) {
             const int row = base + lane;
             const bool in = lane < kWarps && row < n;
             bool ends = in && row == n - 1;
-            Judge p = {}, q = {};
+            Weighed p = {}, q = {};
             if (in && temp.greedy) {
-                ends = ends || s_j.best[lane] < 0;
+                ends = ends || s_l.best[lane] < 0;
             } else if (in) {
                 const bool with = a.draft != nullptr && !ends;
 #pragma unroll 1
                 for (int i = 0; i <= with; ++i) {
                     q = p;
-                    p = {s_j.z[lane][with - i], s_j.u[lane][with - i], s_j.m[lane][with - i], inverse(s_j.z[lane][with - i])};
+                    p = {s_l.z[lane][with - i], s_l.u[lane][with - i], s_l.m[lane][with - i], inverse(s_l.z[lane][with - i])};
                 }
                 ends = ends || !accepts(a.uniform[r0 + row + 1], p, q, with);
             }
             const unsigned mask = __ballot_sync(kFull, ends);
             if (mask != 0 && lane == __ffs(mask) - 1) {
-                s_j.stop = row;
-                s_j.stop_m[0] = p.m;
-                s_j.stop_m[1] = q.m;
-                s_j.stop_inv[0] = p.inv;
-                s_j.stop_inv[1] = q.inv;
-                s_j.stop_best = s_j.best[lane] < 0 ? -1 - s_j.best[lane] : s_j.best[lane];
+                s_l.stop = row;
+                s_l.stop_m[0] = p.m;
+                s_l.stop_m[1] = q.m;
+                s_l.stop_inv[0] = p.inv;
+                s_l.stop_inv[1] = q.inv;
+                s_l.stop_best = s_l.best[lane] < 0 ? -1 - s_l.best[lane] : s_l.best[lane];
             }
         }
         __syncthreads();
     }
-    if (s_j.bad) {
+    if (s_l.bad) {
         if (lead) answer(0, -1);
         return;
     }
-    const int stop = s_j.stop;
+    const int stop = s_l.stop;
     const int row = r0 + stop;
     if (temp.greedy) {
-        if (lead) answer(stop, s_j.stop_best);
+        if (lead) answer(stop, s_l.stop_best);
         return;
     }
-    Draw<L> d = {Row<L>(a.logits, a.ld, row, a.V), Row<L>(a.logits, a.ld, row, a.V), Scale(s_j.stop_m[0], temp.it), Scale(s_j.stop_m[1], temp.it), s_j.stop_inv[0], s_j.stop_inv[1], 0, -1};
+    Draw<L> d = {Row<L>(a.logits, a.ld, row, a.V), Row<L>(a.logits, a.ld, row, a.V), Scale(s_l.stop_m[0], temp.it), Scale(s_l.stop_m[1], temp.it), s_l.stop_inv[0], s_l.stop_inv[1], 0, -1};
     if (stop < n - 1) {
         d.mode = 1;
         d.without = a.tokens[row + 1];
@@ -720,10 +720,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyAr
         }
         if (tid == 0) {
             const long long t = __double2ll_rd(__dmul_rn(static_cast<double>(a.uniform[r0]), __ll2double_rn(total)));
-            s_j.target = max(0ll, min(t, total - 1));
+            s_l.target = max(0ll, min(t, total - 1));
         }
         __syncthreads();
-        target = s_j.target;
+        target = s_l.target;
         if (target < before || target >= before + own) return;
         search = true;
     }

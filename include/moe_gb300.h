@@ -785,7 +785,7 @@ moe_status_t moe_linear_w4(const void* x, long long ld_x, int T, const moe_w4* w
  *
  * Rows q_start[s] .. q_start[s+1]-1 of a step are a sequence's newest known
  * token and its n drafts behind it.  logits of a row are the target's for the
- * place behind it, so row r judges the draft tokens[r+1].  With p the
+ * place behind it, so row r decides on the draft tokens[r+1].  With p the
  * target's and q the drafting model's distribution at a row, the draft x is
  * accepted if uniform[r+1] * q(x) < p(x); the first one that is not ends
  * the run, and the next token is drawn from max(p - q, 0); with all accepted it

@@ -140,7 +140,7 @@ class Server:
             self.x.add_(layer.forward(self.x.bfloat16(), self.caches[i], self.q_start, self.drafts + 1, place, self.pages.score, fresh=i == 0))
         moe.moe_linear_w4(self.x.bfloat16(), self.head, self.logits, st=self.status)
 
-    def judge(self):
+    def accept(self):
         """Drafts that the model takes stay, the others' tokens leave the cache."""
         moe.moe_verify_drafts(self.logits, self.tokens, self.uniform, self.q_start, self.accepted, self.next, self.n_new,
                               temperature=self.temperature, workspace=self.ws, st=self.status)
@@ -152,7 +152,7 @@ class Server:
 
     def step(self):
         self.ahead()
-        self.judge()
+        self.accept()
         self.cut()
 
     def draw(self, rng):
@@ -196,7 +196,7 @@ def test_steps_with_drafts_and_eviction():
         # the head: exact products, sums of 256 in fp32, 2^-24 a step relative to their magnitudes
         x, w = host(server.x.bfloat16().double()), _w4_of(server.head)
         assert (np.abs(host(server.logits.double()) - x @ w.T) <= 256 * 2.0 ** -24 * (np.abs(x) @ np.abs(w).T)).all()
-        server.judge()
+        server.accept()
         want = _verify.verify(host(server.logits), host(server.tokens), host(server.uniform), host(server.q_start), None, host(server.temperature))
         for mine, theirs in zip((server.accepted, server.next, server.n_new), want):
             assert np.array_equal(host(mine), theirs)
