@@ -290,9 +290,11 @@ __global__ void __launch_bounds__(kThreads, 2) verify_rows_kernel(const VerifyAr
     __syncthreads();
     cluster.barrier_wait();
     const int s = s_seq;
-    if (s < 0) return;               // the whole cluster
-    const Temp temp = temp_of(a, s);
-    if (temp.bad || (draft && temp.greedy)) return;
+    const Temp temp = s < 0 ? Temp{1.f, false, true} : temp_of(a, s);
+    if (temp.bad || (draft && temp.greedy)) {              // the whole cluster
+        if (part == 0 && tid == 0) a.maxima[item] = NAN;   // (where bad starts give a row to two sequences the other one finds it bad)
+        return;
+    }
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
@@ -384,7 +386,10 @@ __global__ void __launch_bounds__(kMaxThreads) verify_max_kernel(const VerifyArg
     const Temp temp = s < 0 ? Temp{-1.f, false, true} : temp_of(a, s);
     const bool needed = !temp.bad && !(draft && temp.greedy);
     if (chunk == 0 && tid == 0) a.scale[item] = !needed ? -1.f : temp.greedy ? 0.f : temp.it;
-    if (!needed) return;
+    if (!needed) {
+        if (tid == 0) a.maxima[blockIdx.x] = NAN;          // (see above)
+        return;
+    }
     const Row<L> rw(draft ? a.draft : a.logits, draft ? a.ld_draft : a.ld, row, a.V);
     const int v0 = chunk * a.max_per + tid, v1 = min(rw.n, (chunk + 1) * a.max_per);
     uint4 held[kChunkHeld];
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyAr
             for (int q = 0; q <= with; ++q) {
                 const float l = in ? load_one<L>(q ? a.draft : a.logits, (r0 + j) * (q ? a.ld_draft : a.ld) + x) : 0.f;
                 const RowInfo r = row_info(a, r0 + j + q * a.T, lane);
-                bad = bad || r.bad;
+                bad = bad || r.bad || (temp.greedy && r.best >= a.V);      // (the latter: a row of two sequences, weighed for the other)
                 if (q == 0) best = r.best;
                 if (lane == 0) {
                     s_l.z[warp][q] = r.z;

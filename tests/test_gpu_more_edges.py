@@ -302,3 +302,27 @@ def test_prompts_and_single_tokens_in_one_call(lengths, rows):
     st = status_tensor()
     got = host(c.run(st=st))
     assert st.tolist() == [3, 0] and np.array_equal(got[0], c.score[0]) and np.array_equal(got[1:], good[1:])
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("temps", [(np.nan, 1.0, 1.0), (np.nan, 1.0, 0.0), (0.0, 1.0, 1.0), (1.0, 1.0, 0.0), (1.0, 0.0, 0.5)])
+def test_starts_that_give_a_row_to_two_sequences(many, temps):
+    """A bad q_start is reported; what its neighbours answer stays within their rows and the vocabulary."""
+    rng = np.random.default_rng(45)
+    V, extra = 700, 310 if many else 0
+    T = 6 + extra
+    logits, draft = (dev(rng.normal(size=(T, V)).astype(np.float32)) for _ in range(2))
+    tokens, uniform = dev(rng.integers(0, V, T).astype(np.int32)), dev(rng.random(T).astype(np.float32))
+    q_start = dev(np.array([0, 5, 2, 6] + list(range(7, 7 + extra)), np.int32))
+    S = 3 + extra
+    temp = dev(np.array(list(temps) + [1.0] * extra, np.float32))
+    for model in (None, draft):
+        acc, nxt, n_new = (torch.full((S,), -77, dtype=torch.int32, device=DEV) for _ in range(3))
+        ws, st = torch.full((moe.verify_workspace(T, S, V),), 255, dtype=torch.uint8, device=DEV), status_tensor()
+        moe.moe_verify_drafts(logits, tokens, uniform, q_start, acc, nxt, n_new, draft_logits=model, temperature=temp, workspace=ws, st=st)
+        a, n = host(acc), host(nxt)
+        assert st.tolist()[0] != 0 and a[1] == 0 and n[1] == -1
+        assert ((a >= 0) & (a <= 4)).all() and ((n >= -1) & (n < V)).all()
+        if extra:
+            want = _verify.verify(host(logits)[6:], host(tokens)[6:], host(uniform)[6:], np.arange(extra + 1), None, np.ones(extra, np.float32))
+            assert np.array_equal(a[3:], want[0]) and np.array_equal(n[3:], want[1])
