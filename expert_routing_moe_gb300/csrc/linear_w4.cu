@@ -11,8 +11,8 @@
 // memory in a fixed order.  A piece of weights is on its way while the one
 // before is multiplied, the first one's bytes before the kernel before has ended.
 //
-// What bounds it: one token through 5120 x 2048 takes 3.7 us (the call's host
-// time), a head of 128001 x 2048 for five tokens 36.6 us for 148 MB (4.0 TB/s;
+// What bounds it: one token through 5120 x 2048 takes 3.7 us (a chain of
+// loads; 3.1 us of host time), a head of 128001 x 2048 for five tokens 36.6 us for 148 MB (4.0 TB/s;
 // 22 us at the rate of a copy): 15 instructions turn eight codes into bf16,
 // 25 codes a clock and SM, and 443 go with a piece of 32 x 128 in all, at
 // 63% of the issue slots.  (Two pieces ahead: 41.5 us, a CTA less fits; four
