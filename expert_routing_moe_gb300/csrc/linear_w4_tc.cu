@@ -17,7 +17,7 @@
 //
 // Warps: 0-15 convert (eight for each half, in two groups that take the steps in
 // turn) and write the outputs, 16 and 17 issue a half's products each, 18 copies the
-// weights' tiles, 19 the tokens (or 19-22, with plain loads, where rows of x do not start at 16-byte boundaries).
+// weights' tiles, 19 the tokens (or 19-26, with plain loads, where rows of x do not start at 16-byte boundaries).
 // TMEM columns: D 2 x 192, A 2 halves x 2 buffers x 32.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -46,7 +46,10 @@ constexpr int kBBytes = kMaxTok * kStep * 2;
 constexpr int kRawOff = kB * kBBytes;
 constexpr int kSmem = kRawOff + kHalves * kRaw * kW4Bytes + 1024;   // slack for 1024-byte alignment
 constexpr int kColA = kHalves * kMaxTok;  // TMEM column of the A buffers
-constexpr int kLoaders = 4;               // warps that load x where TMA cannot
+constexpr int kTeams = 2;                 // of warps that load x where TMA cannot: they take the steps in turn
+constexpr int kTeam = 4;                  // warps of one
+constexpr int kLoaders = kTeams * kTeam;
+constexpr int kLoadTok = kTeam * 16;      // tokens of a team at a time
 constexpr int kConv = 16;                 // warps that convert
 constexpr int kWarpMma = kConv, kWarpW = kConv + 2, kWarpX = kConv + 3;
 
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
     if (threadIdx.x == 0) {
         for (int i = 0; i < kHalves * kRaw; ++i) { mbar_init(bar(B_WF + i), 1); mbar_init(bar(B_WE + i), 8); }
         for (int i = 0; i < 4; ++i) { mbar_init(bar(B_AF + i), 4); mbar_init(bar(B_AE + i), 1); }
-        for (int i = 0; i < kB; ++i) { mbar_init(bar(B_BF + i), TMA ? 1 : kLoaders); mbar_init(bar(B_BE + i), kHalves); }
+        for (int i = 0; i < kB; ++i) { mbar_init(bar(B_BF + i), TMA ? 1 : kTeam); mbar_init(bar(B_BE + i), kHalves); }
         mbar_init(bar(B_DF), kHalves);
         mbar_init(bar(B_DE), kConv);
         for (int i = 0; i < kHalves; ++i) mbar_init(bar(B_DRAIN + i), 1);
@@ -164,21 +167,87 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
                     }
             }
         } else {
-            for (int i = first; i < w.total && ok; i += by)
-                for (int k = 2 * c0; k < 2 * c1 && ok; ++k, ++n) {
-                    const int st = n % kB;
-                    ok = mbar_wait(bar(B_BE + st), ((n / kB) & 1) ^ 1, &s_abort, a.st, kSiteBEmpty);
-                    ok = __all_sync(kFull, ok);
-                    if (!ok) break;
-                    uint8_t* dst = smem + st * kBBytes;
-                    for (int u = threadIdx.x - kWarpX * 32; u < tok * 8; u += kLoaders * 32) {
-                        const int r = u >> 3, seg = u & 7;
-                        *reinterpret_cast<uint4*>(dst + r * 128 + ((seg ^ (r & 7)) * 16)) = load_x8(a, w.t0(i) + r, k * kStep + seg * 8);
-                    }
+            // A thread has half of a token's 64 numbers, 64 tokens at a time: five 16-byte words that hold them, shifted into
+            // place.  The words of the two turns to come are on their way meanwhile.
+            const int team = (warp - kWarpX) / kTeam, half = threadIdx.x & 1, r = (threadIdx.x - kWarpX * 32) % (kTeam * 32) >> 1;
+            const int turns = (tok + kLoadTok - 1) / kLoadTok, k0 = 2 * c0 + team;      // (a tile has an even number of steps)
+            n = team;
+            struct At {
+                int i, k, turn, t;                         // t: token of the thread's first turn
+            };
+            auto next = [&](At& at) {
+                if (++at.turn < turns) return;
+                at.turn = 0;
+                if ((at.k += kTeams) < 2 * c1) return;
+                at.k = k0;
+                at.i += by;
+                at.t = w.t0(at.i) + r;
+            };
+            const __nv_bfloat16* x0 = a.x + half * 32;
+            auto place = [&](const At& at, const __nv_bfloat16*& p, int& left) {
+                const int t = at.t + at.turn * kLoadTok;
+                p = x0 + (t * a.ld_x + at.k * kStep);
+                left = t < a.T ? max(0, min(32, a.K - half * 32 - at.k * kStep)) : 0;       // numbers that there are
+            };
+            auto fetch = [&](uint32_t (&v)[20], const At& at) {
+                if (at.i >= w.total) return;
+                const __nv_bfloat16* p;
+                int left;
+                place(at, p, left);
+                const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+                const uint4* words = reinterpret_cast<const uint4*>(from & ~static_cast<uintptr_t>(15));
+                const int bytes = left > 0 ? static_cast<int>(from & 15) + 2 * left : 0;
+#pragma unroll
+                for (int x = 0; x < 5; ++x) {
+                    const uint4 q = 16 * x < bytes ? __ldg(words + x) : make_uint4(0u, 0u, 0u, 0u);
+                    v[4 * x] = q.x; v[4 * x + 1] = q.y; v[4 * x + 2] = q.z; v[4 * x + 3] = q.w;
+                }
+            };
+            At here = {first, k0, 0, w.t0(first) + r}, ahead = here;
+            auto turn = [&](uint32_t (&v)[20]) {
+                const int st = n % kB;
+                if (here.turn == 0) ok = wait_warp(bar(B_BE + st), ((n / kB) & 1) ^ 1, &s_abort, a.st, kSiteBEmpty);
+                if (!ok) return;
+                const __nv_bfloat16* p;
+                int left;
+                place(here, p, left);
+                const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15), to = here.turn * kLoadTok + r;
+                // whole words, two and one at a time, then half a word
+#pragma unroll
+                for (int x = 0; x < 18; ++x) v[x] = off & 8 ? v[x + 2] : v[x];
+#pragma unroll
+                for (int x = 0; x < 17; ++x) v[x] = off & 4 ? v[x + 1] : v[x];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) v[x] = __funnelshift_r(v[x], v[x + 1], (off & 2) * 8);
+                if (left < 32) {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) v[x] = left >= 2 * x + 2 ? v[x] : left == 2 * x + 1 ? v[x] & 0xffffu : 0u;
+                }
+                if (to < tok) {
+                    uint8_t* dst = smem + st * kBBytes + to * 128;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        *reinterpret_cast<uint4*>(dst + (((half * 4 + x) ^ (to & 7)) * 16)) = make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                }
+                if (here.turn == turns - 1) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_BF + st));
+                    n += kTeams;
                 }
+                next(here);
+                fetch(v, ahead);
+                next(ahead);
+            };
+            uint32_t even[20], odd[20];
+            fetch(even, ahead);
+            next(ahead);
+            fetch(odd, ahead);
+            next(ahead);
+            while (ok && here.i < w.total) {
+                turn(even);
+                if (ok && here.i < w.total) turn(odd);
+            }
         }
     } else if (warp >= kWarpMma && warp < kWarpMma + kHalves) {
         // ---------------- products: a warp for each half ----------------
