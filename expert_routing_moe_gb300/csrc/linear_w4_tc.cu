@@ -15,12 +15,18 @@
 // share a tile's columns and add up their parts through each other's shared
 // memory: 300 tokens through 8192 x 2048 30.4 -> 18.6 us, 100 44.7 -> 14.1.
 //
+// Rows of x that start anywhere are loaded by eight warps, which costs a step 1150 clocks instead of 630: 43 tokens
+// through 6847 x 36585 70 us (6848: 41), 1000 through 2049 x 5120 42 (2056: 17).  (Four warps a unit of eight numbers at a
+// time: 256 us; eight lanes a token, four turns ahead: 118; warps whose rows begin alike, so that only halves
+// are shifted: 69.)
+//
 // Warps: 0-15 convert (eight for each half, in two groups that take the steps in
 // turn) and write the outputs, 16 and 17 issue a half's products each, 18 copies the
 // weights' tiles, 19 the tokens (or 19-26, with plain loads, where rows of x do not start at 16-byte boundaries).
 // TMEM columns: D 2 x 192, A 2 halves x 2 buffers x 32.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -448,14 +454,14 @@ cudaError_t launch(const LinearArgs& a, const LinearTile& t, cudaStream_t s) {
 }  // namespace
 
 // Tokens of a tile, and CTAs that share one: those that make the longest CTA's time shortest.  A step of 64 columns takes 4 clocks
-// a token and some 100 more, or 630 for the conversion of its weights, whichever is longer, and a tile its outputs; parts
+// a token and some 100 more, or 630 for the conversion of its weights (1150 where x is loaded without TMA), whichever is longer, and a tile its outputs; parts
 // meet in 2000 clocks more, and clusters of four and eight leave some SMs without work.  (2001 tokens through 5120 x 2048 with 64,
 // 96, 128, 144, 160 tokens a tile: 58.0, 37.6, 39.2, 28.1, 29.8 us; 8192 tokens with 128, 144, 160: 112, 104, 98 us.)
 LinearTile linear_w4_tile(const LinearArgs& a) {
     LinearTile best = {16, 1, 1e300};
     for (int tok = 16; tok <= kMaxTok && tok < a.T + 16; tok += 16) {
         const long long tiles = tiles_of(a, tok);
-        const double step = 4.0 * tok + 100.0 > 630.0 ? 4.0 * tok + 100.0 : 630.0;
+        const double least = a.wide ? 630.0 : 1150.0, step = std::max(4.0 * tok + 100.0, least);
         for (int split = 1; split <= kMaxSplit && split <= a.kt; split *= 2) {
             if (split > 1 && tiles > clusters_of(split)) break;
             const long long waves = split > 1 ? 1 : (tiles + sm_count() - 1) / sm_count();
