@@ -144,7 +144,7 @@ __device__ __forceinline__ float max_run<__nv_bfloat16>(uint4 x) {
 }
 
 // What two tokens weigh relative to the row's strongest: 2^t, t = n + f, the series of 2^f by Horner.  Every operation is
-// rounded as the definition has it (a product by -1 is exact, so t - n may be a fused product).
+// rounded as the definition has it (a product by -1 is exact, so t - n may be a fused product).  For logits up to m.
 struct Scale {
     float2 minus_m, it;
     __device__ Scale(float m, float it_) : minus_m(make_float2(-m, -m)), it(make_float2(it_, it_)) {}
@@ -516,16 +516,17 @@ struct Draw {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    // the weights of a run's numbers two by two; less than half a unit outside the row
+    // the weights of a run's numbers two by two; less than half a unit in the places outside the row, where both are -inf
     template <typename F>
     __device__ __forceinline__ void run(int v, uint4 x, uint4 y, F use) const {
         const int e = p.first(v);
         x = mask_run(p, x, v);
+        // (a logit above its row's maximum, as what lies beside the row may be, has no weight: its exponent can reach the sign)
+        if (mode == 2) y = mask_run(p, y, v);
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
             float2 w = weight2(make_float2(as_float<L>(x, i), as_float<L>(x, i + 1)), sp);
             if (mode == 2) {
-                // (p is nothing outside the row, and what is negative then is nothing too)
                 const float2 o = mul2(weight2(make_float2(as_float<L>(y, i), as_float<L>(y, i + 1)), sq), both(iq));
                 w = fma2(o, both(-1.f), mul2(w, both(ip)));
                 w = make_float2(fmaxf(w.x, 0.f), fmaxf(w.y, 0.f));
