@@ -60,7 +60,7 @@ struct VerifyArgs {
     int items;                       // rows of the target, then of the drafting model
     int max_chunks, max_per;         // chunks of a row and their 16-byte runs, for the maxima
     int chunks, per;                 // for the sums
-    float* scale;                    // [items]: 1 / temperature, 0: greedy, below: not needed
+    float* scale;                    // [items]: what the row was weighed with: 1 / temperature, 0: greedy, below: it was not
     float* maxima;                   // [items][max_chunks]
     ChunkSum* sums;                  // [items][chunks]
     moe_dev_status* st;
@@ -217,6 +217,8 @@ __device__ __forceinline__ Temp temp_of(const VerifyArgs& a, int s) {
     r.it = r.bad || r.greedy ? 1.f : __fdiv_rn(kLog2eF, t);
     return r;
 }
+// What a sequence's rows are weighed with, as it stands beside their sums.
+__device__ __forceinline__ float scale_of(const Temp& t) { return t.bad ? -1.f : t.greedy ? 0.f : t.it; }
 // Rows of sequence s; none if they are not rows of the step.
 __device__ __forceinline__ bool seq_rows(const VerifyArgs& a, int s, int& r0, int& r1) {
     r0 = a.q_start[s];
@@ -230,6 +232,21 @@ __device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
     return v;
+}
+
+// Sequence of an item's row, -1 without one.  Bad starts can give a row to several: it is the first one's, so that all
+// CTAs of the row find the same.
+template <int THREADS>
+__device__ __forceinline__ int find_seq(const VerifyArgs& a, int row, bool draft, int* s_seq) {
+    if (threadIdx.x == 0) *s_seq = 0x7fffffff;
+    __syncthreads();
+    for (int s = threadIdx.x; s < a.S; s += THREADS) {
+        const int r0 = __ldg(a.q_start + s), r1 = __ldg(a.q_start + s + 1);
+        // a drafting model's row is read for the draft behind it
+        if (r0 >= 0 && r0 <= row && row + (draft ? 1 : 0) < r1 && r1 <= a.T) atomicMin(s_seq, s);
+    }
+    __syncthreads();
+    return *s_seq == 0x7fffffff ? -1 : *s_seq;
 }
 
 // What acceptance needs of a row: the sum of its weights, its largest logit, the weight of the draft behind it and 2^42 / z.
@@ -270,29 +287,23 @@ __global__ void __launch_bounds__(kThreads, 2) verify_rows_kernel(const VerifyAr
     const int item = blockIdx.x / parts;
     const bool draft = item >= a.T;
     const int row = draft ? item - a.T : item;
-    if (tid == 0) s_seq = -1;
     cluster.barrier_arrive();        // waited for before the cluster's shared memory is written
     const Row<L> rw(draft ? a.draft : a.logits, draft ? a.ld_draft : a.ld, row, a.V);
     const int v0 = static_cast<int>(static_cast<long long>(rw.n) * part / parts), v1 = static_cast<int>(static_cast<long long>(rw.n) * (part + 1) / parts);
     uint4 held[kHeld];
-    __syncthreads();
     pdl_wait();
     pdl_trigger();
     // the row is on its way while its sequence is looked for
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
         if (v0 + tid + i * kThreads < v1) held[i] = __ldg(rw.runs + v0 + tid + i * kThreads);
-    for (int s = tid; s < a.S; s += kThreads) {
-        const int r0 = a.q_start[s], r1 = a.q_start[s + 1];
-        // a drafting model's row is read for the draft behind it
-        if (r0 >= 0 && r0 <= row && row + (draft ? 1 : 0) < r1 && r1 <= a.T) s_seq = s;
-    }
-    __syncthreads();
+    const int s = find_seq<kThreads>(a, row, draft, &s_seq);
     cluster.barrier_wait();
-    const int s = s_seq;
     const Temp temp = s < 0 ? Temp{1.f, false, true} : temp_of(a, s);
-    if (temp.bad || (draft && temp.greedy)) {              // the whole cluster
-        if (part == 0 && tid == 0) a.maxima[item] = NAN;   // (where bad starts give a row to two sequences the other one finds it bad)
+    const bool needed = !temp.bad && !(draft && temp.greedy);
+    if (part == 0 && tid == 0) a.scale[item] = needed ? scale_of(temp) : -1.f;
+    if (!needed) {                                         // the whole cluster
+        if (part == 0 && tid == 0) a.maxima[item] = NAN;   // (a sequence that reads the row all the same finds it bad)
         return;
     }
     float m = -INFINITY;
@@ -357,21 +368,6 @@ __global__ void __launch_bounds__(kThreads, 2) verify_rows_kernel(const VerifyAr
     }
 }
 
-// Sequence of an item's row, -1 without one.
-__device__ __forceinline__ int find_seq(const VerifyArgs& a, int row, bool draft, int* s_seq) {
-    if (threadIdx.x == 0) *s_seq = -1;
-    __syncthreads();
-    for (int s = threadIdx.x; s < a.S; s += kMaxThreads) {
-        const int r0 = __ldg(a.q_start + s), r1 = __ldg(a.q_start + s + 1);
-        // a drafting model's row is read for the draft behind it
-        if (r0 >= 0 && r0 <= row && row + (draft ? 1 : 0) < r1 && r1 <= a.T) *s_seq = s;
-    }
-    __syncthreads();
-    const int s = *s_seq;
-    if (s < 0) return -1;
-    return s;
-}
-
 template <typename L>
 __global__ void __launch_bounds__(kMaxThreads) verify_max_kernel(const VerifyArgs a) {
     __shared__ int s_seq;
@@ -382,10 +378,10 @@ __global__ void __launch_bounds__(kMaxThreads) verify_max_kernel(const VerifyArg
     const int row = draft ? item - a.T : item;
     pdl_wait();
     pdl_trigger();
-    const int s = find_seq(a, row, draft, &s_seq);
-    const Temp temp = s < 0 ? Temp{-1.f, false, true} : temp_of(a, s);
+    const int s = find_seq<kMaxThreads>(a, row, draft, &s_seq);
+    const Temp temp = s < 0 ? Temp{1.f, false, true} : temp_of(a, s);
     const bool needed = !temp.bad && !(draft && temp.greedy);
-    if (chunk == 0 && tid == 0) a.scale[item] = !needed ? -1.f : temp.greedy ? 0.f : temp.it;
+    if (chunk == 0 && tid == 0) a.scale[item] = needed ? scale_of(temp) : -1.f;
     if (!needed) {
         if (tid == 0) a.maxima[blockIdx.x] = NAN;          // (see above)
         return;
@@ -473,16 +469,18 @@ __global__ void __launch_bounds__(kSumThreads, 8) verify_sum_kernel(const Verify
     if (lane == 0) a.sums[unit] = {sum, 0x7fffffff, 0};
 }
 
-// A row's maximum and sum, by a warp.
+// A row's maximum and sum, by a warp, for a sequence that takes them with `scale`.  Bad too where the row was weighed for another
+// sequence with another temperature.
 struct RowInfo {
     float m;
     bool bad;
     long long z;
     int best;
 };
-__device__ __forceinline__ RowInfo row_info(const VerifyArgs& a, int item, int lane) {
+__device__ __forceinline__ RowInfo row_info(const VerifyArgs& a, int item, float scale, int lane) {
+    const float with = __ldcg(a.scale + item);
     RowInfo r = {row_max(a, item, lane), false, 0, 0x7fffffff};
-    r.bad = !(r.m - r.m == 0.f);
+    r.bad = !(r.m - r.m == 0.f) || with != scale;
     if (r.bad) return r;
     for (int i = lane; i < a.chunks; i += 32) {
         const int4 c = __ldcg(reinterpret_cast<const int4*>(a.sums + static_cast<size_t>(item) * a.chunks + i));
@@ -591,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyAr
 #pragma unroll 1
             for (int q = 0; q <= with; ++q) {
                 const float l = in ? load_one<L>(q ? a.draft : a.logits, (r0 + j) * (q ? a.ld_draft : a.ld) + x) : 0.f;
-                const RowInfo r = row_info(a, r0 + j + q * a.T, lane);
-                bad = bad || r.bad || (temp.greedy && r.best >= a.V);      // (the latter: a row of two sequences, weighed for the other)
+                const RowInfo r = row_info(a, r0 + j + q * a.T, scale_of(temp), lane);
+                bad = bad || r.bad;
                 if (q == 0) best = r.best;
                 if (lane == 0) {
                     s_l.z[warp][q] = r.z;

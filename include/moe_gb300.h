@@ -811,7 +811,8 @@ moe_status_t moe_linear_w4(const void* x, long long ld_x, int T, const moe_w4* w
  * draft_logits), and so is a temperature that is NaN, negative or infinite
  * (detail = -1 - sequence) and a draft outside [0, V) (MOE_DEV_BAD_INDEX, detail = row):
  * such a sequence has accepted 0 and next -1.  A bad q_start is reported (MOE_DEV_BAD_INDEX, detail = sequence)
- * and its sequence counts as without rows.
+ * and its sequence counts as without rows; where starts around it give a row to several sequences,
+ * the row is weighed for the first of them, and one with another temperature has accepted 0 and next -1.
  *
  * Whole numbers decide, so that results do not depend on the order of a sum:
  * with m the row's maximum, it = log2(e) / temperature,
