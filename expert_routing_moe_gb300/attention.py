@@ -91,9 +91,8 @@ class KvPages:
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
                 n = self.score.shape[0]
                 own = torch.arange(n, device=parent.device)
-                # (parents that are refused leave everything as it was)
-                good = ((parent >= -1) & (parent < n)).all()
-                self.score.copy_(self.score[torch.where(good & (parent >= 0), parent.long(), own)])
+                # (a parent that is refused leaves its own sequence as it was, and the others move)
+                self.score.copy_(self.score[torch.where((parent >= 0) & (parent < n), parent.long(), own)])
 
     def compact(self, stream=None) -> torch.Tensor:
         """Moves the pages in use to the lowest numbers; their count [1] int32."""
