@@ -54,7 +54,8 @@ __device__ __forceinline__ void put_y(const LinearArgs& a, int t, int n, float v
     else static_cast<float*>(a.y)[at] = a.add ? static_cast<float*>(a.y)[at] + v : v;
 }
 
-// How the kernel for many tokens cuts a call: tokens of a tile, CTAs that share one, and the clocks that it should take.
+// How the kernel for many tokens cuts a call: tokens of a tile, CTAs that share one, and the clocks that it should take (for rows of
+// x at 16-byte boundaries).
 struct LinearTile {
     int tok, split;
     double clocks;

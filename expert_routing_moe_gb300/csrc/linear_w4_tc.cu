@@ -457,19 +457,27 @@ cudaError_t launch(const LinearArgs& a, const LinearTile& t, cudaStream_t s) {
 // a token and some 100 more, or 630 for the conversion of its weights (1150 where x is loaded without TMA), whichever is longer, and a tile its outputs; parts
 // meet in 2000 clocks more, and clusters of four and eight leave some SMs without work.  (2001 tokens through 5120 x 2048 with 64,
 // 96, 128, 144, 160 tokens a tile: 58.0, 37.6, 39.2, 28.1, 29.8 us; 8192 tokens with 128, 144, 160: 112, 104, 98 us.)
-LinearTile linear_w4_tile(const LinearArgs& a) {
+static LinearTile best_tile(const LinearArgs& a, double least, int only) {
     LinearTile best = {16, 1, 1e300};
     for (int tok = 16; tok <= kMaxTok && tok < a.T + 16; tok += 16) {
         const long long tiles = tiles_of(a, tok);
-        const double least = a.wide ? 630.0 : 1150.0, step = std::max(4.0 * tok + 100.0, least);
+        const double step = std::max(4.0 * tok + 100.0, least);
         for (int split = 1; split <= kMaxSplit && split <= a.kt; split *= 2) {
             if (split > 1 && tiles > clusters_of(split)) break;
+            if (only > 0 && split != only) continue;
             const long long waves = split > 1 ? 1 : (tiles + sm_count() - 1) / sm_count();
             const double clocks = static_cast<double>(waves) * (2.0 * ((a.kt + split - 1) / split) * step + 1500.0 + 12.0 * tok) + (split > 1 ? 2000.0 + 8.0 * tok : 0.0);
             if (clocks < best.clocks) best = {tok, split, clocks};
         }
     }
     return best;
+}
+// The order of the sums goes by the kernel and by how many CTAs share a tile, so both are chosen as if x's rows started at
+// 16-byte boundaries; only a tile's tokens go by where they do start.
+LinearTile linear_w4_tile(const LinearArgs& a) {
+    LinearTile t = best_tile(a, 630.0, 0);
+    if (!a.wide) t.tok = best_tile(a, 1150.0, t.split).tok;
+    return t;
 }
 
 cudaError_t launch_linear_w4_tc(const LinearArgs& a, const LinearTile& t, cudaStream_t s) {

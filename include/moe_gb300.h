@@ -676,8 +676,8 @@ size_t moe_kv4_pool_workspace(int S, int n_pages);
  * The cache's values are not read.  Products run on the tensor cores with fp32
  * sums, keys exact: in fp16 with q scaled by a power of two of its row, or, where a
  * sequence has many rows, in bf16 (q as it is).  Exponentials and their sums are
- * fp32, added in an order that depends on sizes alone, so results are
- * reproducible bit for bit.  A page outside the pool, a length beyond the table
+ * fp32, added in an order that depends on the sizes, the sequences' lengths and rows and the
+ * device's number of SMs alone, so results are reproducible bit for bit.  A page outside the pool, a length beyond the table
  * or a bad q_start is reported (MOE_DEV_BAD_INDEX) and adds nothing.
  * Limits: those of moe_attention_kv4.
  */
@@ -769,8 +769,8 @@ moe_status_t moe_w4_pack(const void* w, int dtype, long long ld, const moe_w4* o
  *   add   nonzero: added to what y holds (F32 only), e.g. a residual
  *   st    an internal wait that gave up (MOE_DEV_TIMEOUT); no number of x or w is reported
  * Products are exact, sums fp32, results rounded once to y's type.  Sums are added
- * in an order that depends on sizes alone, so results are reproducible bit
- * for bit.
+ * in an order that depends on the sizes and the device's number of SMs alone, not on
+ * where rows start, so results are reproducible bit for bit.
  * Limits: N, K <= 2^24, T <= 2^20.
  */
 moe_status_t moe_linear_w4(const void* x, long long ld_x, int T, const moe_w4* w, const float* bias, void* y,
