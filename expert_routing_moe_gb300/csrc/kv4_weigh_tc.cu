@@ -611,15 +611,13 @@ __global__ void __launch_bounds__(kKeys) weigh_join_kernel(const WeighArgs a, vo
 
 // q [T][n_kv][group][D] with rows ld_q numbers apart: boxes of 64 numbers, the group's heads, one key head, ntok tokens.
 bool map_queries(CUtensorMap* m, const WeighArgs& a, int ntok) {
-    auto fn = encode_fn();
-    if (fn == nullptr) return false;
     const cuuint64_t D = a.c.head_dim;
     cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(a.group), static_cast<cuuint64_t>(a.c.n_kv), static_cast<cuuint64_t>(a.T)};
     cuuint64_t strides[3] = {D * 2, D * 2 * a.group, static_cast<cuuint64_t>(a.ld_q) * 2};
     cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.group), 1, static_cast<cuuint32_t>(ntok)};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<__nv_bfloat16*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<__nv_bfloat16*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <int D>

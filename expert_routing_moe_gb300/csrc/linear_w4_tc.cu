@@ -416,14 +416,12 @@ __global__ void __launch_bounds__((kWarpX + (TMA ? 1 : kLoaders)) * 32, 1) linea
 
 // [T][K] bf16 with rows `ld` numbers apart, boxes of 64 columns and `tok` rows with the 128-byte swizzle.
 bool map_tokens(CUtensorMap* m, const LinearArgs& a, int tok) {
-    auto fn = encode_fn();
-    if (fn == nullptr) return false;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.T)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.ld_x) * 2};
     cuuint32_t box[2] = {kStep, static_cast<cuuint32_t>(tok)};
     cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<__nv_bfloat16*>(a.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<__nv_bfloat16*>(a.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <bool TMA, bool SPLIT>
