@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kMaxStaged = 128 * 1024;   // bytes of x in shared memory
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -238,10 +239,13 @@ __global__ void __launch_bounds__(kThreads) w4_pack_kernel(const W* w, long long
 template <int NT, int MT, bool STAGED>
 cudaError_t launch_few(const LinearArgs& a, int sms, cudaStream_t s) {
     constexpr int rows = 16 * MT;
-    const size_t red = kWarps * 8 * NT * (rows + 4) * sizeof(float);
+    constexpr int red = kWarps * 8 * NT * (rows + 4) * sizeof(float);
     const size_t smem = 2 * red + (STAGED ? static_cast<size_t>(a.kt) * kW4Tile * 16 * NT : 0);
-    if (smem > 48 * 1024) {          // (a call of some 0.3 us that a short product can do without)
-        const cudaError_t e = cudaFuncSetAttribute(linear_w4_kernel<NT, MT, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // (a call of some 0.3 us that a short product can do without; it sets the most that there is, so that threads do not undo each
+    // other's setting)
+    if (smem > 48 * 1024) {
+        constexpr int room = 2 * red + (STAGED ? kMaxStaged : 0);
+        const cudaError_t e = cudaFuncSetAttribute(linear_w4_kernel<NT, MT, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
         if (e != cudaSuccess) return e;
     }
     const int steps = (a.N + rows - 1) / rows, fit = static_cast<int>((227 * 1024) / (smem + 1024));
@@ -259,7 +263,7 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
     if (a.N <= 16 * sms * 2) return launch_few<NT, 1, false>(a, sms, s);
     // (more than 16 tokens through that many rows go to the kernel for many)
     if constexpr (NT < 4)
-        if (a.N > 32 * sms * 3 && static_cast<size_t>(a.kt) * kW4Tile * 16 * NT <= 128 * 1024) return launch_few<NT, 2, true>(a, sms, s);
+        if (a.N > 32 * sms * 3 && static_cast<size_t>(a.kt) * kW4Tile * 16 * NT <= kMaxStaged) return launch_few<NT, 2, true>(a, sms, s);
     return launch_few<NT, 2, false>(a, sms, s);
 }
 
