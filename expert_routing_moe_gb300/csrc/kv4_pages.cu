@@ -345,8 +345,10 @@ cudaError_t launch_kv4_reserve(const moe_kv4_pool& p, const int32_t* n_new, void
 
 cudaError_t launch_kv4_assign(const moe_kv4_pool& p, const int32_t* parent, moe_dev_status* st, cudaStream_t s) {
     if (p.max_pages < 1) return cudaSuccess;
-    const size_t smem = static_cast<size_t>(p.S) * (kAssignCols + 1) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(kv4_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    constexpr int seq = (kAssignCols + 1) * sizeof(int);
+    const size_t smem = static_cast<size_t>(p.S) * seq;
+    // (the most that there is, so that threads with pools of other sizes do not undo each other's setting)
+    cudaError_t e = cudaFuncSetAttribute(kv4_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPoolMaxSeqs * seq);
     if (e != cudaSuccess) return e;
     return launch_pdl(kv4_assign_kernel, dim3((p.max_pages + kAssignCols - 1) / kAssignCols), dim3(kAssignThreads), smem, s, p, parent, st);
 }

@@ -48,3 +48,18 @@ def test_heads_of_other_widths(T, widths):
     torch.cuda.synchronize()
     assert _at_once(calls, 20000) == []
     assert all(torch.equal(want, y) for want, y in outs)
+
+
+def test_forks_of_few_and_of_many_sequences():
+    """A fork's tables pass through shared memory, whose size goes by the number of sequences."""
+    calls, pools = [], []
+    for S in (3, 2500):
+        pages = moe.KvPages(1, S, 1, 64, S, 64, DEV)
+        pages.reserve(torch.full((S,), 5, dtype=torch.int32, device=DEV))
+        parent, s = torch.arange(S, dtype=torch.int32, device=DEV).flip(0).contiguous(), torch.cuda.Stream()
+        pools.append((pages, pages.page_table.clone()))
+        calls.append(lambda pages=pages, parent=parent, s=s: moe.moe_kv4_assign(pages.pool, parent, pages.status, stream=s))
+    torch.cuda.synchronize()
+    assert _at_once(calls, 20000) == []
+    # (an even number of turns)
+    assert all(torch.equal(pages.page_table, table) and pages.device_status()[0] == 0 for pages, table in pools)
