@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     int want = k;                       // of those whose higher bits are the prefix's
     for (int pass = 0; pass < 3 && k > 0; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        for (int j = m0 + tid; j < m1; j += kSelThreads) {
+        // (unsigned: a step beyond the last place of the longest tables is not below it)
+        for (unsigned j = static_cast<unsigned>(m0) + tid; j < static_cast<unsigned>(m1); j += kSelThreads) {
             const uint32_t o = order_of(score[j]);
             if (pass == 0 || (o >> (shift + bits)) == (prefix >> (shift + bits))) atomicAdd(&s_hist[o >> shift & ((1u << bits) - 1)], 1);
         }
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
         __syncthreads();
     }
     // prefix: the score of the last one that is kept; `want` of those that have it are, the first ones
-    const int each = (c1 - c0 + kSelThreads - 1) / kSelThreads, j0 = min(c1, c0 + tid * each), j1 = min(c1, j0 + each);
+    const int each = (c1 - c0 + kSelThreads - 1) / kSelThreads, j0 = min(c1, c0 + tid * each), j1 = j0 + min(c1 - j0, each);
     // 1: kept, 2: kept if it is among the first `want`, 0: not
     auto kind = [&](int j) {
         if (j < lo || j >= hi) return 1;
@@ -317,25 +318,26 @@ __device__ __forceinline__ void move_book(const EvictArgs& a, const EvictWs& w, 
     float* score = a.score + s * a.ld_score;
     // a score moves to a place at or before its own: what is written has been read
     constexpr int kEach = 12;
-    for (int i0 = 0; i0 < r.now; i0 += kMoveThreads * kEach) {
+    const unsigned now = r.now;           // (unsigned: a step beyond the last place of the longest tables is not below it)
+    for (unsigned i0 = 0; i0 < now; i0 += kMoveThreads * kEach) {
         int from[kEach];
         float v[kEach];
 #pragma unroll
         for (int u = 0; u < kEach; ++u) {
-            const int i = i0 + u * kMoveThreads + tid;
-            from[u] = i < r.now ? kept[i] : -1;
+            const unsigned i = i0 + u * kMoveThreads + tid;
+            from[u] = i < now ? kept[i] : -1;
         }
 #pragma unroll
         for (int u = 0; u < kEach; ++u) v[u] = from[u] >= 0 ? score[from[u]] : 0.f;
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < kEach; ++u) {
-            const int i = i0 + u * kMoveThreads + tid;
-            if (i < r.now) score[i] = v[u];
+            const unsigned i = i0 + u * kMoveThreads + tid;
+            if (i < now) score[i] = v[u];
         }
     }
     __syncthreads();
-    for (int i = r.now + tid; i < r.len; i += kMoveThreads) score[i] = 0.f;
+    for (unsigned i = now + tid; i < static_cast<unsigned>(r.len); i += kMoveThreads) score[i] = 0.f;
     int32_t* row = a.p.page_table + static_cast<long long>(s) * a.p.max_pages;
     const int* old_page = w.old_page + static_cast<long long>(s) * a.p.max_pages;
     const int* rank = w.rank + static_cast<long long>(s) * a.p.max_pages;
@@ -509,7 +511,8 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const Evict
         for (int c0 = r.first + part * kMovePages; c0 - part * kMovePages < end; c0 += parts * kMovePages) {
             __syncthreads();                               // the sources before have been read
             if (tid < kMovePages * kPage) {
-                const int i = c0 * kPage + tid, src = i < r.now ? kept[i] : -1;
+                const long long i = static_cast<long long>(c0) * kPage + tid;
+                const int src = i < r.now ? kept[i] : -1;
                 s_src[tid / kPage].set(tid % kPage, src < 0 ? nullptr : head + old_page[src / kPage] * a.p.page_bytes, src & (kPage - 1));
             }
             const int c = c0 + mine;
