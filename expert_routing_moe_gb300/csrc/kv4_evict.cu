@@ -14,14 +14,15 @@
 // up to 16 pages into registers, meets, then writes them: whatever it writes has
 // been read by then.  A sequence whose pages all go to free ones needs no meeting.
 //
-// 32001 tokens of 48 layers (4 heads of 128) cut to 8192: 182 us onto free pages,
-// 221 in place, of which the selection takes 23; 32 sequences of 8 layers 155.
+// 32001 tokens of 48 layers (4 heads of 128) cut to 8192: 168 us onto free pages,
+// 181 in place, of which the selection takes 23; 32 sequences of 8 layers 141 and 154.
 // 453 MB are to be moved, which is 67 us at the rate of a copy; kept tokens lie
 // scattered, 64 bytes of keys and as many of values that they share with a
 // neighbour, so that whole sectors of others come with them.  (A CTA a page, whose
 // threads look for their sources in the list: 353 us; sources of a page's tokens in
 // shared memory, three warps a page: 238; the next pages' sources looked for ahead: 207
-// against 200; four pages a CTA in three warps each 200, two pages 185, in six warps each 182;
+// against 200; four pages a CTA in three warps each 200, two pages 185, in six warps each 182, and 168
+// with a loop of its own for pages that need no meeting;
 // sources made out of line, so that nothing spills: 197.)
 #include <cooperative_groups.h>
 
@@ -520,17 +521,31 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const Evict
             uint8_t* to = nullptr;
             if (live) to = head + (rank[c] >= 0 ? w.free_pages[r.base + rank[c]] : old_page[c]) * a.p.page_bytes;
             __syncthreads();
+            if (apart) {
+                if (live && role < 2) {
+                    KeyPart<D> g;
+                    g.read(s_src[mine], role, lane);
+                    g.write(to, role, lane);
+                } else if (live) {
+                    ValuePart<D> g;
+                    g.read(s_src[mine], role - 2, lane);
+                    g.write(to, role - 2, lane);
+                }
+                continue;
+            }
             // what is written has been read by then (pages that come later read neither)
-            if (role < 2) {
-                KeyPart<D> g;
-                if (live) g.read(s_src[mine], role, lane);
-                if (!apart) meet(cluster, parts);
-                if (live) g.write(to, role, lane);
-            } else {
-                ValuePart<D> g;
-                if (live) g.read(s_src[mine], role - 2, lane);
-                if (!apart) meet(cluster, parts);
-                if (live) g.write(to, role - 2, lane);
+            union {                                        // (a warp has keys or values, in the same registers)
+                KeyPart<D> keys;
+                ValuePart<D> values;
+            } g;
+            if (live) {
+                if (role < 2) g.keys.read(s_src[mine], role, lane);
+                else g.values.read(s_src[mine], role - 2, lane);
+            }
+            meet(cluster, parts);
+            if (live) {
+                if (role < 2) g.keys.write(to, role, lane);
+                else g.values.write(to, role - 2, lane);
             }
         }
     }
