@@ -773,7 +773,8 @@ class Weight4:
     @classmethod
     def pack(cls, w, st=None, stream=None) -> "Weight4":
         """w [N][K] bf16 or fp32, rounded to 4 bits."""
-        out = cls.empty(w.shape[0], w.shape[1], w.device)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            out = cls.empty(w.shape[0], w.shape[1], w.device)
         moe_w4_pack(w, out, st, stream)
         return out
 
