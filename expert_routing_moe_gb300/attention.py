@@ -56,7 +56,8 @@ class KvPages:
 
     evicts: also has the workspace of evict(), and `score` [max_seqs][places of
     max_len] fp32, zero, which AttentionLayer.forward adds to.  Scores follow
-    their tokens in evict() and assign(), and restore() brings them back too."""
+    their tokens in evict() and assign(), and restore() brings them back too.
+    A token that comes in a pass without a score has what was last in its place."""
 
     def __init__(self, n_layers: int, n_pages: int, n_kv: int, head_dim: int, max_seqs: int, max_len: int, device="cuda", evicts: bool = False):
         cols = -(-max_len // abi.MOE_KV4_PAGE)
@@ -85,7 +86,8 @@ class KvPages:
         abi.moe_kv4_reserve(self.pool, n_new, self.workspace, self.status, stream)
 
     def assign(self, parent: torch.Tensor, stream=None):
-        """Sequence s becomes what parent[s] was; -1 frees it."""
+        """Sequence s becomes what parent[s] was, its score among it; -1 frees it.  A parent
+        outside [-1, max_seqs) is reported and its sequence kept (moe_kv4_assign)."""
         abi.moe_kv4_assign(self.pool, parent, self.status, stream)
         if self.score is not None:
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):

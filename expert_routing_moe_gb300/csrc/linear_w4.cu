@@ -13,9 +13,10 @@
 //
 // What bounds it: one token through 5120 x 2048 takes 3.7 us (a chain of
 // loads; 3.1 us of host time), a head of 128001 x 2048 for five tokens 36.6 us for 148 MB (4.0 TB/s;
-// 22 us at the rate of a copy): 15 instructions turn eight codes into bf16,
-// 25 codes a clock and SM, and 443 go with a piece of 32 x 128 in all, at
-// 63% of the issue slots.  (Two pieces ahead: 41.5 us, a CTA less fits; four
+// 22 us at the rate of a copy).  No unit is full: issue slots 64%, ALUs 55%, DRAM
+// 43%.  443 instructions go with a piece of 32 x 128, of which 240 turn codes into bf16 (15
+// for eight); with 2048 columns a warp has two pieces, then eight warps
+// store their sums, meet and add up eight, which is much of the rest.  (Two pieces ahead: 41.5 us, a CTA less fits; four
 // CTAs an SM: 39.5 with spills; sums of two steps joined at a time: 38.4;
 // pieces of all steps in equal runs for the warps, without a join a step: 43.7.)
 #include <cuda_bf16.h>
@@ -174,7 +175,8 @@ __global__ void __launch_bounds__(kThreads) linear_w4_kernel(const LinearArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// Packing: a warp for each row (of the padded ones too, whose tiles are zero).
+// Packing: a warp for each row (of the padded ones too, whose tiles are zero).  5120 x 2048 take 25 us in bf16 and 45 in fp32
+// (4 and 7 us of bytes): a lane's columns lie 32 apart from the next one's.  It runs once a weight.
 // ---------------------------------------------------------------------------
 template <typename W>
 __device__ __forceinline__ float load_w(const W* w, int k, int K) {
@@ -271,7 +273,8 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
 
 // Clocks that the kernel for few tokens should take, for 9 to 64 of them.  (Both sides, few / many: through 2048 x 2048 16
 // tokens 3.7 / 6.2 us, 32 5.1 / 6.8, 48 8.6 / 7.4, 64 9.6 / 8.1; 8192 x 2048: 9.6 / 10.3, 15.2 / 10.9, 25.6 / 11.5, 29.5 / 12.2; 2048 x
-// 5120: 6.0 / 7.5, 11.4 / 8.2, 15.6 / 8.8, 17.0 / 9.3; 2048 x 32000: 16.9 / 13.9, 28.4 / 14.2, 51 / 14.6, 55 / 15.0.)
+// 5120: 6.0 / 7.5, 11.4 / 8.2, 15.6 / 8.8, 17.0 / 9.3; 2048 x 32000: 16.9 / 13.9, 28.4 / 14.2, 51 / 14.6, 55 / 15.0.  Rows of x that
+// start anywhere, where the choice is the same: 32 tokens, 4096 x 2048 25.5 / 10.1; 15 tokens, 5391 x 26969 68 / 52.)
 static double few_clocks(const LinearArgs& a) {
     const double rows = a.N * 1e-3 * a.kt;
     return 1000.0 + rows * (a.T <= 16 ? 53.0 : a.T <= 32 ? 142.0 : 285.0);
